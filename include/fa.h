@@ -282,9 +282,106 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
                  void* dq, void* dk, void* dv, int B, int H, int Nq, int Nk, int d, float scale, int causal,
                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Paged K/V caches -------------------------------------------------------
+ * A pool of num_pages pages of `page` rows (16, 32, 64 or 128) holds the keys
+ * (another one the values) of many sequences, of K/V head hk in
+ *   k_pages, v_pages  [num_pages, Hkv, page, d]: bf16, or e4m3 codes (e4m3 != 0)
+ *   k_scale, v_scale  fp32 [num_pages, Hkv], e4m3 only: the real value of a code
+ *                     c of page i and head hk is e4m3(c) * scale[i, hk]
+ *   block_table       int32 [B, >= width]: page of positions 0 .. page-1 of
+ *                     sequence b, of the next `page` positions, and so on; rows
+ *                     table_stride apart (elements). Entries past a sequence's
+ *                     length are not read.
+ * Both entry points leave alone what they cannot place: a table entry that is
+ * not in [0, num_pages) is skipped (its keys are hidden, its rows not written),
+ * lengths are clipped to the cache. Such a call is reported afterwards by
+ * fa_get_device_status() as FA_ERR_INVALID_ARG. */
+
+/* Norms of query and key heads, position rotation, and append of k and v to a
+ * paged cache, in one pass over a step's projections.
+ *   q  bf16 [T, H, d]   k, v  bf16 [T, Hkv, d]   T new tokens, sequence after
+ *      sequence: those of sequence b are cu_seqlens[b] .. cu_seqlens[b+1]-1
+ *      (int32 [B+1] on the device), or T / B each when cu_seqlens is NULL.
+ *   seqlens_k  int32 [B]: lengths L_b with the new tokens counted (what
+ *      fa_decode_paged takes next), so token i of n_b is at position
+ *      p = L_b - n_b + i.
+ *   q_weight, k_weight  bf16 [d] or NULL: each head is first normalised,
+ *      x / sqrt(mean(x^2) + eps) * weight.
+ *   rot, turns, interleaved, rot_scale  The first `rot` elements of every q and
+ *      k head (a multiple of 16, 0 for none) are turned in pairs j, elements
+ *      (j, j + rot/2), or (2j, 2j + 1) when interleaved != 0, by the angle
+ *      2 pi frac(p * turns[j] / 2^64), times rot_scale:
+ *      (a, b) -> rot_scale * (a cos - b sin, b cos + a sin). turns: int64
+ *      [rot/2] on the device, the frequency in 2^-64 turns a position (modulo
+ *      2^64): the product modulo 2^64 is exact at every position.
+ *   q_out  bf16 [T, H, d]; may be q.   k_out  bf16 [T, Hkv, d], the turned keys
+ *      (for attention among the new tokens), or NULL; may be k.
+ *   strides  int64 [10], host memory: token and head strides, in elements, of q,
+ *      k, v, q_out, k_out in that order (multiples of 8; the d elements of a
+ *      head are contiguous), so q, k and v can be parts of one projection.
+ *   max_new  the most new tokens of one sequence when cu_seqlens is given (0:
+ *      not known; sequences with more are clipped and reported).
+ * k and v go to the row of their position, in bf16 or as e4m3 codes. The scale
+ * of an e4m3 page is a power of two, the least 2^e, e >= -40, with
+ * |x| <= 448 * 2^e over the rows of this sequence that the page holds. Rows that
+ * earlier calls wrote keep their scale while it suffices; when it grows their
+ * codes are rounded again to the new one. Rounding is to nearest even from the
+ * fp32 result; an infinity or NaN is stored as the NaN code and left out of the
+ * scale. A call that starts at row 0 of a page takes nothing from the page's old
+ * contents or scale.
+ * Every page that a call writes must belong to one sequence (pages shared by
+ * several sequences may be read, not appended to). Rows of q_out and k_out of
+ * tokens past cu_seqlens[B] are left as they were. T = 0 is a no-op. d = 64 or
+ * 128. One launch on `stream`. Errors: FA_ERR_INVALID_ARG for NULL tensors, bad
+ * sizes, H not a multiple of Hkv, T not a multiple of B without cu_seqlens;
+ * FA_ERR_UNSUPPORTED for other d, rot or page sizes, strides that are not
+ * multiples of 8, or pointers that are not 16-byte (turns 8-byte, other arrays
+ * 4-byte) aligned. */
+fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
+                          void* v_pages, float* k_scale, float* v_scale, const int* block_table, int64_t table_stride,
+                          const int* seqlens_k, const int* cu_seqlens, const int64_t* turns, const void* q_weight,
+                          const void* k_weight, const int64_t* strides, int B, int T, int H, int Hkv, int d,
+                          int num_pages, int page, int table_width, int e4m3, int rot, int interleaved,
+                          float rot_scale, float eps, int max_new, void* stream);
+
+/* Bytes of device workspace fa_decode_paged needs: the split-KV partial states
+ * (256 when one split suffices). Returns 0 for invalid arguments. */
+size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int num_splits);
+
+/* fa_decode_grouped over a paged cache: the last Nq tokens of every sequence
+ * attend to its keys in the pool. Sequence b holds L_b = seqlens_k[b] keys, its
+ * new ones among them; token t sees key j iff j <= L_b - Nq + t; query head h
+ * reads K/V head h / (H/Hkv). A token that sees no key gets o = 0, lse = -inf.
+ *   q, o       bf16 [B, H, Nq, d] with element strides q_strides, o_strides
+ *              (int64 [3], host memory: batch, head, token; multiples of 8; d
+ *              contiguous). Token-major tensors, as fa_append_paged returns them,
+ *              are passed by their strides.
+ *   lse        fp32 [B, H, Nq] (may be NULL)
+ *   max_len    no sequence is longer (a bound the host knows, at most the
+ *              positions a block-table row covers, and at most 2^30; longer ones
+ *              are clipped and reported). It sets the splits.
+ *   num_splits 1 .. 1024 splits of the keys (rounded to whole 128-key pieces), or
+ *              0: chosen so that the launch fills the GPU.
+ *   scales of e4m3 pages: any finite positive factors (fa_append_paged writes
+ *              powers of two, which add no rounding).
+ *   workspace  device memory of fa_decode_paged_workspace_size() bytes, 256-byte
+ *              aligned, owned by the caller, overwritten; calls that may overlap
+ *              on the GPU need their own. Unused (may be NULL) with one split.
+ * Products with e4m3 pages run in f16 on the codes, with fp32 accumulation and
+ * the weights rounded to f16; with bf16 pages in bf16. A NaN or infinity in v
+ * reaches the rows of its sequence's last Nq tokens. Errors as for
+ * fa_decode_grouped. One launch, two with more than one split. */
+fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
+                          const float* k_scale, const float* v_scale, const int* block_table, int64_t table_stride,
+                          const int* seqlens_k, void* o, const int64_t* o_strides, float* lse, int B, int H, int Hkv,
+                          int Nq, int d, int num_pages, int page, int max_len, int e4m3, float scale, int num_splits,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then returns and clears the device status word of
  * the current device: FA_ERR_TIMEOUT if a bounded wait gave up since the
- * last call, FA_ERR_CUDA if the stream reported an error, else FA_OK. */
+ * last call, FA_ERR_CUDA if the stream reported an error, FA_ERR_INVALID_ARG if
+ * a paged or packed call met a page, length or offset outside its arrays, else
+ * FA_OK. */
 fa_status fa_get_device_status(void* stream);
 
 /* Limit, in nanoseconds, on every wait inside the library's kernels

@@ -11,6 +11,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "fa.h"
@@ -21,6 +22,7 @@
 #include "materialized.cuh"
 #include "fa_common.cuh"
 #include "fa_debug.cuh"
+#include "paged.cuh"
 
 // Causal unit order for K/V larger than L2 (see below): off by default. With a
 // 40 MB budget the long-context launches read 1.3x their Q+K+V from DRAM
@@ -110,6 +112,10 @@ fa_status device_state(DeviceState** out) {
     if ((e = fa::bwd_set_attributes(128)) != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(bwd d=128)");
     if ((e = fa::materialized_set_attributes()) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(materialized softmax)");
+    if ((e = fa::append_paged_set_attributes()) != cudaSuccess)
+      return cuda_fail(e, "cudaFuncSetAttribute(paged append)");
+    if ((e = fa::decode_paged_set_attributes()) != cudaSuccess)
+      return cuda_fail(e, "cudaFuncSetAttribute(paged decode)");
     if ((e = fa::decode_grouped_set_attributes(64)) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(grouped decode d=64)");
     if ((e = fa::decode_grouped_set_attributes(128)) != cudaSuccess)
@@ -789,6 +795,200 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
   return FA_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Paged caches
+namespace {
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+// The split of a paged decode: `chunk` keys for each of `S` splits.
+struct PagedSplit {
+  int S, chunk;
+};
+// Without a request, splits are made until about PAGED_CTAS blocks run (several
+// rounds of two a SM, so that ragged lengths even out), none shorter than 128
+// keys (one tile for each warp of e4m3 pages at d = 128).
+constexpr int PAGED_CTAS = 2432;
+PagedSplit paged_split(int B, int Hkv, int R, int max_len, int num_splits) {
+  long long S = num_splits;
+  const long long len = std::max(1, max_len);
+  if (S <= 0) {
+    const long long rows = fa::decode_paged_rows(R);
+    const long long ctas = static_cast<long long>(B) * Hkv * ((R + rows - 1) / rows);
+    S = std::min((PAGED_CTAS + ctas - 1) / ctas, (len + 127) / 128);
+    S = std::max(1LL, std::min(S, 1024LL));
+  }
+  const long long chunk = ((len + S - 1) / S + 127) / 128 * 128;
+  S = (len + chunk - 1) / chunk;
+  return {static_cast<int>(S), static_cast<int>(chunk)};
+}
+
+bool paged_decode_sizes_ok(int B, int H, int Hkv, int Nq, int max_len, int num_splits) {
+  return B >= 1 && H >= 1 && Hkv >= 1 && Nq >= 1 && H % Hkv == 0 && max_len >= 0 && max_len <= (1 << 30) && num_splits >= 0 &&
+         num_splits <= 1024 && static_cast<long long>(H / Hkv) * Nq <= 128 &&
+         static_cast<long long>(B) * H * Nq <= INT_MAX;
+}
+
+// What the two paged entry points check of the pool alike.
+fa_status check_pool(const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                     const int* table, const int* seqlens, int num_pages, int page, int e4m3) {
+  if (!k_pages || !v_pages || !table || !seqlens)
+    return fail(FA_ERR_INVALID_ARG, "k_pages, v_pages, block_table and seqlens_k must be non-NULL");
+  if (num_pages < 1) return fail(FA_ERR_INVALID_ARG, "num_pages must be >= 1");
+  if (e4m3 && (!k_scale || !v_scale)) return fail(FA_ERR_INVALID_ARG, "e4m3 pages need k_scale and v_scale");
+  if (!fa::paged_page_ok(page)) return fail(FA_ERR_UNSUPPORTED, "page size %d unsupported (16, 32, 64 or 128)", page);
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16)) return fail(FA_ERR_UNSUPPORTED, "k_pages and v_pages must be 16-byte aligned");
+  for (const void* x : {static_cast<const void*>(k_scale), static_cast<const void*>(v_scale),
+                        static_cast<const void*>(table), static_cast<const void*>(seqlens)})
+    if (!aligned(x, 4)) return fail(FA_ERR_UNSUPPORTED, "scales, block_table and seqlens_k must be 4-byte aligned");
+  return FA_OK;
+}
+
+// Element strides of a strided operand: multiples of 8 (16-byte rows), not negative.
+bool strides_ok(std::initializer_list<int64_t> st) {
+  for (int64_t s : st)
+    if (s < 0 || s % 8 != 0) return false;
+  return true;
+}
+
+}  // namespace
+
+fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
+                          void* v_pages, float* k_scale, float* v_scale, const int* block_table, int64_t table_stride,
+                          const int* seqlens_k, const int* cu_seqlens, const int64_t* turns, const void* q_weight,
+                          const void* k_weight, const int64_t* strides, int B, int T, int H, int Hkv, int d,
+                          int num_pages, int page, int table_width, int e4m3, int rot, int interleaved,
+                          float rot_scale, float eps, int max_new, void* stream) {
+  t_detail[0] = 0;
+  if (B < 1 || T < 0 || H < 1 || Hkv < 1 || table_width < 1)
+    return fail(FA_ERR_INVALID_ARG, "need B, H, Hkv, table_width >= 1 and T >= 0 (got %d %d %d %d %d)", B, H, Hkv,
+                table_width, T);
+  if (H % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "H (%d) must be a multiple of Hkv (%d)", H, Hkv);
+  if (rot < 0 || rot > d) return fail(FA_ERR_INVALID_ARG, "rot (%d) must be in [0, d]", rot);
+  if (!std::isfinite(rot_scale) || !std::isfinite(eps) || eps < 0.f)
+    return fail(FA_ERR_INVALID_ARG, "rot_scale must be finite, eps finite and >= 0");
+  if (cu_seqlens == nullptr && T % B != 0)
+    return fail(FA_ERR_INVALID_ARG, "without cu_seqlens every sequence has T / B tokens: T (%d) must be a multiple of B (%d)",
+                T, B);
+  if (max_new < 0) return fail(FA_ERR_INVALID_ARG, "max_new must be >= 0");
+  if (static_cast<int64_t>(num_pages < 1 ? 1 : table_width) * page > INT_MAX)
+    return fail(FA_ERR_INVALID_ARG, "table_width * page is too large");
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
+  if (rot % 16 != 0) return fail(FA_ERR_UNSUPPORTED, "rot (%d) must be a multiple of 16", rot);
+  if (fa_status s = check_pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, num_pages, page, e4m3)) return s;
+  if (T == 0) return FA_OK;
+  if (!q || !k || !v || !q_out || !strides) return fail(FA_ERR_INVALID_ARG, "q, k, v, q_out and strides must be non-NULL");
+  if (rot > 0 && !turns) return fail(FA_ERR_INVALID_ARG, "a rotation needs turns");
+  for (const void* x : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_out), q_weight, k_weight})
+    if (!aligned(x, 16)) return fail(FA_ERR_UNSUPPORTED, "q, k, v, the outputs and the weights must be 16-byte aligned");
+  if (!aligned(turns, 8) || !aligned(cu_seqlens, 4)) return fail(FA_ERR_UNSUPPORTED, "turns must be 8-byte, cu_seqlens 4-byte aligned");
+  if (table_stride < table_width && B > 1) return fail(FA_ERR_INVALID_ARG, "table_stride is below table_width");
+  for (int i = 0; i < 10; ++i)
+    if (!strides_ok({strides[i]})) return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements and >= 0");
+  const int n_max = cu_seqlens == nullptr ? T / B : std::min(max_new > 0 ? max_new : T, T);
+  const long long rect = (static_cast<long long>(n_max) + page - 2) / page + 1;
+  const bool use_rect = cu_seqlens == nullptr || rect * B <= T / page + 2LL * B;
+  if ((use_rect ? rect * B : T / page + 2LL * B) * Hkv > INT_MAX)
+    return fail(FA_ERR_INVALID_ARG, "B, T and Hkv give too many blocks");
+
+  DeviceState* st = nullptr;
+  if (fa_status s = device_state(&st)) return s;
+  fa::AppendPagedParams p{};
+  p.q = q, p.k = k, p.v = v, p.q_out = q_out, p.k_out = k_out;
+  p.k_pages = k_pages, p.v_pages = v_pages, p.k_scale = k_scale, p.v_scale = v_scale;
+  p.table = block_table, p.seqlens = seqlens_k, p.cu = cu_seqlens;
+  p.turns = reinterpret_cast<const long long*>(turns);
+  p.q_weight = q_weight, p.k_weight = k_weight;
+  p.qst = strides[0], p.qsh = strides[1], p.kst = strides[2], p.ksh = strides[3], p.vst = strides[4];
+  p.vsh = strides[5], p.qost = strides[6], p.qosh = strides[7], p.kost = strides[8], p.kosh = strides[9];
+  p.table_stride = table_stride;
+  p.B = B, p.T = T, p.H = H, p.Hkv = Hkv, p.G = H / Hkv, p.d = d;
+  p.width = table_width, p.page = page, p.page_shift = log2_of(page), p.num_pages = num_pages;
+  p.rot = rot, p.interleaved = interleaved ? 1 : 0;
+  p.rot_scale = rot_scale, p.eps = eps;
+  p.max_new = n_max;
+  p.per_seq = use_rect ? static_cast<int>(rect) : 0;
+  p.status = st->status;
+  // Rows in parallel: all of a page's where the call has as many; the heads share what is left of 256 threads.
+  const int lanes = d / 16, groups = 256 / lanes;
+  int rows = 1;
+  while (rows < std::min(page, n_max) && rows < groups) rows *= 2;
+  p.rows_par = rows;
+  p.head_slots = std::max(1, std::min(groups / rows, p.G + 2));
+  p.stash_rows = std::min(page, n_max);
+  cudaError_t e = fa::launch_append_paged(e4m3 != 0, p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
+  t_launches += 1;
+  return FA_OK;
+}
+
+size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int num_splits) {
+  if (!paged_decode_sizes_ok(B, H, Hkv, Nq, max_len, num_splits) || (d != 64 && d != 128)) return 0;
+  const PagedSplit sp = paged_split(B, Hkv, H / Hkv * Nq, max_len, num_splits);
+  if (sp.S == 1) return 256;
+  const size_t parts = static_cast<size_t>(B) * H * Nq * sp.S;
+  return ((parts * d * 4 + 255) & ~size_t(255)) + ((parts * 8 + 255) & ~size_t(255));
+}
+
+fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
+                          const float* k_scale, const float* v_scale, const int* block_table, int64_t table_stride,
+                          const int* seqlens_k, void* o, const int64_t* o_strides, float* lse, int B, int H, int Hkv,
+                          int Nq, int d, int num_pages, int page, int max_len, int e4m3, float scale, int num_splits,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  t_detail[0] = 0;
+  if (!q || !o || !q_strides || !o_strides) return fail(FA_ERR_INVALID_ARG, "q, o and their strides must be non-NULL");
+  if (B < 1 || H < 1 || Hkv < 1 || Nq < 1 || max_len < 0 || max_len > (1 << 30))
+    return fail(FA_ERR_INVALID_ARG, "need B, H, Hkv, Nq >= 1 and max_len in [0, 2^30] (got %d %d %d %d %d)", B, H, Hkv, Nq,
+                max_len);
+  if (H % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "H (%d) must be a multiple of Hkv (%d)", H, Hkv);
+  if (num_splits < 0 || num_splits > 1024) return fail(FA_ERR_INVALID_ARG, "num_splits must be in [0, 1024]");
+  if (fa_status s = check_scale(scale)) return s;
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
+  const int R = H / Hkv > 128 ? 129 : H / Hkv * std::min(Nq, 129);
+  if (R > 128) return fail(FA_ERR_UNSUPPORTED, "(H / Hkv) * Nq query rows per K/V head; at most 128");
+  if (fa_status s = check_pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, num_pages, page, e4m3)) return s;
+  if (!aligned(q, 16) || !aligned(o, 16)) return fail(FA_ERR_UNSUPPORTED, "q and o must be 16-byte aligned");
+  if (!strides_ok({q_strides[0], q_strides[1], q_strides[2], o_strides[0], o_strides[1], o_strides[2]}))
+    return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements and >= 0");
+  if (lse && !aligned(lse, 4)) return fail(FA_ERR_UNSUPPORTED, "lse must be 4-byte aligned");
+  if (B > 1 && table_stride < (static_cast<int64_t>(max_len) + page - 1) / page)
+    return fail(FA_ERR_INVALID_ARG, "max_len needs %lld pages a sequence, table_stride is %lld",
+                (static_cast<long long>(max_len) + page - 1) / page, static_cast<long long>(table_stride));
+  const PagedSplit sp = paged_split(B, Hkv, R, max_len, num_splits);
+  const int rows = fa::decode_paged_rows(R), row_tiles = (R + rows - 1) / rows;
+  if (static_cast<long long>(B) * Hkv * sp.S * row_tiles > INT_MAX || static_cast<long long>(B) * H * Nq > INT_MAX)
+    return fail(FA_ERR_INVALID_ARG, "B * H * Nq * splits is too large");
+  const size_t need = fa_decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits);
+  if (sp.S > 1 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+    return fail(FA_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
+
+  DeviceState* st = nullptr;
+  if (fa_status s = device_state(&st)) return s;
+  fa::DecodePagedParams p{};
+  p.q = q, p.k = k_pages, p.v = v_pages, p.k_scale = k_scale, p.v_scale = v_scale;
+  p.table = block_table, p.table_stride = table_stride, p.seqlens = seqlens_k;
+  p.o = o, p.lse = lse;
+  p.qsb = q_strides[0], p.qsh = q_strides[1], p.qst = q_strides[2];
+  p.osb = o_strides[0], p.osh = o_strides[1], p.ost = o_strides[2];
+  p.B = B, p.H = H, p.Hkv = Hkv, p.G = H / Hkv, p.Nq = Nq, p.R = R;
+  p.max_len = max_len;
+  p.page = page, p.page_shift = log2_of(page), p.num_pages = num_pages;
+  p.S = sp.S, p.chunk = sp.chunk, p.row_tiles = row_tiles;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const size_t parts = static_cast<size_t>(B) * H * Nq * sp.S;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((parts * d * 4 + 255) & ~size_t(255)));
+  p.status = st->status;
+  cudaError_t e = fa::launch_decode_paged(d, e4m3 != 0, p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+  t_launches += sp.S == 1 ? 1 : 2;
+  return FA_OK;
+}
+
 fa_status fa_get_device_status(void* stream) {
   t_detail[0] = 0;
   DeviceState* st = nullptr;
@@ -804,6 +1004,10 @@ fa_status fa_get_device_status(void* stream) {
     if ((e = cudaMemsetAsync(st->status, 0, sizeof(word), s)) != cudaSuccess) return cuda_fail(e, "clear status");
     if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
   }
+  if (word & (fa::FA_DEV_BAD_PAGE | fa::FA_DEV_BAD_LENS) && !(word & fa::FA_DEV_TIMEOUT))
+    return fail(FA_ERR_INVALID_ARG, "%s", word & fa::FA_DEV_BAD_PAGE
+                                             ? "a block-table entry did not name a page of the pool; its rows were skipped"
+                                             : "lengths or offsets lay outside their arrays and were clipped");
   if (word & fa::FA_DEV_TIMEOUT) return fail(FA_ERR_TIMEOUT, "a bounded wait inside a kernel gave up");
   return FA_OK;
 }

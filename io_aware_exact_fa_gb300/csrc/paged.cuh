@@ -1,0 +1,95 @@
+// Paged K/V caches: the parts the append and decode kernels and the host side
+// of the C ABI share.
+//
+// A pool holds num_pages pages of `page` rows for each K/V head, contiguous as
+// [num_pages, Hkv, page, d]; row b of the block table lists the pages of
+// sequence b in order, so position p of it lives in row p % page of page
+// table[b][p / page]. Pages have 16, 32, 64 or 128 rows: a run of 16 positions
+// that starts at a multiple of 16 lies within one page.
+#pragma once
+
+#include "fa_common.cuh"
+
+namespace fa {
+
+constexpr unsigned int FA_DEV_BAD_PAGE = 2u;  // status word: a block-table entry outside the pool was skipped
+constexpr unsigned int FA_DEV_BAD_LENS = 4u;  // status word: lengths or offsets outside their arrays were clipped
+
+constexpr int PAGED_SCALE_EXP_MIN = -40;      // least exponent of an e4m3 page's scale
+
+inline bool paged_page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+// A sequence's length, clipped to the `most` keys the call covers.
+__host__ __device__ __forceinline__ int paged_clip_len(int len, int most) {
+  return len < 0 ? 0 : (len > most ? most : len);
+}
+
+// Element offset of row `row` (0 .. page - 1) of page `id` of K/V head `hk`, or
+// -1 when the table entry does not name a page of the pool. 64-bit: a pool may
+// hold more than 2^31 elements.
+__host__ __device__ __forceinline__ long long paged_row_offset(int id, int num_pages, int Hkv, int hk, int page,
+                                                               int row, int d) {
+  if (static_cast<unsigned int>(id) >= static_cast<unsigned int>(num_pages)) return -1;
+  return ((static_cast<long long>(id) * Hkv + hk) * page + row) * d;
+}
+
+struct DecodePagedParams {
+  const void* q;             // bf16, element strides qsb / qsh / qst of batch, head, token; d contiguous
+  const void* k;             // pool of K pages: bf16 or e4m3 codes
+  const void* v;             // pool of V pages
+  const float* k_scale;      // e4m3: fp32 [num_pages, Hkv]
+  const float* v_scale;
+  const int* table;          // int32 [B, >= max_len / page], row stride table_stride
+  const int* seqlens;        // int32 [B]
+  void* o;                   // bf16, element strides osb / osh / ost
+  float* lse;                // fp32 [B, H, Nq] or nullptr
+  float* ws_o;               // fp32 [rows, S, d] unnormalised partial outputs (S > 1)
+  float* ws_ml;              // fp32 [rows, S, 2] partial (base in log2 units, sum)
+  long long qsb, qsh, qst, osb, osh, ost, table_stride;
+  int B, H, Hkv, G, Nq, R;   // R = G * Nq query rows per K/V head
+  int max_len;               // lengths are clipped to this; at most width * page and S * chunk
+  int page, page_shift, num_pages;
+  int S, chunk;              // split s covers keys [s * chunk, (s + 1) * chunk)
+  int row_tiles;             // tiles of 8 * NR query rows per K/V head
+  float scale_log2;          // scale * log2(e)
+  unsigned int* status;      // device status word
+};
+
+// Query rows of one CTA of the paged decode: 8 where a K/V head has that few, else 16.
+__host__ __device__ constexpr int decode_paged_rows(int R) { return R <= 8 ? 8 : 16; }
+
+struct AppendPagedParams {
+  const void* q;             // bf16, element strides of token and head; d contiguous
+  const void* k;
+  const void* v;
+  void* q_out;               // bf16, its own strides; may be q itself
+  void* k_out;               // bf16 or nullptr; may be k itself
+  void* k_pages;             // bf16, or e4m3 codes with the scales below
+  void* v_pages;
+  float* k_scale;
+  float* v_scale;
+  const int* table;
+  const int* seqlens;        // int32 [B]: lengths with the new tokens counted
+  const int* cu;             // int32 [B + 1]: first new token of each sequence, or nullptr (uniform)
+  const long long* turns;    // int64 [rot / 2]: each pair's frequency in 2^-64 turns a position
+  const void* q_weight;      // bf16 [d] or nullptr
+  const void* k_weight;
+  long long qst, qsh, kst, ksh, vst, vsh, qost, qosh, kost, kosh, table_stride;
+  int B, T, H, Hkv, G, d;
+  int width, page, page_shift, num_pages;
+  int rot, interleaved;
+  int max_new;               // most new tokens of one sequence
+  int per_seq;               // > 0: blocks are B x per_seq pages; 0: found through cu
+  int rows_par, head_slots;  // thread groups of a block: rows in parallel x heads in parallel
+  int stash_rows;            // rows of the e4m3 key stash in shared memory
+  float rot_scale, eps;
+  unsigned int* status;
+};
+
+cudaError_t append_paged_set_attributes();
+cudaError_t launch_append_paged(bool f8, const AppendPagedParams& p, cudaStream_t stream);
+
+cudaError_t decode_paged_set_attributes();
+cudaError_t launch_decode_paged(int d, bool f8, const DecodePagedParams& p, cudaStream_t stream);
+
+}  // namespace fa

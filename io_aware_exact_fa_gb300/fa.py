@@ -45,6 +45,9 @@ EXPORTS = {
     "fa_decode_splitkv_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
     "fa_decode_grouped_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_decode_grouped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "fa_append_paged": (_i, [_vp] * 9 + [_vp, _i64] + [_vp] * 6 + [_i] * 11 + [_f, _f, _i, _vp]),
+    "fa_decode_paged_workspace_size": (_sz, [_i] * 7),
+    "fa_decode_paged": (_i, [_vp] * 7 + [_i64, _vp, _vp, _vp, _vp] + [_i] * 9 + [_f, _i, _vp, _sz, _vp]),
     "fa_materialized_workspace_size": (_sz, [_i, _i, _i, _i]),
     "fa_fwd_materialized": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
     "fa_bwd_workspace_size": (_sz, [_i, _i, _i, _i]),
@@ -306,6 +309,228 @@ def decode_grouped(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                                 int(num_splits), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                 _stream_ptr(stream))
     _check(rc, "fa_decode_grouped")
+    return out, lse
+
+
+# --------------------------------------------------------------------------- paged caches
+
+def rotary_turns(rot: int, base: float = 10000.0, scaling: Optional[Tuple] = None,
+                 device: Optional[torch.device] = None) -> torch.Tensor:
+    """Rotation frequencies for ``append_paged``: int64 [rot / 2], each base**(-2j / rot) radians a
+    position as a fraction of a turn in units of 2**-64.
+
+    ``scaling`` stretches them for contexts longer than a model was trained on:
+      ("linear", f)                 every frequency divided by f (positions interpolated);
+      ("base", f)                   the base raised to base * f**(rot / (rot - 2)), which divides the
+                                    lowest frequency by f and leaves the highest alone;
+      ("by_parts", f, n, slow, fast) frequencies that turn fewer than ``slow`` times in the n positions
+                                    of training are divided by f, those that turn more than ``fast``
+                                    times are left alone, linearly blended (in turns) between.
+    """
+    if rot <= 0 or rot % 2:
+        raise ValueError("rot must be positive and even")
+    kind = scaling[0] if scaling else None
+    if kind not in (None, "linear", "base", "by_parts"):
+        raise ValueError(f"unknown scaling {kind!r}")
+    if kind and not scaling[1] >= 1:
+        raise ValueError("the scaling factor must be >= 1")
+    if kind == "base":
+        if rot < 4:
+            raise ValueError("base scaling needs rot >= 4")
+        base = base * scaling[1] ** (rot / (rot - 2))
+    out = []
+    for j in range(rot // 2):
+        t = base ** (-2.0 * j / rot) / (2.0 * math.pi)      # turns a position
+        if kind == "linear":
+            t /= scaling[1]
+        elif kind == "by_parts":
+            _, f, n, slow, fast = scaling
+            keep = min(1.0, max(0.0, (t * n - slow) / (fast - slow)))
+            t = t / f * (1.0 - keep) + t * keep
+        u = int(t * 2.0 ** 64) % (1 << 64)
+        out.append(u - (1 << 64) if u >= 1 << 63 else u)
+    return torch.tensor(out, dtype=torch.int64, device=device if device is not None else "cuda")
+
+
+def _on(t: torch.Tensor, name: str, dtype, device) -> None:
+    """A CUDA tensor of the given type on the call's device; strided layouts are the caller's to check."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, q on {device}")
+
+
+def _whole(t: torch.Tensor, name: str, dtype, device, shape=None) -> None:
+    _on(t, name, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _heads(t: torch.Tensor, name: str, device, shape) -> None:
+    """A bf16 tensor whose last dimension is contiguous; its other strides may be any multiple of 8."""
+    _on(t, name, torch.bfloat16, device)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _strides(t: torch.Tensor, dims) -> list:
+    """Element strides for the C ABI; a dimension of one element has none that matters."""
+    return [t.stride(i) if t.shape[i] > 1 else 0 for i in dims]
+
+
+def _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, device):
+    """Checks the paged cache; returns (pages, page size, e4m3?)."""
+    e4m3 = isinstance(k_pages, torch.Tensor) and k_pages.dtype in (torch.float8_e4m3fn, torch.uint8)
+    kind = k_pages.dtype if e4m3 else torch.bfloat16
+    _whole(k_pages, "k_pages", kind, device)
+    _whole(v_pages, "v_pages", kind, device)
+    if k_pages.dim() != 4 or k_pages.shape[1] != Hkv or k_pages.shape[3] != d or v_pages.shape != k_pages.shape:
+        raise ValueError(f"k_pages and v_pages must be [num_pages, {Hkv}, page, {d}]")
+    n, page = k_pages.shape[0], k_pages.shape[2]
+    if e4m3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("e4m3 pages need k_scale and v_scale")
+        _whole(k_scale, "k_scale", torch.float32, device, (n, Hkv))
+        _whole(v_scale, "v_scale", torch.float32, device, (n, Hkv))
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("bf16 pages take no scales")
+    _on(block_table, "block_table", torch.int32, device)
+    _whole(seqlens_k, "seqlens_k", torch.int32, device)
+    if block_table.dim() != 2 or block_table.stride(1) != 1 and block_table.shape[1] > 1:
+        raise ValueError("block_table must be [B, width] with contiguous rows")
+    if seqlens_k.shape != (block_table.shape[0],):
+        raise ValueError("seqlens_k must be int32 [B], with the rows of block_table")
+    return n, page, e4m3
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _call(device: torch.device, stream: Optional[torch.cuda.Stream], fn, args, where: str) -> None:
+    """Calls the library with the tensors' device current, on ``stream`` or that device's current stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, _stream_ptr(stream)), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream_ptr(stream)), where)
+
+
+_I64x10 = ctypes.c_int64 * 10
+_I64x3 = ctypes.c_int64 * 3
+
+
+def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 block_table: torch.Tensor, seqlens_k: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                 max_new: int = 0, turns: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 rot_scale: float = 1.0, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, with_k: bool = True,
+                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Norms, rotates and appends a step's tokens to a paged cache (fa.h fa_append_paged).
+
+    q [T,H,d], k/v [T,Hkv,d] bf16 (parts of one projection are taken as they are); k_pages/v_pages
+    [num_pages,Hkv,page,d] bf16, or float8_e4m3fn / uint8 codes with fp32 scales [num_pages,Hkv]; block_table int32
+    [B,width]; seqlens_k int32 [B] with the new tokens counted; cu_seqlens int32 [B+1], or None for T / B tokens each.
+    ``turns`` (``rotary_turns``) sets the rotation, None for none; the weights bf16 [d] the norms, None for none.
+    Returns the turned q [T,H,d] and k [T,Hkv,d] (None without ``with_k``)."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [T, H, d]")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [T, Hkv, d]")
+    dev = q.device
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    _heads(q, "q", dev, (T, H, d)); _heads(k, "k", dev, (T, Hkv, d)); _heads(v, "v", dev, (T, Hkv, d))
+    n, page, e4m3 = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, dev)
+    B = seqlens_k.shape[0]
+    if cu_seqlens is not None:
+        _whole(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
+    rot = 0
+    if turns is not None:
+        _whole(turns, "turns", torch.int64, dev)
+        rot = 2 * turns.numel()
+    if q_weight is not None:
+        _whole(q_weight, "q_weight", torch.bfloat16, dev, (d,))
+    if k_weight is not None:
+        _whole(k_weight, "k_weight", torch.bfloat16, dev, (d,))
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _heads(q_out, "q_out", dev, (T, H, d))
+    if k_out is None and with_k:
+        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
+    elif k_out is not None:
+        _heads(k_out, "k_out", dev, (T, Hkv, d))
+    st = _I64x10(*_strides(q, (0, 1)), *_strides(k, (0, 1)), *_strides(v, (0, 1)), *_strides(q_out, (0, 1)),
+                 *(_strides(k_out, (0, 1)) if k_out is not None else (0, 0)))
+    _call(dev, stream, _lib.fa_append_paged,
+          (_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+           _ptr(v_scale), _ptr(block_table), block_table.stride(0), _ptr(seqlens_k), _ptr(cu_seqlens), _ptr(turns),
+           _ptr(q_weight), _ptr(k_weight), st, B, T, H, Hkv, d, n, page, block_table.shape[1], int(e4m3), rot,
+           int(bool(interleaved)), float(rot_scale), float(eps), int(max_new)), "fa_append_paged")
+    return q_out, k_out
+
+
+def decode_paged_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int, max_len: int, num_splits: int = 0) -> int:
+    return int(_lib.fa_decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits))
+
+
+def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                 seqlens_k: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                 max_len: Optional[int] = None, num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, with_lse: bool = True,
+                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Grouped decode over a paged cache (fa.h fa_decode_paged): q [B,H,Nq,d] bf16, any strides with d contiguous
+    (``append_paged``'s q of B x Nq tokens is ``q.view(B, Nq, H, d).transpose(1, 2)``), the pool and table as for
+    ``append_paged`` -> (o [B,H,Nq,d] bf16, lse [B,H,Nq] fp32). ``max_len`` bounds the lengths (default: all that a
+    row of the table covers); ``num_splits`` 0 lets the library choose."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
+    dev = q.device
+    B, H, Nq, d = q.shape
+    _heads(q, "q", dev, (B, H, Nq, d))
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a CUDA tensor [num_pages, Hkv, page, d]")
+    Hkv = k_pages.shape[1]
+    n, page, e4m3 = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, dev)
+    if seqlens_k.shape[0] != B:
+        raise ValueError("seqlens_k and block_table must have B rows")
+    most = block_table.shape[1] * page
+    if max_len is None:
+        max_len = most
+    elif not 0 <= max_len <= most:
+        raise ValueError(f"max_len must be in [0, {most}], what a row of block_table covers")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _heads(out, "out", dev, (B, H, Nq, d))
+    if lse is not None:
+        _whole(lse, "lse", torch.float32, dev, (B, H, Nq))
+    elif with_lse:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(1, decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits)),
+                                dtype=torch.uint8, device=dev)
+    else:
+        _whole(workspace, "workspace", workspace.dtype, dev)
+    _call(dev, stream, _lib.fa_decode_paged,
+          (_ptr(q), _I64x3(*_strides(q, (0, 1, 2))), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+           _ptr(block_table), block_table.stride(0), _ptr(seqlens_k), _ptr(out), _I64x3(*_strides(out, (0, 1, 2))),
+           _ptr(lse), B, H, Hkv, Nq, d, n, page, int(max_len), int(e4m3), float(scale), int(num_splits),
+           _ptr(workspace), workspace.numel() * workspace.element_size()), "fa_decode_paged")
     return out, lse
 
 
