@@ -93,6 +93,37 @@ fa_status fa_fwd_masked(const void* q, const void* k, const void* v, void* o, fl
                         const uint32_t* keep_bits, int64_t mstride_b, int64_t mstride_h,
                         int64_t mstride_q, void* stream);
 
+/* Bytes of device workspace fa_fwd_packed needs: a list of its row blocks. 0
+ * for invalid arguments. */
+size_t fa_fwd_packed_workspace_size(int B, int total_q, int H, int Hkv);
+
+/* fa_fwd over packed sequences of different lengths with grouped K/V heads.
+ *   q, o   bf16 [total_q, H, d]     k, v   bf16 [total_k, Hkv, d]
+ *   cu_seqlens_q, cu_seqlens_k  int32 [B+1] on the device: sequence b owns rows
+ *          cu[b] .. cu[b+1]-1 (cu_seqlens_k NULL: those of cu_seqlens_q).
+ *          Lengths of zero are fine. Offsets are read on the device when the
+ *          call runs, so a captured call follows new ones; decreasing offsets or
+ *          offsets past the tensors are clipped and reported by
+ *          fa_get_device_status() as FA_ERR_INVALID_ARG.
+ *   strides  int64 [8], host memory: row and head strides, in elements, of q, k,
+ *          v, o in that order (multiples of 8; the d elements of a head are
+ *          contiguous), so q, k and v can be parts of one projection.
+ *   lse    fp32 [H, total_q] (may be NULL)
+ * Query head h reads K/V head h / (H/Hkv). Inside a sequence, with causal != 0,
+ * query i sees key j iff j <= i + Lk - Lq (its queries are its last positions);
+ * rows that see no key get o = 0, lse = -inf. Sequences never reach one another,
+ * whatever the values of their rows. Rows of o and columns of lse past
+ * cu_seqlens_q[B] are left as they were.
+ *   workspace  device memory of fa_fwd_packed_workspace_size() bytes, 256-byte
+ *              aligned, owned by the caller, overwritten; calls that may overlap
+ *              on the GPU need their own.
+ * total_q = 0 is a no-op. Two launches (the list, the tiles). Errors as for
+ * fa_fwd, plus FA_ERR_WORKSPACE, H not a multiple of Hkv, and
+ * FA_ERR_UNSUPPORTED for strides that are not positive multiples of 8. */
+fa_status fa_fwd_packed(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
+                        const int* cu_seqlens_q, const int* cu_seqlens_k, int B, int total_q, int total_k, int H,
+                        int Hkv, int d, float scale, int causal, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Forward pass on FP8 inputs ("FlashAttention: Attention Is Limited by
  * Memory, Not Math", section "FlashAttention 1, 2 and 3", lists FP8 support
  * among FlashAttention-3's changes; the pages give no further detail).

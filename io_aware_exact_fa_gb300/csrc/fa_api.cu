@@ -22,6 +22,7 @@
 #include "materialized.cuh"
 #include "fa_common.cuh"
 #include "fa_debug.cuh"
+#include "packed.cuh"
 #include "paged.cuh"
 
 // Causal unit order for K/V larger than L2 (see below): off by default. With a
@@ -112,6 +113,7 @@ fa_status device_state(DeviceState** out) {
     if ((e = fa::bwd_set_attributes(128)) != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(bwd d=128)");
     if ((e = fa::materialized_set_attributes()) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(materialized softmax)");
+    if ((e = fa::packed_set_attributes()) != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(packed prefill)");
     if ((e = fa::append_paged_set_attributes()) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(paged append)");
     if ((e = fa::decode_paged_set_attributes()) != cudaSuccess)
@@ -129,6 +131,10 @@ fa_status device_state(DeviceState** out) {
       if (regs != fa::prefill_launch_regs(d))
         return fail(FA_ERR_UNSUPPORTED, "prefill kernel (d=%d%s) built with %d registers, expected %d", d,
                     f8 ? ", e4m3" : "", regs, fa::prefill_launch_regs(d));
+      const int pregs = fa::packed_num_regs(d);
+      if (pregs != fa::prefill_launch_regs(d))
+        return fail(FA_ERR_UNSUPPORTED, "packed prefill kernel (d=%d) built with %d registers, expected %d", d, pregs,
+                    fa::prefill_launch_regs(d));
     }
     if (g_encode == nullptr) {
       void* fn = nullptr;
@@ -986,6 +992,124 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   cudaError_t e = fa::launch_decode_paged(d, e4m3 != 0, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
   t_launches += sp.S == 1 ? 1 : 2;
+  return FA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Packed prefill
+namespace {
+
+// Tensor map of bf16 rows of d elements of `heads` heads with the given row and
+// head strides (elements), in boxes of 128 rows x 64 elements (128-byte swizzle).
+fa_status encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int d, int64_t row_stride,
+                          int64_t head_stride) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+  // the stride of a dimension of one element is never used, but must be valid
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(rows > 1 ? row_stride : d) * 2,
+                           static_cast<cuuint64_t>(heads > 1 ? head_stride : d) * 2};
+  cuuint32_t box[3] = {64, 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  return FA_OK;
+}
+
+bool packed_pairs(int H, int Hkv) { return (H / Hkv) % 2 == 0; }
+// Row blocks of a packed batch of total_q rows in B sequences, at most.
+long long packed_entries(int B, int total_q, int H, int Hkv) {
+  return total_q / fa::packed_block_rows(packed_pairs(H, Hkv)) + static_cast<long long>(B);
+}
+
+}  // namespace
+
+size_t fa_fwd_packed_workspace_size(int B, int total_q, int H, int Hkv) {
+  if (B < 1 || total_q < 0 || H < 1 || Hkv < 1 || H % Hkv != 0) return 0;
+  return 256 + static_cast<size_t>(packed_entries(B, total_q, H, Hkv)) * 32;
+}
+
+fa_status fa_fwd_packed(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
+                        const int* cu_seqlens_q, const int* cu_seqlens_k, int B, int total_q, int total_k, int H,
+                        int Hkv, int d, float scale, int causal, void* workspace, size_t workspace_bytes, void* stream) {
+  t_detail[0] = 0;
+  if (B < 1 || H < 1 || Hkv < 1 || total_q < 0 || total_k < 0)
+    return fail(FA_ERR_INVALID_ARG, "need B, H, Hkv >= 1 and total_q, total_k >= 0 (got %d %d %d %d %d)", B, H, Hkv, total_q,
+                total_k);
+  if (H % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "H (%d) must be a multiple of Hkv (%d)", H, Hkv);
+  if (cu_seqlens_k == nullptr && total_q != total_k)
+    return fail(FA_ERR_INVALID_ARG, "without cu_seqlens_k k and v have the rows of q (%d, not %d)", total_q, total_k);
+  if (fa_status s = check_scale(scale)) return s;
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
+  if (total_q == 0) return FA_OK;
+  if (!q || !o || !strides || !cu_seqlens_q) return fail(FA_ERR_INVALID_ARG, "q, o, strides and cu_seqlens_q must be non-NULL");
+  if (total_k > 0 && (!k || !v)) return fail(FA_ERR_INVALID_ARG, "k and v must be non-NULL");
+  for (int i = 0; i < 8; ++i) {
+    const bool head = i & 1;
+    const int extent = head ? ((i == 2 * 1 + 1 || i == 2 * 2 + 1) ? Hkv : H) : ((i == 2 || i == 4) ? total_k : total_q);
+    if (extent > 1 && (strides[i] <= 0 || strides[i] % 8 != 0 || strides[i] > (1ll << 38)))
+      return fail(FA_ERR_UNSUPPORTED, "strides must be positive multiples of 8 elements");
+  }
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
+    return fail(FA_ERR_UNSUPPORTED, "q, k, v, o must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4))
+    return fail(FA_ERR_UNSUPPORTED, "lse and the offsets must be 4-byte aligned");
+  const bool pairs = packed_pairs(H, Hkv);
+  const long long entries = packed_entries(B, total_q, H, Hkv);
+  const int head_units = pairs ? H / 2 : H;
+  // key-tile rows are addressed up to one tile past the end
+  if (entries * head_units > INT_MAX || total_q > INT_MAX - 512 || total_k > INT_MAX - 512)
+    return fail(FA_ERR_INVALID_ARG, "B, total_q and H give too many tiles");
+  const size_t need = fa_fwd_packed_workspace_size(B, total_q, H, Hkv);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+    return fail(FA_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
+
+  DeviceState* st = nullptr;
+  if (fa_status s = device_state(&st)) return s;
+  CUtensorMap tq, tk, tv, to;
+  if (fa_status s = encode_rows_map(&tq, q, total_q, H, d, strides[0], strides[1])) return s;
+  if (fa_status s = encode_rows_map(&to, o, total_q, H, d, strides[6], strides[7])) return s;
+  if (total_k > 0) {
+    if (fa_status s = encode_rows_map(&tk, k, total_k, Hkv, d, strides[2], strides[3])) return s;
+    if (fa_status s = encode_rows_map(&tv, v, total_k, Hkv, d, strides[4], strides[5])) return s;
+  } else {
+    tk = tv = tq;  // no key: no tile is loaded through them
+  }
+  fa::PrefillParams p{};
+  p.o = o;
+  p.lse = lse;
+  p.B = B, p.H = H, p.Nq = total_q, p.Nk = total_k;
+  p.causal = causal ? 1 : 0;
+  // scale's sign and zero as in the dense forward pass
+  p.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 1.17549435e-38f);
+  p.negate_s = scale < 0.f ? 1 : 0;
+  p.o_scale = 1.f;
+  p.dbg = FA_DEBUG ? st->debug : nullptr;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  p.status = st->status;
+  p.max_ctas = st->num_sms;
+  fa::PackedPlan plan{};
+  plan.cu_q = cu_seqlens_q;
+  plan.cu_k = cu_seqlens_k ? cu_seqlens_k : cu_seqlens_q;
+  plan.n_entries = static_cast<int*>(workspace);
+  plan.entries = reinterpret_cast<int4*>(static_cast<char*>(workspace) + 256);
+  plan.B = B, plan.total_q = total_q, plan.total_k = total_k;
+  plan.block_rows = fa::packed_block_rows(pairs);
+  plan.causal = p.causal;
+  plan.max_entries = static_cast<int>(entries);
+  while ((((total_k + fa::BLOCK_N - 1) / fa::BLOCK_N) >> plan.shift) >= 1024) ++plan.shift;
+  plan.status = st->status;
+  fa::PackedArgs pk{};
+  pk.entries = plan.entries;
+  pk.n_entries = plan.n_entries;
+  pk.head_units = head_units;
+  pk.pair_heads = pairs ? 1 : 0;
+  pk.G = H / Hkv, pk.Hkv = Hkv;
+  pk.total_q = total_q, pk.total_k = total_k;
+  pk.ost = total_q > 1 ? strides[6] : d, pk.osh = H > 1 ? strides[7] : d;
+  cudaError_t e = fa::launch_packed(d, tq, tk, tv, to, p, pk, plan, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "packed prefill launch");
+  t_launches += 2;
   return FA_OK;
 }
 

@@ -41,6 +41,7 @@
 
 #include "fa_debug.cuh"
 #include "fa_ptx.cuh"
+#include "packed.cuh"
 
 namespace fa {
 
@@ -349,6 +350,46 @@ __device__ __forceinline__ Unit unit_info(const PrefillParams& p, int u, int kv_
   w.act1 = only != 0;
   return w;
 }
+// A work unit of a packed batch: two 128-row Q tiles that read the same keys.
+// With an even number of query heads per K/V head the tiles are the same rows
+// of two neighbouring heads, so they visit the same key tiles (no causal
+// imbalance between them) and a sequence of up to 128 rows fills both; else
+// they are two row tiles of one head, as in the dense kernel.
+struct PackedUnit {
+  int n0, n1;            // key tiles Q tile t visits
+  bool act0, act1;       // whether Q tile t has rows
+  int q_off, k_off;      // the sequence's first row in q and in k, v
+  int Lq, Lk;            // its lengths
+  int h0, h1, hk;        // head of each tile, and their K/V head
+  int r0, r1;            // first row of each tile, within the sequence
+};
+__device__ __forceinline__ PackedUnit packed_unit_info(const PrefillParams& p, const PackedArgs& a, int u) {
+  const int e = u / a.head_units, hu = u - e * a.head_units;
+  const int4 x = a.entries[2 * e], y = a.entries[2 * e + 1];
+  PackedUnit w;
+  w.q_off = x.x;
+  w.k_off = x.y;
+  w.Lq = x.z;
+  w.Lk = x.w;
+  w.h0 = a.pair_heads ? 2 * hu : hu;
+  w.h1 = a.pair_heads ? 2 * hu + 1 : hu;
+  w.hk = w.h0 / a.G;
+  w.r0 = y.x;
+  w.r1 = a.pair_heads ? y.x : y.x + BLOCK_M;
+  const int nkv = (w.Lk + BLOCK_N - 1) / BLOCK_N;
+  auto tiles = [&](int r) {
+    if (r >= w.Lq) return 0;
+    if (!p.causal) return nkv;
+    const int last_key = min(r + BLOCK_M - 1, w.Lq - 1) + (w.Lk - w.Lq);
+    return last_key < 0 ? 0 : min(nkv, last_key / BLOCK_N + 1);
+  };
+  w.n0 = tiles(w.r0);
+  w.n1 = tiles(w.r1);
+  w.act0 = w.r0 < w.Lq;
+  w.act1 = w.r1 < w.Lq;
+  return w;
+}
+
 // The k-th unit of CTA c of G, or a value >= U when it has no k-th unit.
 // Round robin; with `snake` every other round runs in reverse CTA order, so
 // with units sorted longest first the per-CTA sums stay balanced.
@@ -356,11 +397,15 @@ __device__ __forceinline__ int unit_of(int c, int k, int G, bool snake) {
   return k * G + ((snake && (k & 1)) ? (G - 1 - c) : c);
 }
 
-template <int D, bool F8>
+// PK: a packed batch (fa_fwd_packed). Its tensor maps run over all rows of the
+// batch, so a tile may hold rows of the next sequence: their scores are masked
+// like keys past the end, their V rows are cleared before the product (a weight
+// of zero would not silence an infinity or NaN), their O rows are not written.
+template <int D, bool F8, bool PK = false>
 __global__ void __launch_bounds__(prefill_threads(D), 1)
     fa_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                      const PrefillParams p) {
+                      const PrefillParams p, const PackedArgs pk) {
   using C = PrefillCfg<D, F8>;
   constexpr int NK = C::NK, NV = C::NV, NR = C::NR;
   extern __shared__ uint8_t smem_raw[];
@@ -398,10 +443,21 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
   const int sw = warp;
   const bool alloc_warp = producer && pw == 1;  // the first MMA issuer allocates and frees TMEM
   const uint64_t lim = p.wait_limit_ns;
-  const int U = p.units;
+  __shared__ uint64_t v_tail;  // PK: V of a sequence's ragged last key tile landed
+  int U = p.units;
   const int G = static_cast<int>(gridDim.x);
   const int cta = static_cast<int>(blockIdx.x);
-  const bool snake = p.causal != 0;
+  const bool snake = PK || p.causal != 0;  // packed units are sorted longest first
+  if constexpr (PK) {
+    // the unit list comes from the launch before, which may still be running
+    pdl_wait();
+    U = *pk.n_entries * pk.head_units;
+    if (cta >= U) return;  // (uniform; the grid is an upper bound)
+  }
+  auto unit_of_pass = [&](int u, int kv_keep) {
+    if constexpr (PK) return packed_unit_info(p, pk, u);
+    else return unit_info(p, u, kv_keep);
+  };
   // With one key mask broadcast over the rows of a head, key tiles after the
   // last one with any key kept are skipped by every role; the host then
   // launches one CTA per unit and warp 11 finds that tile before set-up ends.
@@ -436,6 +492,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     for (int i = 0; i < NR; ++i) mbar_init(rel + i, Q_TILES);  // both MMA-issuing warps
     mbar_init(unit_done, Q_TILES);
     mbar_init(drain, Q_TILES);
+    if constexpr (PK) mbar_init(&v_tail, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -475,11 +532,21 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         return __all_sync(0xffffffffu, w) != 0;
       };
       int g = 0, nlk = 0, nlv = 0;
+      [[maybe_unused]] int ntail = 0;
+      const int rows_k = PK ? pk.total_k : p.Nk, heads_k = PK ? pk.Hkv : p.B * p.H;
+      auto k_row = [&](const auto& w, int jj) {
+        if constexpr (PK) return w.k_off + jj * BLOCK_N;
+        else return jj * BLOCK_N;
+      };
+      auto k_head = [&](const auto& w) {
+        if constexpr (PK) return w.hk;
+        else return w.bh;
+      };
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int u = unit_at(k);
         if (u >= U) break;
-        const Unit w = unit_info(p, u, kv_keep);
+        const auto w = unit_of_pass(u, kv_keep);
         const int n_max = max(w.n0, w.n1);
         for (int jj = 0; jj < n_max; ++jj, ++g) {
           if (!(ok = wait_rel(g - NK))) break;
@@ -487,17 +554,42 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
             uint8_t* dst = sK + (g % NK) * C::TILE_BYTES;
             mbar_arrive_expect_tx(full_k + (g % NK), C::TILE_BYTES);
             for (int b = 0; b < C::NBOX; ++b)
-              if (dbg_tma_ok(p.dbg, DBG_LOAD_K, C::BOX_ELEMS * b, jj * BLOCK_N, w.bh, D, p.Nk, p.B * p.H, C::ESZ))
-                tma_load_3d(dst + b * C::BOX_BYTES, &tmK, full_k + (g % NK), C::BOX_ELEMS * b, jj * BLOCK_N, w.bh);
+              if (dbg_tma_ok(p.dbg, DBG_LOAD_K, C::BOX_ELEMS * b, k_row(w, jj), k_head(w), D, rows_k, heads_k, C::ESZ))
+                tma_load_3d(dst + b * C::BOX_BYTES, &tmK, full_k + (g % NK), C::BOX_ELEMS * b, k_row(w, jj), k_head(w));
           }
           ++nlk;
           if (!(ok = wait_rel(g - NV))) break;
+          uint8_t* dst = sV + (g % NV) * C::TILE_BYTES;
+          bool tail = false;  // rows of the next sequence follow in this tile (past the last row, zeros do)
+          if constexpr (PK) tail = (jj + 1) * BLOCK_N > w.Lk && w.k_off + w.Lk < pk.total_k;
+          uint64_t* vbar = tail ? &v_tail : full_v + (g % NV);
           if (leader) {
-            uint8_t* dst = sV + (g % NV) * C::TILE_BYTES;
-            mbar_arrive_expect_tx(full_v + (g % NV), C::TILE_BYTES);
+            mbar_arrive_expect_tx(vbar, C::TILE_BYTES);
             for (int b = 0; b < C::NBOX; ++b)
-              if (dbg_tma_ok(p.dbg, DBG_LOAD_V, C::BOX_ELEMS * b, jj * BLOCK_N, w.bh, D, p.Nk, p.B * p.H, C::ESZ))
-                tma_load_3d(dst + b * C::BOX_BYTES, &tmV, full_v + (g % NV), C::BOX_ELEMS * b, jj * BLOCK_N, w.bh);
+              if (dbg_tma_ok(p.dbg, DBG_LOAD_V, C::BOX_ELEMS * b, k_row(w, jj), k_head(w), D, rows_k, heads_k, C::ESZ))
+                tma_load_3d(dst + b * C::BOX_BYTES, &tmV, vbar, C::BOX_ELEMS * b, k_row(w, jj), k_head(w));
+          }
+          if constexpr (PK) {
+            if (tail) {
+              // once the tile landed, clear the rows past the sequence and only then hand it on
+              ok = mbar_wait(&v_tail, static_cast<uint32_t>(ntail & 1), lim, p.status, abort_flag);
+              ++ntail;
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) {
+                mbar_wait_drain(&v_tail, static_cast<uint32_t>((ntail - 1) & 1), lim);
+                break;
+              }
+              constexpr int CPR = C::ROW_BYTES / 16;
+              const int from = w.Lk - jj * BLOCK_N;
+              for (int x = lane; x < (BLOCK_N - from) * CPR * C::NBOX; x += 32) {
+                const int row = from + x / (CPR * C::NBOX), rest = x % (CPR * C::NBOX);
+                st_shared_v4(smem_u32(dst) + (rest / CPR) * C::BOX_BYTES + row * C::ROW_BYTES + (rest % CPR) * 16, 0u,
+                             0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (leader) mbar_arrive(full_v + (g % NV));
+            }
           }
           ++nlv;
         }
@@ -520,7 +612,8 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       for (int k = 0; ok; ++k) {
         const int u = unit_at(k);
         if (u >= U) break;
-        const Unit w = unit_info(p, u, kv_keep);
+        const auto w = unit_of_pass(u, kv_keep);
+        const int rows_q = PK ? pk.total_q : p.n_qpairs * Q_TILES * BLOCK_M, heads_q = PK ? p.H : p.B * p.H;
         for (int t = 0; t < Q_TILES && ok; ++t) {
           uint64_t* qf = q_full + C::QB * t + qbuf(k);
           if (k >= C::QB) {
@@ -538,11 +631,18 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
               mbar_arrive_expect_tx(qf, C::TILE_BYTES);
               // (the second tile of the last pair may start past Nq: it then
               // reads zeros and computes nothing; the pair grid bounds it)
+              int q_row, q_head;
+              if constexpr (PK) {
+                q_row = w.q_off + (t ? w.r1 : w.r0);
+                q_head = t ? w.h1 : w.h0;
+              } else {
+                q_row = w.pair * (Q_TILES * BLOCK_M) + t * BLOCK_M;
+                q_head = w.bh;
+              }
               for (int b = 0; b < C::NBOX; ++b)
-                if (dbg_tma_ok(p.dbg, DBG_LOAD_Q, C::BOX_ELEMS * b, w.pair * (Q_TILES * BLOCK_M) + t * BLOCK_M, w.bh,
-                               D, p.n_qpairs * Q_TILES * BLOCK_M, p.B * p.H, C::ESZ))
+                if (dbg_tma_ok(p.dbg, DBG_LOAD_Q, C::BOX_ELEMS * b, q_row, q_head, D, rows_q, heads_q, C::ESZ))
                   tma_load_3d(sQ + (qbuf(k) * Q_TILES + t) * C::TILE_BYTES + b * C::BOX_BYTES, &tmQ, qf,
-                              C::BOX_ELEMS * b, w.pair * (Q_TILES * BLOCK_M) + t * BLOCK_M, w.bh);
+                              C::BOX_ELEMS * b, q_row, q_head);
             } else {
               mbar_arrive(qf);  // a tile this unit does not compute: the phase completes empty
             }
@@ -620,7 +720,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       for (int k = 0; ok && (!C::SOLO_ISSUE || lane == 0); ++k) {
         const int u = unit_at(k);
         if (u >= U) break;
-        const Unit w = unit_info(p, u, kv_keep);
+        const auto w = unit_of_pass(u, kv_keep);
         const int nt = t ? w.n1 : w.n0;
         const int ct = t ? c1 : c0;  // this tile's step count before the unit
         const int n_max = max(w.n0, w.n1);
@@ -795,7 +895,6 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     const uint32_t tP = tmem + lane_base + C::P_COL + C::P_STRIDE * t;
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f2pack(sl2, sl2);
-    const int delta = p.Nk - p.Nq;
     const int nwords = (p.Nk + 31) >> 5;
     uint8_t* sO = C::O_STAGE ? smem + C::O_OFF + t * C::O_TILE_BYTES : sQ + t * C::TILE_BYTES;
     const bool storer = wq == 0 && lane == 0;
@@ -808,11 +907,22 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
     for (int k = 0;; ++k) {
       const int u = unit_at(k);
       if (u >= U) break;
-      const Unit w = unit_info(p, u, kv_keep);
-      const int bh = w.bh;
+      const auto w = unit_of_pass(u, kv_keep);
       const int n = t ? w.n1 : w.n0;
       const bool active = t ? w.act1 : w.act0;  // else another unit computes these rows
-      const int r0 = w.pair * (Q_TILES * BLOCK_M) + t * BLOCK_M;
+      int bh, r0, Nq, Nk;  // head (of all sequences, or of the packed batch), first row, lengths
+      if constexpr (PK) {
+        bh = t ? w.h1 : w.h0;
+        r0 = t ? w.r1 : w.r0;
+        Nq = w.Lq;
+        Nk = w.Lk;
+      } else {
+        bh = w.bh;
+        r0 = w.pair * (Q_TILES * BLOCK_M) + t * BLOCK_M;
+        Nq = p.Nq;
+        Nk = p.Nk;
+      }
+      const int delta = Nk - Nq;
       const int qi = r0 + row;
       const int diag = qi + delta;      // last key this row may see (causal)
       const int tile_lim = r0 + delta;  // last key the first row of the tile may see
@@ -869,12 +979,12 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         // tiles whose 128 keys are all kept for every row of the warp skip the
         // element-wise mask (warp-uniform choice of code path)
         const bool all_kept = __all_sync(0xffffffffu, keep_all) != 0;
-        const bool need_mask = (kbase + BLOCK_N > p.Nk) || (p.causal && kbase + BLOCK_N - 1 > tile_lim) || !all_kept;
+        const bool need_mask = (kbase + BLOCK_N > Nk) || (p.causal && kbase + BLOCK_N - 1 > tile_lim) || !all_kept;
         if (need_mask) {
           if (all_kept) {
             // every key of the tile kept: keys past min(Nk - 1, diag) are
             // hidden, a threshold (much cheaper than testing mask bits)
-            const int lim = min(p.causal ? diag : INT_MAX, p.Nk - 1) - kbase;  // last visible column
+            const int lim = min(p.causal ? diag : INT_MAX, Nk - 1) - kbase;  // last visible column
 #pragma unroll
             for (int c = 0; c < BLOCK_N; ++c)
               if (c > lim) s[c] = f2u(-INFINITY);
@@ -988,6 +1098,11 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       if (C::O_STAGE && k > 0) named_bar_sync(1 + t, 128);
       if (ok && active) {
         const float inv = (l > 0.f) ? p.o_scale / l : 0.f;  // o_scale: the v descale (1 for bf16)
+        // a packed tile that the next sequence's rows share is written row by row
+        const bool by_rows = PK && r0 + BLOCK_M > Nq;
+        uint8_t* orow = nullptr;
+        if constexpr (PK)
+          orow = static_cast<uint8_t*>(p.o) + 2 * ((w.q_off + qi) * static_cast<long long>(pk.ost) + bh * static_cast<long long>(pk.osh));
         const uint32_t srow = smem_u32(sO) + static_cast<uint32_t>(row) * 128u;
 #pragma unroll
         for (int ch = 0; ch < D / 32; ++ch) {
@@ -999,29 +1114,39 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
-          uint32_t pk[16];
+          uint32_t ow[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(u2f(o[2 * i]) * inv, u2f(o[2 * i + 1]) * inv);
+          for (int i = 0; i < 16; ++i) ow[i] = pack_bf16x2(u2f(o[2 * i]) * inv, u2f(o[2 * i + 1]) * inv);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             const int c = ch * 4 + v;  // 16-byte chunk of the row: box c / 8, chunk c % 8 of the box
             const uint32_t a = srow + static_cast<uint32_t>((c >> 3) * C::O_BOX_BYTES) +
                                (static_cast<uint32_t>((c & 7) ^ (row & 7)) << 4);
-            st_shared_v4(a, pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+            if (by_rows) {
+              if (qi < Nq)
+                *reinterpret_cast<uint4*>(orow + c * 16) = make_uint4(ow[4 * v], ow[4 * v + 1], ow[4 * v + 2], ow[4 * v + 3]);
+            } else {
+              st_shared_v4(a, ow[4 * v], ow[4 * v + 1], ow[4 * v + 2], ow[4 * v + 3]);
+            }
           }
         }
-        if (p.lse != nullptr && qi < p.Nq)
-          p.lse[static_cast<size_t>(bh) * p.Nq + qi] =
+        size_t lse_at;
+        if constexpr (PK) lse_at = static_cast<size_t>(bh) * pk.total_q + w.q_off + qi;
+        else lse_at = static_cast<size_t>(bh) * p.Nq + qi;
+        if (p.lse != nullptr && qi < Nq)
+          p.lse[lse_at] =
               (l > 0.f) ? (m + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
       }
       fence_proxy_async_smem();
       named_bar_sync(1 + t, 128);  // every thread of the tile, every unit, on every path
       if (storer && *abort_flag == 0) {
-        if (active && r0 < p.Nq) {
+        if (PK ? active && r0 + BLOCK_M <= Nq : active && r0 < p.Nq) {
+          int o_row = r0;
+          if constexpr (PK) o_row += w.q_off;
 #pragma unroll
           for (int b = 0; b < C::NBOX_O; ++b)
-            if (dbg_tma_ok(p.dbg, DBG_STORE_O, 64 * b, r0, bh, D, p.Nq, p.B * p.H, 2))
-              tma_store_3d(&tmO, sO + b * C::O_BOX_BYTES, 64 * b, r0, bh);
+            if (dbg_tma_ok(p.dbg, DBG_STORE_O, 64 * b, o_row, bh, D, PK ? pk.total_q : p.Nq, PK ? p.H : p.B * p.H, 2))
+              tma_store_3d(&tmO, sO + b * C::O_BOX_BYTES, 64 * b, o_row, bh);
           bulk_commit_group();
           if (!(C::O_STAGE && FA_LATE_STORE_WAIT)) bulk_wait_group_read_all();
         }
@@ -1089,8 +1214,131 @@ static cudaError_t launch_prefill_t(const CUtensorMap& tq, const CUtensorMap& tk
   const long long units = p.units;
   const bool trim = p.keep != nullptr && p.msq == 0;
   const long long ctas = (trim || !C::PERSIST) ? units : std::min<long long>(units, std::max(1, p.max_ctas));
-  fa_prefill_kernel<D, F8><<<static_cast<unsigned>(ctas), prefill_threads(D), C::SMEM, stream>>>(tq, tk, tv, to, p);
+  fa_prefill_kernel<D, F8><<<static_cast<unsigned>(ctas), prefill_threads(D), C::SMEM, stream>>>(tq, tk, tv, to, p,
+                                                                                               PackedArgs{});
   return cudaGetLastError();
+}
+
+// ---- packed batches
+namespace {
+constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_BUCKETS = 1024;
+}  // namespace
+
+// Lists the row blocks (of block_rows rows) of a packed batch, those that visit
+// the most key tiles first, as entries {q_off, k_off, Lq, Lk}, {first row}; one
+// CTA. A counting sort by the number of key tiles: equal counts come in any
+// order, which changes which CTA computes a block and nothing else.
+__global__ void __launch_bounds__(PLAN_THREADS) fa_packed_plan_kernel(const PackedPlan a) {
+  __shared__ int hist[PLAN_BUCKETS];
+  __shared__ int wsum[PLAN_THREADS / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  static_assert(PLAN_BUCKETS == PLAN_THREADS, "one thread scans one bucket");
+  pdl_launch_dependents();
+  hist[tid] = 0;
+  __syncthreads();
+  bool bad = false;
+  // a sequence's rows and keys, clipped to the tensors
+  auto seq = [&](int b, int4& x) {
+    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1), k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
+    x.x = min(max(q0, 0), a.total_q);
+    x.y = min(max(k0, 0), a.total_k);
+    x.z = max(min(max(q1, 0), a.total_q) - x.x, 0);
+    x.w = max(min(max(k1, 0), a.total_k) - x.y, 0);
+    bad = bad || q0 != x.x || k0 != x.y || q1 != x.x + x.z || k1 != x.y + x.w;
+  };
+  auto bucket = [&](const int4& x, int i) {  // 0: the most key tiles
+    const int last_row = min((i + 1) * a.block_rows, x.z) - 1;
+    const int keys = a.causal ? min(x.w, max(last_row + 1 + x.w - x.z, 0)) : x.w;
+    return PLAN_BUCKETS - 1 - min((((keys + BLOCK_N - 1) / BLOCK_N) >> a.shift), PLAN_BUCKETS - 1);
+  };
+  for (int b = warp; b < a.B; b += PLAN_THREADS / 32) {
+    int4 x;
+    seq(b, x);
+    const int nb = (x.z + a.block_rows - 1) / a.block_rows;
+    for (int i = lane; i < nb; i += 32) atomicAdd(&hist[bucket(x, i)], 1);
+  }
+  if (bad) atomicOr(a.status, FA_DEV_BAD_LENS);
+  __syncthreads();
+  // exclusive scan of the buckets
+  const int n = hist[tid];
+  int inc = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = wsum[lane];
+    int s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    wsum[lane] = s - w;
+    if (lane == 31) *a.n_entries = min(s, a.max_entries);
+  }
+  __syncthreads();
+  hist[tid] = wsum[warp] + inc - n;
+  __syncthreads();
+  for (int b = warp; b < a.B; b += PLAN_THREADS / 32) {
+    int4 x;
+    seq(b, x);
+    const int nb = (x.z + a.block_rows - 1) / a.block_rows;
+    for (int i = lane; i < nb; i += 32) {
+      const int at = atomicAdd(&hist[bucket(x, i)], 1);
+      if (at < a.max_entries) {  // (offsets that overlap could list more)
+        a.entries[2 * at] = x;
+        a.entries[2 * at + 1] = make_int4(i * a.block_rows, 0, 0, 0);
+      }
+    }
+  }
+}
+
+template <int D>
+static cudaError_t launch_packed_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const CUtensorMap& to, const PrefillParams& p, const PackedArgs& pk,
+                                   const PackedPlan& plan, cudaStream_t stream) {
+  using C = PrefillCfg<D, false>;
+  fa_packed_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(plan);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long units = static_cast<long long>(plan.max_entries) * pk.head_units;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(C::PERSIST ? std::min<long long>(units, std::max(1, p.max_ctas)) : units));
+  cfg.blockDim = dim3(prefill_threads(D));
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_prefill_kernel<D, false, true>, tq, tk, tv, to, p, pk);
+}
+cudaError_t launch_packed(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const CUtensorMap& to, const PrefillParams& p, const PackedArgs& pk, const PackedPlan& plan,
+                          cudaStream_t stream) {
+  return d == 64 ? launch_packed_t<64>(tq, tk, tv, to, p, pk, plan, stream)
+                 : launch_packed_t<128>(tq, tk, tv, to, p, pk, plan, stream);
+}
+template <int D>
+static cudaError_t packed_attr_t() {
+  return cudaFuncSetAttribute(fa_prefill_kernel<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              PrefillCfg<D, false>::SMEM);
+}
+cudaError_t packed_set_attributes() {
+  const cudaError_t e = packed_attr_t<64>();
+  return e != cudaSuccess ? e : packed_attr_t<128>();
+}
+int packed_num_regs(int d) {
+  cudaFuncAttributes a{};
+  const cudaError_t e = d == 64 ? cudaFuncGetAttributes(&a, fa_prefill_kernel<64, false, true>)
+                                : cudaFuncGetAttributes(&a, fa_prefill_kernel<128, false, true>);
+  return e == cudaSuccess ? a.numRegs : -1;
 }
 
 // The instantiations: bf16 and e4m3, each at d = 64 and 128.

@@ -45,6 +45,8 @@ EXPORTS = {
     "fa_decode_splitkv_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
     "fa_decode_grouped_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_decode_grouped": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "fa_fwd_packed_workspace_size": (_sz, [_i] * 4),
+    "fa_fwd_packed": (_i, [_vp] * 8 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]),
     "fa_append_paged": (_i, [_vp] * 9 + [_vp, _i64] + [_vp] * 6 + [_i] * 11 + [_f, _f, _i, _vp]),
     "fa_decode_paged_workspace_size": (_sz, [_i] * 7),
     "fa_decode_paged": (_i, [_vp] * 7 + [_i64, _vp, _vp, _vp, _vp] + [_i] * 9 + [_f, _i, _vp, _sz, _vp]),
@@ -531,6 +533,59 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
            _ptr(block_table), block_table.stride(0), _ptr(seqlens_k), _ptr(out), _I64x3(*_strides(out, (0, 1, 2))),
            _ptr(lse), B, H, Hkv, Nq, d, n, page, int(max_len), int(e4m3), float(scale), int(num_splits),
            _ptr(workspace), workspace.numel() * workspace.element_size()), "fa_decode_paged")
+    return out, lse
+
+
+# --------------------------------------------------------------------------- packed prefill
+
+def fwd_packed_workspace_size(B: int, total_q: int, H: int, Hkv: int) -> int:
+    return int(_lib.fa_fwd_packed_workspace_size(B, total_q, H, Hkv))
+
+
+_I64x8 = ctypes.c_int64 * 8
+
+
+def fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+               cu_seqlens_k: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = False,
+               workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, with_lse: bool = True,
+               stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention inside each of B packed sequences, grouped K/V heads (fa.h fa_fwd_packed): q [total_q,H,d], k/v
+    [total_k,Hkv,d] bf16 (parts of one projection are taken as they are), cu_seqlens int32 [B+1] ->
+    (o [total_q,H,d] bf16, lse [H,total_q] fp32). Rows behind the last sequence are left as they were."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [total_q, H, d]")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [total_k, Hkv, d]")
+    dev = q.device
+    Tq, H, d = q.shape
+    Tk, Hkv = k.shape[0], k.shape[1]
+    _heads(q, "q", dev, (Tq, H, d)); _heads(k, "k", dev, (Tk, Hkv, d)); _heads(v, "v", dev, (Tk, Hkv, d))
+    _whole(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
+    B = cu_seqlens_q.numel() - 1
+    if cu_seqlens_q.dim() != 1 or B < 1:
+        raise ValueError("cu_seqlens_q must be int32 [B + 1], B >= 1")
+    if cu_seqlens_k is not None:
+        _whole(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, (B + 1,))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty((Tq, H, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _heads(out, "out", dev, (Tq, H, d))
+    if lse is not None:
+        _whole(lse, "lse", torch.float32, dev, (H, Tq))
+    elif with_lse:
+        lse = torch.empty((H, Tq), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(1, fwd_packed_workspace_size(B, Tq, H, Hkv)), dtype=torch.uint8, device=dev)
+    else:
+        _whole(workspace, "workspace", workspace.dtype, dev)
+    st = _I64x8(*_strides(q, (0, 1)), *_strides(k, (0, 1)), *_strides(v, (0, 1)), *_strides(out, (0, 1)))
+    _call(dev, stream, _lib.fa_fwd_packed,
+          (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), st, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, Tq, Tk, H,
+           Hkv, d, float(scale), int(bool(causal)), _ptr(workspace), workspace.numel() * workspace.element_size()),
+          "fa_fwd_packed")
     return out, lse
 
 

@@ -90,6 +90,36 @@ def test_decode_workspace(fa):
     assert fa.decode_paged_workspace_size(1, 1, 1, 1, 64, 1 << 30) <= 1024 * 66 * 4 + 512
 
 
+def _packed(fa, **kw):
+    a = dict(q=P, k=P, v=P, o=P, lse=P, strides=[512, 64, 128, 64, 128, 64, 512, 64], cu_q=P, cu_k=None, B=2, tq=100,
+             tk=100, H=8, Hkv=2, d=64, scale=0.125, causal=1, ws=P, bytes=1 << 20)
+    a.update(kw)
+    a["strides"] = None if a["strides"] is None else (ctypes.c_int64 * 8)(*a["strides"])
+    return fa.lib.fa_fwd_packed(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(o=None), INVALID), (dict(strides=None), INVALID),
+    (dict(cu_q=None), INVALID), (dict(B=0), INVALID), (dict(H=7), INVALID), (dict(Hkv=0), INVALID),
+    (dict(tq=-1), INVALID), (dict(tk=99), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(B=1 << 30, H=64), INVALID), (dict(d=80), UNSUPPORTED), (dict(q=P + 8), UNSUPPORTED),
+    (dict(o=P + 2), UNSUPPORTED), (dict(lse=P + 1), UNSUPPORTED), (dict(cu_q=P + 2), UNSUPPORTED),
+    (dict(cu_k=P + 2), UNSUPPORTED), (dict(strides=[512, 60, 128, 64, 128, 64, 512, 64]), UNSUPPORTED),
+    (dict(strides=[512, 64, 0, 64, 128, 64, 512, 64]), UNSUPPORTED),
+    (dict(strides=[512, 64, 128, 64, 128, -64, 512, 64]), UNSUPPORTED), (dict(ws=None), WORKSPACE),
+    (dict(ws=P + 128), WORKSPACE), (dict(bytes=256), WORKSPACE), (dict(tq=0, tk=0, q=None, k=None, v=None, o=None), 0),
+])
+def test_packed_refusals(fa, kw, want):
+    assert _packed(fa, **kw) == want, fa.lib.fa_last_error_detail()
+
+
+def test_packed_workspace(fa):
+    # pairs of heads: 128-row blocks; an odd group: 256-row blocks; at most one ragged block a sequence
+    assert fa.fwd_packed_workspace_size(3, 1000, 8, 2) == 256 + (1000 // 128 + 3) * 32
+    assert fa.fwd_packed_workspace_size(3, 1000, 6, 2) == 256 + (1000 // 256 + 3) * 32
+    assert fa.fwd_packed_workspace_size(3, 1000, 6, 4) == 0 and fa.fwd_packed_workspace_size(0, 1, 1, 1) == 0
+
+
 def test_page_lookup_on_the_host(tmp_path):
     """The kernels' page lookup and length clipping, compiled for the host: entries outside the pool are refused,
     offsets do not wrap at 2^31 or 2^32 elements."""
