@@ -39,6 +39,12 @@ namespace fa {
 namespace {
 
 constexpr int AP_MAX_THREADS = 256;
+#ifndef AP_BATCH
+#define AP_BATCH 2      // heads whose loads a thread has in flight
+#endif
+#ifndef AP_CTAS
+#define AP_CTAS 3       // blocks an SM should hold
+#endif
 
 __device__ __forceinline__ uint4 ldg16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 
@@ -91,7 +97,7 @@ __device__ __forceinline__ uint32_t to_codes4(const float* x, float inv) {
 }  // namespace
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(AP_MAX_THREADS) fa_append_paged_kernel(const AppendPagedParams p) {
+__global__ void __launch_bounds__(AP_MAX_THREADS, AP_CTAS) fa_append_paged_kernel(const AppendPagedParams p) {
   constexpr int LPR = D / 16;  // lanes of a row, 16 elements each
   extern __shared__ __align__(16) float ap_stash[];  // F8: rotated keys, [stash_rows][D]
   __shared__ int s_seq;
@@ -168,94 +174,108 @@ __global__ void __launch_bounds__(AP_MAX_THREADS) fa_append_paged_kernel(const A
   const int c1 = p.interleaved || !turned ? c0 + 8 : p.rot / 2 + 8 * u;
   float am_k = 0.f, am_v = 0.f;
   if (slot < p.head_slots) {
-    long long tj[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) tj[j] = turned ? __ldg(p.turns + 8 * u + j) : 0;
     for (int r = row_lane; r < nrows; r += p.rows_par) {
       const long long tok = tok0 + r;
-      const long long pos = first + r0 + r;
       float cs[8], sn[8];
-      if (turned) {
+      for (int h0 = slot; h0 < p.G + 2; h0 += AP_BATCH * p.head_slots) {
+        // the loads of AP_BATCH heads are in flight together
+        uint4 raw[AP_BATCH][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // signed 64-bit fraction of a turn in [-1/2, 1/2)
-          const long long a = static_cast<long long>(static_cast<unsigned long long>(pos) * static_cast<unsigned long long>(tj[j]));
-          const float hi = static_cast<float>(static_cast<int>(a >> 32)), lo = static_cast<float>(static_cast<uint32_t>(a));
-          const float f = fmaf(lo, 5.42101086242752217e-20f, hi * 2.3283064365386963e-10f);  // 2^-64, 2^-32
-          sincospif(2.f * f, &sn[j], &cs[j]);
-          sn[j] *= p.rot_scale;
-          cs[j] *= p.rot_scale;
-        }
-      }
-      for (int hh = slot; hh < p.G + 2; hh += p.head_slots) {
-        const bool is_v = hh == p.G + 1, is_k = hh == p.G;
-        const uint16_t* src = is_v   ? static_cast<const uint16_t*>(p.v) + tok * p.vst + hk * p.vsh
-                              : is_k ? static_cast<const uint16_t*>(p.k) + tok * p.kst + hk * p.ksh
-                                     : static_cast<const uint16_t*>(p.q) + tok * p.qst + (hk * p.G + hh) * p.qsh;
-        const uint4 raw0 = ldg16(src + c0), raw1 = ldg16(src + c1);
-        if (!F8 && is_v) {
-          if (store) {
-            uint16_t* dst = static_cast<uint16_t*>(p.v_pages) + pbase + static_cast<long long>(r0 + r) * D;
-            *reinterpret_cast<uint4*>(dst + c0) = raw0;
-            *reinterpret_cast<uint4*>(dst + c1) = raw1;
+        for (int j = 0; j < AP_BATCH; ++j) {
+          const int hh = h0 + j * p.head_slots;
+          if (hh < p.G + 2) {
+            const uint16_t* src = hh == p.G + 1 ? static_cast<const uint16_t*>(p.v) + tok * p.vst + hk * p.vsh
+                                  : hh == p.G   ? static_cast<const uint16_t*>(p.k) + tok * p.kst + hk * p.ksh
+                                                : static_cast<const uint16_t*>(p.q) + tok * p.qst + (hk * p.G + hh) * p.qsh;
+            raw[j][0] = ldg16(src + c0);
+            raw[j][1] = ldg16(src + c1);
           }
-          continue;
         }
-        float x[16];
-        unpack8(raw0, x);
-        unpack8(raw1, x + 8);
-        if (is_v) {
-          am_v = fmaxf(am_v, finite_amax(x));
-          continue;
-        }
-        const void* wt = is_k ? p.k_weight : p.q_weight;
-        if (wt != nullptr) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(gmask, ss, o);
-          const float rs = __frsqrt_rn(fmaf(ss, 1.f / D, p.eps));
-          float w[16];
-          unpack8(ldg16(static_cast<const uint16_t*>(wt) + c0), w);
-          unpack8(ldg16(static_cast<const uint16_t*>(wt) + c1), w + 8);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = x[e] * rs * w[e];
-        }
-        if (turned) {
+        if (h0 == slot && turned) {
+          const unsigned long long pos = static_cast<unsigned long long>(first + r0 + r);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float a = p.interleaved ? x[2 * j] : x[j], bb = p.interleaved ? x[2 * j + 1] : x[j + 8];
-            const float ya = fmaf(a, cs[j], -bb * sn[j]), yb = fmaf(bb, cs[j], a * sn[j]);
-            if (p.interleaved) {
-              x[2 * j] = ya;
-              x[2 * j + 1] = yb;
-            } else {
-              x[j] = ya;
-              x[j + 8] = yb;
-            }
+            // signed 64-bit fraction of a turn in [-1/2, 1/2)
+            const long long a = static_cast<long long>(pos * static_cast<unsigned long long>(__ldg(p.turns + 8 * u + j)));
+            const float hi = static_cast<float>(static_cast<int>(a >> 32)), lo = static_cast<float>(static_cast<uint32_t>(a));
+            const float f = fmaf(lo, 5.42101086242752217e-20f, hi * 2.3283064365386963e-10f);  // 2^-64, 2^-32
+            sincospif(2.f * f, &sn[j], &cs[j]);
+            sn[j] *= p.rot_scale;
+            cs[j] *= p.rot_scale;
           }
         }
-        const uint4 y0 = pack8(x), y1 = pack8(x + 8);
-        uint16_t* out = is_k ? (p.k_out == nullptr ? nullptr : static_cast<uint16_t*>(p.k_out) + tok * p.kost + hk * p.kosh)
-                             : static_cast<uint16_t*>(p.q_out) + tok * p.qost + (hk * p.G + hh) * p.qosh;
-        if (out != nullptr) {
-          *reinterpret_cast<uint4*>(out + c0) = y0;
-          *reinterpret_cast<uint4*>(out + c1) = y1;
-        }
-        if (is_k && store) {
-          if constexpr (F8) {
-            am_k = fmaxf(am_k, finite_amax(x));
-            float* st = ap_stash + r * D;
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              *reinterpret_cast<float4*>(st + c0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-              *reinterpret_cast<float4*>(st + c1 + e) = make_float4(x[8 + e], x[9 + e], x[10 + e], x[11 + e]);
+        for (int j = 0; j < AP_BATCH; ++j) {
+          const int hh = h0 + j * p.head_slots;
+          if (hh >= p.G + 2) break;
+          const bool is_v = hh == p.G + 1, is_k = hh == p.G;
+          if (!F8 && is_v) {
+            if (store) {
+              uint16_t* dst = static_cast<uint16_t*>(p.v_pages) + pbase + static_cast<long long>(r0 + r) * D;
+              *reinterpret_cast<uint4*>(dst + c0) = raw[j][0];
+              *reinterpret_cast<uint4*>(dst + c1) = raw[j][1];
             }
-          } else {
-            uint16_t* dst = static_cast<uint16_t*>(p.k_pages) + pbase + static_cast<long long>(r0 + r) * D;
-            *reinterpret_cast<uint4*>(dst + c0) = y0;
-            *reinterpret_cast<uint4*>(dst + c1) = y1;
+            continue;
+          }
+          float x[16];
+          unpack8(raw[j][0], x);
+          unpack8(raw[j][1], x + 8);
+          if (is_v) {
+            am_v = fmaxf(am_v, finite_amax(x));
+            continue;
+          }
+          const void* wt = is_k ? p.k_weight : p.q_weight;
+          if (wt != nullptr) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(gmask, ss, o);
+            const float rs = __frsqrt_rn(fmaf(ss, 1.f / D, p.eps));
+            float w[16];
+            unpack8(ldg16(static_cast<const uint16_t*>(wt) + c0), w);
+            unpack8(ldg16(static_cast<const uint16_t*>(wt) + c1), w + 8);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = x[e] * rs * w[e];
+          }
+          if (turned) {
+            if (p.interleaved) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float ya = fmaf(x[2 * e], cs[e], -x[2 * e + 1] * sn[e]);
+                x[2 * e + 1] = fmaf(x[2 * e + 1], cs[e], x[2 * e] * sn[e]);
+                x[2 * e] = ya;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float ya = fmaf(x[e], cs[e], -x[e + 8] * sn[e]);
+                x[e + 8] = fmaf(x[e + 8], cs[e], x[e] * sn[e]);
+                x[e] = ya;
+              }
+            }
+          }
+          const uint4 y0 = pack8(x), y1 = pack8(x + 8);
+          uint16_t* out = is_k ? (p.k_out == nullptr ? nullptr : static_cast<uint16_t*>(p.k_out) + tok * p.kost + hk * p.kosh)
+                               : static_cast<uint16_t*>(p.q_out) + tok * p.qost + (hk * p.G + hh) * p.qosh;
+          if (out != nullptr) {
+            *reinterpret_cast<uint4*>(out + c0) = y0;
+            *reinterpret_cast<uint4*>(out + c1) = y1;
+          }
+          if (is_k && store) {
+            if constexpr (F8) {
+              am_k = fmaxf(am_k, finite_amax(x));
+              float* st = ap_stash + r * D;
+#pragma unroll
+              for (int e = 0; e < 8; e += 4) {
+                *reinterpret_cast<float4*>(st + c0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                *reinterpret_cast<float4*>(st + c1 + e) = make_float4(x[8 + e], x[9 + e], x[10 + e], x[11 + e]);
+              }
+            } else {
+              uint16_t* dst = static_cast<uint16_t*>(p.k_pages) + pbase + static_cast<long long>(r0 + r) * D;
+              *reinterpret_cast<uint4*>(dst + c0) = y0;
+              *reinterpret_cast<uint4*>(dst + c1) = y1;
+            }
           }
         }
       }

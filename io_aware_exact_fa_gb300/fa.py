@@ -354,76 +354,94 @@ def rotary_turns(rot: int, base: float = 10000.0, scaling: Optional[Tuple] = Non
     return torch.tensor(out, dtype=torch.int64, device=device if device is not None else "cuda")
 
 
-def _on(t: torch.Tensor, name: str, dtype, device) -> None:
+# The checks below run before every call of a serving step, so each tensor's properties are asked for once, and a
+# device is compared by its index (-1 for host tensors).
+
+def _on(t: torch.Tensor, name: str, dtype, dev: int) -> None:
     """A CUDA tensor of the given type on the call's device; strided layouts are the caller's to check."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, q on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, q on cuda:{dev}")
 
 
-def _whole(t: torch.Tensor, name: str, dtype, device, shape=None) -> None:
-    _on(t, name, dtype, device)
+def _whole(t: torch.Tensor, name: str, dtype, dev: int, shape=None) -> int:
+    """A contiguous tensor (of the given shape); returns its address."""
+    _on(t, name, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, name: str, device, shape) -> None:
-    """A bf16 tensor whose last dimension is contiguous; its other strides may be any multiple of 8."""
-    _on(t, name, torch.bfloat16, device)
-    if tuple(t.shape) != shape:
+def _heads(t: torch.Tensor, name: str, dev: int, shape) -> Tuple[int, ...]:
+    """A bf16 tensor whose last dimension is contiguous; its other strides may be any multiple of 8. Returns the
+    strides of the others for the C ABI: a dimension of one element has none that matters."""
+    _on(t, name, torch.bfloat16, dev)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.stride(-1) != 1:
+    st = t.stride()
+    if st[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
+    if 1 in shape:
+        return tuple(x if n > 1 else 0 for x, n in zip(st[:-1], shape))
+    return st[:-1]
 
 
-def _strides(t: torch.Tensor, dims) -> list:
-    """Element strides for the C ABI; a dimension of one element has none that matters."""
-    return [t.stride(i) if t.shape[i] > 1 else 0 for i in dims]
-
-
-def _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, device):
-    """Checks the paged cache; returns (pages, page size, e4m3?)."""
-    e4m3 = isinstance(k_pages, torch.Tensor) and k_pages.dtype in (torch.float8_e4m3fn, torch.uint8)
-    kind = k_pages.dtype if e4m3 else torch.bfloat16
-    _whole(k_pages, "k_pages", kind, device)
-    _whole(v_pages, "v_pages", kind, device)
-    if k_pages.dim() != 4 or k_pages.shape[1] != Hkv or k_pages.shape[3] != d or v_pages.shape != k_pages.shape:
+def _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv: int, d: int, dev: int):
+    """Checks the paged cache; returns (its addresses as the C ABI takes them, pages, page size, e4m3?, B, width)."""
+    if not isinstance(k_pages, torch.Tensor):
+        raise ValueError("k_pages must be a CUDA tensor")
+    kind = k_pages.dtype
+    e4m3 = kind is torch.float8_e4m3fn or kind is torch.uint8
+    if not e4m3:
+        kind = torch.bfloat16
+    kp = _whole(k_pages, "k_pages", kind, dev)
+    shape = k_pages.shape
+    if len(shape) != 4 or shape[1] != Hkv or shape[3] != d:
         raise ValueError(f"k_pages and v_pages must be [num_pages, {Hkv}, page, {d}]")
-    n, page = k_pages.shape[0], k_pages.shape[2]
+    vp = _whole(v_pages, "v_pages", kind, dev, shape)
+    n, page = shape[0], shape[2]
+    ks = vs = None
     if e4m3:
         if k_scale is None or v_scale is None:
             raise ValueError("e4m3 pages need k_scale and v_scale")
-        _whole(k_scale, "k_scale", torch.float32, device, (n, Hkv))
-        _whole(v_scale, "v_scale", torch.float32, device, (n, Hkv))
+        ks = _whole(k_scale, "k_scale", torch.float32, dev, (n, Hkv))
+        vs = _whole(v_scale, "v_scale", torch.float32, dev, (n, Hkv))
     elif k_scale is not None or v_scale is not None:
         raise ValueError("bf16 pages take no scales")
-    _on(block_table, "block_table", torch.int32, device)
-    _whole(seqlens_k, "seqlens_k", torch.int32, device)
-    if block_table.dim() != 2 or block_table.stride(1) != 1 and block_table.shape[1] > 1:
-        raise ValueError("block_table must be [B, width] with contiguous rows")
-    if seqlens_k.shape != (block_table.shape[0],):
-        raise ValueError("seqlens_k must be int32 [B], with the rows of block_table")
-    return n, page, e4m3
+    _on(block_table, "block_table", torch.int32, dev)
+    tab = block_table.shape
+    if len(tab) != 2:
+        raise ValueError("block_table must be [B, width]")
+    ts = block_table.stride()
+    if ts[1] != 1 and tab[1] > 1:
+        raise ValueError("the rows of block_table must be contiguous")
+    lens = _whole(seqlens_k, "seqlens_k", torch.int32, dev, (tab[0],))
+    return (kp, vp, ks, vs, block_table.data_ptr(), ts[0], lens), n, page, e4m3, tab[0], tab[1]
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _call(device: torch.device, stream: Optional[torch.cuda.Stream], fn, args, where: str) -> None:
+def _call(dev: int, stream: Optional[torch.cuda.Stream], fn, args, where: str) -> None:
     """Calls the library with the tensors' device current, on ``stream`` or that device's current stream."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, _stream_ptr(stream)), where)
+    if stream is None:
+        st = _raw_stream(dev)
+    elif stream.device.index == dev:
+        st = stream.cuda_stream
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream_ptr(stream)), where)
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, st)
+    if rc != FA_OK:
+        raise FAError(rc, where)
 
 
 _I64x10 = ctypes.c_int64 * 10
@@ -449,37 +467,30 @@ def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: tor
         raise ValueError("q must be a CUDA tensor [T, H, d]")
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a CUDA tensor [T, Hkv, d]")
-    dev = q.device
-    T, H, d = q.shape
-    Hkv = k.shape[1]
-    _heads(q, "q", dev, (T, H, d)); _heads(k, "k", dev, (T, Hkv, d)); _heads(v, "v", dev, (T, Hkv, d))
-    n, page, e4m3 = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, dev)
-    B = seqlens_k.shape[0]
-    if cu_seqlens is not None:
-        _whole(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
-    rot = 0
+    dev = q.get_device()
+    T, H, d = q_shape = q.shape
+    kv_shape = (T, k.shape[1], d)
+    Hkv = kv_shape[1]
+    st = _heads(q, "q", dev, q_shape) + _heads(k, "k", dev, kv_shape) + _heads(v, "v", dev, kv_shape)
+    pool, n, page, e4m3, B, width = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, dev)
+    kp, vp, ks, vs, table, table_stride, lens = pool
+    cu = None if cu_seqlens is None else _whole(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
+    rot, tp = 0, None
     if turns is not None:
-        _whole(turns, "turns", torch.int64, dev)
+        tp = _whole(turns, "turns", torch.int64, dev)
         rot = 2 * turns.numel()
-    if q_weight is not None:
-        _whole(q_weight, "q_weight", torch.bfloat16, dev, (d,))
-    if k_weight is not None:
-        _whole(k_weight, "k_weight", torch.bfloat16, dev, (d,))
+    qw = None if q_weight is None else _whole(q_weight, "q_weight", torch.bfloat16, dev, (d,))
+    kw = None if k_weight is None else _whole(k_weight, "k_weight", torch.bfloat16, dev, (d,))
     if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _heads(q_out, "q_out", dev, (T, H, d))
+        q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+    st += _heads(q_out, "q_out", dev, q_shape)
     if k_out is None and with_k:
-        k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=dev)
-    elif k_out is not None:
-        _heads(k_out, "k_out", dev, (T, Hkv, d))
-    st = _I64x10(*_strides(q, (0, 1)), *_strides(k, (0, 1)), *_strides(v, (0, 1)), *_strides(q_out, (0, 1)),
-                 *(_strides(k_out, (0, 1)) if k_out is not None else (0, 0)))
+        k_out = torch.empty(kv_shape, dtype=torch.bfloat16, device=q.device)
+    st += (0, 0) if k_out is None else _heads(k_out, "k_out", dev, kv_shape)
     _call(dev, stream, _lib.fa_append_paged,
-          (_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-           _ptr(v_scale), _ptr(block_table), block_table.stride(0), _ptr(seqlens_k), _ptr(cu_seqlens), _ptr(turns),
-           _ptr(q_weight), _ptr(k_weight), st, B, T, H, Hkv, d, n, page, block_table.shape[1], int(e4m3), rot,
-           int(bool(interleaved)), float(rot_scale), float(eps), int(max_new)), "fa_append_paged")
+          (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), kp, vp,
+           ks, vs, table, table_stride, lens, cu, tp, qw, kw, _I64x10(*st), B, T, H, Hkv, d, n, page, width, e4m3, rot,
+           bool(interleaved), rot_scale, eps, max_new), "fa_append_paged")
     return q_out, k_out
 
 
@@ -499,40 +510,35 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     row of the table covers); ``num_splits`` 0 lets the library choose."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
-    dev = q.device
-    B, H, Nq, d = q.shape
-    _heads(q, "q", dev, (B, H, Nq, d))
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("k_pages must be a CUDA tensor [num_pages, Hkv, page, d]")
+    dev = q.get_device()
+    B, H, Nq, d = q_shape = q.shape
+    qs = _heads(q, "q", dev, q_shape)
     Hkv = k_pages.shape[1]
-    n, page, e4m3 = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, dev)
-    if seqlens_k.shape[0] != B:
+    pool, n, page, e4m3, rows, width = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, dev)
+    if rows != B:
         raise ValueError("seqlens_k and block_table must have B rows")
-    most = block_table.shape[1] * page
+    kp, vp, ks, vs, table, table_stride, lens = pool
     if max_len is None:
-        max_len = most
-    elif not 0 <= max_len <= most:
-        raise ValueError(f"max_len must be in [0, {most}], what a row of block_table covers")
+        max_len = width * page
+    elif not 0 <= max_len <= width * page:
+        raise ValueError(f"max_len must be in [0, {width * page}], what a row of block_table covers")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _heads(out, "out", dev, (B, H, Nq, d))
-    if lse is not None:
-        _whole(lse, "lse", torch.float32, dev, (B, H, Nq))
-    elif with_lse:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+        out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+    os_ = _heads(out, "out", dev, q_shape)
+    if lse is None and with_lse:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    lp = None if lse is None else _whole(lse, "lse", torch.float32, dev, (B, H, Nq))
     if workspace is None:
         workspace = torch.empty(max(1, decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits)),
-                                dtype=torch.uint8, device=dev)
-    else:
-        _whole(workspace, "workspace", workspace.dtype, dev)
+                                dtype=torch.uint8, device=q.device)
+    wp = _whole(workspace, "workspace", workspace.dtype, dev)
     _call(dev, stream, _lib.fa_decode_paged,
-          (_ptr(q), _I64x3(*_strides(q, (0, 1, 2))), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-           _ptr(block_table), block_table.stride(0), _ptr(seqlens_k), _ptr(out), _I64x3(*_strides(out, (0, 1, 2))),
-           _ptr(lse), B, H, Hkv, Nq, d, n, page, int(max_len), int(e4m3), float(scale), int(num_splits),
-           _ptr(workspace), workspace.numel() * workspace.element_size()), "fa_decode_paged")
+          (q.data_ptr(), _I64x3(*qs), kp, vp, ks, vs, table, table_stride, lens, out.data_ptr(), _I64x3(*os_), lp, B, H,
+           Hkv, Nq, d, n, page, max_len, e4m3, scale, num_splits, wp, workspace.nbytes), "fa_decode_paged")
     return out, lse
 
 
@@ -557,35 +563,30 @@ def fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
         raise ValueError("q must be a CUDA tensor [total_q, H, d]")
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a CUDA tensor [total_k, Hkv, d]")
-    dev = q.device
-    Tq, H, d = q.shape
+    dev = q.get_device()
+    Tq, H, d = q_shape = q.shape
     Tk, Hkv = k.shape[0], k.shape[1]
-    _heads(q, "q", dev, (Tq, H, d)); _heads(k, "k", dev, (Tk, Hkv, d)); _heads(v, "v", dev, (Tk, Hkv, d))
-    _whole(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
+    kv_shape = (Tk, Hkv, d)
+    st = _heads(q, "q", dev, q_shape) + _heads(k, "k", dev, kv_shape) + _heads(v, "v", dev, kv_shape)
+    cq = _whole(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
     B = cu_seqlens_q.numel() - 1
     if cu_seqlens_q.dim() != 1 or B < 1:
         raise ValueError("cu_seqlens_q must be int32 [B + 1], B >= 1")
-    if cu_seqlens_k is not None:
-        _whole(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, (B + 1,))
+    ck = None if cu_seqlens_k is None else _whole(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, (B + 1,))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((Tq, H, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _heads(out, "out", dev, (Tq, H, d))
-    if lse is not None:
-        _whole(lse, "lse", torch.float32, dev, (H, Tq))
-    elif with_lse:
-        lse = torch.empty((H, Tq), dtype=torch.float32, device=dev)
+        out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+    st += _heads(out, "out", dev, q_shape)
+    if lse is None and with_lse:
+        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    lp = None if lse is None else _whole(lse, "lse", torch.float32, dev, (H, Tq))
     if workspace is None:
-        workspace = torch.empty(max(1, fwd_packed_workspace_size(B, Tq, H, Hkv)), dtype=torch.uint8, device=dev)
-    else:
-        _whole(workspace, "workspace", workspace.dtype, dev)
-    st = _I64x8(*_strides(q, (0, 1)), *_strides(k, (0, 1)), *_strides(v, (0, 1)), *_strides(out, (0, 1)))
+        workspace = torch.empty(max(1, fwd_packed_workspace_size(B, Tq, H, Hkv)), dtype=torch.uint8, device=q.device)
+    wp = _whole(workspace, "workspace", workspace.dtype, dev)
     _call(dev, stream, _lib.fa_fwd_packed,
-          (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), st, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, Tq, Tk, H,
-           Hkv, d, float(scale), int(bool(causal)), _ptr(workspace), workspace.numel() * workspace.element_size()),
-          "fa_fwd_packed")
+          (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, _I64x8(*st), cq, ck, B, Tq, Tk, H, Hkv, d, scale,
+           bool(causal), wp, workspace.nbytes), "fa_fwd_packed")
     return out, lse
 
 
