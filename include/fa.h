@@ -366,8 +366,8 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
  * 128. One launch on `stream`. Errors: FA_ERR_INVALID_ARG for NULL tensors, bad
  * sizes, H not a multiple of Hkv, T not a multiple of B without cu_seqlens;
  * FA_ERR_UNSUPPORTED for other d, rot or page sizes, strides that are not
- * multiples of 8, or pointers that are not 16-byte (turns 8-byte, other arrays
- * 4-byte) aligned. */
+ * multiples of 8, or pointers that are not 16-byte (scales, table, lengths and
+ * offsets 4-byte) aligned. */
 fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
                           void* v_pages, float* k_scale, float* v_scale, const int* block_table, int64_t table_stride,
                           const int* seqlens_k, const int* cu_seqlens, const int64_t* turns, const void* q_weight,

@@ -891,14 +891,14 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
   if (rot > 0 && !turns) return fail(FA_ERR_INVALID_ARG, "a rotation needs turns");
   for (const void* x : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_out), q_weight, k_weight})
     if (!aligned(x, 16)) return fail(FA_ERR_UNSUPPORTED, "q, k, v, the outputs and the weights must be 16-byte aligned");
-  if (!aligned(turns, 8) || !aligned(cu_seqlens, 4)) return fail(FA_ERR_UNSUPPORTED, "turns must be 8-byte, cu_seqlens 4-byte aligned");
+  if (!aligned(turns, 16) || !aligned(cu_seqlens, 4)) return fail(FA_ERR_UNSUPPORTED, "turns must be 16-byte, cu_seqlens 4-byte aligned");
   if (table_stride < table_width && B > 1) return fail(FA_ERR_INVALID_ARG, "table_stride is below table_width");
   for (int i = 0; i < 10; ++i)
     if (!strides_ok({strides[i]})) return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements and >= 0");
   const int n_max = cu_seqlens == nullptr ? T / B : std::min(max_new > 0 ? max_new : T, T);
   const long long rect = (static_cast<long long>(n_max) + page - 2) / page + 1;
   const bool use_rect = cu_seqlens == nullptr || rect * B <= T / page + 2LL * B;
-  if ((use_rect ? rect * B : T / page + 2LL * B) * Hkv > INT_MAX)
+  if ((use_rect ? rect * B : T / page + 2LL * B) * Hkv > INT_MAX / 2 || static_cast<long long>(T) > INT_MAX / 2)
     return fail(FA_ERR_INVALID_ARG, "B, T and Hkv give too many blocks");
 
   DeviceState* st = nullptr;
@@ -919,13 +919,9 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
   p.max_new = n_max;
   p.per_seq = use_rect ? static_cast<int>(rect) : 0;
   p.status = st->status;
-  // Rows in parallel: all of a page's where the call has as many; the heads share what is left of 256 threads.
-  const int lanes = d / 16, groups = 256 / lanes;
-  int rows = 1;
-  while (rows < std::min(page, n_max) && rows < groups) rows *= 2;
-  p.rows_par = rows;
-  p.head_slots = std::max(1, std::min(groups / rows, p.G + 2));
-  p.stash_rows = std::min(page, n_max);
+  p.kv_blocks = static_cast<int>((use_rect ? rect * B : T / page + 2LL * B) * Hkv);
+  p.max_rows = std::min(page, n_max);
+  p.q_blocks_wanted = 6 * st->num_sms;
   cudaError_t e = fa::launch_append_paged(e4m3 != 0, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
   t_launches += 1;

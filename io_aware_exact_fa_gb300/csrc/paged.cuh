@@ -79,9 +79,11 @@ struct AppendPagedParams {
   int width, page, page_shift, num_pages;
   int rot, interleaved;
   int max_new;               // most new tokens of one sequence
-  int per_seq;               // > 0: blocks are B x per_seq pages; 0: found through cu
-  int rows_par, head_slots;  // thread groups of a block: rows in parallel x heads in parallel
-  int stash_rows;            // rows of the e4m3 key stash in shared memory
+  int per_seq;               // > 0: K/V blocks are B x per_seq pages; 0: found through cu
+  int kv_blocks;             // K/V blocks (pages x K/V heads); the query blocks follow
+  int max_rows;              // most new rows of one page
+  int q_blocks_wanted;       // query blocks that fill the GPU a few times over
+  int q_slots;               // heads of a row that a query block takes side by side
   float rot_scale, eps;
   unsigned int* status;
 };

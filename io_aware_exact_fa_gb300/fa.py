@@ -354,38 +354,40 @@ def rotary_turns(rot: int, base: float = 10000.0, scaling: Optional[Tuple] = Non
     return torch.tensor(out, dtype=torch.int64, device=device if device is not None else "cuda")
 
 
-# The checks below run before every call of a serving step, so each tensor's properties are asked for once, and a
-# device is compared by its index (-1 for host tensors).
+# The checks below run before every call of a serving step: each tensor's properties are asked for once, a device is
+# compared by its index (-1 for host tensors), and the reason of a refusal is worked out only once there is one.
 
-def _on(t: torch.Tensor, name: str, dtype, dev: int) -> None:
-    """A CUDA tensor of the given type on the call's device; strided layouts are the caller's to check."""
+_BF16, _F32, _I32, _CODES = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+
+
+def _refusal(t, name: str, dtype, dev: int, shape, layout: str) -> ValueError:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+        return ValueError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        return ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, q on cuda:{dev}")
+        return ValueError(f"{name} is on {t.device}, q on cuda:{dev}")
+    if shape is not None and t.shape != shape:
+        return ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return ValueError(f"{name} must {layout}")
 
 
 def _whole(t: torch.Tensor, name: str, dtype, dev: int, shape=None) -> int:
-    """A contiguous tensor (of the given shape); returns its address."""
-    _on(t, name, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    """A contiguous tensor (of the given shape) on the call's device; returns its address."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()
+            or (shape is not None and t.shape != shape)):
+        raise _refusal(t, name, dtype, dev, shape, "be contiguous")
     return t.data_ptr()
 
 
 def _heads(t: torch.Tensor, name: str, dev: int, shape) -> Tuple[int, ...]:
     """A bf16 tensor whose last dimension is contiguous; its other strides may be any multiple of 8. Returns the
     strides of the others for the C ABI: a dimension of one element has none that matters."""
-    _on(t, name, torch.bfloat16, dev)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
+        raise _refusal(t, name, _BF16, dev, shape, "")
     st = t.stride()
     if st[-1] != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+        raise _refusal(t, name, _BF16, dev, shape, "have a contiguous last dimension")
     if 1 in shape:
         return tuple(x if n > 1 else 0 for x, n in zip(st[:-1], shape))
     return st[:-1]
@@ -396,9 +398,9 @@ def _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv: int, 
     if not isinstance(k_pages, torch.Tensor):
         raise ValueError("k_pages must be a CUDA tensor")
     kind = k_pages.dtype
-    e4m3 = kind is torch.float8_e4m3fn or kind is torch.uint8
+    e4m3 = kind is _CODES or kind is torch.uint8
     if not e4m3:
-        kind = torch.bfloat16
+        kind = _BF16
     kp = _whole(k_pages, "k_pages", kind, dev)
     shape = k_pages.shape
     if len(shape) != 4 or shape[1] != Hkv or shape[3] != d:
@@ -409,18 +411,16 @@ def _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv: int, 
     if e4m3:
         if k_scale is None or v_scale is None:
             raise ValueError("e4m3 pages need k_scale and v_scale")
-        ks = _whole(k_scale, "k_scale", torch.float32, dev, (n, Hkv))
-        vs = _whole(v_scale, "v_scale", torch.float32, dev, (n, Hkv))
+        ks = _whole(k_scale, "k_scale", _F32, dev, (n, Hkv))
+        vs = _whole(v_scale, "v_scale", _F32, dev, (n, Hkv))
     elif k_scale is not None or v_scale is not None:
         raise ValueError("bf16 pages take no scales")
-    _on(block_table, "block_table", torch.int32, dev)
-    tab = block_table.shape
-    if len(tab) != 2:
-        raise ValueError("block_table must be [B, width]")
-    ts = block_table.stride()
-    if ts[1] != 1 and tab[1] > 1:
-        raise ValueError("the rows of block_table must be contiguous")
-    lens = _whole(seqlens_k, "seqlens_k", torch.int32, dev, (tab[0],))
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not _I32 or block_table.get_device() != dev:
+        raise _refusal(block_table, "block_table", _I32, dev, None, "")
+    tab, ts = block_table.shape, block_table.stride()
+    if len(tab) != 2 or (ts[1] != 1 and tab[1] > 1):
+        raise ValueError("block_table must be [B, width] with contiguous rows")
+    lens = _whole(seqlens_k, "seqlens_k", _I32, dev, (tab[0],))
     return (kp, vp, ks, vs, block_table.data_ptr(), ts[0], lens), n, page, e4m3, tab[0], tab[1]
 
 
@@ -462,7 +462,8 @@ def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: tor
     [num_pages,Hkv,page,d] bf16, or float8_e4m3fn / uint8 codes with fp32 scales [num_pages,Hkv]; block_table int32
     [B,width]; seqlens_k int32 [B] with the new tokens counted; cu_seqlens int32 [B+1], or None for T / B tokens each.
     ``turns`` (``rotary_turns``) sets the rotation, None for none; the weights bf16 [d] the norms, None for none.
-    Returns the turned q [T,H,d] and k [T,Hkv,d] (None without ``with_k``)."""
+    Returns the turned q [T,H,d] and k [T,Hkv,d] (None without ``with_k``); outputs that are not given are laid out like
+    q and k where those are dense, else contiguous."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
         raise ValueError("q must be a CUDA tensor [T, H, d]")
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
@@ -474,18 +475,18 @@ def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: tor
     st = _heads(q, "q", dev, q_shape) + _heads(k, "k", dev, kv_shape) + _heads(v, "v", dev, kv_shape)
     pool, n, page, e4m3, B, width = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, dev)
     kp, vp, ks, vs, table, table_stride, lens = pool
-    cu = None if cu_seqlens is None else _whole(cu_seqlens, "cu_seqlens", torch.int32, dev, (B + 1,))
+    cu = None if cu_seqlens is None else _whole(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,))
     rot, tp = 0, None
     if turns is not None:
         tp = _whole(turns, "turns", torch.int64, dev)
         rot = 2 * turns.numel()
-    qw = None if q_weight is None else _whole(q_weight, "q_weight", torch.bfloat16, dev, (d,))
-    kw = None if k_weight is None else _whole(k_weight, "k_weight", torch.bfloat16, dev, (d,))
+    qw = None if q_weight is None else _whole(q_weight, "q_weight", _BF16, dev, (d,))
+    kw = None if k_weight is None else _whole(k_weight, "k_weight", _BF16, dev, (d,))
     if q_out is None:
-        q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty_like(q)
     st += _heads(q_out, "q_out", dev, q_shape)
     if k_out is None and with_k:
-        k_out = torch.empty(kv_shape, dtype=torch.bfloat16, device=q.device)
+        k_out = torch.empty_like(k)
     st += (0, 0) if k_out is None else _heads(k_out, "k_out", dev, kv_shape)
     _call(dev, stream, _lib.fa_append_paged,
           (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), kp, vp,
@@ -507,7 +508,7 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     """Grouped decode over a paged cache (fa.h fa_decode_paged): q [B,H,Nq,d] bf16, any strides with d contiguous
     (``append_paged``'s q of B x Nq tokens is ``q.view(B, Nq, H, d).transpose(1, 2)``), the pool and table as for
     ``append_paged`` -> (o [B,H,Nq,d] bf16, lse [B,H,Nq] fp32). ``max_len`` bounds the lengths (default: all that a
-    row of the table covers); ``num_splits`` 0 lets the library choose."""
+    row of the table covers); ``num_splits`` 0 lets the library choose. Without ``out``, o is laid out like q where that is dense."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
@@ -527,14 +528,14 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q)
     os_ = _heads(out, "out", dev, q_shape)
     if lse is None and with_lse:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    lp = None if lse is None else _whole(lse, "lse", torch.float32, dev, (B, H, Nq))
+        lse = q.new_empty((B, H, Nq), dtype=_F32)
+    lp = None if lse is None else _whole(lse, "lse", _F32, dev, (B, H, Nq))
     if workspace is None:
-        workspace = torch.empty(max(1, decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits)),
-                                dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(max(1, decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits)),
+                                dtype=torch.uint8)
     wp = _whole(workspace, "workspace", workspace.dtype, dev)
     _call(dev, stream, _lib.fa_decode_paged,
           (q.data_ptr(), _I64x3(*qs), kp, vp, ks, vs, table, table_stride, lens, out.data_ptr(), _I64x3(*os_), lp, B, H,
@@ -568,21 +569,21 @@ def fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     Tk, Hkv = k.shape[0], k.shape[1]
     kv_shape = (Tk, Hkv, d)
     st = _heads(q, "q", dev, q_shape) + _heads(k, "k", dev, kv_shape) + _heads(v, "v", dev, kv_shape)
-    cq = _whole(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
+    cq = _whole(cu_seqlens_q, "cu_seqlens_q", _I32, dev)
     B = cu_seqlens_q.numel() - 1
     if cu_seqlens_q.dim() != 1 or B < 1:
         raise ValueError("cu_seqlens_q must be int32 [B + 1], B >= 1")
-    ck = None if cu_seqlens_k is None else _whole(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, (B + 1,))
+    ck = None if cu_seqlens_k is None else _whole(cu_seqlens_k, "cu_seqlens_k", _I32, dev, (B + 1,))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q)
     st += _heads(out, "out", dev, q_shape)
     if lse is None and with_lse:
-        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
-    lp = None if lse is None else _whole(lse, "lse", torch.float32, dev, (H, Tq))
+        lse = q.new_empty((H, Tq), dtype=_F32)
+    lp = None if lse is None else _whole(lse, "lse", _F32, dev, (H, Tq))
     if workspace is None:
-        workspace = torch.empty(max(1, fwd_packed_workspace_size(B, Tq, H, Hkv)), dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(max(1, fwd_packed_workspace_size(B, Tq, H, Hkv)), dtype=torch.uint8)
     wp = _whole(workspace, "workspace", workspace.dtype, dev)
     _call(dev, stream, _lib.fa_fwd_packed,
           (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, _I64x8(*st), cq, ck, B, Tq, Tk, H, Hkv, d, scale,
