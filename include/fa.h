@@ -375,8 +375,8 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
                           int num_pages, int page, int table_width, int e4m3, int rot, int interleaved,
                           float rot_scale, float eps, int max_new, void* stream);
 
-/* Bytes of device workspace fa_decode_paged needs: the split-KV partial states
- * (256 when one split suffices). Returns 0 for invalid arguments. */
+/* Bytes of device workspace fa_decode_paged needs: the partial states of the
+ * ranges it shares the keys out in. Returns 0 for invalid arguments. */
 size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int num_splits);
 
 /* fa_decode_grouped over a paged cache: the last Nq tokens of every sequence
@@ -388,20 +388,20 @@ size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int 
  *              contiguous). Token-major tensors, as fa_append_paged returns them,
  *              are passed by their strides.
  *   lse        fp32 [B, H, Nq] (may be NULL)
- *   max_len    no sequence is longer (a bound the host knows, at most the
- *              positions a block-table row covers, and at most 2^30; longer ones
- *              are clipped and reported). It sets the splits.
- *   num_splits 1 .. 1024 splits of the keys (rounded to whole 128-key pieces), or
- *              0: chosen so that the launch fills the GPU.
+ *   max_len    no sequence is longer (at most the positions a block-table row
+ *              covers, and at most 2^30; longer ones are clipped and reported).
+ *   num_splits 0: the keys of the whole batch are shared out in equal ranges, one
+ *              for each warp that the GPU holds, whatever the lengths;
+ *              1 .. 1024: in so many ranges a sequence and K/V head on average.
  *   scales of e4m3 pages: any finite positive factors (fa_append_paged writes
  *              powers of two, which add no rounding).
  *   workspace  device memory of fa_decode_paged_workspace_size() bytes, 256-byte
  *              aligned, owned by the caller, overwritten; calls that may overlap
- *              on the GPU need their own. Unused (may be NULL) with one split.
+ *              on the GPU need their own.
  * Products with e4m3 pages run in f16 on the codes, with fp32 accumulation and
  * the weights rounded to f16; with bf16 pages in bf16. A NaN or infinity in v
  * reaches the rows of its sequence's last Nq tokens. Errors as for
- * fa_decode_grouped. One launch, two with more than one split. */
+ * fa_decode_grouped. Two launches (the ranges, their merge). */
 fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
                           const float* k_scale, const float* v_scale, const int* block_table, int64_t table_stride,
                           const int* seqlens_k, void* o, const int64_t* o_strides, float* lse, int B, int H, int Hkv,

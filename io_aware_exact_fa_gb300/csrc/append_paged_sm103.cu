@@ -541,7 +541,8 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
           if (!(w ? rvv : rk)) continue;
           uint32_t* at4 = reinterpret_cast<uint32_t*>(w ? vp : kp) + x;
           const uint32_t old = *at4;
-          const uint32_t h0 = e4m3x2_to_f16x2(old), h1 = e4m3x2_to_f16x2(old >> 16);
+          uint32_t h0, h1;
+          e4m3x4_to_f16x2x2(old, h0, h1);
           const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
           const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
           *at4 = to_codes4(f0.x, f0.y, f1.x, f1.y, w ? fv : fk);

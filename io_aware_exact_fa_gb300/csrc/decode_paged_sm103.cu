@@ -23,14 +23,23 @@
 // M side of S^T = K Q^T and the head dimension the M side of O^T = V^T P^T, the
 // 8 (or 16) query rows the N side, and neither product pads the rows past 8.
 //
-// Split-KV: CTA (row tile, split, K/V head, sequence); its 4 warps take tiles of
-// KS keys in turn, each with a private ring of asynchronous 16-byte copies, so
-// there is no barrier inside the loop. A tile's 16-key groups may lie in
-// different pages; one lane per group looks the page up. The fragments are read
-// straight from the copied rows: the order of the contraction over d (for S) and
-// of the output rows (for O^T) is free, so each lane takes whole 16-byte pieces
-// of its rows, and the shared-memory positions of the pieces are XORed with the
-// row so that those reads touch every bank once.
+// Work split: all keys of the batch, as tiles of KS keys laid end to end (sequence
+// by sequence, K/V head by K/V head), are shared out in equal contiguous ranges,
+// one for each warp that the GPU holds, so ragged lengths leave no SM idle and no
+// warp starts anew for every chunk (blocks of one chunk each spent a third of
+// their time filling and draining: 73 against 97 us for two sequences of 110k
+// tokens). A warp walks its range through a private ring of asynchronous 16-byte
+// copies that runs on across sequences; it meets no other warp, so there is no
+// barrier at all. Where a sequence's keys of one head lie in several ranges, each
+// warp leaves its base, sum and output, and the merge kernel joins them; which
+// ranges those are, both kernels work out from the lengths on the device.
+//
+// A tile's 16-key groups may lie in different pages; one lane per group looks the
+// page up, a tile ahead. The fragments are read straight from the copied rows: the
+// order of the contraction over d (for S) and of the output rows (for O^T) is
+// free, so each lane takes whole 16-byte pieces of its rows, and the shared-memory
+// positions of the pieces are XORed with the row so that those reads touch every
+// bank once.
 #include <cuda_bf16.h>
 
 #include "mma_sync.cuh"
@@ -42,8 +51,15 @@ namespace {
 
 constexpr int DP_WARPS = 4;
 constexpr int DP_THREADS = 32 * DP_WARPS;
-constexpr int DP_STAGES = 3;           // tiles in each warp's ring
-constexpr int DP_HALF_BYTES = 4096;    // K (or V) bytes of a tile
+#ifndef DP_HALF
+#define DP_HALF 4096
+#endif
+#ifndef DP_STAGES1
+#define DP_STAGES1 2                   // tiles in each warp's ring, with 8 query rows ..
+#endif
+#ifndef DP_STAGES2
+#define DP_STAGES2 3                   // .. and with 16
+#endif
 constexpr float DP_RESCALE_LOG2 = 8.f; // the base moves when a score passes it by more than this
 
 template <int D, bool F8, int NR>
@@ -51,7 +67,8 @@ struct DpCfg {
   static constexpr int ESZ = F8 ? 1 : 2;
   static constexpr int RB = D * ESZ;             // bytes of a key's row: 64, 128 or 256
   static constexpr int CR = RB / 16;             // 16-byte pieces of a row
-  static constexpr int KS = DP_HALF_BYTES / RB;  // keys of a tile: 64, 32 or 16
+  static constexpr int HALF = RB == 256 ? 4096 : DP_HALF;  // K (or V) bytes of a tile
+  static constexpr int KS = HALF / RB;           // its keys
   static constexpr int KG = KS / 16;             // its 16-key groups
   static constexpr int EPC = 16 / ESZ;           // elements of a piece
   static constexpr int DL = D / 4;               // elements of a K row that one lane holds
@@ -59,14 +76,11 @@ struct DpCfg {
   static constexpr int KST = D / 16;             // k-steps of S^T, and M tiles of O^T
   static constexpr int ROWS = 8 * NR;
   static constexpr int META = KG * 2 * 4;        // e4m3 scales of a tile
-  static constexpr int STAGE = 2 * DP_HALF_BYTES;
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int DP_STAGES = NR == 1 ? DP_STAGES1 : DP_STAGES2;
   static constexpr int RING = DP_WARPS * DP_STAGES * STAGE;
   static constexpr int META_OFF = RING;
   static constexpr int SMEM = RING + DP_WARPS * DP_STAGES * META;
-  // after the loop the ring holds the warps' outputs and their (base, sum)
-  static constexpr int OROW = D + 4;             // floats of a row: 8-byte stores of a half-warp hit every bank once
-  static constexpr int ML_OFF = DP_WARPS * ROWS * OROW * 4;
-  static_assert(ML_OFF + DP_WARPS * ROWS * 8 <= RING, "the merge area fits the ring");
 };
 
 // Byte offset of 16-byte piece c of row r in a tile of RB-byte rows.
@@ -84,135 +98,134 @@ __device__ __forceinline__ int dp_k_piece(int tig, int i) {
   if constexpr (F8 && D == 64) return tig;
   else return 2 * tig + (i & 1) + 8 * (i >> 1);
 }
-// Position (j * 8 + gid) * 2 + e of element d of an output row: lane group gid
-// holds it in M tile j, fragment row gid + 8 e.
+// First of the four output elements 4 jj .. 4 jj + 3 (of its D / 8) that lane group gid holds: M tile j has 2j, 2j + 1.
 template <int D, bool F8>
-__device__ __forceinline__ int dp_o_pos(int d) {
-  int gid, j2;
-  if constexpr (!F8 && D == 128) {
-    gid = (d >> 3) & 7;
-    j2 = (d & 7) + ((d >> 6) << 3);
-  } else {
-    gid = d / (D / 8);
-    j2 = d % (D / 8);
-  }
-  return ((j2 >> 1) * 8 + gid) * 2 + (j2 & 1);
+__device__ __forceinline__ int dp_o_elem(int gid, int jj) {
+  if constexpr (!F8 && D == 128) return (gid + 8 * (jj >> 1)) * 8 + (jj & 1) * 4;
+  else return gid * (D / 8) + 4 * jj;
+}
+
+// How the batch's tiles are shared out: tile t of the whole (sequence by
+// sequence, K/V head by K/V head) belongs to range t's; range r has tiles
+// begin(r) .. begin(r + 1) - 1, none of them empty.
+struct DpRanges {
+  long long tiles, n;  // all tiles; ranges
+  __device__ __forceinline__ DpRanges(long long tiles_, int most) : tiles(tiles_), n(most < tiles_ ? most : tiles_) {}
+  __device__ __forceinline__ long long begin(long long r) const { return r * tiles / n; }
+};
+
+__device__ __forceinline__ int dp_len(const DecodePagedParams& p, int b) {
+  return paged_clip_len(__ldg(p.seqlens + b), p.max_len);
 }
 
 }  // namespace
 
 template <int D, bool F8, int NR>
-__global__ void __launch_bounds__(DP_THREADS, 2) fa_decode_paged_kernel(const DecodePagedParams p) {
+__global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(NR)) fa_decode_paged_kernel(const DecodePagedParams p) {
   using C = DpCfg<D, F8, NR>;
   extern __shared__ __align__(128) uint8_t dp_smem[];
   const uint32_t sbase = smem_u32(dp_smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
-
-  // block -> (row tile, K/V head, split, sequence); row tiles of the same keys are neighbours
-  int x = static_cast<int>(blockIdx.x);
-  const int rt = x % p.row_tiles;
-  x /= p.row_tiles;
-  const int hk = x % p.Hkv;
-  x /= p.Hkv;
-  const int s = x % p.S;
-  const int b = x / p.S;
+  constexpr unsigned ALL = 0xffffffffu;
 
   pdl_launch_dependents();
-  const int raw_len = __ldg(p.seqlens + b);
-  const int L = paged_clip_len(raw_len, p.max_len);
-  if (L != raw_len && s == 0 && rt == 0 && hk == 0 && threadIdx.x == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
-  const int k0 = s * p.chunk;
-  if (k0 >= L && s > 0) return;  // this split has no key: the merge does not read it
-  const int kend = min(L, k0 + p.chunk);
-
-  // ---- Q: lane (gid, tig) holds its elements of query row gid of every 8-row tile
-  uint32_t qf[NR][C::KST][2];
-  float c1[NR][2];   // factor of the scores of rows 2tig and 2tig + 1 (log2 units)
-  int lim[NR][2];    // last key those rows see
-  const uint16_t* qp = static_cast<const uint16_t*>(p.q) + b * p.qsb;
+  // ---- this warp's range of tiles, and where it starts. The row tiles of the same keys are neighbouring warps.
+  const int worker = static_cast<int>(blockIdx.x) * DP_WARPS + warp;
+  const int rt = worker % p.row_tiles;
+  const int range = worker / p.row_tiles;
+  long long sum = 0;
+  bool clipped = false;
+  for (int b = lane; b < p.B; b += 32) {
+    const int L = dp_len(p, b);
+    clipped = clipped || L != __ldg(p.seqlens + b);
+    sum += (L + C::KS - 1) / C::KS;
+  }
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const int r = rt * C::ROWS + n * 8 + gid;
-    const bool in = r < p.R;
-    const uint16_t* qr = qp + (hk * p.G + (in ? r / p.Nq : 0)) * p.qsh + (in ? r % p.Nq : 0) * p.qst;
-    uint2 raw[C::KST];
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(ALL, sum, o);
+  if (worker == 0 && __any_sync(ALL, clipped) && lane == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
+  const DpRanges ranges(sum * p.Hkv, p.n_ranges);
+  if (range >= ranges.n) return;
+  const long long t0 = ranges.begin(range);
+  int todo = static_cast<int>(ranges.begin(range + 1) - t0);  // tiles to compute (the host keeps a range below 2^31)
+  int b = 0, hk = 0, i = 0, L = 0, nt = 0;        // position: sequence, K/V head, tile; its length and tiles
+  {
+    long long base = 0;  // tiles of one K/V head of the sequences before
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int mine = b0 + lane < p.B ? dp_len(p, b0 + lane) : 0;
+      const int n = (mine + C::KS - 1) / C::KS;
+      int inc = n;
 #pragma unroll
-    for (int j = 0; j < C::KST; ++j) {  // elements 4j .. 4j + 3 of the lane's
-      const int d0 = dp_k_piece<D, F8>(tig, 4 * j / C::EPC) * C::EPC + (4 * j) % C::EPC;
-      raw[j] = in ? __ldg(reinterpret_cast<const uint2*>(qr + d0)) : make_uint2(0u, 0u);
-    }
-    float row_factor = 1.f;
-    if constexpr (F8) {
-      // The products with the codes run in f16 (every e4m3 code is an f16
-      // value). The row's power of two 2^x brings its largest element to [1, 2):
-      // elements down to 2^-14 of it keep all their 8 bits, smaller ones are
-      // off by at most 2^-25 of the largest, below fp32 accumulation's own error.
-      float amax = 0.f;
-#pragma unroll
-      for (int j = 0; j < C::KST; ++j) {
-        const uint32_t w[2] = {raw[j].x, raw[j].y};
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(ALL, inc, o);
+        if (lane >= o) inc += y;
       }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -120), 120);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-      row_factor = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-#pragma unroll
-      for (int j = 0; j < C::KST; ++j) {
-        qf[n][j][0] = pack_f16x2(__uint_as_float(raw[j].x << 16) * down, __uint_as_float(raw[j].x & 0xffff0000u) * down);
-        qf[n][j][1] = pack_f16x2(__uint_as_float(raw[j].y << 16) * down, __uint_as_float(raw[j].y & 0xffff0000u) * down);
+      const unsigned past = __ballot_sync(ALL, (base + inc) * p.Hkv > t0);
+      if (past != 0u) {
+        const int at = __ffs(past) - 1;
+        b = b0 + at;
+        L = __shfl_sync(ALL, mine, at);
+        nt = __shfl_sync(ALL, n, at);
+        const long long rest = t0 - (base + __shfl_sync(ALL, inc, at) - nt) * p.Hkv;
+        hk = static_cast<int>(rest / nt);
+        i = static_cast<int>(rest % nt);
+        break;
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < C::KST; ++j) {
-        qf[n][j][0] = raw[j].x;
-        qf[n][j][1] = raw[j].y;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      c1[n][e] = p.scale_log2 * (F8 ? __shfl_sync(0xffffffffu, row_factor, (2 * tig + e) * 4) : 1.f);
-      const int r2 = rt * C::ROWS + n * 8 + 2 * tig + e;
-      lim[n][e] = min(kend - 1, r2 < p.R ? L - p.Nq + r2 % p.Nq : kend - 1);
+      base += __shfl_sync(ALL, inc, 31);
     }
   }
-
-  // ---- the warp's tiles: base key k0 + (warp + 4 i) KS
-  const int ntiles_cta = (kend - k0 + C::KS - 1) / C::KS;  // (negative spans give no tile)
-  const int ntiles = ntiles_cta > warp ? (ntiles_cta - warp + DP_WARPS - 1) / DP_WARPS : 0;
-  const uint32_t ring = sbase + warp * (DP_STAGES * C::STAGE);
-  const uint32_t meta = sbase + C::META_OFF + warp * (DP_STAGES * C::META);
-  const int* trow = p.table + b * p.table_stride;
-  const int full_lim = min(kend - 1, L - p.Nq);  // every row sees the keys up to here
-  uint32_t hidden = 0u;                          // 4 bits for each of 8 tiles: groups whose page is not in the pool
-
-  auto tile_key = [&](int i) { return k0 + (warp + DP_WARPS * i) * C::KS; };
-  // page of 16-key group `lane` of tile i; -1 past the keys or for other lanes
-  auto page_of = [&](int i) -> int {
-    const int key = tile_key(i) + 16 * lane;
-    return (lane < C::KG && i < ntiles && key < kend) ? __ldg(trow + (key >> p.page_shift)) : -1;
+  // the next tile after (b, hk, i)
+  auto advance = [&](int& b_, int& hk_, int& i_, int& L_, int& nt_) {
+    if (++i_ < nt_) return;
+    i_ = 0;
+    if (++hk_ < p.Hkv) return;
+    hk_ = 0;
+    do {
+      if (++b_ >= p.B) return;  // past the last tile
+      L_ = dp_len(p, b_);
+      nt_ = (L_ + C::KS - 1) / C::KS;
+    } while (nt_ == 0);
   };
-  auto issue = [&](int i, int id) {
-    if (i < ntiles) {
-      const int key0 = tile_key(i);
+
+  // ---- the copies, which run ahead of the computation: position of the next tile to copy, and its pages
+  const uint32_t ring = sbase + warp * (C::DP_STAGES * C::STAGE);
+  const uint32_t meta = sbase + C::META_OFF + warp * (C::DP_STAGES * C::META);
+  const uint8_t* my_ring = dp_smem + warp * (C::DP_STAGES * C::STAGE);
+  const uint8_t* my_meta = dp_smem + C::META_OFF + warp * (C::DP_STAGES * C::META);
+  int cb = b, chk = hk, ci = i, cL = L, cnt = nt;
+  int to_copy = todo;
+  uint32_t copied = 0u;          // tiles copied so far
+  uint32_t hidden = 0u;          // 4 bits for each of 8 tiles: groups whose page is not in the pool
+  // page of 16-key group `lane` of the next tile; -1 past the keys or for other lanes
+  auto page_of = [&]() -> int {
+    const int key = ci * C::KS + 16 * lane;
+    return (lane < C::KG && to_copy > 0 && key < cL) ? __ldg(p.table + cb * p.table_stride + (key >> p.page_shift)) : -1;
+  };
+  int id = page_of();
+  constexpr int RPI = 32 / C::CR;                                        // rows of one copy instruction of the warp
+  constexpr int PERIOD = C::RB == 64 ? 1 : (8 / RPI > 1 ? 8 / RPI : 1);  // after which the swizzle repeats
+  const int piece = lane % C::CR, rin = lane / C::CR;
+  uint32_t dst[PERIOD];
+#pragma unroll
+  for (int u = 0; u < PERIOD; ++u) dst[u] = dp_swz<C::RB>(u * RPI + rin, piece) - u * RPI * C::RB;
+  const uint32_t src_lane = rin * C::RB + piece * 16;
+  auto issue = [&]() {
+    if (to_copy > 0) {
+      const int key0 = ci * C::KS;
       const int gkey = key0 + 16 * lane;
-      const bool want = lane < C::KG && gkey < kend;
-      long long off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, gkey & (p.page - 1), D) : -1;
-      const unsigned bad = __ballot_sync(0xffffffffu, want && off < 0);
+      const bool want = lane < C::KG && gkey < cL;
+      const long long off = want ? paged_row_offset(id, p.num_pages, p.Hkv, chk, p.page, gkey & (p.page - 1), D) : -1;
+      const unsigned bad = __ballot_sync(ALL, want && off < 0);
       if (bad != 0u && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
-      const uint32_t sh = 4u * (static_cast<uint32_t>(i) & 7u);
+      const uint32_t sh = 4u * (copied & 7u);
       hidden = (hidden & ~(0xfu << sh)) | ((bad & 0xfu) << sh);
-      const uint32_t slot = static_cast<uint32_t>(i % DP_STAGES);
-      const uint32_t kdst = ring + slot * C::STAGE, vdst = kdst + DP_HALF_BYTES;
+      const uint32_t slot = copied % C::DP_STAGES;
+      const uint32_t kdst = ring + slot * C::STAGE;
       if constexpr (F8) {
         if (lane < C::KG) {
           const uint32_t m = meta + slot * C::META + lane * 8u;
           if (off >= 0) {
-            const long long sc = static_cast<long long>(id) * p.Hkv + hk;
+            const long long sc = static_cast<long long>(id) * p.Hkv + chk;
             cp_async4(m, p.k_scale + sc);
             cp_async4(m + 4u, p.v_scale + sc);
           } else {
@@ -221,347 +234,439 @@ __global__ void __launch_bounds__(DP_THREADS, 2) fa_decode_paged_kernel(const De
           }
         }
       }
-      constexpr int RPI = 32 / C::CR;        // rows of one copy instruction of the warp
-      const int piece = lane % C::CR, rin = lane / C::CR;
 #pragma unroll
       for (int g = 0; g < C::KG; ++g) {
-        const long long goff = __shfl_sync(0xffffffffu, off, g);
-        const int left = goff < 0 ? 0 : kend - (key0 + 16 * g);  // rows of the group to read
+        const long long goff = __shfl_sync(ALL, off, g);
+        const int left = goff < 0 ? 0 : cL - (key0 + 16 * g);  // rows of the group to read
         const uint8_t* kg = static_cast<const uint8_t*>(p.k) + (goff < 0 ? 0 : goff) * C::ESZ;
         const uint8_t* vg = static_cast<const uint8_t*>(p.v) + (goff < 0 ? 0 : goff) * C::ESZ;
+        if (left >= 16) {
+          kg += src_lane;
+          vg += src_lane;
 #pragma unroll
-        for (int u = 0; u < 16 / RPI; ++u) {
-          const int row = u * RPI + rin;
-          const uint32_t dst = dp_swz<C::RB>(16 * g + row, piece);
-          const uint32_t n = row < left ? 16u : 0u;
-          const size_t so = n ? static_cast<size_t>(row) * C::RB + piece * 16 : 0;
-          cp_async16(kdst + dst, kg + so, n);
-          cp_async16(vdst + dst, vg + so, n);
+          for (int u = 0; u < 16 / RPI; ++u) {
+            const uint32_t to = kdst + dst[u % PERIOD] + (16 * g + u * RPI) * C::RB;
+            cp_async16(to, kg + u * RPI * C::RB, 16u);
+            cp_async16(to + C::HALF, vg + u * RPI * C::RB, 16u);
+          }
+        } else {  // the rows past the sequence's end become zeros
+#pragma unroll
+          for (int u = 0; u < 16 / RPI; ++u) {
+            const int row = u * RPI + rin;
+            const uint32_t to = kdst + dst[u % PERIOD] + (16 * g + u * RPI) * C::RB;
+            const uint32_t n = row < left ? 16u : 0u, so = n ? row * C::RB + piece * 16 : 0;
+            cp_async16(to, kg + so, n);
+            cp_async16(to + C::HALF, vg + so, n);
+          }
         }
       }
+      ++copied;
+      --to_copy;
+      advance(cb, chk, ci, cL, cnt);
+      id = page_of();
     }
     cp_async_commit();
   };
+#pragma unroll
+  for (int k = 0; k < C::DP_STAGES - 1; ++k) issue();
 
-  float M[NR][2], l[NR][2];
-  float oacc[NR][C::KST][4];
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    M[n][0] = M[n][1] = -INFINITY;
-    l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-    for (int j = 0; j < C::KST; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) oacc[n][j][e] = 0.f;
-  }
-
-  int id_next = page_of(0);
-#pragma unroll
-  for (int i = 0; i < DP_STAGES - 1; ++i) {
-    const int id = id_next;
-    id_next = page_of(i + 1);
-    issue(i, id);
-  }
-  for (int i = 0; i < ntiles; ++i) {
-    cp_async_wait<DP_STAGES - 2>();
-    __syncwarp();  // tile i landed for every lane, and every lane is done with tile i - 1's slot
-    {
-      const int id = id_next;
-      id_next = page_of(i + DP_STAGES);
-      issue(i + DP_STAGES - 1, id);
-    }
-    const uint32_t slot = static_cast<uint32_t>(i % DP_STAGES);
-    const uint32_t kt = ring + slot * C::STAGE, vt = kt + DP_HALF_BYTES;
-    const int key0 = tile_key(i);
-
-    // ---- S^T: 16 keys x 8 rows for each group and row tile
-    float sc[C::KG][NR][4];
-#pragma unroll
-    for (int g = 0; g < C::KG; ++g) {
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[g][n][e] = 0.f;
-#pragma unroll
-      for (int i2 = 0; i2 < C::NPK; ++i2) {
-        const int piece = dp_k_piece<D, F8>(tig, i2);
-        const uint4 ra = ld_shared_v4(kt + dp_swz<C::RB>(16 * g + gid, piece));
-        const uint4 rb = ld_shared_v4(kt + dp_swz<C::RB>(16 * g + gid + 8, piece));
-        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-        if constexpr (F8) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t a0 = e4m3x2_to_f16x2(wa[w]), a2 = e4m3x2_to_f16x2(wa[w] >> 16);
-            const uint32_t a1 = e4m3x2_to_f16x2(wb[w]), a3 = e4m3x2_to_f16x2(wb[w] >> 16);
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-              mma_16816<true>(sc[g][n], a0, a1, a2, a3, qf[n][i2 * 4 + w][0], qf[n][i2 * 4 + w][1]);
-          }
-        } else {
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-              mma_16816<false>(sc[g][n], wa[2 * w], wb[2 * w], wa[2 * w + 1], wb[2 * w + 1], qf[n][i2 * 2 + w][0],
-                               qf[n][i2 * 2 + w][1]);
-        }
-      }
-    }
-
-    // ---- z = y + log2 c, masked; the base moves only when a row passes it by 2^8
-    float rv[C::KG];
-    float mx[NR][2];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-    const uint32_t hid = (hidden >> (4u * (static_cast<uint32_t>(i) & 7u))) & 0xfu;
-    const bool need_mask = key0 + C::KS - 1 > full_lim || hid != 0u;
-#pragma unroll
-    for (int g = 0; g < C::KG; ++g) {
-      float ka = 1.f, ev = 0.f;
-      rv[g] = 1.f;
-      if constexpr (F8) {
-        const float c = ld_shared_f32(meta + slot * C::META + g * 8u + 4u);
-        ka = ld_shared_f32(meta + slot * C::META + g * 8u);
-        ev = lg2_approx(c);
-        rv[g] = __fdividef(1.f, c);
-      }
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float z = F8 ? fmaf(sc[g][n][e], c1[n][e & 1] * ka, ev) : sc[g][n][e] * c1[n][e & 1];
-          if (need_mask) {
-            const int key = key0 + 16 * g + gid + (e >> 1) * 8;
-            if (key > lim[n][e & 1] || ((hid >> g) & 1u)) z = -INFINITY;
-          }
-          sc[g][n][e] = z;
-          mx[n][e & 1] = fmaxf(mx[n][e & 1], z);
-        }
-    }
-    bool over = false;
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
-      over = over || mx[n][0] > M[n][0] + DP_RESCALE_LOG2 || mx[n][1] > M[n][1] + DP_RESCALE_LOG2;
-    if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float m = fmaxf(mx[n][e], M[n][e]);
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          const float alpha = m == -INFINITY ? 1.f : ex2_approx(M[n][e] - m);
-          M[n][e] = m;
-          l[n][e] *= alpha;
-#pragma unroll
-          for (int j = 0; j < C::KST; ++j) {
-            oacc[n][j][e] *= alpha;
-            oacc[n][j][e + 2] *= alpha;
-          }
-        }
-    }
-    // ---- W = 2^(z - M), its sums, and W as the B operand (rows on the columns): 8x8 transposes
-    uint32_t pf[C::KG][NR][2];
+  uint32_t done = 0u;  // tiles computed
+  while (todo > 0) {
+    // ================================================================ one segment: keys of (b, hk) from tile i on
+    const int i0 = i;
+    const int i1 = todo < nt - i ? i + todo : nt;
+    // ---- Q: lane (gid, tig) holds its elements of query row gid of every 8-row tile
+    uint32_t qf[NR][C::KST][2];
+    float c1[NR][2];   // factor of the scores of rows 2tig and 2tig + 1 (log2 units)
+    int lim[NR][2];    // last key those rows see
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      const float m0 = M[n][0] == -INFINITY ? 0.f : M[n][0], m1 = M[n][1] == -INFINITY ? 0.f : M[n][1];
+      const int r = rt * C::ROWS + n * 8 + gid;
+      const bool in = r < p.R;
+      const uint16_t* qr = static_cast<const uint16_t*>(p.q) + b * p.qsb + (hk * p.G + (in ? r / p.Nq : 0)) * p.qsh +
+                           (in ? r % p.Nq : 0) * p.qst;
+      uint2 raw[C::KST];
 #pragma unroll
-      for (int g = 0; g < C::KG; ++g) {
-        const float w0 = ex2_approx(sc[g][n][0] - m0), w1 = ex2_approx(sc[g][n][1] - m1);
-        const float w2 = ex2_approx(sc[g][n][2] - m0), w3 = ex2_approx(sc[g][n][3] - m1);
-        l[n][0] = F8 ? fmaf(w0 + w2, rv[g], l[n][0]) : l[n][0] + (w0 + w2);
-        l[n][1] = F8 ? fmaf(w1 + w3, rv[g], l[n][1]) : l[n][1] + (w1 + w3);
-        pf[g][n][0] = movmatrix_trans(F8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1));
-        pf[g][n][1] = movmatrix_trans(F8 ? pack_f16x2(w2, w3) : pack_bf16x2(w2, w3));
+      for (int j = 0; j < C::KST; ++j) {  // elements 4j .. 4j + 3 of the lane's
+        const int d0 = dp_k_piece<D, F8>(tig, 4 * j / C::EPC) * C::EPC + (4 * j) % C::EPC;
+        raw[j] = in ? __ldg(reinterpret_cast<const uint2*>(qr + d0)) : make_uint2(0u, 0u);
       }
-    }
-    // ---- O^T += V^T W^T
-#pragma unroll
-    for (int g = 0; g < C::KG; ++g) {
-      const uint32_t r0 = 16 * g + 2 * tig;
+      float row_factor = 1.f;
       if constexpr (F8) {
-        constexpr int NW32 = D / 32;  // 32-bit words of the lane's codes: 4 or 2
-        uint32_t v[4][NW32];
+        // The products with the codes run in f16 (every e4m3 code is an f16
+        // value). The row's power of two 2^x brings its largest element to [1, 2):
+        // elements down to 2^-14 of it keep all their 8 bits, smaller ones are
+        // off by at most 2^-25 of the largest, below fp32 accumulation's own error.
+        float amax = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t row = r0 + (q & 1) + 8 * (q >> 1);
-          if constexpr (D == 128) {
-            const uint4 y = ld_shared_v4(vt + dp_swz<C::RB>(row, gid));
-            v[q][0] = y.x;
-            v[q][1] = y.y;
-            v[q][2] = y.z;
-            v[q][3] = y.w;
-          } else {
-            const uint2 y = ld_shared_v2(vt + dp_swz<C::RB>(row, gid >> 1) + (gid & 1) * 8u);
-            v[q][0] = y.x;
-            v[q][1] = y.y;
-          }
+        for (int j = 0; j < C::KST; ++j) {
+          const uint32_t w[2] = {raw[j].x, raw[j].y};
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
         }
+        amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, 2));
+        const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -120), 120);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        row_factor = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
-        for (int w = 0; w < NW32; ++w) {
-          const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-          const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t xa = h ? x1 : x0, ya = h ? y1 : y0;
-            const uint32_t a0 = e4m3x2_to_f16x2(xa), a1 = e4m3x2_to_f16x2(xa >> 16);
-            const uint32_t a2 = e4m3x2_to_f16x2(ya), a3 = e4m3x2_to_f16x2(ya >> 16);
-#pragma unroll
-            for (int n = 0; n < NR; ++n) mma_16816<true>(oacc[n][2 * w + h], a0, a1, a2, a3, pf[g][n][0], pf[g][n][1]);
-          }
+        for (int j = 0; j < C::KST; ++j) {
+          qf[n][j][0] = pack_f16x2(__uint_as_float(raw[j].x << 16) * down, __uint_as_float(raw[j].x & 0xffff0000u) * down);
+          qf[n][j][1] = pack_f16x2(__uint_as_float(raw[j].y << 16) * down, __uint_as_float(raw[j].y & 0xffff0000u) * down);
         }
       } else {
 #pragma unroll
-        for (int hp = 0; hp < D / 64; ++hp) {  // pieces gid and (d = 128) gid + 8
-          uint32_t v[4][4];
+        for (int j = 0; j < C::KST; ++j) {
+          qf[n][j][0] = raw[j].x;
+          qf[n][j][1] = raw[j].y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        c1[n][e] = p.scale_log2 * (F8 ? __shfl_sync(ALL, row_factor, (2 * tig + e) * 4) : 1.f);
+        const int r2 = rt * C::ROWS + n * 8 + 2 * tig + e;
+        lim[n][e] = min(L - 1, r2 < p.R ? L - p.Nq + r2 % p.Nq : L - 1);
+      }
+    }
+    const int full_lim = min(L - 1, L - p.Nq);  // every row sees the keys up to here
+
+    float M[NR][2], l[NR][2];
+    float oacc[NR][C::KST][4];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      M[n][0] = M[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < C::KST; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) oacc[n][j][e] = 0.f;
+    }
+
+    for (; i < i1; ++i, ++done) {
+      cp_async_wait<C::DP_STAGES - 2>();
+      __syncwarp();  // the tile landed for every lane, and every lane is done with the one before's slot
+      issue();
+      const uint32_t slot = done % C::DP_STAGES;
+      const uint8_t* kt = my_ring + slot * C::STAGE;
+      const uint8_t* vt = kt + C::HALF;
+      const int key0 = i * C::KS;
+      // ---- S^T: 16 keys x 8 rows for each group and row tile
+      float sc[C::KG][NR][4];
+#pragma unroll
+      for (int g = 0; g < C::KG; ++g) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[g][n][e] = 0.f;
+#pragma unroll
+        for (int i2 = 0; i2 < C::NPK; ++i2) {
+          const int piece = dp_k_piece<D, F8>(tig, i2);
+          const uint4 ra = *reinterpret_cast<const uint4*>(kt + dp_swz<C::RB>(16 * g + gid, piece));
+          const uint4 rb = *reinterpret_cast<const uint4*>(kt + dp_swz<C::RB>(16 * g + gid + 8, piece));
+          const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+          if constexpr (F8) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16x2x2(wa[w], a0, a2);
+              e4m3x4_to_f16x2x2(wb[w], a1, a3);
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                mma_16816<true>(sc[g][n], a0, a1, a2, a3, qf[n][i2 * 4 + w][0], qf[n][i2 * 4 + w][1]);
+            }
+          } else {
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                mma_16816<false>(sc[g][n], wa[2 * w], wb[2 * w], wa[2 * w + 1], wb[2 * w + 1], qf[n][i2 * 2 + w][0],
+                                 qf[n][i2 * 2 + w][1]);
+          }
+        }
+      }
+
+      // ---- z = y + log2 c, masked; the base moves only when a row passes it by 2^8
+      float rv[C::KG];
+      float mx[NR][2];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) mx[n][0] = mx[n][1] = -INFINITY;
+      const uint32_t hid = (hidden >> (4u * (done & 7u))) & 0xfu;
+      const bool need_mask = key0 + C::KS - 1 > full_lim || hid != 0u;
+#pragma unroll
+      for (int g = 0; g < C::KG; ++g) {
+        float ka = 1.f, ev = 0.f;
+        rv[g] = 1.f;
+        if constexpr (F8) {
+          const float2 ac = *reinterpret_cast<const float2*>(my_meta + slot * C::META + g * 8);
+          const float c = ac.y;
+          ka = ac.x;
+          ev = lg2_approx(c);
+          rv[g] = __fdividef(1.f, c);
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float z = F8 ? fmaf(sc[g][n][e], c1[n][e & 1] * ka, ev) : sc[g][n][e] * c1[n][e & 1];
+            if (need_mask) {
+              const int key = key0 + 16 * g + gid + (e >> 1) * 8;
+              if (key > lim[n][e & 1] || ((hid >> g) & 1u)) z = -INFINITY;
+            }
+            sc[g][n][e] = z;
+            mx[n][e & 1] = fmaxf(mx[n][e & 1], z);
+          }
+      }
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+        over = over || mx[n][0] > M[n][0] + DP_RESCALE_LOG2 || mx[n][1] > M[n][1] + DP_RESCALE_LOG2;
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float m = fmaxf(mx[n][e], M[n][e]);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            const float alpha = m == -INFINITY ? 1.f : ex2_approx(M[n][e] - m);
+            M[n][e] = m;
+            l[n][e] *= alpha;
+#pragma unroll
+            for (int j = 0; j < C::KST; ++j) {
+              oacc[n][j][e] *= alpha;
+              oacc[n][j][e + 2] *= alpha;
+            }
+          }
+      }
+      // ---- W = 2^(z - M), its sums, and W as the B operand (rows on the columns): 8x8 transposes
+      uint32_t pf[C::KG][NR][2];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float m0 = M[n][0] == -INFINITY ? 0.f : M[n][0], m1 = M[n][1] == -INFINITY ? 0.f : M[n][1];
+#pragma unroll
+        for (int g = 0; g < C::KG; ++g) {
+          const float w0 = ex2_approx(sc[g][n][0] - m0), w1 = ex2_approx(sc[g][n][1] - m1);
+          const float w2 = ex2_approx(sc[g][n][2] - m0), w3 = ex2_approx(sc[g][n][3] - m1);
+          l[n][0] = F8 ? fmaf(w0 + w2, rv[g], l[n][0]) : l[n][0] + (w0 + w2);
+          l[n][1] = F8 ? fmaf(w1 + w3, rv[g], l[n][1]) : l[n][1] + (w1 + w3);
+          pf[g][n][0] = movmatrix_trans(F8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1));
+          pf[g][n][1] = movmatrix_trans(F8 ? pack_f16x2(w2, w3) : pack_bf16x2(w2, w3));
+        }
+      }
+      // ---- O^T += V^T W^T
+#pragma unroll
+      for (int g = 0; g < C::KG; ++g) {
+        const uint32_t r0 = 16 * g + 2 * tig;
+        if constexpr (F8) {
+          constexpr int NW32 = D / 32;  // 32-bit words of the lane's codes: 4 or 2
+          uint32_t v[4][NW32];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint4 y = ld_shared_v4(vt + dp_swz<C::RB>(r0 + (q & 1) + 8 * (q >> 1), gid + 8 * hp));
-            v[q][0] = y.x;
-            v[q][1] = y.y;
-            v[q][2] = y.z;
-            v[q][3] = y.w;
+            const uint32_t row = r0 + (q & 1) + 8 * (q >> 1);
+            if constexpr (D == 128) {
+              const uint4 y = *reinterpret_cast<const uint4*>(vt + dp_swz<C::RB>(row, gid));
+              v[q][0] = y.x;
+              v[q][1] = y.y;
+              v[q][2] = y.z;
+              v[q][3] = y.w;
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(vt + dp_swz<C::RB>(row, gid >> 1) + (gid & 1) * 8u);
+              v[q][0] = y.x;
+              v[q][1] = y.y;
+            }
           }
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
-            const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+          for (int w = 0; w < NW32; ++w) {
+            const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+            const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
-              mma_16816<false>(oacc[n][4 * hp + w], a0, a1, a2, a3, pf[g][n][0], pf[g][n][1]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t xa = h ? x1 : x0, ya = h ? y1 : y0;
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16x2x2(xa, a0, a1);
+              e4m3x4_to_f16x2x2(ya, a2, a3);
+#pragma unroll
+              for (int n = 0; n < NR; ++n) mma_16816<true>(oacc[n][2 * w + h], a0, a1, a2, a3, pf[g][n][0], pf[g][n][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int hp = 0; hp < D / 64; ++hp) {  // pieces gid and (d = 128) gid + 8
+            uint32_t v[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint4 y = *reinterpret_cast<const uint4*>(vt + dp_swz<C::RB>(r0 + (q & 1) + 8 * (q >> 1), gid + 8 * hp));
+              v[q][0] = y.x;
+              v[q][1] = y.y;
+              v[q][2] = y.z;
+              v[q][3] = y.w;
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+              const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                mma_16816<false>(oacc[n][4 * hp + w], a0, a1, a2, a3, pf[g][n][0], pf[g][n][1]);
+            }
           }
         }
       }
     }
-  }
 
-  // ---- join the warps: bases and sums, then the rescaled outputs, in shared memory
+    // ---- the segment's end: sums over the lanes, then the result, or this range's part of it
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = l[n][e];
+        t += __shfl_xor_sync(ALL, t, 4);
+        t += __shfl_xor_sync(ALL, t, 8);
+        t += __shfl_xor_sync(ALL, t, 16);
+        const int rl = n * 8 + 2 * tig + e, rr = rt * C::ROWS + rl;
+        if (rr >= p.R) continue;
+        // (scores that were all NaN leave the base where it was: their sum is NaN, and so is the row)
+        const float m = M[n][e] == -INFINITY && t != 0.f ? 0.f : M[n][e];
+        if (i0 == 0 && i1 == nt) {
+          // the whole sequence; a row that sees no key has m = -inf, t = 0
+          const float inv = m == -INFINITY ? 0.f : 1.f / t;
+          const int h = hk * p.G + rr / p.Nq, tok = rr % p.Nq;
+          uint16_t* op = static_cast<uint16_t*>(p.o) + b * p.osb + h * p.osh + tok * p.ost;
+#pragma unroll
+          for (int jj = 0; jj < C::KST / 2; ++jj)
+            *reinterpret_cast<uint2*>(op + dp_o_elem<D, F8>(gid, jj)) =
+                make_uint2(pack_bf16x2(oacc[n][2 * jj][e] * inv, oacc[n][2 * jj][e + 2] * inv),
+                           pack_bf16x2(oacc[n][2 * jj + 1][e] * inv, oacc[n][2 * jj + 1][e + 2] * inv));
+          if (p.lse != nullptr && gid == 0)
+            p.lse[(static_cast<long long>(b) * p.H + h) * p.Nq + tok] =
+                m == -INFINITY ? -INFINITY : (m + lg2_approx(t)) * 0.69314718055994530942f;
+        } else {
+          // ranges and (sequence, head) pairs both only grow along the tiles, so their sum numbers the parts
+          const long long part =
+              ((static_cast<long long>(range) + static_cast<long long>(b) * p.Hkv + hk) * p.row_tiles + rt) * C::ROWS + rl;
+          float* op = p.ws_o + part * D;
+#pragma unroll
+          for (int jj = 0; jj < C::KST / 2; ++jj)
+            *reinterpret_cast<float4*>(op + dp_o_elem<D, F8>(gid, jj)) = make_float4(
+                oacc[n][2 * jj][e], oacc[n][2 * jj][e + 2], oacc[n][2 * jj + 1][e], oacc[n][2 * jj + 1][e + 2]);
+          if (gid == 0) *reinterpret_cast<float2*>(p.ws_ml + part * 2) = make_float2(m, t);
+        }
+      }
+    // where the merge finds the parts of (b, hk)
+    if (lane == 0 && rt == 0) {
+      int* ends = p.ws_ends + 2 * (static_cast<long long>(b) * p.Hkv + hk);
+      if (i0 == 0) ends[0] = range;
+      if (i1 == nt) ends[1] = range;
+    }
+    todo -= i1 - i0;
+    if (todo > 0) {
+      i = nt - 1;  // the last tile of (b, hk) is done
+      advance(b, hk, i, L, nt);
+    }
+  }
   cp_async_wait<0>();
-  __syncthreads();
-  float* so = reinterpret_cast<float*>(dp_smem);
-  float2* sml = reinterpret_cast<float2*>(dp_smem + C::ML_OFF);
-#pragma unroll
-  for (int n = 0; n < NR; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float t = l[n][e];
-      t += __shfl_xor_sync(0xffffffffu, t, 4);
-      t += __shfl_xor_sync(0xffffffffu, t, 8);
-      t += __shfl_xor_sync(0xffffffffu, t, 16);
-      if (gid == 0) sml[warp * C::ROWS + n * 8 + 2 * tig + e] = make_float2(M[n][e], t);
-    }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    float f[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = n * 8 + 2 * tig + e;
-      float m = sml[r].x;
-#pragma unroll
-      for (int w = 1; w < DP_WARPS; ++w) m = fmaxf(m, sml[w * C::ROWS + r].x);
-      f[e] = M[n][e] == -INFINITY ? 0.f : ex2_approx(M[n][e] - m);
-    }
-#pragma unroll
-    for (int j = 0; j < C::KST; ++j) {
-      float* dst = so + (warp * C::ROWS + n * 8 + 2 * tig) * C::OROW + (j * 8 + gid) * 2;
-      *reinterpret_cast<float2*>(dst) = make_float2(oacc[n][j][0] * f[0], oacc[n][j][2] * f[0]);
-      *reinterpret_cast<float2*>(dst + C::OROW) = make_float2(oacc[n][j][1] * f[1], oacc[n][j][3] * f[1]);
-    }
-  }
-  __syncthreads();
-  const bool last = p.S == 1;  // no merge follows
-  for (int i = threadIdx.x; i < C::ROWS * (D / 2); i += DP_THREADS) {
-    const int r = i / (D / 2), d = 2 * (i % (D / 2));
-    const int rr = rt * C::ROWS + r;
-    if (rr >= p.R) break;  // rows are in order
-    float m = sml[r].x;
-#pragma unroll
-    for (int w = 1; w < DP_WARPS; ++w) m = fmaxf(m, sml[w * C::ROWS + r].x);
-    float lt = 0.f, o0 = 0.f, o1 = 0.f;
-    const int pos = dp_o_pos<D, F8>(d);
-#pragma unroll
-    for (int w = 0; w < DP_WARPS; ++w) {
-      const float2 ml = sml[w * C::ROWS + r];
-      lt += ml.x == -INFINITY ? 0.f : ml.y * ex2_approx(ml.x - m);
-      const float2 y = *reinterpret_cast<const float2*>(so + (w * C::ROWS + r) * C::OROW + pos);
-      o0 += y.x;
-      o1 += y.y;
-    }
-    const int h = hk * p.G + rr / p.Nq, t = rr % p.Nq;
-    const long long row = (static_cast<long long>(b) * p.H + h) * p.Nq + t;
-    if (last) {
-      // a row that sees no key: m = -inf, lt = 0
-      const float inv = m == -INFINITY ? 0.f : 1.f / lt;
-      uint16_t* op = static_cast<uint16_t*>(p.o) + b * p.osb + h * p.osh + t * p.ost + d;
-      *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(o0 * inv, o1 * inv);
-      if (p.lse != nullptr && d == 0) p.lse[row] = m == -INFINITY ? -INFINITY : (m + lg2_approx(lt)) * 0.69314718055994530942f;
-    } else {
-      const long long part = row * p.S + s;
-      *reinterpret_cast<float2*>(p.ws_o + part * D + d) = make_float2(o0, o1);
-      if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + part * 2) = make_float2(m, lt);
-    }
-  }
 }
 
-// Joins the splits of one query row: M = max m_s, O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s over
-// the splits that hold keys. One CTA a row; warp w takes splits w, w + 4, ..
-template <int D>
-__global__ void __launch_bounds__(128) fa_decode_paged_merge_kernel(const DecodePagedParams p) {
-  __shared__ float sm[4], sl[4];
-  __shared__ float so[4][D];
-  const int row = static_cast<int>(blockIdx.x);
+// Joins the parts of the query rows whose keys lie in several ranges: M = max m_r,
+// O = sum 2^(m_r - M) o_r / sum 2^(m_r - M) l_r. WPR warps a row (one where a row
+// has a few parts, eight where long sequences have many); a warp has up to eight
+// parts in flight. Rows of one range were written by the decode kernel itself;
+// rows of an empty sequence, which no range holds, are written here.
+constexpr int DP_MERGE_WARPS = 8;
+template <int D, int WPR>
+__global__ void __launch_bounds__(32 * DP_MERGE_WARPS) fa_decode_paged_merge_kernel(const DecodePagedParams p, int rows) {
+  __shared__ float sm[DP_MERGE_WARPS], sl[DP_MERGE_WARPS];
+  __shared__ float so[WPR > 1 ? DP_MERGE_WARPS : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = row % p.Nq, bh = row / p.Nq;
+  const int w = warp % WPR;  // of the row's warps
+  const int row = static_cast<int>(blockIdx.x) * (DP_MERGE_WARPS / WPR) + warp / WPR;
+  const bool in = row < p.B * p.H * p.Nq;
+  const int t = in ? row % p.Nq : 0, bh = in ? row / p.Nq : 0;
   const int h = bh % p.H, b = bh / p.H;
-  const int L = paged_clip_len(__ldg(p.seqlens + b), p.max_len);
-  const int ns = max(1, (L + p.chunk - 1) / p.chunk);
+  const int hk = h / p.G, rr = (h - hk * p.G) * p.Nq + t;
+  const int L = dp_len(p, b);
+  // (every warp waits, also those with nothing to join: what follows this launch may not pass the decode kernel)
   pdl_wait();
-  const float* ml = p.ws_ml + static_cast<long long>(row) * p.S * 2;
-  float m = -INFINITY;
-  for (int s = threadIdx.x; s < ns; s += 128) m = fmaxf(m, __ldcg(ml + 2 * s));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) sm[warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  constexpr int EL = D / 32;
-  float acc[EL], lt = 0.f;
+  const int2 ends = L > 0 ? __ldcg(reinterpret_cast<const int2*>(p.ws_ends) + static_cast<long long>(b) * p.Hkv + hk)
+                          : make_int2(0, -1);
+  if (!in || ends.x == ends.y) return;  // (with WPR > 1 the same for the block: it is one row)
+  const int ns = ends.y - ends.x + 1;
+  const long long step = static_cast<long long>(p.row_tiles) * rows;  // parts from one range to the next
+  const long long part0 = (ends.x + static_cast<long long>(b) * p.Hkv + hk) * step + (rr / rows) * rows + rr % rows;
+  constexpr int EL = D / 32, FLIGHT = 8;
+  float acc[EL], lt = 0.f, m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < EL; ++e) acc[e] = 0.f;
-  const float* po = p.ws_o + static_cast<long long>(row) * p.S * D + lane * EL;
-#pragma unroll 4
-  for (int s = warp; s < ns; s += 4) {
-    const float2 x = __ldcg(reinterpret_cast<const float2*>(ml) + s);
-    const float w = x.x == -INFINITY ? 0.f : ex2_approx(x.x - m);
-    lt = fmaf(w, x.y, lt);
-    float y[EL];
-    if constexpr (EL == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(po + static_cast<long long>(s) * D));
-      y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(po + static_cast<long long>(s) * D));
-      y[0] = v.x, y[1] = v.y;
+  for (int s0 = w; s0 < ns; s0 += FLIGHT * WPR) {
+    float2 ml[FLIGHT];
+    float y[FLIGHT][EL];
+#pragma unroll
+    for (int j = 0; j < FLIGHT; ++j) {
+      const int s = s0 + j * WPR;
+      ml[j] = make_float2(-INFINITY, 0.f);
+      if (s < ns) {
+        const long long part = part0 + s * step;
+        ml[j] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + part);
+        if constexpr (EL == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_o + part * D) + lane);
+          y[j][0] = v.x, y[j][1] = v.y, y[j][2] = v.z, y[j][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ws_o + part * D) + lane);
+          y[j][0] = v.x, y[j][1] = v.y;
+        }
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int j = 0; j < FLIGHT; ++j) mn = fmaxf(mn, ml[j].x);
+    if (mn == -INFINITY) continue;  // nothing seen so far
+    const float a = ex2_approx(m - mn);
+    lt *= a;
+#pragma unroll
+    for (int e = 0; e < EL; ++e) acc[e] *= a;
+#pragma unroll
+    for (int j = 0; j < FLIGHT; ++j) {
+      if (ml[j].x == -INFINITY) continue;  // no part, or one that saw no key
+      const float wgt = ex2_approx(ml[j].x - mn);
+      lt = fmaf(wgt, ml[j].y, lt);
+#pragma unroll
+      for (int e = 0; e < EL; ++e) acc[e] = fmaf(wgt, y[j][e], acc[e]);
+    }
+    m = mn;
+  }
+  if constexpr (WPR > 1) {
+    if (lane == 0) {
+      sm[w] = m;
+      sl[w] = lt;
     }
 #pragma unroll
-    for (int e = 0; e < EL; ++e) acc[e] = fmaf(w, y[e], acc[e]);
-  }
+    for (int e = 0; e < EL; ++e) so[w][lane * EL + e] = acc[e];
+    __syncthreads();
+    if (w > 0) return;
+    m = sm[0];
 #pragma unroll
-  for (int e = 0; e < EL; ++e) so[warp][lane * EL + e] = acc[e];
-  if (lane == 0) sl[warp] = lt;
-  __syncthreads();
-  if (threadIdx.x < D / 2) {
-    const int d = 2 * threadIdx.x;
-    const float tot = (sl[0] + sl[1]) + (sl[2] + sl[3]);
-    const float inv = m == -INFINITY ? 0.f : 1.f / tot;
-    const float o0 = (so[0][d] + so[1][d]) + (so[2][d] + so[3][d]);
-    const float o1 = (so[0][d + 1] + so[1][d + 1]) + (so[2][d + 1] + so[3][d + 1]);
-    uint16_t* op = static_cast<uint16_t*>(p.o) + b * p.osb + h * p.osh + t * p.ost + d;
-    *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(o0 * inv, o1 * inv);
-    if (p.lse != nullptr && d == 0)
-      p.lse[row] = m == -INFINITY ? -INFINITY : (m + lg2_approx(tot)) * 0.69314718055994530942f;
+    for (int x = 1; x < WPR; ++x) m = fmaxf(m, sm[x]);
+    lt = 0.f;
+#pragma unroll
+    for (int e = 0; e < EL; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) {
+      const float f = sm[x] == -INFINITY ? 0.f : ex2_approx(sm[x] - m);
+      lt = fmaf(f, sl[x], lt);
+#pragma unroll
+      for (int e = 0; e < EL; ++e) acc[e] = fmaf(f, so[x][lane * EL + e], acc[e]);
+    }
   }
+  const float inv = m == -INFINITY ? 0.f : 1.f / lt;
+  uint16_t* op = static_cast<uint16_t*>(p.o) + b * p.osb + h * p.osh + t * p.ost + lane * EL;
+  if constexpr (EL == 4)
+    *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (p.lse != nullptr && lane == 0)
+    p.lse[row] = m == -INFINITY ? -INFINITY : (m + lg2_approx(lt)) * 0.69314718055994530942f;
 }
 
 template <int D, bool F8, int NR>
@@ -580,21 +685,25 @@ cudaError_t decode_paged_set_attributes() {
 
 template <int D, bool F8, int NR>
 static cudaError_t dp_launch(const DecodePagedParams& p, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(static_cast<long long>(p.row_tiles) * p.Hkv * p.S * p.B);
-  fa_decode_paged_kernel<D, F8, NR><<<grid, DP_THREADS, DpCfg<D, F8, NR>::SMEM, stream>>>(p);
+  using C = DpCfg<D, F8, NR>;
+  const long long workers = static_cast<long long>(p.n_ranges) * p.row_tiles;
+  fa_decode_paged_kernel<D, F8, NR><<<static_cast<unsigned>((workers + DP_WARPS - 1) / DP_WARPS), DP_THREADS, C::SMEM, stream>>>(p);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.S == 1) return e;
-  // the merge's CTAs may be set up while the last splits run; it waits for them before it reads
+  if (e != cudaSuccess) return e;
+  // the merge's CTAs may be set up while the last ranges run; those that read parts wait for them
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.H * p.Nq));
-  cfg.blockDim = dim3(128);
+  const long long rows = static_cast<long long>(p.B) * p.H * p.Nq;
+  const bool many = p.n_ranges / (static_cast<long long>(p.B) * p.Hkv) > 8;  // parts of a row, on average
+  cfg.gridDim = dim3(static_cast<unsigned>(many ? rows : (rows + DP_MERGE_WARPS - 1) / DP_MERGE_WARPS));
+  cfg.blockDim = dim3(32 * DP_MERGE_WARPS);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_decode_paged_merge_kernel<D>, p);
+  return many ? cudaLaunchKernelEx(&cfg, fa_decode_paged_merge_kernel<D, DP_MERGE_WARPS>, p, C::ROWS)
+              : cudaLaunchKernelEx(&cfg, fa_decode_paged_merge_kernel<D, 1>, p, C::ROWS);
 }
 
 template <int D, bool F8>

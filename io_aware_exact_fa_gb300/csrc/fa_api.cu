@@ -811,26 +811,30 @@ int log2_of(int x) {
   return s;
 }
 
-// The split of a paged decode: `chunk` keys for each of `S` splits.
-struct PagedSplit {
-  int S, chunk;
+// Ranges that a paged decode shares the batch's keys out in: one for each warp
+// that the GPU holds (and row tile), or `num_splits` for each sequence and K/V
+// head on average.
+constexpr int PAGED_SMS = 152;
+int paged_row_tiles(int R) { return (R + fa::decode_paged_rows(R) - 1) / fa::decode_paged_rows(R); }
+int paged_ranges(int B, int Hkv, int R, int num_splits) {
+  if (num_splits > 0) return static_cast<int>(std::min(static_cast<long long>(num_splits) * B * Hkv, 1LL << 20));
+  const int warps = PAGED_SMS * 4 * fa::decode_paged_ctas(fa::decode_paged_rows(R) / 8);
+  return std::max(1, warps / paged_row_tiles(R));
+}
+
+// Layout of the paged decode's workspace: outputs, (base, sum) pairs, range ends.
+struct PagedWorkspace {
+  size_t ml, ends, bytes;
 };
-// Without a request, splits are made until about PAGED_CTAS blocks run (several
-// rounds of two a SM, so that ragged lengths even out), none shorter than 128
-// keys (one tile for each warp of e4m3 pages at d = 128).
-constexpr int PAGED_CTAS = 2432;
-PagedSplit paged_split(int B, int Hkv, int R, int max_len, int num_splits) {
-  long long S = num_splits;
-  const long long len = std::max(1, max_len);
-  if (S <= 0) {
-    const long long rows = fa::decode_paged_rows(R);
-    const long long ctas = static_cast<long long>(B) * Hkv * ((R + rows - 1) / rows);
-    S = std::min((PAGED_CTAS + ctas - 1) / ctas, (len + 127) / 128);
-    S = std::max(1LL, std::min(S, 1024LL));
-  }
-  const long long chunk = ((len + S - 1) / S + 127) / 128 * 128;
-  S = (len + chunk - 1) / chunk;
-  return {static_cast<int>(S), static_cast<int>(chunk)};
+PagedWorkspace paged_workspace(int B, int Hkv, int R, int d, int num_splits) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t pairs = static_cast<size_t>(B) * Hkv;
+  const size_t parts = (paged_ranges(B, Hkv, R, num_splits) + pairs) * paged_row_tiles(R) * fa::decode_paged_rows(R);
+  PagedWorkspace w{};
+  w.ml = up(parts * d * 4);
+  w.ends = w.ml + up(parts * 8);
+  w.bytes = w.ends + up(pairs * 8);
+  return w;
 }
 
 bool paged_decode_sizes_ok(int B, int H, int Hkv, int Nq, int max_len, int num_splits) {
@@ -930,10 +934,7 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
 
 size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int num_splits) {
   if (!paged_decode_sizes_ok(B, H, Hkv, Nq, max_len, num_splits) || (d != 64 && d != 128)) return 0;
-  const PagedSplit sp = paged_split(B, Hkv, H / Hkv * Nq, max_len, num_splits);
-  if (sp.S == 1) return 256;
-  const size_t parts = static_cast<size_t>(B) * H * Nq * sp.S;
-  return ((parts * d * 4 + 255) & ~size_t(255)) + ((parts * 8 + 255) & ~size_t(255));
+  return paged_workspace(B, Hkv, H / Hkv * Nq, d, num_splits).bytes;
 }
 
 fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
@@ -960,12 +961,12 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   if (B > 1 && table_stride < (static_cast<int64_t>(max_len) + page - 1) / page)
     return fail(FA_ERR_INVALID_ARG, "max_len needs %lld pages a sequence, table_stride is %lld",
                 (static_cast<long long>(max_len) + page - 1) / page, static_cast<long long>(table_stride));
-  const PagedSplit sp = paged_split(B, Hkv, R, max_len, num_splits);
-  const int rows = fa::decode_paged_rows(R), row_tiles = (R + rows - 1) / rows;
-  if (static_cast<long long>(B) * Hkv * sp.S * row_tiles > INT_MAX || static_cast<long long>(B) * H * Nq > INT_MAX)
-    return fail(FA_ERR_INVALID_ARG, "B * H * Nq * splits is too large");
+  const int row_tiles = paged_row_tiles(R), ranges = paged_ranges(B, Hkv, R, num_splits);
+  if (static_cast<long long>(B) * H * Nq > INT_MAX - 16 ||
+      static_cast<double>(B) * Hkv * max_len / 16 > 2e9 * ranges)  // (tiles of a range are counted in 32 bits)
+    return fail(FA_ERR_INVALID_ARG, "B * H * Nq or B * Hkv * max_len is too large");
   const size_t need = fa_decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits);
-  if (sp.S > 1 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
     return fail(FA_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
 
   DeviceState* st = nullptr;
@@ -979,15 +980,16 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   p.B = B, p.H = H, p.Hkv = Hkv, p.G = H / Hkv, p.Nq = Nq, p.R = R;
   p.max_len = max_len;
   p.page = page, p.page_shift = log2_of(page), p.num_pages = num_pages;
-  p.S = sp.S, p.chunk = sp.chunk, p.row_tiles = row_tiles;
+  p.n_ranges = ranges, p.row_tiles = row_tiles;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const size_t parts = static_cast<size_t>(B) * H * Nq * sp.S;
+  const PagedWorkspace w = paged_workspace(B, Hkv, R, d, num_splits);
   p.ws_o = static_cast<float*>(workspace);
-  p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((parts * d * 4 + 255) & ~size_t(255)));
+  p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.ml);
+  p.ws_ends = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.ends);
   p.status = st->status;
   cudaError_t e = fa::launch_decode_paged(d, e4m3 != 0, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
-  t_launches += sp.S == 1 ? 1 : 2;
+  t_launches += 2;
   return FA_OK;
 }
 

@@ -43,20 +43,29 @@ struct DecodePagedParams {
   const int* seqlens;        // int32 [B]
   void* o;                   // bf16, element strides osb / osh / ost
   float* lse;                // fp32 [B, H, Nq] or nullptr
-  float* ws_o;               // fp32 [rows, S, d] unnormalised partial outputs (S > 1)
-  float* ws_ml;              // fp32 [rows, S, 2] partial (base in log2 units, sum)
+  float* ws_o;               // fp32 [n_ranges + B * Hkv, row_tiles, rows, d] unnormalised parts of outputs
+  float* ws_ml;              // fp32 [n_ranges + B * Hkv, row_tiles, rows, 2] their (base in log2 units, sum)
+  int* ws_ends;              // int32 [B * Hkv, 2] first and last range that holds keys of a (sequence, K/V head)
   long long qsb, qsh, qst, osb, osh, ost, table_stride;
   int B, H, Hkv, G, Nq, R;   // R = G * Nq query rows per K/V head
-  int max_len;               // lengths are clipped to this; at most width * page and S * chunk
+  int max_len;               // lengths are clipped to this; at most width * page
   int page, page_shift, num_pages;
-  int S, chunk;              // split s covers keys [s * chunk, (s + 1) * chunk)
-  int row_tiles;             // tiles of 8 * NR query rows per K/V head
+  int n_ranges;              // the batch's keys are shared out in at most so many ranges
+  int row_tiles;             // tiles of 8 or 16 query rows per K/V head
   float scale_log2;          // scale * log2(e)
   unsigned int* status;      // device status word
 };
 
-// Query rows of one CTA of the paged decode: 8 where a K/V head has that few, else 16.
+// Query rows of one warp of the paged decode: 8 where a K/V head has that few, else 16.
 __host__ __device__ constexpr int decode_paged_rows(int R) { return R <= 8 ? 8 : 16; }
+// Blocks of four such warps that an SM holds, for warps of 8 row_groups rows.
+#ifndef DP_CTAS1
+#define DP_CTAS1 3
+#endif
+#ifndef DP_CTAS2
+#define DP_CTAS2 2
+#endif
+__host__ __device__ constexpr int decode_paged_ctas(int row_groups) { return row_groups == 1 ? DP_CTAS1 : DP_CTAS2; }
 
 struct AppendPagedParams {
   const void* q;             // bf16, element strides of token and head; d contiguous

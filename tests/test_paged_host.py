@@ -79,15 +79,19 @@ def test_decode_refusals(fa, kw, want):
 
 
 def test_decode_workspace(fa):
-    # explicit splits: one partial (o, m, l) for each row and split of whole 128-key pieces
-    n = fa.decode_paged_workspace_size(3, 8, 2, 2, 64, 1000, 4)    # 256 keys a split: 4
-    assert n >= 3 * 8 * 2 * 4 * (64 + 2) * 4 and n % 256 == 0
-    assert fa.decode_paged_workspace_size(3, 8, 2, 2, 64, 100, 4) == 256    # one 128-key piece: one split
+    # a partial (o, m, l) for each range, and one more for each sequence and K/V head: 4 splits a pair on average, two
+    # rows a pair padded to eight
+    n = fa.decode_paged_workspace_size(3, 4, 2, 1, 64, 1000, 4)
+    assert n % 256 == 0 and 0 <= n - (3 * 2 * 4 + 3 * 2) * 8 * (64 + 2) * 4 < 3 * 256
+    # 18 rows: two tiles of sixteen
+    n = fa.decode_paged_workspace_size(3, 18, 2, 2, 128, 1000, 1)
+    assert n % 256 == 0 and 0 <= n - (3 * 2 + 3 * 2) * 2 * 16 * (128 + 2) * 4 < 3 * 256
     assert fa.decode_paged_workspace_size(3, 8, 3, 2, 64, 100, 4) == 0
     assert fa.decode_paged_workspace_size(3, 8, 2, 2, 80, 100, 4) == 0
     assert fa.decode_paged_workspace_size(1, 8, 2, 64, 64, 100, 4) == 0     # 256 rows
-    # the library's own choice never exceeds the framework's 1024 splits
-    assert fa.decode_paged_workspace_size(1, 1, 1, 1, 64, 1 << 30) <= 1024 * 66 * 4 + 512
+    # the library's own choice does not grow with the lengths
+    assert (fa.decode_paged_workspace_size(1, 1, 1, 1, 64, 1 << 30) == fa.decode_paged_workspace_size(1, 1, 1, 1, 64, 10)
+            < 16 << 20)
 
 
 def _packed(fa, **kw):
