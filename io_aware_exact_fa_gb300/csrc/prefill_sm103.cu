@@ -1087,7 +1087,9 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         if (storer) bulk_wait_group_read_all();
         named_bar_sync(1 + t, 128);
       }
-      if (ok && active && (n > 0 || !C::O_STAGE)) {
+      // (In a packed batch a tile without rows waits for its Q phase as well: the store's thread arrives on q_free for
+      // every unit, and without that wait a run of such units would carry it phases ahead of the Q producer.)
+      if (ok && (active || (PK && !C::O_STAGE)) && (n > 0 || !C::O_STAGE)) {
         ok = (n > 0) ? mbar_wait(o_done + t, static_cast<uint32_t>((ct + n - 1) & 1), lim, p.status, abort_flag)
                      : mbar_wait(q_full + C::QB * t + qbuf(k), qpar(k), lim, p.status, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
@@ -1306,9 +1308,15 @@ static cudaError_t launch_packed_t(const CUtensorMap& tq, const CUtensorMap& tk,
   fa_packed_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(plan);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // At d = 128 a CTA for every unit, handed out as CTAs finish, where there are
+  // few units an SM (six sequences of up to 1024 queries, 440 units: 127 against
+  // 133 us); with more, one CTA an SM walking many, which spares the set-up of
+  // short units (eight of 200-2048, 1024 units: 93 against 101 us; two of
+  // 7000-8192, 1968 units: 767 against 780 us).
   const long long units = static_cast<long long>(plan.max_entries) * pk.head_units;
+  const bool persist = D == 64 || units > 4LL * p.max_ctas;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(C::PERSIST ? std::min<long long>(units, std::max(1, p.max_ctas)) : units));
+  cfg.gridDim = dim3(static_cast<unsigned>(persist ? std::min<long long>(units, std::max(1, p.max_ctas)) : units));
   cfg.blockDim = dim3(prefill_threads(D));
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;

@@ -531,7 +531,7 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
         out = torch.empty_like(q)
     os_ = _heads(out, "out", dev, q_shape)
     if lse is None and with_lse:
-        lse = q.new_empty((B, H, Nq), dtype=_F32)
+        lse = torch.empty((B, H, Nq), dtype=_F32, device=q.device)
     lp = None if lse is None else _whole(lse, "lse", _F32, dev, (B, H, Nq))
     if workspace is None:
         workspace = q.new_empty(max(1, decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits)),
@@ -580,7 +580,7 @@ def fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
         out = torch.empty_like(q)
     st += _heads(out, "out", dev, q_shape)
     if lse is None and with_lse:
-        lse = q.new_empty((H, Tq), dtype=_F32)
+        lse = torch.empty((H, Tq), dtype=_F32, device=q.device)
     lp = None if lse is None else _whole(lse, "lse", _F32, dev, (H, Tq))
     if workspace is None:
         workspace = q.new_empty(max(1, fwd_packed_workspace_size(B, Tq, H, Hkv)), dtype=torch.uint8)

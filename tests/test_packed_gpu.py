@@ -115,6 +115,29 @@ def test_long_rows_of_every_tile(fa, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv", [(3, 1), (4, 2)])
+def test_many_short_units(fa, H, Hkv, d):
+    """Several times more units than SMs, most of them of one row block whose second tile (odd groups) has no row, with
+    a few that see no key at all: every CTA walks a run of such units."""
+    rng = np.random.default_rng(2)
+    B = 700
+    lq = rng.integers(1, 60, B)
+    lq[::7] = 200
+    lk = lq + rng.integers(-3, 40, B)
+    lk[::5] = 0
+    lk = np.maximum(lk, 0)
+    cu_q, cu_k = cum(lq), cum(lk)
+    q, k, v = inputs(cu_q[-1], cu_k[-1], H, Hkv, d, seed=d)
+    o, lse = fa.fwd_packed(q, k, v, i32(cu_q), i32(cu_k), causal=True)
+    assert fa.device_status() == fa.FA_OK
+    some = [0, 1, 5, 7, 35, *rng.integers(0, B, 40).tolist()]
+    for b in some:
+        a0, a1, b0, b1 = cu_q[b], cu_q[b + 1], cu_k[b], cu_k[b + 1]
+        ro, rl = OP.packed(to64(q[a0:a1]), to64(k[b0:b1]), to64(v[b0:b1]), [0, a1 - a0], [0, b1 - b0], 1 / math.sqrt(d), True)
+        compare(to64(o[a0:a1]).reshape(-1, d), to64(lse[:, a0:a1]).T.reshape(-1), ro.reshape(-1, d), rl.T.reshape(-1), f"{b}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_against_the_dense_forward(fa, d):
     """One sequence, one head per K/V head: the same attention as fa_fwd on the same rows, bit for bit where both walk
     the same tiles (an odd group takes the dense kernel's tiles)."""
