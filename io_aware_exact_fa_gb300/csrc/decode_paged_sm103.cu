@@ -51,33 +51,27 @@ namespace {
 
 constexpr int DP_WARPS = 4;
 constexpr int DP_THREADS = 32 * DP_WARPS;
-#ifndef DP_HALF
-#define DP_HALF 4096
-#endif
-#ifndef DP_STAGES1
-#define DP_STAGES1 2                   // tiles in each warp's ring, with 8 query rows ..
-#endif
-#ifndef DP_STAGES2
-#define DP_STAGES2 3                   // .. and with 16
-#endif
 constexpr float DP_RESCALE_LOG2 = 8.f; // the base moves when a score passes it by more than this
 
 template <int D, bool F8, int NR>
 struct DpCfg {
+  static constexpr int ROWS = 8 * NR;            // query rows of a warp
   static constexpr int ESZ = F8 ? 1 : 2;
   static constexpr int RB = D * ESZ;             // bytes of a key's row: 64, 128 or 256
   static constexpr int CR = RB / 16;             // 16-byte pieces of a row
-  static constexpr int HALF = RB == 256 ? 4096 : DP_HALF;  // K (or V) bytes of a tile
+  static constexpr int HALF = 4096;              // K (or V) bytes of a tile
   static constexpr int KS = HALF / RB;           // its keys
   static constexpr int KG = KS / 16;             // its 16-key groups
   static constexpr int EPC = 16 / ESZ;           // elements of a piece
   static constexpr int DL = D / 4;               // elements of a K row that one lane holds
   static constexpr int NPK = DL / EPC;           // as pieces
   static constexpr int KST = D / 16;             // k-steps of S^T, and M tiles of O^T
-  static constexpr int ROWS = 8 * NR;
   static constexpr int META = KG * 2 * 4;        // e4m3 scales of a tile
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int DP_STAGES = NR == 1 ? DP_STAGES1 : DP_STAGES2;
+  // Tiles in each warp's ring: what fits beside the warps an SM holds. (Three tiles for eight warps against two for
+  // twelve: 136 against 130 us at 8 rows, e4m3, d = 128. Tiles of half the size, four to a ring: 134. Sixteen warps
+  // of those: 133.)
+  static constexpr int DP_STAGES = decode_paged_ctas(D, ROWS) == 3 ? 2 : 3;
   static constexpr int RING = DP_WARPS * DP_STAGES * STAGE;
   static constexpr int META_OFF = RING;
   static constexpr int SMEM = RING + DP_WARPS * DP_STAGES * META;
@@ -114,6 +108,9 @@ struct DpRanges {
   __device__ __forceinline__ long long begin(long long r) const { return r * tiles / n; }
 };
 
+// What a row's scores count from.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+
 __device__ __forceinline__ int dp_len(const DecodePagedParams& p, int b) {
   return paged_clip_len(__ldg(p.seqlens + b), p.max_len);
 }
@@ -121,7 +118,7 @@ __device__ __forceinline__ int dp_len(const DecodePagedParams& p, int b) {
 }  // namespace
 
 template <int D, bool F8, int NR>
-__global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(NR)) fa_decode_paged_kernel(const DecodePagedParams p) {
+__global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_decode_paged_kernel(const DecodePagedParams p) {
   using C = DpCfg<D, F8, NR>;
   extern __shared__ __align__(128) uint8_t dp_smem[];
   const uint32_t sbase = smem_u32(dp_smem);
@@ -386,7 +383,8 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(NR)) fa_decode_p
         }
       }
 
-      // ---- z = y + log2 c, masked; the base moves only when a row passes it by 2^8
+      // ---- z - M for z = y + log2 c, in packed fp32 pairs (rows 2tig and 2tig + 1). The base M moves only when a row
+      // passes it by 2^8; a row without one yet (M = -inf) counts from 0 and takes its first.
       float rv[C::KG];
       float mx[NR][2];
 #pragma unroll
@@ -405,56 +403,70 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(NR)) fa_decode_p
           rv[g] = __fdividef(1.f, c);
         }
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+        for (int n = 0; n < NR; ++n) {
+          const uint64_t c2 = F8 ? f2pack(c1[n][0] * ka, c1[n][1] * ka) : f2pack(c1[n][0], c1[n][1]);
+          const uint64_t b2 = f2pack(ev - base_of(M[n][0]), ev - base_of(M[n][1]));
+          float(&z)[4] = sc[g][n];
+          f2unpack(ffma2(f2pack(z[0], z[1]), c2, b2), z[0], z[1]);
+          f2unpack(ffma2(f2pack(z[2], z[3]), c2, b2), z[2], z[3]);
+          if (need_mask) {
+            const int key = key0 + 16 * g + gid;
+            const bool gone = (hid >> g) & 1u;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float z = F8 ? fmaf(sc[g][n][e], c1[n][e & 1] * ka, ev) : sc[g][n][e] * c1[n][e & 1];
-            if (need_mask) {
-              const int key = key0 + 16 * g + gid + (e >> 1) * 8;
-              if (key > lim[n][e & 1] || ((hid >> g) & 1u)) z = -INFINITY;
-            }
-            sc[g][n][e] = z;
-            mx[n][e & 1] = fmaxf(mx[n][e & 1], z);
+            for (int e = 0; e < 4; ++e)
+              if (key + (e >> 1) * 8 > lim[n][e & 1] || gone) z[e] = -INFINITY;
           }
+          mx[n][0] = fmax3(mx[n][0], z[0], z[2]);
+          mx[n][1] = fmax3(mx[n][1], z[1], z[3]);
+        }
       }
       bool over = false;
 #pragma unroll
       for (int n = 0; n < NR; ++n)
-        over = over || mx[n][0] > M[n][0] + DP_RESCALE_LOG2 || mx[n][1] > M[n][1] + DP_RESCALE_LOG2;
-      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          over = over || mx[n][e] > (M[n][e] == -INFINITY ? -INFINITY : DP_RESCALE_LOG2);
+      if (__any_sync(ALL, over)) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(mx[n][e], M[n][e]);
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float alpha = m == -INFINITY ? 1.f : ex2_approx(M[n][e] - m);
-            M[n][e] = m;
+            float up = mx[n][e];
+            up = fmaxf(up, __shfl_xor_sync(ALL, up, 4));
+            up = fmaxf(up, __shfl_xor_sync(ALL, up, 8));
+            up = fmaxf(up, __shfl_xor_sync(ALL, up, 16));
+            const bool none = M[n][e] == -INFINITY;
+            if (none) M[n][e] = up;                 // (still -inf when this tile shows the row nothing)
+            else M[n][e] += up = fmaxf(up, 0.f);    // the base only rises
+            up = up == -INFINITY ? 0.f : up;
+            const float alpha = none ? 1.f : ex2_approx(-up);  // (without a base nothing was summed)
             l[n][e] *= alpha;
 #pragma unroll
             for (int j = 0; j < C::KST; ++j) {
               oacc[n][j][e] *= alpha;
               oacc[n][j][e + 2] *= alpha;
             }
+#pragma unroll
+            for (int g = 0; g < C::KG; ++g) {
+              sc[g][n][e] -= up;
+              sc[g][n][e + 2] -= up;
+            }
           }
       }
       // ---- W = 2^(z - M), its sums, and W as the B operand (rows on the columns): 8x8 transposes
       uint32_t pf[C::KG][NR][2];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        const float m0 = M[n][0] == -INFINITY ? 0.f : M[n][0], m1 = M[n][1] == -INFINITY ? 0.f : M[n][1];
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int g = 0; g < C::KG; ++g) {
-          const float w0 = ex2_approx(sc[g][n][0] - m0), w1 = ex2_approx(sc[g][n][1] - m1);
-          const float w2 = ex2_approx(sc[g][n][2] - m0), w3 = ex2_approx(sc[g][n][3] - m1);
-          l[n][0] = F8 ? fmaf(w0 + w2, rv[g], l[n][0]) : l[n][0] + (w0 + w2);
-          l[n][1] = F8 ? fmaf(w1 + w3, rv[g], l[n][1]) : l[n][1] + (w1 + w3);
+          const float w0 = ex2_approx(sc[g][n][0]), w1 = ex2_approx(sc[g][n][1]);
+          const float w2 = ex2_approx(sc[g][n][2]), w3 = ex2_approx(sc[g][n][3]);
+          const uint64_t ws = fadd2(f2pack(w0, w1), f2pack(w2, w3));
+          const uint64_t l2 = f2pack(l[n][0], l[n][1]);
+          f2unpack(F8 ? ffma2(ws, f2pack(rv[g], rv[g]), l2) : fadd2(l2, ws), l[n][0], l[n][1]);
           pf[g][n][0] = movmatrix_trans(F8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1));
           pf[g][n][1] = movmatrix_trans(F8 ? pack_f16x2(w2, w3) : pack_bf16x2(w2, w3));
         }
-      }
       // ---- O^T += V^T W^T
 #pragma unroll
       for (int g = 0; g < C::KG; ++g) {

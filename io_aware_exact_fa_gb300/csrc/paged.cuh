@@ -58,14 +58,9 @@ struct DecodePagedParams {
 
 // Query rows of one warp of the paged decode: 8 where a K/V head has that few, else 16.
 __host__ __device__ constexpr int decode_paged_rows(int R) { return R <= 8 ? 8 : 16; }
-// Blocks of four such warps that an SM holds, for warps of 8 row_groups rows.
-#ifndef DP_CTAS1
-#define DP_CTAS1 3
-#endif
-#ifndef DP_CTAS2
-#define DP_CTAS2 2
-#endif
-__host__ __device__ constexpr int decode_paged_ctas(int row_groups) { return row_groups == 1 ? DP_CTAS1 : DP_CTAS2; }
+// Blocks of four such warps that an SM holds: three, but two where 16 rows of 128 values each leave no registers for
+// more (e4m3, d = 64, 16 rows: 47 against 53 us with two; d = 128: 114 against 117 us the other way).
+__host__ __device__ constexpr int decode_paged_ctas(int d, int rows) { return rows == 16 && d == 128 ? 2 : 3; }
 
 struct AppendPagedParams {
   const void* q;             // bf16, element strides of token and head; d contiguous
