@@ -425,6 +425,18 @@ def _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv: int, 
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+try:  # the allocator without the dispatcher before it (half the time of torch.empty); on the current device
+    _empty_here = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:
+    _empty_here = None
+
+
+def _empty(shape: Tuple[int, ...], strides: Tuple[int, ...], dtype, dev: int) -> torch.Tensor:
+    """A new tensor on device ``dev``; shape and strides are plain tuples."""
+    if _empty_here is not None and _current_device() == dev:
+        return _empty_here(shape, strides, dtype)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
 
 
 def _call(dev: int, stream: Optional[torch.cuda.Stream], fn, args, where: str) -> None:
@@ -435,7 +447,7 @@ def _call(dev: int, stream: Optional[torch.cuda.Stream], fn, args, where: str) -
         st = stream.cuda_stream
     else:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         rc = fn(*args, st)
     else:
         with torch.cuda.device(dev):
@@ -462,8 +474,7 @@ def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: tor
     [num_pages,Hkv,page,d] bf16, or float8_e4m3fn / uint8 codes with fp32 scales [num_pages,Hkv]; block_table int32
     [B,width]; seqlens_k int32 [B] with the new tokens counted; cu_seqlens int32 [B+1], or None for T / B tokens each.
     ``turns`` (``rotary_turns``) sets the rotation, None for none; the weights bf16 [d] the norms, None for none.
-    Returns the turned q [T,H,d] and k [T,Hkv,d] (None without ``with_k``); outputs that are not given are laid out like
-    q and k where those are dense, else contiguous."""
+    Returns the turned q [T,H,d] and k [T,Hkv,d] (None without ``with_k``), contiguous unless given."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
         raise ValueError("q must be a CUDA tensor [T, H, d]")
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
@@ -483,11 +494,17 @@ def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: tor
     qw = None if q_weight is None else _whole(q_weight, "q_weight", _BF16, dev, (d,))
     kw = None if k_weight is None else _whole(k_weight, "k_weight", _BF16, dev, (d,))
     if q_out is None:
-        q_out = torch.empty_like(q)
-    st += _heads(q_out, "q_out", dev, q_shape)
-    if k_out is None and with_k:
-        k_out = torch.empty_like(k)
-    st += (0, 0) if k_out is None else _heads(k_out, "k_out", dev, kv_shape)
+        q_out = _empty((T, H, d), (H * d, d, 1), _BF16, dev)
+        st += (H * d, d)
+    else:
+        st += _heads(q_out, "q_out", dev, q_shape)
+    if k_out is not None:
+        st += _heads(k_out, "k_out", dev, kv_shape)
+    elif with_k:
+        k_out = _empty((T, Hkv, d), (Hkv * d, d, 1), _BF16, dev)
+        st += (Hkv * d, d)
+    else:
+        st += (0, 0)
     _call(dev, stream, _lib.fa_append_paged,
           (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), kp, vp,
            ks, vs, table, table_stride, lens, cu, tp, qw, kw, _I64x10(*st), B, T, H, Hkv, d, n, page, width, e4m3, rot,
@@ -508,7 +525,7 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     """Grouped decode over a paged cache (fa.h fa_decode_paged): q [B,H,Nq,d] bf16, any strides with d contiguous
     (``append_paged``'s q of B x Nq tokens is ``q.view(B, Nq, H, d).transpose(1, 2)``), the pool and table as for
     ``append_paged`` -> (o [B,H,Nq,d] bf16, lse [B,H,Nq] fp32). ``max_len`` bounds the lengths (default: all that a
-    row of the table covers); ``num_splits`` 0 lets the library choose. Without ``out``, o is laid out like q where that is dense."""
+    row of the table covers); ``num_splits`` 0 lets the library choose. Without ``out``, o is token-major where q is, else contiguous."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
@@ -528,11 +545,17 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
-    os_ = _heads(out, "out", dev, q_shape)
-    if lse is None and with_lse:
-        lse = torch.empty((B, H, Nq), dtype=_F32, device=q.device)
-    lp = None if lse is None else _whole(lse, "lse", _F32, dev, (B, H, Nq))
+        # laid out like q where that is token-major, else contiguous
+        os_ = (Nq * H * d, d, H * d) if qs[1] == d and qs[2] == H * d else (H * Nq * d, Nq * d, d)
+        out = _empty((B, H, Nq, d), os_ + (1,), _BF16, dev)
+    else:
+        os_ = _heads(out, "out", dev, q_shape)
+    lp = None
+    if lse is not None:
+        lp = _whole(lse, "lse", _F32, dev, (B, H, Nq))
+    elif with_lse:
+        lse = _empty((B, H, Nq), (H * Nq, Nq, 1), _F32, dev)
+        lp = lse.data_ptr()
     if workspace is None:
         workspace = q.new_empty(max(1, decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits)),
                                 dtype=torch.uint8)
@@ -577,11 +600,16 @@ def fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
-    st += _heads(out, "out", dev, q_shape)
-    if lse is None and with_lse:
-        lse = torch.empty((H, Tq), dtype=_F32, device=q.device)
-    lp = None if lse is None else _whole(lse, "lse", _F32, dev, (H, Tq))
+        st += (H * d, d)
+        out = _empty((Tq, H, d), (H * d, d, 1), _BF16, dev)
+    else:
+        st += _heads(out, "out", dev, q_shape)
+    lp = None
+    if lse is not None:
+        lp = _whole(lse, "lse", _F32, dev, (H, Tq))
+    elif with_lse:
+        lse = _empty((H, Tq), (Tq, 1), _F32, dev)
+        lp = lse.data_ptr()
     if workspace is None:
         workspace = q.new_empty(max(1, fwd_packed_workspace_size(B, Tq, H, Hkv)), dtype=torch.uint8)
     wp = _whole(workspace, "workspace", workspace.dtype, dev)
