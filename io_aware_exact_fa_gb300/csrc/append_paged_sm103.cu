@@ -310,6 +310,9 @@ __device__ __forceinline__ bool tokens_of(const AppendPagedParams& p, int b, int
   return false;
 }
 
+// A sequence's length; far below zero (an error in any case) it would overflow the position arithmetic.
+__device__ __forceinline__ int length_of(const AppendPagedParams& p, int b) { return max(__ldg(p.seqlens + b), -(1 << 30)); }
+
 // ---- query block: rows tok0 .. of the step, all heads
 template <int D, bool INTER>
 __device__ __forceinline__ void query_block(const AppendPagedParams& p, int block, int* s_pos, uint4* ring) {
@@ -324,7 +327,7 @@ __device__ __forceinline__ void query_block(const AppendPagedParams& p, int bloc
     const int n = p.T / p.B;
     for (int r = tid; r < rows; r += nt) {
       const int tok = tok0 + r, b = tok / n;
-      s_pos[r] = tok < p.T ? __ldg(p.seqlens + b) - (b + 1) * n + tok : NONE;
+      s_pos[r] = tok < p.T ? length_of(p, b) - n + (tok - b * n) : NONE;
     }
   } else {
     for (int r = tid; r < rows; r += nt) s_pos[r] = NONE;
@@ -334,7 +337,7 @@ __device__ __forceinline__ void query_block(const AppendPagedParams& p, int bloc
       if (!tokens_of(p, b, t0, n) && block == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
       const int a = max(t0, tok0), e = min(t0 + n, tok0 + rows);
       if (a < e) {
-        const int L = __ldg(p.seqlens + b);
+        const int L = length_of(p, b);
         for (int t = a; t < e; ++t) s_pos[t - tok0] = L - n + (t - t0);
       }
     }
@@ -422,7 +425,7 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
   }
   int t0, n;
   (void)tokens_of(p, b, t0, n);
-  const int L = __ldg(p.seqlens + b);
+  const int L = length_of(p, b);
   const int start = L - n;
   const int page0 = (start >> p.page_shift) + i;                 // this block's page of the sequence
   const long long first = static_cast<long long>(page0) << p.page_shift;

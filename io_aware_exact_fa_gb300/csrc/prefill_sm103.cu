@@ -1230,73 +1230,101 @@ constexpr int PLAN_BUCKETS = 1024;
 // Lists the row blocks (of block_rows rows) of a packed batch, those that visit
 // the most key tiles first, as entries {q_off, k_off, Lq, Lk}, {first row}; one
 // CTA. A counting sort by the number of key tiles: equal counts come in any
-// order, which changes which CTA computes a block and nothing else.
+// order, which changes which CTA computes a block and nothing else. Sequences
+// are read PLAN_THREADS at a time, one by each thread; their blocks are then
+// dealt out to all threads alike, however the lengths differ. (A warp for each
+// sequence in turn took 26 us for 700 sequences.)
 __global__ void __launch_bounds__(PLAN_THREADS) fa_packed_plan_kernel(const PackedPlan a) {
+  static_assert(PLAN_BUCKETS == PLAN_THREADS, "one thread scans one bucket");
   __shared__ int hist[PLAN_BUCKETS];
   __shared__ int wsum[PLAN_THREADS / 32];
+  __shared__ int start[PLAN_THREADS];  // first block of each of the sequences in hand
+  __shared__ int4 seqs[PLAN_THREADS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  static_assert(PLAN_BUCKETS == PLAN_THREADS, "one thread scans one bucket");
   pdl_launch_dependents();
   hist[tid] = 0;
-  __syncthreads();
   bool bad = false;
-  // a sequence's rows and keys, clipped to the tensors
-  auto seq = [&](int b, int4& x) {
-    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1), k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
-    x.x = min(max(q0, 0), a.total_q);
-    x.y = min(max(k0, 0), a.total_k);
-    x.z = max(min(max(q1, 0), a.total_q) - x.x, 0);
-    x.w = max(min(max(k1, 0), a.total_k) - x.y, 0);
-    bad = bad || q0 != x.x || k0 != x.y || q1 != x.x + x.z || k1 != x.y + x.w;
+  // exclusive scan over the block's threads; every thread gets the total as well
+  auto scan = [&](int n, int& total) {
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    const int w = wsum[lane];  // (32 warps: one sum a lane)
+    int ws = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, ws, o);
+      if (lane >= o) ws += y;
+    }
+    total = __shfl_sync(0xffffffffu, ws, 31);
+    const int before = __shfl_sync(0xffffffffu, ws - w, warp);
+    __syncthreads();
+    return before + inc - n;
+  };
+  // reads sequences b0 .. b0 + PLAN_THREADS - 1; returns the number of their blocks
+  auto read = [&](int b0) {
+    const int b = b0 + tid;
+    int4 x = make_int4(0, 0, 0, 0);
+    if (b < a.B) {  // the sequence's rows and keys, clipped to the tensors
+      const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1), k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
+      x.x = min(max(q0, 0), a.total_q);
+      x.y = min(max(k0, 0), a.total_k);
+      x.z = max(min(max(q1, 0), a.total_q) - x.x, 0);
+      x.w = max(min(max(k1, 0), a.total_k) - x.y, 0);
+      bad = bad || q0 != x.x || k0 != x.y || q1 != x.x + x.z || k1 != x.y + x.w;
+    }
+    int total;
+    start[tid] = scan((x.z + a.block_rows - 1) / a.block_rows, total);
+    seqs[tid] = x;
+    __syncthreads();
+    return total;
+  };
+  // the sequence in hand that block i belongs to: the last one that starts at or before it
+  const int steps = 32 - __clz(min(a.B, PLAN_THREADS));
+  auto find = [&](int i) {
+    int lo = 0;
+    for (int w = 1 << (steps - 1); w > 0; w >>= 1)
+      if (lo + w < PLAN_THREADS && start[lo + w] <= i) lo += w;
+    return lo;
   };
   auto bucket = [&](const int4& x, int i) {  // 0: the most key tiles
     const int last_row = min((i + 1) * a.block_rows, x.z) - 1;
     const int keys = a.causal ? min(x.w, max(last_row + 1 + x.w - x.z, 0)) : x.w;
     return PLAN_BUCKETS - 1 - min((((keys + BLOCK_N - 1) / BLOCK_N) >> a.shift), PLAN_BUCKETS - 1);
   };
-  for (int b = warp; b < a.B; b += PLAN_THREADS / 32) {
-    int4 x;
-    seq(b, x);
-    const int nb = (x.z + a.block_rows - 1) / a.block_rows;
-    for (int i = lane; i < nb; i += 32) atomicAdd(&hist[bucket(x, i)], 1);
+  const bool once = a.B <= PLAN_THREADS;  // all sequences stay in hand
+  int total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += PLAN_THREADS) {
+    total = read(b0);  // (it synchronises: the counters are clear)
+    for (int i = tid; i < total; i += PLAN_THREADS) {
+      const int sq = find(i);
+      atomicAdd(&hist[bucket(seqs[sq], i - start[sq])], 1);
+    }
+    __syncthreads();
   }
   if (bad) atomicOr(a.status, FA_DEV_BAD_LENS);
+  int all;
+  const int offset = scan(hist[tid], all);
+  hist[tid] = offset;
+  if (tid == 0) *a.n_entries = min(all, a.max_entries);
   __syncthreads();
-  // exclusive scan of the buckets
-  const int n = hist[tid];
-  int inc = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  if (lane == 31) wsum[warp] = inc;
-  __syncthreads();
-  if (warp == 0) {
-    const int w = wsum[lane];
-    int s = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    wsum[lane] = s - w;
-    if (lane == 31) *a.n_entries = min(s, a.max_entries);
-  }
-  __syncthreads();
-  hist[tid] = wsum[warp] + inc - n;
-  __syncthreads();
-  for (int b = warp; b < a.B; b += PLAN_THREADS / 32) {
-    int4 x;
-    seq(b, x);
-    const int nb = (x.z + a.block_rows - 1) / a.block_rows;
-    for (int i = lane; i < nb; i += 32) {
-      const int at = atomicAdd(&hist[bucket(x, i)], 1);
+  for (int b0 = 0; b0 < a.B; b0 += PLAN_THREADS) {
+    if (!once) total = read(b0);
+    for (int i = tid; i < total; i += PLAN_THREADS) {
+      const int sq = find(i);
+      const int4 x = seqs[sq];
+      const int at = atomicAdd(&hist[bucket(x, i - start[sq])], 1);
       if (at < a.max_entries) {  // (offsets that overlap could list more)
         a.entries[2 * at] = x;
-        a.entries[2 * at + 1] = make_int4(i * a.block_rows, 0, 0, 0);
+        a.entries[2 * at + 1] = make_int4((i - start[sq]) * a.block_rows, 0, 0, 0);
       }
     }
+    __syncthreads();
   }
 }
 

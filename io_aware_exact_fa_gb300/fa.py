@@ -439,12 +439,18 @@ def _empty(shape: Tuple[int, ...], strides: Tuple[int, ...], dtype, dev: int) ->
     return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
 
 
-def _call(dev: int, stream: Optional[torch.cuda.Stream], fn, args, where: str) -> None:
-    """Calls the library with the tensors' device current, on ``stream`` or that device's current stream."""
+def _call(dev: int, stream: Optional[torch.cuda.Stream], fn, args, where: str, made=()) -> None:
+    """Calls the library with the tensors' device current, on ``stream`` or that device's current stream. ``made``:
+    tensors that were made for the call, or None; another stream than the current one is made known to the allocator,
+    which would otherwise hand their memory out again while the call still runs."""
     if stream is None:
         st = _raw_stream(dev)
     elif stream.device.index == dev:
         st = stream.cuda_stream
+        if st != _raw_stream(dev):
+            for t in made:
+                if t is not None:
+                    t.record_stream(stream)
     else:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     if _current_device() == dev:
@@ -508,7 +514,7 @@ def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: tor
     _call(dev, stream, _lib.fa_append_paged,
           (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), kp, vp,
            ks, vs, table, table_stride, lens, cu, tp, qw, kw, _I64x10(*st), B, T, H, Hkv, d, n, page, width, e4m3, rot,
-           bool(interleaved), rot_scale, eps, max_new), "fa_append_paged")
+           bool(interleaved), rot_scale, eps, max_new), "fa_append_paged", (q_out, k_out))
     return q_out, k_out
 
 
@@ -562,7 +568,8 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     wp = _whole(workspace, "workspace", workspace.dtype, dev)
     _call(dev, stream, _lib.fa_decode_paged,
           (q.data_ptr(), _I64x3(*qs), kp, vp, ks, vs, table, table_stride, lens, out.data_ptr(), _I64x3(*os_), lp, B, H,
-           Hkv, Nq, d, n, page, max_len, e4m3, scale, num_splits, wp, workspace.nbytes), "fa_decode_paged")
+           Hkv, Nq, d, n, page, max_len, e4m3, scale, num_splits, wp, workspace.nbytes), "fa_decode_paged",
+          (out, lse, workspace))
     return out, lse
 
 
@@ -615,7 +622,7 @@ def fwd_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     wp = _whole(workspace, "workspace", workspace.dtype, dev)
     _call(dev, stream, _lib.fa_fwd_packed,
           (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, _I64x8(*st), cq, ck, B, Tq, Tk, H, Hkv, d, scale,
-           bool(causal), wp, workspace.nbytes), "fa_fwd_packed")
+           bool(causal), wp, workspace.nbytes), "fa_fwd_packed", (out, lse, workspace))
     return out, lse
 
 

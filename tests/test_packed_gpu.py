@@ -252,6 +252,42 @@ def test_serving_run(fa):
         assert (ld[b, :, 0] - lp[:, t]).abs().max() <= 2e-3
 
 
+def test_plan_of_many_sequences(fa):
+    """More sequences than the list's CTA has threads, empty ones and a long one among them: every row is computed once,
+    with its own sequence's keys. (Each sequence's values are one constant of its own, so its rows return that constant.)"""
+    rng = np.random.default_rng(7)
+    B, d = 2600, 64
+    lq = rng.integers(0, 5, B)
+    lq[1500], lq[2599] = 1000, 130
+    cu = cum(lq)
+    T = cu[-1]
+    q, k, _ = inputs(T, T, 2, 2, d, seed=1)
+    own = torch.repeat_interleave(torch.arange(B) % 251, torch.tensor(lq)).cuda()
+    v = own.to(torch.bfloat16)[:, None, None].expand(T, 2, d).contiguous()
+    o, lse = fa.fwd_packed(q, k, v, i32(cu))
+    assert fa.device_status() == fa.FA_OK
+    # integers up to 250 are bf16 values; the weights' sum and the sum of the rounded weights differ by at most 2^-8
+    assert ((o.float() - v.float()).abs() <= 2.0 ** -8 * v.float() * 2).all() and torch.isfinite(lse).all()
+
+
+def test_calls_on_another_stream(fa):
+    """Outputs and workspaces that a call makes stay its own while it runs on a stream that is not current."""
+    lq = [300, 200, 100] * 6
+    cu = i32(cum(lq))
+    q, k, v = inputs(sum(lq), sum(lq), 8, 2, 128, seed=6)
+    want, lse = fa.fwd_packed(q, k, v, cu, causal=True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got.append(fa.fwd_packed(q, k, v, cu, causal=True, stream=side))
+        torch.full((1 << 20,), 3.0, device="cuda")   # current-stream work that takes memory the side stream still uses, if let
+    side.synchronize()
+    assert fa.device_status() == fa.FA_OK
+    for o, l in got:
+        assert torch.equal(o, want) and torch.equal(l, lse)
+
+
 def test_binding_refusals(fa):
     q, k, v = inputs(10, 10, 4, 2, 64, seed=1)
     cu = i32([0, 10])
