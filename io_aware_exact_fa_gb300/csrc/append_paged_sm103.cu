@@ -25,12 +25,15 @@
 // on, so no sum or maximum goes through global atomics; it turns the keys, keeps
 // them in fp32 in shared memory until the page's largest value is known, and
 // writes the codes. A query block takes rows of the step and streams their query
-// heads through registers with two heads' loads always in flight; a row's angles
-// (with the norm's weights multiplied in) are computed once for all its heads.
+// heads through rings of asynchronous copies, each one thread's own, so loads stay
+// in flight without registers; a row's angles (with the norm's weights multiplied
+// in) are computed once for all its heads.
 // What bounds it: HBM for prompts (q read and written, k and v read, the cache
 // written) as long as the instructions per value stay few (packed fp32
-// arithmetic; one kind of block for both was 1.5 times slower), launch and load
-// latency for a step of single tokens.
+// arithmetic; one kind of block for both took 147 us in place of 132), launch and
+// load latency for a step of single tokens. Measured, 32 query and 8 K/V heads,
+// d = 128, e4m3: 26.7k prompt tokens with norms 114 us (5.8 TB/s, 0.85 of the copy
+// rate); 256 sequences of one token 7.9 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
