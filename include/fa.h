@@ -336,7 +336,8 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
  *      (int32 [B+1] on the device), or T / B each when cu_seqlens is NULL.
  *   seqlens_k  int32 [B]: lengths L_b with the new tokens counted (what
  *      fa_decode_paged takes next), so token i of n_b is at position
- *      p = L_b - n_b + i.
+ *      p = L_b - n_b + i. The tokens of a sequence of length 0 are padding (of a
+ *      captured batch, say): nothing is written for them.
  *   q_weight, k_weight  bf16 [d] or NULL: each head is first normalised,
  *      x / sqrt(mean(x^2) + eps) * weight.
  *   rot, turns, interleaved, rot_scale  The first `rot` elements of every q and

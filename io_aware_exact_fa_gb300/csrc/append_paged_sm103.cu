@@ -330,7 +330,8 @@ __device__ __forceinline__ void query_block(const AppendPagedParams& p, int bloc
     const int n = p.T / p.B;
     for (int r = tid; r < rows; r += nt) {
       const int tok = tok0 + r, b = tok / n;
-      s_pos[r] = tok < p.T ? length_of(p, b) - n + (tok - b * n) : NONE;
+      const int L = tok < p.T ? length_of(p, b) : 0;
+      s_pos[r] = L != 0 ? L - n + (tok - b * n) : NONE;
     }
   } else {
     for (int r = tid; r < rows; r += nt) s_pos[r] = NONE;
@@ -341,7 +342,8 @@ __device__ __forceinline__ void query_block(const AppendPagedParams& p, int bloc
       const int a = max(t0, tok0), e = min(t0 + n, tok0 + rows);
       if (a < e) {
         const int L = length_of(p, b);
-        for (int t = a; t < e; ++t) s_pos[t - tok0] = L - n + (t - t0);
+        if (L != 0)
+          for (int t = a; t < e; ++t) s_pos[t - tok0] = L - n + (t - t0);
       }
     }
   }
@@ -432,7 +434,7 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
   const int start = L - n;
   const int page0 = (start >> p.page_shift) + i;                 // this block's page of the sequence
   const long long first = static_cast<long long>(page0) << p.page_shift;
-  if (n == 0 || first >= L) return;                              // (uniform over the block)
+  if (n == 0 || L == 0 || first >= L) return;                    // (uniform over the block)
   const int r0 = start > first ? start - static_cast<int>(first) : 0;           // its new rows r0 .. r1 - 1
   const int r1 = static_cast<int>(L - first < p.page ? L - first : p.page);
   const int nrows = r1 - r0;

@@ -11,7 +11,6 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <initializer_list>
 #include <mutex>
 
 #include "fa.h"
@@ -858,12 +857,9 @@ fa_status check_pool(const void* k_pages, const void* v_pages, const float* k_sc
   return FA_OK;
 }
 
-// Element strides of a strided operand: multiples of 8 (16-byte rows), not negative.
-bool strides_ok(std::initializer_list<int64_t> st) {
-  for (int64_t s : st)
-    if (s < 0 || s % 8 != 0) return false;
-  return true;
-}
+// Element strides of a strided operand: multiples of 8 (16-byte rows), not
+// negative; that of a dimension of one element does not matter.
+bool stride_ok(int64_t stride, int extent) { return extent <= 1 || (stride >= 0 && stride % 8 == 0); }
 
 }  // namespace
 
@@ -897,8 +893,11 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
     if (!aligned(x, 16)) return fail(FA_ERR_UNSUPPORTED, "q, k, v, the outputs and the weights must be 16-byte aligned");
   if (!aligned(turns, 16) || !aligned(cu_seqlens, 4)) return fail(FA_ERR_UNSUPPORTED, "turns must be 16-byte, cu_seqlens 4-byte aligned");
   if (table_stride < table_width && B > 1) return fail(FA_ERR_INVALID_ARG, "table_stride is below table_width");
-  for (int i = 0; i < 10; ++i)
-    if (!strides_ok({strides[i]})) return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements and >= 0");
+  for (int i = 0; i < 10; ++i) {  // token and head strides of q, k, v, q_out, k_out
+    const int heads = (i == 1 || i == 7) ? H : Hkv;
+    if ((i < 8 || k_out) && !stride_ok(strides[i], (i & 1) ? heads : T))
+      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements and >= 0");
+  }
   const int n_max = cu_seqlens == nullptr ? T / B : std::min(max_new > 0 ? max_new : T, T);
   const long long rect = (static_cast<long long>(n_max) + page - 2) / page + 1;
   const bool use_rect = cu_seqlens == nullptr || rect * B <= T / page + 2LL * B;
@@ -955,8 +954,10 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   if (R > 128) return fail(FA_ERR_UNSUPPORTED, "(H / Hkv) * Nq query rows per K/V head; at most 128");
   if (fa_status s = check_pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, num_pages, page, e4m3)) return s;
   if (!aligned(q, 16) || !aligned(o, 16)) return fail(FA_ERR_UNSUPPORTED, "q and o must be 16-byte aligned");
-  if (!strides_ok({q_strides[0], q_strides[1], q_strides[2], o_strides[0], o_strides[1], o_strides[2]}))
-    return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements and >= 0");
+  const int extent[3] = {B, H, Nq};
+  for (int i = 0; i < 3; ++i)
+    if (!stride_ok(q_strides[i], extent[i]) || !stride_ok(o_strides[i], extent[i]))
+      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements and >= 0");
   if (lse && !aligned(lse, 4)) return fail(FA_ERR_UNSUPPORTED, "lse must be 4-byte aligned");
   if (B > 1 && table_stride < (static_cast<int64_t>(max_len) + page - 1) / page)
     return fail(FA_ERR_INVALID_ARG, "max_len needs %lld pages a sequence, table_stride is %lld",

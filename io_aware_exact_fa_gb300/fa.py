@@ -381,15 +381,13 @@ def _whole(t: torch.Tensor, name: str, dtype, dev: int, shape=None) -> int:
 
 
 def _heads(t: torch.Tensor, name: str, dev: int, shape) -> Tuple[int, ...]:
-    """A bf16 tensor whose last dimension is contiguous; its other strides may be any multiple of 8. Returns the
-    strides of the others for the C ABI: a dimension of one element has none that matters."""
+    """A bf16 tensor whose last dimension is contiguous; its other strides may be any multiple of 8. Returns them for the
+    C ABI (which does not look at the stride of a dimension of one element)."""
     if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
         raise _refusal(t, name, _BF16, dev, shape, "")
     st = t.stride()
     if st[-1] != 1:
         raise _refusal(t, name, _BF16, dev, shape, "have a contiguous last dimension")
-    if 1 in shape:
-        return tuple(x if n > 1 else 0 for x, n in zip(st[:-1], shape))
     return st[:-1]
 
 
@@ -406,7 +404,7 @@ def _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv: int, 
     if len(shape) != 4 or shape[1] != Hkv or shape[3] != d:
         raise ValueError(f"k_pages and v_pages must be [num_pages, {Hkv}, page, {d}]")
     vp = _whole(v_pages, "v_pages", kind, dev, shape)
-    n, page = shape[0], shape[2]
+    n, _, page, _ = shape
     ks = vs = None
     if e4m3:
         if k_scale is None or v_scale is None:
@@ -420,8 +418,9 @@ def _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv: int, 
     tab, ts = block_table.shape, block_table.stride()
     if len(tab) != 2 or (ts[1] != 1 and tab[1] > 1):
         raise ValueError("block_table must be [B, width] with contiguous rows")
-    lens = _whole(seqlens_k, "seqlens_k", _I32, dev, (tab[0],))
-    return (kp, vp, ks, vs, block_table.data_ptr(), ts[0], lens), n, page, e4m3, tab[0], tab[1]
+    B, width = tab
+    lens = _whole(seqlens_k, "seqlens_k", _I32, dev, (B,))
+    return (kp, vp, ks, vs, block_table.data_ptr(), ts[0], lens), n, page, e4m3, B, width
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream

@@ -204,6 +204,42 @@ def test_append_in_place_and_strided_outputs(fa):
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
 
 
+@pytest.mark.parametrize("ragged", [False, True])
+def test_padded_batch(fa, ragged):
+    """Sequences of length 0 are padding: their tokens are left alone, their table rows not read, and decode gives their
+    rows zeros; the others' results are those of the batch without them."""
+    rng = np.random.default_rng(14)
+    H, Hkv, d, page = 4, 2, 64, 16
+    lens, new = [0, 20, 0, 5, 0], [2, 2, 2, 2, 2]
+    table = np.full((5, 2), 99, dtype=np.int32)
+    table[1], table[3, 0] = [2, 0], 4
+    cache = Cache(rng, 5, Hkv, page, d, True)
+    before = [c.view(torch.uint8).clone() for c in cache.gpu] + [s.clone() for s in cache.scale]
+    x = torch.randn(10, H + 2 * Hkv, d, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    split = lambda y: (y[:, :H], y[:, H:H + Hkv], y[:, H + Hkv:])   # noqa: E731
+    turns = fa.rotary_turns(d)
+    cu = cuda(np.arange(0, 11, 2), torch.int32) if ragged else None
+    qo, ko = torch.full((10, H, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((10, Hkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    fa.append_paged(*split(x), *cache.gpu, cuda(table), cuda(lens, torch.int32), cu_seqlens=cu, turns=turns, q_out=qo, k_out=ko,
+                    **cache.kw())
+    o, lse = fa.decode_paged(qo.view(5, 2, H, d).transpose(1, 2), *cache.gpu, cuda(table), cuda(lens, torch.int32), **cache.kw())
+    assert fa.device_status() == fa.FA_OK
+    pad = [0, 1, 4, 5, 8, 9]
+    assert (qo[pad] == 7).all() and (ko[pad] == 7).all()
+    assert (o[[0, 2, 4]] == 0).all() and torch.isneginf(lse[[0, 2, 4]]).all()
+    after = [c.view(torch.uint8).clone() for c in cache.gpu] + [s.clone() for s in cache.scale]
+    for t, b in zip([*cache.gpu, *cache.scale], before):
+        t.view(b.dtype).copy_(b)
+    live = [2, 3, 6, 7]
+    q2, k2 = fa.append_paged(*split(x[live]), *cache.gpu, cuda(table[[1, 3]]), cuda([20, 5], torch.int32), turns=turns, **cache.kw())
+    o2, l2 = fa.decode_paged(q2.view(2, 2, H, d).transpose(1, 2), *cache.gpu, cuda(table[[1, 3]]), cuda([20, 5], torch.int32), **cache.kw())
+    assert fa.device_status() == fa.FA_OK
+    assert torch.equal(q2, qo[live]) and torch.equal(k2, ko[live])
+    assert all(torch.equal(a, b.view(a.dtype)) for a, b in zip(after, [*cache.gpu, *cache.scale]))
+    # other ranges of tiles, so other roundings: each within the tolerance of the exact result
+    assert (o2 - o[[1, 3]]).abs().max() <= 2e-2 and (l2 - lse[[1, 3]]).abs().max() <= 2e-3
+
+
 def test_append_scale_growth_and_odd_values(fa):
     """Token by token into one e4m3 page: the scale follows the largest value so far; infinities and NaN become the NaN
     code and leave the scale alone; an all-zero page has the least scale; a page that starts over forgets its old one."""

@@ -71,7 +71,7 @@ def _decode(fa, **kw):
     (dict(splits=-1), INVALID), (dict(splits=1025), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(e4m3=1), INVALID), (dict(stride=62), INVALID), (dict(d=32), UNSUPPORTED), (dict(Nq=33), UNSUPPORTED),
     (dict(H=1 << 20, Nq=1 << 20), UNSUPPORTED), (dict(page=8), UNSUPPORTED), (dict(q=P + 8), UNSUPPORTED),
-    (dict(o=P + 4), UNSUPPORTED), (dict(lse=P + 2), UNSUPPORTED), (dict(qs=[512, 64, 65]), UNSUPPORTED),
+    (dict(o=P + 4), UNSUPPORTED), (dict(lse=P + 2), UNSUPPORTED), (dict(qs=[512, 64, 65], Nq=2), UNSUPPORTED),
     (dict(k=P + 8), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws=P + 16), WORKSPACE), (dict(bytes=64), WORKSPACE),
 ])
 def test_decode_refusals(fa, kw, want):
