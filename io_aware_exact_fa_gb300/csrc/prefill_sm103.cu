@@ -390,6 +390,33 @@ __device__ __forceinline__ PackedUnit packed_unit_info(const PrefillParams& p, c
   return w;
 }
 
+// Writes 64 bytes of each lane's row (w: 16 words) so that four lanes write 64
+// neighbouring bytes of one row at a time, not 16 bytes of four rows: the lanes
+// of a group of four trade 16-byte pieces, a 4x4 transpose in two steps. `dst`
+// is the group's first row at this lane's piece; `left` rows of it exist. Every
+// lane of the warp takes part. (One row a lane, 16 bytes of 32 rows an
+// instruction, cost more than staging through the Q buffer: 95 against 93 us for
+// eight sequences of 200-2048 rows.)
+__device__ __forceinline__ void put_rows(uint32_t (&w)[16], int lane, uint8_t* dst, long long row_bytes, int left) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const bool up = (lane >> s) & 1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int lo = s == 0 ? 2 * k : k, hi = s == 0 ? 2 * k + 1 : k + 2;  // pieces traded between the two lanes
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = __shfl_xor_sync(0xffffffffu, up ? w[4 * lo + i] : w[4 * hi + i], 1 << s);
+        if (up) w[4 * lo + i] = x;
+        else w[4 * hi + i] = x;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < left) *reinterpret_cast<uint4*>(dst + j * row_bytes) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+
 // The k-th unit of CTA c of G, or a value >= U when it has no k-th unit.
 // Round robin; with `snake` every other round runs in reverse CTA order, so
 // with units sorted longest first the per-CTA sums stay balanced.
@@ -443,6 +470,12 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
   const int sw = warp;
   const bool alloc_warp = producer && pw == 1;  // the first MMA issuer allocates and frees TMEM
   const uint64_t lim = p.wait_limit_ns;
+  // PK at d = 128: there is no room to stage O apart, and staging it in the Q
+  // buffer would keep the next unit's Q waiting for the epilogue; the rows are
+  // written from registers instead (put_rows), and the Q buffer is free after the
+  // unit's last score product.
+  constexpr bool DIRECT = PK && !C::O_STAGE;
+  constexpr bool Q_FREE_EARLY = C::O_STAGE || DIRECT;  // by the issuer, not the store
   __shared__ uint64_t v_tail;  // PK: V of a sequence's ragged last key tile landed
   int U = p.units;
   const int G = static_cast<int>(gridDim.x);
@@ -736,7 +769,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         // that: otherwise q_free_t could run two phases ahead of the Q
         // producer's parity wait on it.
         if (!wait_bar(q_full + C::QB * t + qbuf(k), qpar(k))) break;
-        if (nt == 0 && C::O_STAGE && lane == 0) mbar_arrive(q_free + C::QB * t + qbuf(k));
+        if (nt == 0 && Q_FREE_EARLY && lane == 0) mbar_arrive(q_free + C::QB * t + qbuf(k));
         // Q_t of this unit (descriptor low word)
         const uint32_t q_lo_u = q_lo + static_cast<uint32_t>((qbuf(k) * Q_TILES * C::TILE_BYTES) >> 4);
 
@@ -759,7 +792,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           // the unit's last score MMA: Q_t is free once it (and all before it)
           // completed, and the other issuer may start the next unit
           if (jj == nt - 1) {
-            if (C::O_STAGE && issuer()) mma_commit(q_free + C::QB * t + qbuf(k));
+            if (Q_FREE_EARLY && issuer()) mma_commit(q_free + C::QB * t + qbuf(k));
             if (C::UNIT_DONE_EARLY && issuer()) mma_commit(unit_done);
           }
           issued_any = true;
@@ -1087,9 +1120,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         if (storer) bulk_wait_group_read_all();
         named_bar_sync(1 + t, 128);
       }
-      // (In a packed batch a tile without rows waits for its Q phase as well: the store's thread arrives on q_free for
-      // every unit, and without that wait a run of such units would carry it phases ahead of the Q producer.)
-      if (ok && (active || (PK && !C::O_STAGE)) && (n > 0 || !C::O_STAGE)) {
+      if (ok && active && (n > 0 || !Q_FREE_EARLY)) {
         ok = (n > 0) ? mbar_wait(o_done + t, static_cast<uint32_t>((ct + n - 1) & 1), lim, p.status, abort_flag)
                      : mbar_wait(q_full + C::QB * t + qbuf(k), qpar(k), lim, p.status, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
@@ -1100,11 +1131,13 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
       if (C::O_STAGE && k > 0) named_bar_sync(1 + t, 128);
       if (ok && active) {
         const float inv = (l > 0.f) ? p.o_scale / l : 0.f;  // o_scale: the v descale (1 for bf16)
-        // a packed tile that the next sequence's rows share is written row by row
-        const bool by_rows = PK && r0 + BLOCK_M > Nq;
+        // (a packed tile that the next sequence's rows share is always written row by row)
+        const bool by_rows = DIRECT || (PK && r0 + BLOCK_M > Nq);
+        // first of the four rows whose lanes trade pieces (put_rows), at this lane's 16 bytes of a 64-byte stretch
         uint8_t* orow = nullptr;
         if constexpr (PK)
-          orow = static_cast<uint8_t*>(p.o) + 2 * ((w.q_off + qi) * static_cast<long long>(pk.ost) + bh * static_cast<long long>(pk.osh));
+          orow = static_cast<uint8_t*>(p.o) + (lane & 3) * 16 +
+                 2 * ((w.q_off + (qi & ~3)) * static_cast<long long>(pk.ost) + bh * static_cast<long long>(pk.osh));
         const uint32_t srow = smem_u32(sO) + static_cast<uint32_t>(row) * 128u;
 #pragma unroll
         for (int ch = 0; ch < D / 32; ++ch) {
@@ -1119,15 +1152,14 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           uint32_t ow[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) ow[i] = pack_bf16x2(u2f(o[2 * i]) * inv, u2f(o[2 * i + 1]) * inv);
+          if (by_rows) {
+            if constexpr (PK) put_rows(ow, lane, orow + ch * 64, 2 * static_cast<long long>(pk.ost), Nq - (qi & ~3));
+          } else {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int c = ch * 4 + v;  // 16-byte chunk of the row: box c / 8, chunk c % 8 of the box
-            const uint32_t a = srow + static_cast<uint32_t>((c >> 3) * C::O_BOX_BYTES) +
-                               (static_cast<uint32_t>((c & 7) ^ (row & 7)) << 4);
-            if (by_rows) {
-              if (qi < Nq)
-                *reinterpret_cast<uint4*>(orow + c * 16) = make_uint4(ow[4 * v], ow[4 * v + 1], ow[4 * v + 2], ow[4 * v + 3]);
-            } else {
+            for (int v = 0; v < 4; ++v) {
+              const int c = ch * 4 + v;  // 16-byte chunk of the row: box c / 8, chunk c % 8 of the box
+              const uint32_t a = srow + static_cast<uint32_t>((c >> 3) * C::O_BOX_BYTES) +
+                                 (static_cast<uint32_t>((c & 7) ^ (row & 7)) << 4);
               st_shared_v4(a, ow[4 * v], ow[4 * v + 1], ow[4 * v + 2], ow[4 * v + 3]);
             }
           }
@@ -1139,20 +1171,22 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           p.lse[lse_at] =
               (l > 0.f) ? (m + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
       }
-      fence_proxy_async_smem();
-      named_bar_sync(1 + t, 128);  // every thread of the tile, every unit, on every path
-      if (storer && *abort_flag == 0) {
-        if (PK ? active && r0 + BLOCK_M <= Nq : active && r0 < p.Nq) {
-          int o_row = r0;
-          if constexpr (PK) o_row += w.q_off;
+      if constexpr (!DIRECT) {
+        fence_proxy_async_smem();
+        named_bar_sync(1 + t, 128);  // every thread of the tile, every unit, on every path
+        if (storer && *abort_flag == 0) {
+          if (PK ? active && r0 + BLOCK_M <= Nq : active && r0 < p.Nq) {
+            int o_row = r0;
+            if constexpr (PK) o_row += w.q_off;
 #pragma unroll
-          for (int b = 0; b < C::NBOX_O; ++b)
-            if (dbg_tma_ok(p.dbg, DBG_STORE_O, 64 * b, o_row, bh, D, PK ? pk.total_q : p.Nq, PK ? p.H : p.B * p.H, 2))
-              tma_store_3d(&tmO, sO + b * C::O_BOX_BYTES, 64 * b, o_row, bh);
-          bulk_commit_group();
-          if (!(C::O_STAGE && FA_LATE_STORE_WAIT)) bulk_wait_group_read_all();
+            for (int b = 0; b < C::NBOX_O; ++b)
+              if (dbg_tma_ok(p.dbg, DBG_STORE_O, 64 * b, o_row, bh, D, PK ? pk.total_q : p.Nq, PK ? p.H : p.B * p.H, 2))
+                tma_store_3d(&tmO, sO + b * C::O_BOX_BYTES, 64 * b, o_row, bh);
+            bulk_commit_group();
+            if (!(C::O_STAGE && FA_LATE_STORE_WAIT)) bulk_wait_group_read_all();
+          }
+          if (!C::O_STAGE) mbar_arrive(q_free + C::QB * t + qbuf(k));
         }
-        if (!C::O_STAGE) mbar_arrive(q_free + C::QB * t + qbuf(k));
       }
       ct += n;
     }
