@@ -394,9 +394,9 @@ __device__ __forceinline__ PackedUnit packed_unit_info(const PrefillParams& p, c
 // neighbouring bytes of one row at a time, not 16 bytes of four rows: the lanes
 // of a group of four trade 16-byte pieces, a 4x4 transpose in two steps. `dst`
 // is the group's first row at this lane's piece; `left` rows of it exist. Every
-// lane of the warp takes part. (One row a lane, 16 bytes of 32 rows an
-// instruction, cost more than staging through the Q buffer: 95 against 93 us for
-// eight sequences of 200-2048 rows.)
+// lane of the warp takes part. (Eight sequences of 200-2048 rows, d = 128: 87
+// us; staged through the Q buffer 93; one row a lane, 16 bytes of 32 rows an
+// instruction, 95.)
 __device__ __forceinline__ void put_rows(uint32_t (&w)[16], int lane, uint8_t* dst, long long row_bytes, int left) {
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -1372,9 +1372,9 @@ static cudaError_t launch_packed_t(const CUtensorMap& tq, const CUtensorMap& tk,
   if (e != cudaSuccess) return e;
   // At d = 128 a CTA for every unit, handed out as CTAs finish, where there are
   // few units an SM (six sequences of up to 1024 queries, 440 units: 127 against
-  // 133 us); with more, one CTA an SM walking many, which spares the set-up of
-  // short units (eight of 200-2048, 1024 units: 93 against 101 us; two of
-  // 7000-8192, 1968 units: 767 against 780 us).
+  // 132 us); with more, one CTA an SM walking many, which spares the set-up of
+  // short units (eight of 200-2048, 1024 units: 87 against 99 us; two of
+  // 7000-8192, 1968 units: 760 against 782 us).
   const long long units = static_cast<long long>(plan.max_entries) * pk.head_units;
   const bool persist = D == 64 || units > 4LL * p.max_ctas;
   cudaLaunchConfig_t cfg{};
