@@ -434,7 +434,8 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
   const int start = L - n;
   const int page0 = (start >> p.page_shift) + i;                 // this block's page of the sequence
   const long long first = static_cast<long long>(page0) << p.page_shift;
-  if (n == 0 || L == 0 || first >= L) return;                    // (uniform over the block)
+  // (uniform over the block; blocks below the first sequence's, where tokens come before it, have i < 0)
+  if (n == 0 || L == 0 || i < 0 || first >= L) return;
   const int r0 = start > first ? start - static_cast<int>(first) : 0;           // its new rows r0 .. r1 - 1
   const int r1 = static_cast<int>(L - first < p.page ? L - first : p.page);
   const int nrows = r1 - r0;

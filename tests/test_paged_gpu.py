@@ -240,6 +240,44 @@ def test_padded_batch(fa, ragged):
     assert (o2 - o[[1, 3]]).abs().max() <= 2e-2 and (l2 - lse[[1, 3]]).abs().max() <= 2e-3
 
 
+def test_tokens_before_the_first_sequence(fa):
+    """Offsets that do not start at 0: the tokens before the first sequence are nobody's. Sequences that begin inside a
+    page whose scale was never set keep to their own rows, and the page before it is not touched."""
+    H, Hkv, d, page, skip = 2, 1, 64, 16, 100
+    rng = np.random.default_rng(15)
+    new, lens = [20, 3], [41, 40]
+    cu = [skip, skip + 20, skip + 23]
+    table = np.array([[3, 1, 4], [5, 0, 2]], dtype=np.int32)
+    cache = Cache(rng, 6, Hkv, page, d, True)
+    for s in cache.scale:
+        s.fill_(float("nan"))
+    codes, sc = cache.codes(1), cache.scales(1)
+    x = torch.randn(150, H + 2 * Hkv, d, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    qo = torch.full((150, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    fa.append_paged(x[:, :H], x[:, H:H + 1], x[:, H + 1:], *cache.gpu, cuda(table), cuda(lens, torch.int32),
+                    cu_seqlens=cuda(cu, torch.int32), max_new=20, q_out=qo, **cache.kw())
+    # without max_new as well: the blocks are then found through the offsets
+    qo2 = torch.full((150, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    fa.append_paged(x[:, :H], x[:, H:H + 1], x[:, H + 1:], *cache.gpu, cuda(table), cuda(lens, torch.int32),
+                    cu_seqlens=cuda(cu, torch.int32), q_out=qo2, **cache.kw())
+    assert fa.device_status() == fa.FA_OK
+    live = slice(skip, skip + 23)
+    assert torch.equal(qo, qo2) and torch.equal(qo[live], x[live, :H])
+    assert (qo[:skip] == 7).all() and (qo[skip + 23:] == 7).all()
+    with np.errstate(invalid="ignore"):
+        sc = np.where(np.isnan(sc), 0.0, sc)            # no scale yet: any new one replaces it, held codes stay
+        ref = codes.copy()
+        OP.store_e4m3(to64(x[live, H + 1:]), new, lens, table, page, codes, sc)
+    got = cache.codes(1)
+    fresh = np.zeros(codes.shape, dtype=bool)
+    for b, (n, L) in enumerate(zip(new, lens)):
+        for p in range(L - n, L):
+            fresh[table[b][p // page], :, p % page] = True
+    assert np.array_equal(got[fresh], codes[fresh]) and np.array_equal(got[~fresh], ref[~fresh])
+    untouched = [3, 5, 0]                               # pages before the sequences' first new rows
+    assert np.isnan(to64(cache.scale[1])[untouched]).all()
+
+
 def test_append_scale_growth_and_odd_values(fa):
     """Token by token into one e4m3 page: the scale follows the largest value so far; infinities and NaN become the NaN
     code and leave the scale alone; an all-zero page has the least scale; a page that starts over forgets its old one."""
