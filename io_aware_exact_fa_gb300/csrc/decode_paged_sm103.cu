@@ -136,9 +136,10 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
   const int range = worker / p.row_tiles;
   long long sum = 0;
   bool clipped = false;
+#pragma unroll 4
   for (int b = lane; b < p.B; b += 32) {
-    const int L = dp_len(p, b);
-    clipped = clipped || L != __ldg(p.seqlens + b);
+    const int raw = __ldg(p.seqlens + b), L = paged_clip_len(raw, p.max_len);
+    clipped = clipped || L != raw;
     sum += (L + C::KS - 1) / C::KS;
   }
 #pragma unroll
