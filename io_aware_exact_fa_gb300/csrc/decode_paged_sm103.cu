@@ -74,7 +74,7 @@ struct DpCfg {
   // Tiles in each warp's ring: what fits beside the warps an SM holds. (Three tiles for eight warps against two for
   // twelve: 136 against 130 us at 8 rows, e4m3, d = 128. Tiles of half the size, four to a ring: 134. Sixteen warps
   // of those: 133.)
-  static constexpr int DP_STAGES = decode_paged_ctas(D, ROWS) == 3 ? 2 : 3;
+  static constexpr int DP_STAGES = decode_paged_ctas(D, F8, ROWS) == 3 ? 2 : 3;
   static constexpr int RING = DP_WARPS * DP_STAGES * STAGE;
   static constexpr int META_OFF = RING;
   static constexpr int SMEM = RING + DP_WARPS * DP_STAGES * META;
@@ -121,7 +121,7 @@ __device__ __forceinline__ int dp_len(const DecodePagedParams& p, int b) {
 }  // namespace
 
 template <int D, bool F8, int NR>
-__global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_decode_paged_kernel(const DecodePagedParams p) {
+__global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) fa_decode_paged_kernel(const DecodePagedParams p) {
   using C = DpCfg<D, F8, NR>;
   extern __shared__ __align__(128) uint8_t dp_smem[];
   const uint32_t sbase = smem_u32(dp_smem);

@@ -58,9 +58,12 @@ struct DecodePagedParams {
 
 // Query rows of one warp of the paged decode: 8 where a K/V head has that few, else 16.
 __host__ __device__ constexpr int decode_paged_rows(int R) { return R <= 8 ? 8 : 16; }
-// Blocks of four such warps that an SM holds: three, but two where 16 rows of 128 values each leave no registers for
-// more (e4m3, d = 64, 16 rows: 47 against 53 us with two; d = 128: 114 against 117 us the other way).
-__host__ __device__ constexpr int decode_paged_ctas(int d, int rows) { return rows == 16 && d == 128 ? 2 : 3; }
+// Blocks of four such warps that an SM holds: three, but two at 16 rows of 128 bf16 values (48 sequences, 4 tokens of
+// 32/8 heads: 115 against 117 us; e4m3, where conversions keep the warps waiting, 74 against 76 us the other way, and 47
+// against 53 us at d = 64).
+__host__ __device__ constexpr int decode_paged_ctas(int d, bool f8, int rows) {
+  return rows == 16 && d == 128 && !f8 ? 2 : 3;
+}
 
 struct AppendPagedParams {
   const void* q;             // bf16, element strides of token and head; d contiguous
