@@ -48,13 +48,13 @@ namespace fa {
 
 namespace {
 
-constexpr int AP_THREADS = 256;        // of a block where a page gets many rows, else AP_STEP_THREADS
-constexpr int AP_STEP_THREADS = 64;
+constexpr int AP_THREADS = 256;        // of a block, at most
+constexpr int AP_STEP_THREADS = 64;    // and at least
+// Blocks of AP_THREADS that an SM should hold: four where 64 registers do without spilling (interleaved, bf16 cache:
+// 32 against 34 us for 9.1k tokens of 28 heads), else three (half layout: 111 against 121 us for 26.7k prompt tokens).
+constexpr int ap_ctas(bool f8, bool inter) { return !f8 && inter ? 4 : 3; }
 #ifndef AP_RING
 #define AP_RING 3       // heads of a row whose copies a query thread has in flight
-#endif
-#ifndef AP_CTAS
-#define AP_CTAS 3       // blocks an SM should hold
 #endif
 
 // A unit's 16 elements as four fp32 pairs a (first of each rotation pair) and four
@@ -591,7 +591,7 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
 }  // namespace
 
 template <int D, bool F8, bool INTER>
-__global__ void __launch_bounds__(AP_THREADS, AP_CTAS) fa_append_paged_kernel(const AppendPagedParams p) {
+__global__ void __launch_bounds__(AP_THREADS, ap_ctas(F8, INTER)) fa_append_paged_kernel(const AppendPagedParams p) {
   extern __shared__ __align__(16) uint4 ap_stash[];  // 16-byte pieces, one of each thread next to one another
   __shared__ int s_pos[AP_THREADS / (D / 16)];
   __shared__ unsigned int s_amax[2];
@@ -625,9 +625,10 @@ cudaError_t append_paged_set_attributes() {
 
 template <int D, bool F8, bool INTER>
 static cudaError_t ap_launch(AppendPagedParams p, cudaStream_t stream) {
-  // A step of a few tokens a sequence gives every page a few rows: small blocks, so that an SM holds many of them (256
-  // sequences of one token, 8 K/V heads: 21 us with 256 threads).
-  const int threads = p.max_rows <= AP_STEP_THREADS / (D / 16) ? AP_STEP_THREADS : AP_THREADS;
+  // As many threads as a page's new rows occupy, so that an SM holds many blocks of small pages or short steps (256
+  // sequences of one token, 8 K/V heads: 8 us, 21 with 256 threads; 26.7k prompt tokens into pages of 16: 125 us, 170).
+  int threads = AP_STEP_THREADS;
+  while (threads < AP_THREADS && threads < p.max_rows * (D / 16)) threads *= 2;
   const int groups = threads / (D / 16);
   // Heads side by side in a query block: few where many rows fill the GPU anyway (a row's angles are computed once a
   // slot), many for a short step: slots are added until q_blocks_wanted blocks run. (Six an SM: 115 us for 26.7k prompt
