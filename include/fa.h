@@ -350,8 +350,9 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
  *   q_out  bf16 [T, H, d]; may be q.   k_out  bf16 [T, Hkv, d], the turned keys
  *      (for attention among the new tokens), or NULL; may be k.
  *   strides  int64 [10], host memory: token and head strides, in elements, of q,
- *      k, v, q_out, k_out in that order (multiples of 8; the d elements of a
- *      head are contiguous), so q, k and v can be parts of one projection.
+ *      k, v, q_out, k_out in that order (multiples of 8, those of outputs not 0;
+ *      the d elements of a head are contiguous), so q, k and v can be parts of one
+ *      projection.
  *   max_new  the most new tokens of one sequence when cu_seqlens is given (0:
  *      not known; sequences with more are clipped and reported).
  * k and v go to the row of their position, in bf16 or as e4m3 codes. The scale
@@ -386,8 +387,8 @@ size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int 
  * new ones among them; token t sees key j iff j <= L_b - Nq + t; query head h
  * reads K/V head h / (H/Hkv). A token that sees no key gets o = 0, lse = -inf.
  *   q, o       bf16 [B, H, Nq, d] with element strides q_strides, o_strides
- *              (int64 [3], host memory: batch, head, token; multiples of 8; d
- *              contiguous). Token-major tensors, as fa_append_paged returns them,
+ *              (int64 [3], host memory: batch, head, token; multiples of 8, of o not
+ *              0; d contiguous). Token-major tensors, as fa_append_paged returns them,
  *              are passed by their strides.
  *   lse        fp32 [B, H, Nq] (may be NULL)
  *   max_len    no sequence is longer (at most the positions a block-table row

@@ -859,8 +859,11 @@ fa_status check_pool(const void* k_pages, const void* v_pages, const float* k_sc
 }
 
 // Element strides of a strided operand: multiples of 8 (16-byte rows), not
-// negative; that of a dimension of one element does not matter.
-bool stride_ok(int64_t stride, int extent) { return extent <= 1 || (stride >= 0 && stride % 8 == 0); }
+// negative (of an output: not zero either, where every element has its own
+// place); that of a dimension of one element does not matter.
+bool stride_ok(int64_t stride, int extent, bool output) {
+  return extent <= 1 || (stride >= (output ? 8 : 0) && stride % 8 == 0);
+}
 
 }  // namespace
 
@@ -896,8 +899,8 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
   if (table_stride < table_width && B > 1) return fail(FA_ERR_INVALID_ARG, "table_stride is below table_width");
   for (int i = 0; i < 10; ++i) {  // token and head strides of q, k, v, q_out, k_out
     const int heads = (i == 1 || i == 7) ? H : Hkv;
-    if ((i < 8 || k_out) && !stride_ok(strides[i], (i & 1) ? heads : T))
-      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements and >= 0");
+    if ((i < 8 || k_out) && !stride_ok(strides[i], (i & 1) ? heads : T, i >= 6))
+      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements, >= 0, of outputs > 0");
   }
   const int n_max = cu_seqlens == nullptr ? T / B : std::min(max_new > 0 ? max_new : T, T);
   const long long rect = (static_cast<long long>(n_max) + page - 2) / page + 1;
@@ -957,8 +960,8 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   if (!aligned(q, 16) || !aligned(o, 16)) return fail(FA_ERR_UNSUPPORTED, "q and o must be 16-byte aligned");
   const int extent[3] = {B, H, Nq};
   for (int i = 0; i < 3; ++i)
-    if (!stride_ok(q_strides[i], extent[i]) || !stride_ok(o_strides[i], extent[i]))
-      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements and >= 0");
+    if (!stride_ok(q_strides[i], extent[i], false) || !stride_ok(o_strides[i], extent[i], true))
+      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements, >= 0, of outputs > 0");
   if (lse && !aligned(lse, 4)) return fail(FA_ERR_UNSUPPORTED, "lse must be 4-byte aligned");
   if (B > 1 && table_stride < (static_cast<int64_t>(max_len) + page - 1) / page)
     return fail(FA_ERR_INVALID_ARG, "max_len needs %lld pages a sequence, table_stride is %lld",

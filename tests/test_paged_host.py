@@ -48,6 +48,7 @@ def _append(fa, **kw):
     (dict(q=P + 2), UNSUPPORTED), (dict(k_out=P + 8), UNSUPPORTED), (dict(v_pages=P + 8), UNSUPPORTED),
     (dict(turns=P + 4), UNSUPPORTED), (dict(table=P + 2), UNSUPPORTED), (dict(qw=P + 8), UNSUPPORTED),
     (dict(strides=[512, 60] + [512, 64] * 4), UNSUPPORTED), (dict(strides=[512, -64] + [512, 64] * 4), UNSUPPORTED),
+    (dict(strides=[512, 64] * 3 + [512, 0] + [512, 64]), UNSUPPORTED), (dict(strides=[512, 64] * 4 + [0, 64]), UNSUPPORTED),
     (dict(T=0, q=None, k=None, v=None, q_out=None), 0),
 ])
 def test_append_refusals(fa, kw, want):
@@ -72,6 +73,7 @@ def _decode(fa, **kw):
     (dict(e4m3=1), INVALID), (dict(stride=62), INVALID), (dict(d=32), UNSUPPORTED), (dict(Nq=33), UNSUPPORTED),
     (dict(H=1 << 20, Nq=1 << 20), UNSUPPORTED), (dict(page=8), UNSUPPORTED), (dict(q=P + 8), UNSUPPORTED),
     (dict(o=P + 4), UNSUPPORTED), (dict(lse=P + 2), UNSUPPORTED), (dict(qs=[512, 64, 65], Nq=2), UNSUPPORTED),
+    (dict(os=[512, 0, 64]), UNSUPPORTED),
     (dict(k=P + 8), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws=P + 16), WORKSPACE), (dict(bytes=64), WORKSPACE),
 ])
 def test_decode_refusals(fa, kw, want):
