@@ -632,7 +632,7 @@ static cudaError_t ap_launch(AppendPagedParams p, cudaStream_t stream) {
   const int groups = threads / (D / 16);
   // Heads side by side in a query block: few where many rows fill the GPU anyway (a row's angles are computed once a
   // slot), many for a short step: slots are added until q_blocks_wanted blocks run. (Six an SM: 115 us for 26.7k prompt
-  // tokens, 34 us for 9.1k of 28 heads; four an SM 117 and 34, twelve 121 and 38.)
+  // tokens, 32 us for 9.1k of 28 heads; four an SM 117 and 32, eight 115 and 35.)
   int slots = 1;
   while (slots < groups && slots < p.H && static_cast<long long>(p.T) * slots < static_cast<long long>(groups) * p.q_blocks_wanted)
     slots *= 2;
