@@ -396,13 +396,16 @@ size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int 
  *   num_splits 0: the keys of the whole batch are shared out in equal ranges, one
  *              for each warp that the GPU holds, whatever the lengths;
  *              1 .. 1024: in so many ranges a sequence and K/V head on average.
- *   scales of e4m3 pages: any finite positive factors (fa_append_paged writes
- *              powers of two, which add no rounding).
+ *   scales of e4m3 pages: positive factors, powers of two (as fa_append_paged
+ *              writes them) or not; those of v between 2^-80 and 2^120. Pages of one
+ *              sequence may differ by 2^80: each keeps its own values' precision.
  *   workspace  device memory of fa_decode_paged_workspace_size() bytes, 256-byte
  *              aligned, owned by the caller, overwritten; calls that may overlap
  *              on the GPU need their own.
- * Products with e4m3 pages run in f16 on the codes, with fp32 accumulation and
- * the weights rounded to f16; with bf16 pages in bf16. A NaN or infinity in v
+ * Products with e4m3 pages run in f16 on the codes, with fp32 accumulation, the
+ * weights rounded to f16 (below 2^-14 of a row's largest to 2^-25 of it) and q held
+ * in f16 (elements below 2^-14 of a row's largest to 2^-25 of it); with bf16 pages
+ * in bf16. A NaN or infinity in v
  * reaches the rows of its sequence's last Nq tokens. Errors as for
  * fa_decode_grouped. Two launches (the ranges, their merge). */
 fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,

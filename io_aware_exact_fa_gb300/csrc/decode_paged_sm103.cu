@@ -11,9 +11,11 @@
 // running base M = max z_j,
 //     W_j = 2^(z_j - M),  O = sum_j W_j V~_j / sum_j (W_j / c_j),
 //     lse = ln 2 (M + log2 sum_j (W_j / c_j)),
-// (M may lag behind by 2^8) so the value products run on the codes themselves, whatever the pages' scales
-// are to one another, and neither sum can overflow (append writes powers of two,
-// for which W_j / c_j and the shift by log2 c are exact).
+// (M may lag behind, see DpBase) so the value products run on the codes themselves
+// (append writes powers of two, for which W_j / c_j and the shift by log2 c are
+// exact). W is rounded to f16 for the product, which would cost pages of small
+// values their weights' bits beside a page of large ones: groups of keys whose scale
+// lies far below the largest count their weights from a base of their own (`far`).
 //
 // What bounds it: HBM. Each key and value is read once per K/V head; at 6.8 TB/s
 // an SM takes about 24 bytes a clock, 24 e4m3 codes. The work per code has to
@@ -45,6 +47,8 @@
 // bank once.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "mma_sync.cuh"
 #include "paged.cuh"
 
@@ -54,7 +58,14 @@ namespace {
 
 constexpr int DP_WARPS = 4;
 constexpr int DP_THREADS = 32 * DP_WARPS;
-constexpr float DP_RESCALE_LOG2 = 8.f; // the base moves when a score passes it by more than this
+
+// Where the weights 2^(z - M) lie: the base M is set so that a row's largest z is TOP above it, and moves when one passes
+// it by more than LIMIT. bf16 weights have fp32's exponents; f16 ends at 2^16, and its weights lie as high as that allows,
+// to leave room below for pages whose scales are smaller, up to 2^-GAP times (see `far`).
+template <bool F8>
+struct DpBase {
+  static constexpr float TOP = F8 ? 7.f : 0.f, LIMIT = F8 ? 15.f : 8.f, GAP = TOP;
+};
 
 template <int D, bool F8, int NR>
 struct DpCfg {
@@ -74,7 +85,7 @@ struct DpCfg {
   // Tiles in each warp's ring: what fits beside the warps an SM holds. (Three tiles for eight warps against two for
   // twelve: 136 against 130 us at 8 rows, e4m3, d = 128. Tiles of half the size, four to a ring: 134. Sixteen warps
   // of those: 133.)
-  static constexpr int DP_STAGES = decode_paged_ctas(D, F8, ROWS) == 3 ? 2 : 3;
+  static constexpr int DP_STAGES = decode_paged_ctas(D, ROWS) == 3 ? 2 : 3;
   static constexpr int RING = DP_WARPS * DP_STAGES * STAGE;
   static constexpr int META_OFF = RING;
   static constexpr int SMEM = RING + DP_WARPS * DP_STAGES * META;
@@ -121,7 +132,7 @@ __device__ __forceinline__ int dp_len(const DecodePagedParams& p, int b) {
 }  // namespace
 
 template <int D, bool F8, int NR>
-__global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) fa_decode_paged_kernel(const DecodePagedParams p) {
+__global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_decode_paged_kernel(const DecodePagedParams p) {
   using C = DpCfg<D, F8, NR>;
   extern __shared__ __align__(128) uint8_t dp_smem[];
   const uint32_t sbase = smem_u32(dp_smem);
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
         // The products with the codes run in f16 (every e4m3 code is an f16
         // value). The row's power of two 2^x brings its largest element to [1, 2):
         // elements down to 2^-14 of it keep all their 8 bits, smaller ones are
-        // off by at most 2^-25 of the largest, below fp32 accumulation's own error.
+        // off by at most 2^-25 of 2^x: a score by d 2^-25 max|q| max|k| at most.
         float amax = 0.f;
 #pragma unroll
         for (int j = 0; j < C::KST; ++j) {
@@ -333,6 +344,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
     const int full_lim = min(L - 1, L - p.Nq);  // every row sees the keys up to here
 
     float M[NR][2], l[NR][2];
+    [[maybe_unused]] float ev_most = -INFINITY;  // largest log2 c of the segment's pages so far
     float oacc[NR][C::KST][4];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
@@ -353,13 +365,11 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
       const uint8_t* vt = kt + C::HALF;
       const int key0 = i * C::KS;
       // ---- S^T: 16 keys x 8 rows for each group and row tile
-      float sc[C::KG][NR][4];
-#pragma unroll
-      for (int g = 0; g < C::KG; ++g) {
+      auto scores = [&](int g, float (&s)[NR][4]) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[g][n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
         for (int i2 = 0; i2 < C::NPK; ++i2) {
           const int piece = dp_k_piece<D, F8>(tig, i2);
@@ -374,42 +384,56 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
               e4m3x4_to_f16x2x2(wb[w], a1, a3);
 #pragma unroll
               for (int n = 0; n < NR; ++n)
-                mma_16816<true>(sc[g][n], a0, a1, a2, a3, qf[n][i2 * 4 + w][0], qf[n][i2 * 4 + w][1]);
+                mma_16816<true>(s[n], a0, a1, a2, a3, qf[n][i2 * 4 + w][0], qf[n][i2 * 4 + w][1]);
             }
           } else {
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
               for (int n = 0; n < NR; ++n)
-                mma_16816<false>(sc[g][n], wa[2 * w], wb[2 * w], wa[2 * w + 1], wb[2 * w + 1], qf[n][i2 * 2 + w][0],
+                mma_16816<false>(s[n], wa[2 * w], wb[2 * w], wa[2 * w + 1], wb[2 * w + 1], qf[n][i2 * 2 + w][0],
                                  qf[n][i2 * 2 + w][1]);
           }
         }
-      }
+      };
+      float sc[C::KG][NR][4];
+#pragma unroll
+      for (int g = 0; g < C::KG; ++g) scores(g, sc[g]);
 
       // ---- z - M for z = y + log2 c, in packed fp32 pairs (rows 2tig and 2tig + 1). The base M moves only when a row
-      // passes it by 2^8; a row without one yet (M = -inf) counts from 0 and takes its first.
-      float rv[C::KG];
+      // passes it by more than LIMIT; a row without one yet (M = -inf) counts from 0 and takes its first.
+      float ka[C::KG], ev[C::KG], rv[C::KG];
+      [[maybe_unused]] uint32_t far = 0u;
+      if constexpr (F8) {
+#pragma unroll
+        for (int g = 0; g < C::KG; ++g) {
+          const float2 ac = *reinterpret_cast<const float2*>(my_meta + slot * C::META + g * 8);
+          ka[g] = ac.x;
+          ev[g] = lg2_approx(ac.y);
+          rv[g] = __fdividef(1.f, ac.y);
+          if (ac.x > 0.f) ev_most = fmaxf(ev_most, ev[g]);  // (a group without keys has a = 0)
+        }
+        // A page's scale is in its keys' exponents, so pages of small values have small weights, and f16 keeps a weight's
+        // bits down to 2^-14. With E = ev_most the base is at most max_j (y_j + log2 c_j) - TOP <= max y + E - TOP, hence
+        // z_j - M >= (y_j - max y) - (E - log2 c_j) + TOP: up to GAP = TOP below E a page's scale costs its weights nothing.
+        // A group further below (rare: values of two pages that differ more than 100-fold) is left out here and has its
+        // turn after the others, with weights that count from its own largest.
+#pragma unroll
+        for (int g = 0; g < C::KG; ++g)
+          if (ka[g] > 0.f && ev[g] < ev_most - DpBase<F8>::GAP) far |= 1u << g;  // (the same in every lane)
+      }
       float mx[NR][2];
 #pragma unroll
       for (int n = 0; n < NR; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-      const uint32_t hid = (hidden >> (4u * (done & 7u))) & 0xfu;
+      const uint32_t hid = ((hidden >> (4u * (done & 7u))) & 0xfu) | far;
       const bool need_mask = key0 + C::KS - 1 > full_lim || hid != 0u;
 #pragma unroll
       for (int g = 0; g < C::KG; ++g) {
-        float ka = 1.f, ev = 0.f;
-        rv[g] = 1.f;
-        if constexpr (F8) {
-          const float2 ac = *reinterpret_cast<const float2*>(my_meta + slot * C::META + g * 8);
-          const float c = ac.y;
-          ka = ac.x;
-          ev = lg2_approx(c);
-          rv[g] = __fdividef(1.f, c);
-        }
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-          const uint64_t c2 = F8 ? f2pack(c1[n][0] * ka, c1[n][1] * ka) : f2pack(c1[n][0], c1[n][1]);
-          const uint64_t b2 = f2pack(ev - base_of(M[n][0]), ev - base_of(M[n][1]));
+          const uint64_t c2 = F8 ? f2pack(c1[n][0] * ka[g], c1[n][1] * ka[g]) : f2pack(c1[n][0], c1[n][1]);
+          const float e0 = F8 ? ev[g] : 0.f;
+          const uint64_t b2 = f2pack(e0 - base_of(M[n][0]), e0 - base_of(M[n][1]));
           float(&z)[4] = sc[g][n];
           f2unpack(ffma2(f2pack(z[0], z[1]), c2, b2), z[0], z[1]);
           f2unpack(ffma2(f2pack(z[2], z[3]), c2, b2), z[2], z[3]);
@@ -429,7 +453,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          over = over || mx[n][e] > (M[n][e] == -INFINITY ? -INFINITY : DP_RESCALE_LOG2);
+          over = over || mx[n][e] > (M[n][e] == -INFINITY ? -INFINITY : DpBase<F8>::LIMIT);
       if (__any_sync(ALL, over)) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -440,6 +464,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
             up = fmaxf(up, __shfl_xor_sync(ALL, up, 8));
             up = fmaxf(up, __shfl_xor_sync(ALL, up, 16));
             const bool none = M[n][e] == -INFINITY;
+            up -= DpBase<F8>::TOP;
             if (none) M[n][e] = up;                 // (still -inf when this tile shows the row nothing)
             else M[n][e] += up = fmaxf(up, 0.f);    // the base only rises
             up = up == -INFINITY ? 0.f : up;
@@ -472,8 +497,9 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
           pf[g][n][1] = movmatrix_trans(F8 ? pack_f16x2(w2, w3) : pack_bf16x2(w2, w3));
         }
       // ---- O^T += V^T W^T
-#pragma unroll
-      for (int g = 0; g < C::KG; ++g) {
+      // (FAR: times f for each row)
+      auto product = [&](int g, const uint32_t (&w)[NR][2], auto far_group, const float (&f)[NR][2]) {
+        constexpr bool FAR = decltype(far_group)::value;
         const uint32_t r0 = 16 * g + 2 * tig;
         if constexpr (F8) {
           constexpr int NW32 = D / 32;  // 32-bit words of the lane's codes: 4 or 2
@@ -494,9 +520,9 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
             }
           }
 #pragma unroll
-          for (int w = 0; w < NW32; ++w) {
-            const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-            const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+          for (int x = 0; x < NW32; ++x) {
+            const uint32_t x0 = __byte_perm(v[0][x], v[1][x], 0x5140), x1 = __byte_perm(v[0][x], v[1][x], 0x7362);
+            const uint32_t y0 = __byte_perm(v[2][x], v[3][x], 0x5140), y1 = __byte_perm(v[2][x], v[3][x], 0x7362);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t xa = h ? x1 : x0, ya = h ? y1 : y0;
@@ -504,7 +530,17 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
               e4m3x4_to_f16x2x2(xa, a0, a1);
               e4m3x4_to_f16x2x2(ya, a2, a3);
 #pragma unroll
-              for (int n = 0; n < NR; ++n) mma_16816<true>(oacc[n][2 * w + h], a0, a1, a2, a3, pf[g][n][0], pf[g][n][1]);
+              for (int n = 0; n < NR; ++n) {
+                float(&o)[4] = oacc[n][2 * x + h];
+                if constexpr (FAR) {
+                  float t[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma_16816<true>(t, a0, a1, a2, a3, w[n][0], w[n][1]);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[e] = fmaf(t[e], f[n][e & 1], o[e]);
+                } else {
+                  mma_16816<true>(o, a0, a1, a2, a3, w[n][0], w[n][1]);
+                }
+              }
             }
           }
         } else {
@@ -520,14 +556,56 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, F8, 8 * NR)) 
               v[q][3] = y.w;
             }
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
-              const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t a0 = __byte_perm(v[0][x], v[1][x], 0x5410), a1 = __byte_perm(v[0][x], v[1][x], 0x7632);
+              const uint32_t a2 = __byte_perm(v[2][x], v[3][x], 0x5410), a3 = __byte_perm(v[2][x], v[3][x], 0x7632);
 #pragma unroll
               for (int n = 0; n < NR; ++n)
-                mma_16816<false>(oacc[n][4 * hp + w], a0, a1, a2, a3, pf[g][n][0], pf[g][n][1]);
+                mma_16816<false>(oacc[n][4 * hp + x], a0, a1, a2, a3, w[n][0], w[n][1]);
             }
           }
+        }
+      };
+#pragma unroll
+      for (int g = 0; g < C::KG; ++g) product(g, pf[g], std::false_type{}, M);
+      // ---- the groups left out: with u a row's largest z in the group, W = 2^(u - M) W', W' = 2^(z - u)
+      if constexpr (F8) {
+        // (told to be rare: d = 64 spills otherwise)
+        if (__builtin_expect(far != 0u, 0)) for (uint32_t rest = far; rest != 0u; rest &= rest - 1u) {
+          const int g = __ffs(rest) - 1;
+          const float2 ac = *reinterpret_cast<const float2*>(my_meta + slot * C::META + g * 8);
+          const float lc = lg2_approx(ac.y);
+          float z[NR][4], f[NR][2];
+          uint32_t w[NR][2];
+          scores(g, z);
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = key0 + 16 * g + gid;
+              z[n][e] = key > lim[n][e] ? -INFINITY : fmaf(z[n][e], c1[n][e] * ac.x, lc);
+              z[n][e + 2] = key + 8 > lim[n][e] ? -INFINITY : fmaf(z[n][e + 2], c1[n][e] * ac.x, lc);
+              float u = fmaxf(z[n][e], z[n][e + 2]);
+              u = fmaxf(u, __shfl_xor_sync(ALL, u, 4));
+              u = fmaxf(u, __shfl_xor_sync(ALL, u, 8));
+              u = fmaxf(u, __shfl_xor_sync(ALL, u, 16));
+              const float m = fmaxf(M[n][e], u - DpBase<F8>::TOP), ub = base_of(u);
+              const float alpha = m == M[n][e] ? 1.f : ex2_approx(M[n][e] - m);  // (0 for a row without a base)
+              M[n][e] = m;
+              f[n][e] = ex2_approx(ub - base_of(m));
+              z[n][e] = ex2_approx(z[n][e] - ub);
+              z[n][e + 2] = ex2_approx(z[n][e + 2] - ub);
+              l[n][e] = fmaf(z[n][e] + z[n][e + 2], ex2_approx(ub - lc - base_of(m)), l[n][e] * alpha);
+#pragma unroll
+              for (int j = 0; j < C::KST; ++j) {
+                oacc[n][j][e] *= alpha;
+                oacc[n][j][e + 2] *= alpha;
+              }
+            }
+            w[n][0] = movmatrix_trans(pack_f16x2(z[n][0], z[n][1]));
+            w[n][1] = movmatrix_trans(pack_f16x2(z[n][2], z[n][3]));
+          }
+          product(g, w, std::true_type{}, f);
         }
       }
     }

@@ -815,21 +815,20 @@ int log2_of(int x) {
 // head on average.
 constexpr int PAGED_SMS = 152;
 int paged_row_tiles(int R) { return (R + fa::decode_paged_rows(R) - 1) / fa::decode_paged_rows(R); }
-int paged_ranges(int B, int Hkv, int R, int d, bool f8, int num_splits) {
+int paged_ranges(int B, int Hkv, int R, int d, int num_splits) {
   if (num_splits > 0) return static_cast<int>(std::min(static_cast<long long>(num_splits) * B * Hkv, 1LL << 20));
-  const int warps = PAGED_SMS * 4 * fa::decode_paged_ctas(d, f8, fa::decode_paged_rows(R));
+  const int warps = PAGED_SMS * 4 * fa::decode_paged_ctas(d, fa::decode_paged_rows(R));
   return std::max(1, warps / paged_row_tiles(R));
 }
 
-// Layout of the paged decode's workspace: outputs, (base, sum) pairs, range ends. One size for both types of pages:
-// e4m3's ranges, which are never fewer.
+// Layout of the paged decode's workspace: outputs, (base, sum) pairs, range ends.
 struct PagedWorkspace {
   size_t ml, ends, bytes;
 };
 PagedWorkspace paged_workspace(int B, int Hkv, int R, int d, int num_splits) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t pairs = static_cast<size_t>(B) * Hkv;
-  const size_t parts = (paged_ranges(B, Hkv, R, d, true, num_splits) + pairs) * paged_row_tiles(R) * fa::decode_paged_rows(R);
+  const size_t parts = (paged_ranges(B, Hkv, R, d, num_splits) + pairs) * paged_row_tiles(R) * fa::decode_paged_rows(R);
   PagedWorkspace w{};
   w.ml = up(parts * d * 4);
   w.ends = w.ml + up(parts * 8);
@@ -966,7 +965,7 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   if (B > 1 && table_stride < (static_cast<int64_t>(max_len) + page - 1) / page)
     return fail(FA_ERR_INVALID_ARG, "max_len needs %lld pages a sequence, table_stride is %lld",
                 (static_cast<long long>(max_len) + page - 1) / page, static_cast<long long>(table_stride));
-  const int row_tiles = paged_row_tiles(R), ranges = paged_ranges(B, Hkv, R, d, e4m3 != 0, num_splits);
+  const int row_tiles = paged_row_tiles(R), ranges = paged_ranges(B, Hkv, R, d, num_splits);
   if (static_cast<long long>(B) * H * Nq > INT_MAX - 16 ||
       static_cast<double>(B) * Hkv * max_len / 16 > 2e9 * ranges)  // (tiles of a range are counted in 32 bits)
     return fail(FA_ERR_INVALID_ARG, "B * H * Nq or B * Hkv * max_len is too large");

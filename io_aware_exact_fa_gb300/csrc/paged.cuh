@@ -60,12 +60,10 @@ struct DecodePagedParams {
 // against 124 us for 64 sequences of 4-8k, e4m3; sixteen rows in two warps of 8, which read the keys twice: 67 against 62
 // us for 48 sequences, bf16, d = 64.)
 __host__ __device__ constexpr int decode_paged_rows(int R) { return R <= 8 ? 8 : 16; }
-// Blocks of four such warps that an SM holds: three, but two at 16 rows of 128 bf16 values (48 sequences, 4 tokens of
-// 32/8 heads: 115 against 117 us; e4m3, where conversions keep the warps waiting, 74 against 76 us the other way, and 47
-// against 53 us at d = 64).
-__host__ __device__ constexpr int decode_paged_ctas(int d, bool f8, int rows) {
-  return rows == 16 && d == 128 && !f8 ? 2 : 3;
-}
+// Blocks of four such warps that an SM holds: three, but two at 16 rows of d = 128 (48 sequences, 4 tokens of 32/8 heads:
+// bf16 115 against 117 us; e4m3 76 against 97 us, where the 168 registers a thread of three blocks spill; at d = 64 two
+// blocks take 53 us, three 47).
+__host__ __device__ constexpr int decode_paged_ctas(int d, int rows) { return rows == 16 && d == 128 ? 2 : 3; }
 
 struct AppendPagedParams {
   const void* q;             // bf16, element strides of token and head; d contiguous

@@ -570,3 +570,94 @@ def test_binding_refusals(fa):
     with pytest.raises(fa.FAError):
         app(turns=torch.zeros(4, dtype=torch.int64, device="cuda"))   # rot = 8
     assert fa.device_status() == fa.FA_OK
+
+
+def _attend_bound(q, vals, table, lens, scale, ro):
+    """How far a decode over e4m3 pages may be from the exact ``ro``: half a bf16 step of the output, and of each
+    term p_j |v_j| half an f16 step of its weight (2^-11), as much again for the rounding of the sum it is divided by,
+    of the fp32 score in its exponent and of the fp32 sums."""
+    spread, _ = OP.attend(q, vals[0], np.abs(vals[1]), table, lens, scale)
+    return 2.0 ** -8 * np.abs(ro) + 2.0 ** -10 * spread
+
+
+# exponent by which one page's value scale lies above the others', and by how many nats its only visible key leads
+@pytest.mark.parametrize("span,lead", [(12, 8.0), (16, 6.0), (16, 6.5), (20, 3.5), (7, 9.0), (8, 9.0), (60, 3.0)])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("d,H,Nq", [(64, 4, 1), (64, 4, 3), (128, 4, 1), (128, 7, 2)])
+def test_decode_small_values_beside_a_large_page(fa, d, H, Nq, where, span, lead):
+    """The mass lies on pages of small values, and a page of a far larger scale, whose keys' codes are zero, has the
+    largest score: its scale must not cost the other pages' weights their bits."""
+    page, L = 16, 2000
+    P = L // page
+    rng = np.random.default_rng(span * 100 + d)
+    big = {"first": 0, "middle": P // 2, "last": P - 1}[where]
+    kv = rng.standard_normal((P, 1, page, d)) * 16
+    kv[..., 0] = 0.0
+    kv[big, 0, :, 0] = -256.0                       # the page's other keys are far below
+    kv[big, 0, 0, 0] = 256.0
+    vv = rng.standard_normal((P, 1, page, d)) * 64
+    vv[big] = 0.0
+    table = rng.permutation(P)[None]
+    at = np.argsort(table[0])                       # the position of each page of the pool
+    kc, vc = (torch.from_numpy(np.clip(x[at], -400, 400)).float().to(torch.float8_e4m3fn) for x in (kv, vv))
+    ks, vs = torch.full((P, 1), 2.0 ** -4), torch.full((P, 1), 2.0 ** -6)
+    vs[table[0, big]] = 2.0 ** (span - 6)
+    scale = 1 / math.sqrt(d)
+    q = torch.from_numpy(rng.standard_normal((1, H, Nq, d)) * 0.1)
+    q[..., 0] = lead / (256 * 2.0 ** -4 * scale)
+    q = q.to(torch.bfloat16)
+    vals = [FP8.e4m3_decode(c.view(torch.uint8).numpy()) * to64(s)[:, :, None, None] for c, s in ((kc, ks), (vc, vs))]
+    ro, rl = OP.attend(to64(q), *vals, table, [L], scale)
+    bound = _attend_bound(to64(q), vals, table, [L], scale, ro)
+    for splits in (1, 0):
+        o, lse = fa.decode_paged(q.cuda(), kc.cuda(), vc.cuda(), cuda(table, torch.int32), cuda([L], torch.int32),
+                                 k_scale=ks.cuda(), v_scale=vs.cuda(), scale=scale, num_splits=splits)
+        assert fa.device_status() == fa.FA_OK
+        off = np.abs(to64(o) - ro) - bound
+        assert off.max() <= 0, f"splits {splits}: {off.max():.3e} past the bound, outputs up to {np.abs(ro).max():.3e}"
+        assert np.abs(to64(lse) - rl).max() <= 1e-3
+
+
+@pytest.mark.parametrize("d,H,Nq", [(64, 8, 1), (64, 8, 2), (128, 8, 1), (128, 8, 2)])
+def test_decode_value_scales_of_every_size(fa, d, H, Nq):
+    """Pages whose value scales lie anywhere in 2^-40 .. 2^20, in any order; the larger ones hold zeros but for one
+    element, so every other element comes from the small pages alone."""
+    page, L = 32, 1500
+    P = (L + page - 1) // page
+    rng = np.random.default_rng(d + Nq)
+    e = rng.integers(-40, 21, P)
+    e[3] = 20
+    kv = rng.standard_normal((P, 1, page, d)) * 32
+    vv = rng.standard_normal((P, 1, page, d)) * 64
+    vv[e > -34, :, :, 1:] = 0.0
+    kc, vc = (torch.from_numpy(np.clip(x, -400, 400)).float().to(torch.float8_e4m3fn) for x in (kv, vv))
+    ks, vs = torch.full((P, 1), 2.0 ** -5), torch.exp2(torch.from_numpy(e).float())[:, None]
+    scale = 1 / math.sqrt(d)
+    q = torch.from_numpy(rng.standard_normal((1, H, Nq, d))).to(torch.bfloat16)
+    table = np.arange(P)[None]
+    vals = [FP8.e4m3_decode(c.view(torch.uint8).numpy()) * to64(s)[:, :, None, None] for c, s in ((kc, ks), (vc, vs))]
+    ro, rl = OP.attend(to64(q), *vals, table, [L], scale)
+    bound = _attend_bound(to64(q), vals, table, [L], scale, ro)
+    for splits in (1, 5, 0):
+        o, lse = fa.decode_paged(q.cuda(), kc.cuda(), vc.cuda(), cuda(table, torch.int32), cuda([L], torch.int32),
+                                 k_scale=ks.cuda(), v_scale=vs.cuda(), scale=scale, num_splits=splits)
+        assert fa.device_status() == fa.FA_OK
+        bad = np.abs(to64(o) - ro) > bound
+        assert not bad.any(), f"splits {splits}: {bad.sum()} of {bad.size} past the bound"
+        assert np.abs(to64(lse) - rl).max() <= 1e-3
+
+
+def test_decode_hidden_page_beside_large_scales(fa):
+    """A table entry outside the pool hides its keys also where the other pages' scales lie far above 1."""
+    page, d, H, Hkv = 16, 128, 8, 2
+    cache = Cache(np.random.default_rng(31), 6, Hkv, page, d, True)
+    for s in cache.scale:
+        s.mul_(2.0 ** 20)
+    cache.scale[0].mul_(2.0 ** -20)
+    q = torch.randn(1, H, 1, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    o, lse = fa.decode_paged(q, *cache.gpu, cuda([[0, -1, 2, 3]], torch.int32), cuda([4 * page], torch.int32), **cache.kw())
+    assert fa.device_status() == fa.FA_ERR_INVALID_ARG and fa.device_status() == fa.FA_OK
+    vals = cache.values(0), cache.values(1)
+    ro, rl = OP.attend(to64(q), *vals, [[0, 2, 3]], [3 * page], 1 / math.sqrt(d))
+    assert np.all(np.abs(to64(o) - ro) <= _attend_bound(to64(q), vals, [[0, 2, 3]], [3 * page], 1 / math.sqrt(d), ro))
+    assert np.abs(to64(lse) - rl).max() <= 1e-3
