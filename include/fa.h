@@ -354,7 +354,8 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
  *      the d elements of a head are contiguous), so q, k and v can be parts of one
  *      projection.
  *   max_new  the most new tokens of one sequence when cu_seqlens is given (0:
- *      not known; sequences with more are clipped and reported).
+ *      not known; of sequences with more, the tokens past it are left out, the
+ *      others keep their positions, and the call is reported).
  * k and v go to the row of their position, in bf16 or as e4m3 codes. The scale
  * of an e4m3 page is a power of two, the least 2^e, e >= -40, with
  * |x| <= 448 * 2^e over the rows of this sequence that the page holds. Rows that

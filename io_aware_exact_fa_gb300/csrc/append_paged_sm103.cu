@@ -298,23 +298,21 @@ __device__ __forceinline__ void turn(Unit16& x, const Angles& t) {
   }
 }
 
-// Tokens of sequence b: first, and how many, clipped to what the call covers.
-__device__ __forceinline__ bool tokens_of(const AppendPagedParams& p, int b, int& t0, int& n) {
+// Tokens of sequence b: first, and how many, clipped to what the call covers; `all` of them, from which positions count
+// (token i is at L - all + i also where the last ones were cut off).
+__device__ __forceinline__ bool tokens_of(const AppendPagedParams& p, int b, int& t0, int& n, int& all) {
   if (p.cu == nullptr) {
-    n = p.T / p.B;
+    n = all = p.T / p.B;
     t0 = b * n;
     return true;
   }
   t0 = __ldg(p.cu + b);
-  n = __ldg(p.cu + b + 1) - t0;
+  n = all = static_cast<int>(static_cast<unsigned>(__ldg(p.cu + b + 1)) - static_cast<unsigned>(t0));
   const int most = min(p.max_new, p.T - t0);
   if (t0 >= 0 && n >= 0 && n <= most) return true;
   n = t0 < 0 ? 0 : max(0, min(n, most));
   return false;
 }
-
-// A sequence's length; far below zero (an error in any case) it would overflow the position arithmetic.
-__device__ __forceinline__ int length_of(const AppendPagedParams& p, int b) { return max(__ldg(p.seqlens + b), -(1 << 30)); }
 
 // ---- query block: rows tok0 .. of the step, all heads
 template <int D, bool INTER>
@@ -330,20 +328,20 @@ __device__ __forceinline__ void query_block(const AppendPagedParams& p, int bloc
     const int n = p.T / p.B;
     for (int r = tid; r < rows; r += nt) {
       const int tok = tok0 + r, b = tok / n;
-      const int L = tok < p.T ? length_of(p, b) : 0;
-      s_pos[r] = L != 0 ? L - n + (tok - b * n) : NONE;
+      const int L = tok < p.T ? __ldg(p.seqlens + b) : 0;
+      s_pos[r] = L != 0 ? static_cast<int>(static_cast<unsigned>(L) - n + (tok - b * n)) : NONE;
     }
   } else {
     for (int r = tid; r < rows; r += nt) s_pos[r] = NONE;
     __syncthreads();
     for (int b = tid; b < p.B; b += nt) {
-      int t0, n;
-      if (!tokens_of(p, b, t0, n) && block == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
+      int t0, n, all;
+      if (!tokens_of(p, b, t0, n, all) && block == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
       const int a = max(t0, tok0), e = min(t0 + n, tok0 + rows);
       if (a < e) {
-        const int L = length_of(p, b);
-        if (L != 0)
-          for (int t = a; t < e; ++t) s_pos[t - tok0] = L - n + (t - t0);
+        const int L = __ldg(p.seqlens + b);
+        if (L != 0)  // (a position that wraps lies outside the cache, which the K/V blocks report)
+          for (int t = a; t < e; ++t) s_pos[t - tok0] = static_cast<int>(static_cast<unsigned>(L) - all + (t - t0));
       }
     }
   }
@@ -428,16 +426,16 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
     b = lo;
     i = c - base(b);
   }
-  int t0, n;
-  (void)tokens_of(p, b, t0, n);
-  const int L = length_of(p, b);
-  const int start = L - n;
-  const int page0 = (start >> p.page_shift) + i;                 // this block's page of the sequence
+  int t0, n, all;
+  (void)tokens_of(p, b, t0, n, all);
+  const int L = __ldg(p.seqlens + b);
+  const long long start = static_cast<long long>(L) - all, end = start + n;     // positions
+  const int page0 = static_cast<int>(start >> p.page_shift) + i; // this block's page of the sequence
   const long long first = static_cast<long long>(page0) << p.page_shift;
   // (uniform over the block; blocks below the first sequence's, where tokens come before it, have i < 0)
-  if (n == 0 || L == 0 || i < 0 || first >= L) return;
-  const int r0 = start > first ? start - static_cast<int>(first) : 0;           // its new rows r0 .. r1 - 1
-  const int r1 = static_cast<int>(L - first < p.page ? L - first : p.page);
+  if (n == 0 || L == 0 || i < 0 || first >= end) return;
+  const int r0 = start > first ? static_cast<int>(start - first) : 0;           // its new rows r0 .. r1 - 1
+  const int r1 = static_cast<int>(end - first < p.page ? end - first : p.page);
   const int nrows = r1 - r0;
   const int tok0 = t0 + static_cast<int>(first + r0 - start);    // token of row r0
 

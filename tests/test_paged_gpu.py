@@ -661,3 +661,59 @@ def test_decode_hidden_page_beside_large_scales(fa):
     ro, rl = OP.attend(to64(q), *vals, [[0, 2, 3]], [3 * page], 1 / math.sqrt(d))
     assert np.all(np.abs(to64(o) - ro) <= _attend_bound(to64(q), vals, [[0, 2, 3]], [3 * page], 1 / math.sqrt(d), ro))
     assert np.abs(to64(lse) - rl).max() <= 1e-3
+
+
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("cu,T,max_new,lens", [
+    ([0, 4], 4, 2, [8]),                     # more than max_new
+    ([0, 9], 4, 0, [20]),                    # more than there are
+    ([0, 4, 40], 40, 20, [21, 47]),          # both pages of a clipped sequence
+    ([0, 50, 120], 100, 0, [50, 130]),       # blocks found through the offsets
+    ([0, 2 ** 31 - 1], 4, 0, [2 ** 31 - 1]),
+    ([0, 2 ** 31 - 1], 4, 0, [-2 ** 31]),    # nothing of it has a place
+])
+def test_append_clipped_tokens_keep_their_positions(fa, cu, T, max_new, lens, f8):
+    """A sequence with more new tokens than the call covers is reported; the tokens that the call does cover go to the
+    positions that its length and its offsets give them, and nothing else is written."""
+    H, Hkv, page, d, width = 4, 2, 16, 64, 9
+    rng = np.random.default_rng(6)
+    B = len(lens)
+    table, pool = make_table(rng, B, [width] * B, width)
+    cache = Cache(rng, pool, Hkv, page, d, f8)
+    before = [cache.codes(i) if f8 else cache.values(i) for i in range(2)]
+    scales = [cache.scales(i).copy() if f8 else None for i in range(2)]
+    x = torch.randn(T, H + 2 * Hkv, d, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    qo = torch.full((T, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    ko = torch.full((T, Hkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    turns = fa.rotary_turns(d, BASE)
+    fa.append_paged(x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], *cache.gpu, cuda(table), cuda(lens, torch.int32),
+                    cu_seqlens=cuda(cu, torch.int32), max_new=max_new, turns=turns, q_out=qo, k_out=ko, **cache.kw())
+    assert fa.device_status() == fa.FA_ERR_INVALID_ARG and fa.device_status() == fa.FA_OK
+    most = max_new if max_new else T
+    covered = np.zeros(T, dtype=bool)
+    want = [b.copy() for b in before]
+    for b, L in enumerate(lens):
+        n = cu[b + 1] - cu[b]
+        m = min(n, most, T - cu[b])
+        t = np.arange(cu[b], cu[b] + m)
+        start = L - n
+        placed = start >= 0 and start + m <= width * page
+        if not placed:                       # (none of these cases places a part of a sequence)
+            assert start < -m or start > width * page
+            covered[t] = True                # turned all the same, by positions outside the cache
+            continue
+        covered[t] = True
+        rq, rk, pos = OP.append(to64(x[t, :H]), to64(x[t, H:H + Hkv]), None, [m], [start + m], turns.tolist(), False)
+        near_bf16(to64(qo)[t], rq, f"q {b}")
+        near_bf16(to64(ko)[t], rk, f"k {b}")
+        v = to64(x[t, H + Hkv:])
+        if f8:
+            OP.store_e4m3(v, [m], [start + m], table[b:b + 1], page, want[1], scales[1])
+        else:
+            for i, p in enumerate(pos):
+                want[1][table[b, p // page], :, p % page] = v[i]
+    assert (to64(qo)[~covered] == 7).all() and (to64(ko)[~covered] == 7).all()
+    if f8:
+        assert np.array_equal(cache.codes(1), want[1]) and np.array_equal(cache.scales(1), scales[1])
+    else:
+        assert np.array_equal(cache.values(1), want[1])
