@@ -176,9 +176,11 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// The scale of a page whose new rows reach amax: that of the rows it already holds where it suffices.
+// The scale of a page whose new rows reach amax: that of the rows it already holds where it suffices and is one that
+// append may have written (the reciprocal of a subnormal one would overflow).
 __device__ __forceinline__ float merged_scale(float amax, float old, bool holds) {
-  if (holds && old > 0.f && old <= FLT_MAX && amax <= 448.f * old) return old;
+  constexpr float LEAST = 1.f / static_cast<float>(1ll << -PAGED_SCALE_EXP_MIN);
+  if (holds && old >= LEAST && old <= FLT_MAX && amax <= 448.f * old) return old;
   return scale_for(amax);
 }
 
@@ -556,7 +558,7 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
         }
       }
     }
-    const float ik = 1.f / sk, iv = 1.f / sv;  // exact: powers of two
+    const float ik = 1.f / sk, iv = 1.f / sv;  // exact for powers of two, the scales that append writes
     for (int it = 0; it < rounds; ++it) {
       const int r = it * groups + grp;
       if (r >= nrows) break;

@@ -717,3 +717,18 @@ def test_append_clipped_tokens_keep_their_positions(fa, cu, T, max_new, lens, f8
         assert np.array_equal(cache.codes(1), want[1]) and np.array_equal(cache.scales(1), scales[1])
     else:
         assert np.array_equal(cache.values(1), want[1])
+
+
+def test_append_to_a_page_of_tiny_scale(fa):
+    """A page whose scale lies below every scale that append writes: zeros stay zeros, and the scale becomes one that
+    append writes."""
+    page, d = 16, 64
+    pages = [torch.zeros(1, 1, page, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for p in pages:
+        p[0, 0, 0, :5] = 0x40
+    scale = [torch.full((1, 1), 2.0 ** -140, device="cuda") for _ in range(2)]
+    x = torch.zeros(1, 1, d, dtype=torch.bfloat16, device="cuda")
+    fa.append_paged(x, x, x, *pages, cuda([[0]], torch.int32), cuda([2], torch.int32), k_scale=scale[0], v_scale=scale[1])
+    assert fa.device_status() == fa.FA_OK
+    for p, s in zip(pages, scale):
+        assert (p == 0).all() and (s == 2.0 ** -40).all()   # (2 * 2^-140 is below half of the least code)
