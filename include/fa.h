@@ -406,9 +406,8 @@ size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int 
  * Products with e4m3 pages run in f16 on the codes, with fp32 accumulation, the
  * weights rounded to f16 (below 2^-14 of a row's largest to 2^-25 of it) and q held
  * in f16 (elements below 2^-14 of a row's largest to 2^-25 of it); with bf16 pages
- * in bf16. A NaN or infinity in v
- * reaches the rows of its sequence's last Nq tokens. Errors as for
- * fa_decode_grouped. Two launches (the ranges, their merge). */
+ * in bf16. A NaN or infinity in v reaches the rows of its sequence's last Nq tokens
+ * that see a key. Errors as for fa_decode_grouped. Two launches (the ranges, their merge). */
 fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
                           const float* k_scale, const float* v_scale, const int* block_table, int64_t table_stride,
                           const int* seqlens_k, void* o, const int64_t* o_strides, float* lse, int B, int H, int Hkv,

@@ -624,18 +624,20 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
         // (scores that were all NaN leave the base where it was: their sum is NaN, and so is the row)
         const float m = M[n][e] == -INFINITY && t != 0.f ? 0.f : M[n][e];
         if (i0 == 0 && i1 == nt) {
-          // the whole sequence; a row that sees no key has m = -inf, t = 0
-          const float inv = m == -INFINITY ? 0.f : 1.f / t;
+          // the whole sequence; a row that sees no key has m = -inf, t = 0 (its O may be 0 times a NaN or infinity in v)
+          const bool none = m == -INFINITY;
+          const float inv = 1.f / t;
+          auto out = [&](float y) { return none ? 0.f : y * inv; };
           const int h = hk * p.G + rr / p.Nq, tok = rr % p.Nq;
           uint16_t* op = static_cast<uint16_t*>(p.o) + b * p.osb + h * p.osh + tok * p.ost;
 #pragma unroll
           for (int jj = 0; jj < C::KST / 2; ++jj)
             *reinterpret_cast<uint2*>(op + dp_o_elem<D, F8>(gid, jj)) =
-                make_uint2(pack_bf16x2(oacc[n][2 * jj][e] * inv, oacc[n][2 * jj][e + 2] * inv),
-                           pack_bf16x2(oacc[n][2 * jj + 1][e] * inv, oacc[n][2 * jj + 1][e + 2] * inv));
+                make_uint2(pack_bf16x2(out(oacc[n][2 * jj][e]), out(oacc[n][2 * jj][e + 2])),
+                           pack_bf16x2(out(oacc[n][2 * jj + 1][e]), out(oacc[n][2 * jj + 1][e + 2])));
           if (p.lse != nullptr && gid == 0)
             p.lse[(static_cast<long long>(b) * p.H + h) * p.Nq + tok] =
-                m == -INFINITY ? -INFINITY : (m + lg2_approx(t)) * 0.69314718055994530942f;
+                none ? -INFINITY : (m + lg2_approx(t)) * 0.69314718055994530942f;
         } else {
           // ranges and (sequence, head) pairs both only grow along the tiles, so their sum numbers the parts
           const long long part =

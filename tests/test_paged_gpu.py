@@ -732,3 +732,21 @@ def test_append_to_a_page_of_tiny_scale(fa):
     assert fa.device_status() == fa.FA_OK
     for p, s in zip(pages, scale):
         assert (p == 0).all() and (s == 2.0 ** -40).all()   # (2 * 2^-140 is below half of the least code)
+
+
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_rows_that_see_nothing_beside_nan(fa, d, f8):
+    """A token before the sequence's first key gets zeros and -inf, whatever v holds; the tokens that see the keys get
+    what v holds."""
+    page, H, Hkv, Nq, lens = 16, 4, 2, 5, [3, 2]
+    cache = Cache(np.random.default_rng(2), 3, Hkv, page, d, f8)
+    cache.gpu[1].view(torch.uint8 if f8 else torch.int16).fill_(0x7F if f8 else 0x7FC0)
+    q = torch.randn(2, H, Nq, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    for splits in (0, 1, 3):
+        o, lse = fa.decode_paged(q, *cache.gpu, cuda([[2], [0]], torch.int32), cuda(lens, torch.int32), num_splits=splits,
+                                 **cache.kw())
+        assert fa.device_status() == fa.FA_OK
+        for b, L in enumerate(lens):
+            assert (o[b, :, :Nq - L] == 0).all() and torch.isneginf(lse[b, :, :Nq - L]).all()
+            assert torch.isnan(o[b, :, Nq - L:]).all() and torch.isfinite(lse[b, :, Nq - L:]).all()
