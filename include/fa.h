@@ -111,9 +111,10 @@ size_t fa_fwd_packed_workspace_size(int B, int total_q, int H, int Hkv);
  *   lse    fp32 [H, total_q] (may be NULL)
  * Query head h reads K/V head h / (H/Hkv). Inside a sequence, with causal != 0,
  * query i sees key j iff j <= i + Lk - Lq (its queries are its last positions);
- * rows that see no key get o = 0, lse = -inf. Sequences never reach one another,
- * whatever the values of their rows; inside one, an infinity or NaN in v reaches
- * every row that visits its 128-key tile, also those whose causal mask hides it.
+ * rows that see no key get o = 0, lse = -inf, whatever v holds. Sequences never
+ * reach one another, whatever the values of their rows; inside one, an infinity or
+ * NaN in v reaches every row that sees a key of its 128-key tile, also those whose
+ * causal mask hides it.
  * Rows of o and columns of lse past cu_seqlens_q[B] are left as they were.
  *   workspace  device memory of fa_fwd_packed_workspace_size() bytes, 256-byte
  *              aligned, owned by the caller, overwritten; calls that may overlap

@@ -1151,7 +1151,10 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
           }
           uint32_t ow[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) ow[i] = pack_bf16x2(u2f(o[2 * i]) * inv, u2f(o[2 * i + 1]) * inv);
+          for (int i = 0; i < 16; ++i) {
+            ow[i] = pack_bf16x2(u2f(o[2 * i]) * inv, u2f(o[2 * i + 1]) * inv);
+            if (PK && l == 0.f) ow[i] = 0u;  // a row that sees no key: its O may be 0 times a NaN or infinity in v
+          }
           if (by_rows) {
             if constexpr (PK) put_rows(ow, lane, orow + ch * 64, 2 * static_cast<long long>(pk.ost), Nq - (qi & ~3));
           } else {
@@ -1169,7 +1172,7 @@ __global__ void __launch_bounds__(prefill_threads(D), 1)
         else lse_at = static_cast<size_t>(bh) * p.Nq + qi;
         if (p.lse != nullptr && qi < Nq)
           p.lse[lse_at] =
-              (l > 0.f) ? (m + lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
+              (l > 0.f) ? (m + lg2_approx(l)) * 0.69314718055994530942f : (!PK || l == 0.f) ? -INFINITY : l;  // (l: NaN)
       }
       if constexpr (!DIRECT) {
         fence_proxy_async_smem();

@@ -303,3 +303,21 @@ def test_binding_refusals(fa):
     with pytest.raises(fa.FAError):
         fa.fwd_packed(q, k[:5], v[:5], cu)   # other rows without their offsets
     assert fa.fwd_packed(q[:0], k[:0], v[:0], cu)[0].shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv", [(4, 2), (3, 1)])
+def test_rows_that_see_nothing_beside_nan(fa, H, Hkv, d):
+    """Queries before a sequence's first key get zeros and -inf, whatever v holds; a query of NaN gets NaN in both."""
+    lq, lk = [150, 40], [20, 40]
+    cu_q, cu_k = cum(lq), cum(lk)
+    q, k, v = inputs(cu_q[-1], cu_k[-1], H, Hkv, d, seed=12)
+    v[:20] = float("nan")
+    q[160] = float("nan")
+    o, lse = fa.fwd_packed(q, k, v, i32(cu_q), i32(cu_k), causal=True)
+    assert fa.device_status() == fa.FA_OK
+    assert (o[:130] == 0).all() and torch.isneginf(lse[:, :130]).all()
+    assert torch.isnan(o[130:150]).all() and torch.isfinite(lse[:, 130:150]).all()
+    assert torch.isnan(o[160]).all() and torch.isnan(lse[:, 160]).all()
+    rest = [t for t in range(150, 190) if t != 160]
+    assert torch.isfinite(o[rest]).all() and torch.isfinite(lse[:, rest]).all()
