@@ -106,8 +106,8 @@ size_t fa_fwd_packed_workspace_size(int B, int total_q, int H, int Hkv);
  *          offsets past the tensors are clipped and reported by
  *          fa_get_device_status() as FA_ERR_INVALID_ARG.
  *   strides  int64 [8], host memory: row and head strides, in elements, of q, k,
- *          v, o in that order (multiples of 8; the d elements of a head are
- *          contiguous), so q, k and v can be parts of one projection.
+ *          v, o in that order (positive multiples of 8; no two rows of o overlap, as
+ *          for fa_append_paged; the d elements of a head are contiguous), so q, k and v can be parts of one projection.
  *   lse    fp32 [H, total_q] (may be NULL)
  * Query head h reads K/V head h / (H/Hkv). Inside a sequence, with causal != 0,
  * query i sees key j iff j <= i + Lk - Lq (its queries are its last positions);
@@ -351,9 +351,10 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
  *   q_out  bf16 [T, H, d]; may be q.   k_out  bf16 [T, Hkv, d], the turned keys
  *      (for attention among the new tokens), or NULL; may be k.
  *   strides  int64 [10], host memory: token and head strides, in elements, of q,
- *      k, v, q_out, k_out in that order (multiples of 8, those of outputs not 0;
- *      the d elements of a head are contiguous), so q, k and v can be parts of one
- *      projection.
+ *      k, v, q_out, k_out in that order (multiples of 8; those of an output such
+ *      that no two of its rows of d elements overlap, from the smallest stride to
+ *      the largest each past what the ones before span; the d elements of a head
+ *      are contiguous), so q, k and v can be parts of one projection.
  *   max_new  the most new tokens of one sequence when cu_seqlens is given (0:
  *      not known; of sequences with more, the tokens past it are left out, the
  *      others keep their positions, and the call is reported).
@@ -389,8 +390,8 @@ size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int 
  * new ones among them; token t sees key j iff j <= L_b - Nq + t; query head h
  * reads K/V head h / (H/Hkv). A token that sees no key gets o = 0, lse = -inf.
  *   q, o       bf16 [B, H, Nq, d] with element strides q_strides, o_strides
- *              (int64 [3], host memory: batch, head, token; multiples of 8, of o not
- *              0; d contiguous). Token-major tensors, as fa_append_paged returns them,
+ *              (int64 [3], host memory: batch, head, token; multiples of 8; no two
+ *              rows of o overlap, as for fa_append_paged; d contiguous). Token-major tensors, as fa_append_paged returns them,
  *              are passed by their strides.
  *   lse        fp32 [B, H, Nq] (may be NULL)
  *   max_len    no sequence is longer (at most the positions a block-table row

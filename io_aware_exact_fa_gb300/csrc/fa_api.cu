@@ -858,10 +858,25 @@ fa_status check_pool(const void* k_pages, const void* v_pages, const float* k_sc
 }
 
 // Element strides of a strided operand: multiples of 8 (16-byte rows), not
-// negative (of an output: not zero either, where every element has its own
-// place); that of a dimension of one element does not matter.
-bool stride_ok(int64_t stride, int extent, bool output) {
-  return extent <= 1 || (stride >= (output ? 8 : 0) && stride % 8 == 0);
+// negative; that of a dimension of one element does not matter.
+bool stride_ok(int64_t stride, int extent) { return extent <= 1 || (stride >= 0 && stride % 8 == 0); }
+
+// Whether every row of d elements of an output has its own place: from the
+// smallest stride to the largest, each passes what the dimensions before it span.
+// (Rows that overlap would be written by several threads, in any order.)
+bool rows_apart(const int64_t* strides, const int* extents, int dims, int d) {
+  int64_t span = d;
+  unsigned left = (1u << dims) - 1u;
+  while (left != 0u) {
+    int at = -1;
+    for (int i = 0; i < dims; ++i)
+      if ((left >> i & 1u) && (at < 0 || strides[i] < strides[at])) at = i;
+    left &= ~(1u << at);
+    if (extents[at] <= 1) continue;
+    if (strides[at] < span || strides[at] > (INT64_MAX - span) / extents[at]) return false;
+    span += strides[at] * (extents[at] - 1);
+  }
+  return true;
 }
 
 }  // namespace
@@ -898,9 +913,12 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
   if (table_stride < table_width && B > 1) return fail(FA_ERR_INVALID_ARG, "table_stride is below table_width");
   for (int i = 0; i < 10; ++i) {  // token and head strides of q, k, v, q_out, k_out
     const int heads = (i == 1 || i == 7) ? H : Hkv;
-    if ((i < 8 || k_out) && !stride_ok(strides[i], (i & 1) ? heads : T, i >= 6))
-      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements, >= 0, of outputs > 0");
+    if ((i < 8 || k_out) && !stride_ok(strides[i], (i & 1) ? heads : T))
+      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements, >= 0");
   }
+  const int q_extent[2] = {T, H}, k_extent[2] = {T, Hkv};
+  if (!rows_apart(strides + 6, q_extent, 2, d) || (k_out && !rows_apart(strides + 8, k_extent, 2, d)))
+    return fail(FA_ERR_UNSUPPORTED, "rows of q_out or k_out overlap");
   const int n_max = cu_seqlens == nullptr ? T / B : std::min(max_new > 0 ? max_new : T, T);
   const long long rect = (static_cast<long long>(n_max) + page - 2) / page + 1;
   const bool use_rect = cu_seqlens == nullptr || rect * B <= T / page + 2LL * B;
@@ -959,8 +977,9 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   if (!aligned(q, 16) || !aligned(o, 16)) return fail(FA_ERR_UNSUPPORTED, "q and o must be 16-byte aligned");
   const int extent[3] = {B, H, Nq};
   for (int i = 0; i < 3; ++i)
-    if (!stride_ok(q_strides[i], extent[i], false) || !stride_ok(o_strides[i], extent[i], true))
-      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements, >= 0, of outputs > 0");
+    if (!stride_ok(q_strides[i], extent[i]) || !stride_ok(o_strides[i], extent[i]))
+      return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements, >= 0");
+  if (!rows_apart(o_strides, extent, 3, d)) return fail(FA_ERR_UNSUPPORTED, "rows of o overlap");
   if (lse && !aligned(lse, 4)) return fail(FA_ERR_UNSUPPORTED, "lse must be 4-byte aligned");
   if (B > 1 && table_stride < (static_cast<int64_t>(max_len) + page - 1) / page)
     return fail(FA_ERR_INVALID_ARG, "max_len needs %lld pages a sequence, table_stride is %lld",
@@ -1062,6 +1081,8 @@ fa_status fa_fwd_packed(const void* q, const void* k, const void* v, void* o, fl
   // key-tile rows are addressed up to one tile past the end
   if (entries * head_units > INT_MAX || total_q > INT_MAX - 512 || total_k > INT_MAX - 512)
     return fail(FA_ERR_INVALID_ARG, "B, total_q and H give too many tiles");
+  const int o_extent[2] = {total_q, H};
+  if (!rows_apart(strides + 6, o_extent, 2, d)) return fail(FA_ERR_UNSUPPORTED, "rows of o overlap");
   const size_t need = fa_fwd_packed_workspace_size(B, total_q, H, Hkv);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
     return fail(FA_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);

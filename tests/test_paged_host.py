@@ -232,3 +232,41 @@ def test_oracle_store_matches_whole_quantisation():
     assert scale[1, 0] == s and scale[0, 0] == 7.0
     got = FP8.e4m3_decode(codes[1, 0]) * s
     assert np.all(np.abs(got - x[:, 0]) <= 2 * np.maximum(2.0 ** -4 * np.abs(x[:, 0]), 2.0 ** -10 * s))
+
+
+# What the output may not be: rows of d elements that overlap, which several threads would write in any order.
+@pytest.mark.parametrize("kw,bad", [
+    (dict(strides=[512, 64] * 3 + [512, 8] + [512, 64]), True),             # heads 8 elements apart
+    (dict(strides=[512, 64] * 3 + [504, 64] + [512, 64]), True),            # a token's last head over the next's first
+    (dict(strides=[512, 64] * 3 + [64, 64] + [512, 64]), True),
+    (dict(strides=[512, 64] * 3 + [64, 72] + [512, 64]), True),             # head-major, one row too close
+    (dict(strides=[512, 64] * 4 + [120, 64]), True),                        # k_out: 2 heads
+    (dict(strides=[512, 64] * 4 + [1 << 61, 1 << 62]), True),               # past any address
+    (dict(T=0, strides=[512, 64] * 5), False),
+])
+def test_append_refuses_overlapping_outputs(fa, kw, bad):
+    assert _append(fa, **kw) == (UNSUPPORTED if bad else 0)
+    if bad:
+        assert b"overlap" in fa.lib.fa_last_error_detail()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(os=[512, 8, 64]), dict(os=[504, 64, 64]), dict(os=[64, 64, 64]), dict(os=[512, 64, 64], Nq=2),
+    dict(os=[1024, 64, 504], Nq=2), dict(os=[1016, 64, 512], Nq=2),
+])
+def test_decode_refuses_overlapping_outputs(fa, kw):
+    assert _decode(fa, **kw, qs=[1024, 64, 512]) == UNSUPPORTED and b"overlap" in fa.lib.fa_last_error_detail()
+
+
+@pytest.mark.parametrize("o", [[512, 8], [504, 64], [64, 64], [64, 6328], [8, 512]])
+def test_packed_refuses_overlapping_outputs(fa, o):
+    assert _packed(fa, strides=[512, 64, 128, 64, 128, 64, *o]) == UNSUPPORTED
+    assert b"overlap" in fa.lib.fa_last_error_detail()
+
+
+def test_outputs_apart_are_taken(fa):
+    """The layouts that do not overlap pass the check: the next refusal is another one (no workspace)."""
+    for o, nq in (([512, 64, 64], 1), ([1024, 128, 64], 2), ([1024, 64, 512], 2), ([64, 256, 128], 2), ([8192, 64, 1024], 2)):
+        assert _decode(fa, os=o, Nq=nq, qs=[1024, 64, 512], ws=None) == WORKSPACE
+    for o in ([512, 64], [1024, 128], [64, 6400], [64, 1 << 20]):
+        assert _packed(fa, strides=[512, 64, 128, 64, 128, 64, *o], ws=None) == WORKSPACE
