@@ -423,8 +423,10 @@ def _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv: int, 
     return (kp, vp, ks, vs, block_table.data_ptr(), ts[0], lens), n, page, e4m3, B, width
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (a torch without CUDA has neither, and no tensor for the calls that ask; sizes and refusals work there all the same)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 try:  # the allocator without the dispatcher before it (half the time of torch.empty); on the current device
     _empty_here = torch._C._dynamo.guards._empty_strided_cuda
 except AttributeError:

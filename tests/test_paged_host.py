@@ -6,6 +6,7 @@ import ctypes
 import math
 import os
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -270,3 +271,26 @@ def test_outputs_apart_are_taken(fa):
         assert _decode(fa, os=o, Nq=nq, qs=[1024, 64, 512], ws=None) == WORKSPACE
     for o in ([512, 64], [1024, 128], [64, 6400], [64, 1 << 20]):
         assert _packed(fa, strides=[512, 64, 128, 64, 128, 64, *o], ws=None) == WORKSPACE
+
+
+def test_import_on_a_torch_without_cuda(fa):
+    """The binding imports where torch was built without CUDA (its C module then has none of the CUDA entry points):
+    workspace sizes and refusals need no GPU."""
+    code = """
+import torch
+for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, n):
+        delattr(torch._C, n)
+if hasattr(torch._C._dynamo.guards, "_empty_strided_cuda"):
+    del torch._C._dynamo.guards._empty_strided_cuda
+from io_aware_exact_fa_gb300 import fa
+assert fa.fwd_packed_workspace_size(3, 1000, 8, 2) == 256 + (1000 // 128 + 3) * 32
+assert fa.decode_paged_workspace_size(1, 8, 2, 1, 64, 100) > 0
+x = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+try:
+    fa.fwd_packed(x, x, x, torch.zeros(2, dtype=torch.int32))
+except ValueError as e:
+    print("refused:", e)
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.startswith("refused: q must be a CUDA tensor"), r.stderr
