@@ -810,25 +810,16 @@ int log2_of(int x) {
   return s;
 }
 
-// Ranges that a paged decode shares the batch's keys out in: one for each warp
-// that the GPU holds (and row tile), or `num_splits` for each sequence and K/V
-// head on average.
-constexpr int PAGED_SMS = 152;
-int paged_row_tiles(int R) { return (R + fa::decode_paged_rows(R) - 1) / fa::decode_paged_rows(R); }
-int paged_ranges(int B, int Hkv, int R, int d, int num_splits) {
-  if (num_splits > 0) return static_cast<int>(std::min(static_cast<long long>(num_splits) * B * Hkv, 1LL << 20));
-  const int warps = PAGED_SMS * 4 * fa::decode_paged_ctas(d, fa::decode_paged_rows(R));
-  return std::max(1, warps / paged_row_tiles(R));
-}
-
-// Layout of the paged decode's workspace: outputs, (base, sum) pairs, range ends.
+// Layout of the paged decode's workspace: outputs, (base, sum) pairs, range ends. Its size does not depend on the device:
+// it holds the ranges of the largest number of SMs.
 struct PagedWorkspace {
   size_t ml, ends, bytes;
 };
 PagedWorkspace paged_workspace(int B, int Hkv, int R, int d, int num_splits) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t pairs = static_cast<size_t>(B) * Hkv;
-  const size_t parts = (paged_ranges(B, Hkv, R, d, num_splits) + pairs) * paged_row_tiles(R) * fa::decode_paged_rows(R);
+  const size_t parts = (fa::decode_paged_ranges(fa::DECODE_PAGED_SMS, B, Hkv, R, d, num_splits) + pairs) *
+                       fa::decode_paged_row_tiles(R) * fa::decode_paged_rows(R);
   PagedWorkspace w{};
   w.ml = up(parts * d * 4);
   w.ends = w.ml + up(parts * 8);
@@ -984,16 +975,16 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   if (B > 1 && table_stride < (static_cast<int64_t>(max_len) + page - 1) / page)
     return fail(FA_ERR_INVALID_ARG, "max_len needs %lld pages a sequence, table_stride is %lld",
                 (static_cast<long long>(max_len) + page - 1) / page, static_cast<long long>(table_stride));
-  const int row_tiles = paged_row_tiles(R), ranges = paged_ranges(B, Hkv, R, d, num_splits);
-  if (static_cast<long long>(B) * H * Nq > INT_MAX - 16 ||
-      static_cast<double>(B) * Hkv * max_len / 16 > 2e9 * ranges)  // (tiles of a range are counted in 32 bits)
-    return fail(FA_ERR_INVALID_ARG, "B * H * Nq or B * Hkv * max_len is too large");
+  if (static_cast<long long>(B) * H * Nq > INT_MAX - 16) return fail(FA_ERR_INVALID_ARG, "B * H * Nq is too large");
   const size_t need = fa_decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
     return fail(FA_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
 
   DeviceState* st = nullptr;
   if (fa_status s = device_state(&st)) return s;
+  const int ranges = fa::decode_paged_ranges(st->num_sms, B, Hkv, R, d, num_splits);
+  if (static_cast<double>(B) * Hkv * max_len / 16 > 2e9 * ranges)  // (tiles of a range are counted in 32 bits)
+    return fail(FA_ERR_INVALID_ARG, "B * Hkv * max_len is too large");
   fa::DecodePagedParams p{};
   p.q = q, p.k = k_pages, p.v = v_pages, p.k_scale = k_scale, p.v_scale = v_scale;
   p.table = block_table, p.table_stride = table_stride, p.seqlens = seqlens_k;
@@ -1003,7 +994,7 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   p.B = B, p.H = H, p.Hkv = Hkv, p.G = H / Hkv, p.Nq = Nq, p.R = R;
   p.max_len = max_len;
   p.page = page, p.page_shift = log2_of(page), p.num_pages = num_pages;
-  p.n_ranges = ranges, p.row_tiles = row_tiles;
+  p.n_ranges = ranges, p.row_tiles = fa::decode_paged_row_tiles(R);
   p.scale_log2 = scale * 1.4426950408889634f;
   const PagedWorkspace w = paged_workspace(B, Hkv, R, d, num_splits);
   p.ws_o = static_cast<float*>(workspace);

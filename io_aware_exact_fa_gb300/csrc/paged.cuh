@@ -64,6 +64,19 @@ __host__ __device__ constexpr int decode_paged_rows(int R) { return R <= 8 ? 8 :
 // bf16 115 against 117 us; e4m3 76 against 97 us, where the 168 registers a thread of three blocks spill; at d = 64 two
 // blocks take 53 us, three 47).
 __host__ __device__ constexpr int decode_paged_ctas(int d, int rows) { return rows == 16 && d == 128 ? 2 : 3; }
+__host__ __device__ constexpr int decode_paged_row_tiles(int R) { return (R + decode_paged_rows(R) - 1) / decode_paged_rows(R); }
+// Ranges that the batch's keys are shared out in: one for each warp that `sms` SMs hold (and row tile), or `num_splits`
+// for each sequence and K/V head on average. More ranges than warps would run as a second wave, as long as the first.
+constexpr int DECODE_PAGED_SMS = 152;  // a GB300's; a larger device works with so many of its own
+inline int decode_paged_ranges(int sms, int B, int Hkv, int R, int d, int num_splits) {
+  if (num_splits > 0) {
+    const long long n = static_cast<long long>(num_splits) * B * Hkv;
+    return n < (1 << 20) ? static_cast<int>(n) : 1 << 20;
+  }
+  const int warps = (sms < DECODE_PAGED_SMS ? sms : DECODE_PAGED_SMS) * 4 * decode_paged_ctas(d, decode_paged_rows(R));
+  const int n = warps / decode_paged_row_tiles(R);
+  return n < 1 ? 1 : n;
+}
 
 struct AppendPagedParams {
   const void* q;             // bf16, element strides of token and head; d contiguous

@@ -294,3 +294,34 @@ except ValueError as e:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.startswith("refused: q must be a CUDA tensor"), r.stderr
+
+
+def test_decode_ranges_follow_the_device(tmp_path):
+    """The decode's ranges, compiled for the host: their warps fit the SMs that the device has in one wave, and the
+    workspace, sized without a device, holds the ranges of any."""
+    src = tmp_path / "ranges.cu"
+    src.write_text("""
+#include <cstdio>
+#include "paged.cuh"
+int main() {
+  for (int d : {64, 128})
+    for (int R = 1; R <= 128; ++R) {
+      const int tiles = fa::decode_paged_row_tiles(R), warps = 4 * fa::decode_paged_ctas(d, fa::decode_paged_rows(R));
+      const int most = fa::decode_paged_ranges(fa::DECODE_PAGED_SMS, 3, 2, R, d, 0);
+      for (int sms : {1, 20, 76, 100, 148, 152, 160, 300}) {
+        const int n = fa::decode_paged_ranges(sms, 3, 2, R, d, 0);
+        if (n < 1 || n > most || (n > 1 && n * tiles > sms * warps)) return 1;
+        if (sms <= fa::DECODE_PAGED_SMS && (n + 1) * tiles <= sms * warps) return 2;
+        if (fa::decode_paged_ranges(sms, 3, 2, R, d, 7) != 42) return 3;
+      }
+    }
+  if (fa::decode_paged_ranges(152, 1 << 20, 8, 1, 64, 1024) != 1 << 20) return 4;
+  std::puts("ok");
+}
+""")
+    from io_aware_exact_fa_gb300 import build
+    exe = tmp_path / "ranges"
+    subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-I", build.CSRC, "-I",
+                    build.INCLUDE, str(src), "-o", str(exe)], check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert (r.returncode, r.stdout.strip()) == (0, "ok")
