@@ -336,6 +336,8 @@ def rotary_turns(rot: int, base: float = 10000.0, scaling: Optional[Tuple] = Non
         raise ValueError(f"unknown scaling {kind!r}")
     if kind and not scaling[1] >= 1:
         raise ValueError("the scaling factor must be >= 1")
+    if kind == "by_parts" and not (scaling[2] > 0 and 0 <= scaling[3] < scaling[4]):
+        raise ValueError("by_parts scaling needs n > 0 and 0 <= slow < fast")
     if kind == "base":
         if rot < 4:
             raise ValueError("base scaling needs rot >= 4")

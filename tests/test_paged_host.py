@@ -325,3 +325,9 @@ int main() {
                     build.INCLUDE, str(src), "-o", str(exe)], check=True, capture_output=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert (r.returncode, r.stdout.strip()) == (0, "ok")
+
+
+@pytest.mark.parametrize("parts", [(4096, 2.0, 2.0), (4096, 32.0, 1.0), (4096, -1.0, 2.0), (0, 1.0, 32.0)])
+def test_rotary_turns_refuses_bad_parts(fa, parts):
+    with pytest.raises(ValueError, match="by_parts"):
+        fa.rotary_turns(64, 10000.0, ("by_parts", 4.0, *parts), device="cpu")
