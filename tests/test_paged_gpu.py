@@ -750,3 +750,38 @@ def test_decode_rows_that_see_nothing_beside_nan(fa, d, f8):
         for b, L in enumerate(lens):
             assert (o[b, :, :Nq - L] == 0).all() and torch.isneginf(lse[b, :, :Nq - L]).all()
             assert torch.isnan(o[b, :, Nq - L:]).all() and torch.isfinite(lse[b, :, Nq - L:]).all()
+
+
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("inter,norm,rot_scale", [(True, True, 1.0), (False, False, 1.0), (False, True, 1.3688879454),
+                                                 (True, True, 0.25), (True, False, -2.5), (False, True, 0.0)])
+@pytest.mark.parametrize("d,rot", [(64, 48), (128, 128)])
+def test_append_rotation_scale_and_weights_in_every_layout(fa, d, rot, inter, norm, rot_scale, f8):
+    """A factor on the turned elements (the others keep their size), and norm weights in both layouts."""
+    new, lens, H, Hkv, page = [3, 20], [50, 20], 3, 1, 16
+    rng = np.random.default_rng(d + 2 * inter + norm)
+    T = sum(new)
+    count = [(L + page - 1) // page for L in lens]
+    table, pool = make_table(rng, 2, count, max(count))
+    cache = Cache(rng, pool, Hkv, page, d, f8)
+    codes, sc = cache.codes(0) if f8 else None, cache.scales(0).copy() if f8 else None
+    x = torch.randn(T, H + 2 * Hkv, d, generator=torch.Generator().manual_seed(d)).to(torch.bfloat16).cuda()
+    w = [cuda(1 + 0.3 * rng.standard_normal(d), torch.bfloat16) if norm else None for _ in range(2)]
+    turns = fa.rotary_turns(rot, BASE)
+    q, k = fa.append_paged(x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], *cache.gpu, cuda(table), cuda(lens, torch.int32),
+                           cu_seqlens=cuda([0, 3, 23], torch.int32), turns=turns, interleaved=inter, rot_scale=rot_scale,
+                           q_weight=w[0], k_weight=w[1], eps=1e-5, **cache.kw())
+    assert fa.device_status() == fa.FA_OK
+    rq, rk, pos = OP.append(to64(x[:, :H]), to64(x[:, H:H + Hkv]), None, new, lens, turns.tolist(), inter,
+                            *[None if y is None else to64(y) for y in w], eps=1e-5, rot_scale=float(np.float32(rot_scale)))
+    near_bf16(to64(q), rq, "q")
+    near_bf16(to64(k), rk, "k")
+    seq = np.repeat(np.arange(2), new)
+    got = np.stack([cache.values(0)[table[s, p // page], :, p % page] for s, p in zip(seq, pos)])
+    if not f8:
+        near_bf16(got, rk, "k pages")
+        return
+    OP.store_e4m3(rk, new, lens, table, page, codes, sc)
+    assert np.array_equal(cache.scales(0), sc)
+    step = np.stack([sc[table[s, p // page]] for s, p in zip(seq, pos)])[:, :, None]
+    assert np.all(np.abs(got - rk) <= np.maximum(2.0 ** -4 * np.abs(rk), 2.0 ** -10 * step) * (1 + 2.0 ** -16))
