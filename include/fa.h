@@ -366,8 +366,8 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
  * fp32 result; an infinity or NaN is stored as the NaN code and left out of the
  * scale. A call that starts at row 0 of a page takes nothing from the page's old
  * contents or scale.
- * Every page that a call writes must belong to one sequence (pages shared by
- * several sequences may be read, not appended to). Rows of q_out and k_out of
+ * Every page that a call writes must be listed once, by one sequence (pages that
+ * several sequences or places share may be read, not appended to). Rows of q_out and k_out of
  * tokens past cu_seqlens[B] are left as they were. T = 0 is a no-op. d = 64 or
  * 128. One launch on `stream`. Errors: FA_ERR_INVALID_ARG for NULL tensors, bad
  * sizes, H not a multiple of Hkv, T not a multiple of B without cu_seqlens;

@@ -30,10 +30,10 @@
 // in) are computed once for all its heads.
 // What bounds it: HBM for prompts (q read and written, k and v read, the cache
 // written) as long as the instructions per value stay few (packed fp32
-// arithmetic; one kind of block for both took 147 us in place of 132), launch and
+// arithmetic; with one kind of block for both 147 us in place of 132), launch and
 // load latency for a step of single tokens. Measured, 32 query and 8 K/V heads,
-// d = 128, e4m3: 26.7k prompt tokens with norms 114 us (5.8 TB/s, 0.85 of the copy
-// rate); 256 sequences of one token 7.9 us.
+// d = 128, e4m3: 26.7k prompt tokens with norms 115 us (5.7 TB/s, 0.85 of the copy
+// rate); 256 sequences of one token 8.1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -30,8 +30,8 @@
 // one for each warp that the GPU holds, so ragged lengths leave no SM idle and no
 // warp starts anew for every chunk (blocks of one chunk each spent a third of
 // their time filling and draining: 97 in place of 74 us for two sequences of 110k
-// tokens, 137 in place of 124 us for 64 of 4-8k; e4m3, d = 128, 8 K/V heads:
-// 6.1 and 6.5 TB/s, 0.89 and 0.96 of the copy rate). A warp walks its range
+// tokens, 137 in place of 125 us for 64 of 4-8k; e4m3, d = 128, 8 K/V heads:
+// 6.1 and 6.4 TB/s, 0.89 and 0.95 of the copy rate). A warp walks its range
 // through a private ring of asynchronous 16-byte copies that runs on across
 // sequences; it meets no other warp, so there is no barrier at all. Where a
 // sequence's keys of one head lie in several ranges, each warp leaves its base,
@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
         // bits down to 2^-14. With E = ev_most the base is at most max_j (y_j + log2 c_j) - TOP <= max y + E - TOP, hence
         // z_j - M >= (y_j - max y) - (E - log2 c_j) + TOP: up to GAP = TOP below E a page's scale costs its weights nothing.
         // A group further below (rare: values of two pages that differ more than 100-fold) is left out here and has its
-        // turn after the others, with weights that count from its own largest.
+        // turn after the others, with weights that count from its own largest. (64 sequences of 4-8k, d = 128: 125 us, 129
+        // with every other page's values 2^10 larger, 149 with the first page's alone.)
 #pragma unroll
         for (int g = 0; g < C::KG; ++g)
           if (ka[g] > 0.f && ev[g] < ev_most - DpBase<F8>::GAP) far |= 1u << g;  // (the same in every lane)

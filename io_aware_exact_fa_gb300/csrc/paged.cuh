@@ -100,7 +100,7 @@ struct AppendPagedParams {
   int rot, interleaved;
   int max_new;               // most new tokens of one sequence
   int per_seq;               // > 0: K/V blocks are B x per_seq pages; 0: found through cu
-  int kv_blocks;             // K/V blocks (pages x K/V heads); the query blocks follow
+  int kv_blocks;             // K/V blocks (pages x K/V heads), spread evenly among the query blocks
   int max_rows;              // most new rows of one page
   int q_blocks_wanted;       // query blocks that fill the GPU a few times over
   int q_slots;               // heads of a row that a query block takes side by side
