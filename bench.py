@@ -94,7 +94,8 @@ def barrier(world: int):
 
 
 # headers a kernel source includes besides fa_ptx.cuh and fa_common.cuh
-KERNEL_HEADERS = {"decode_grouped_sm103.cu": ("decode_grouped.cuh",), "materialized_sm103.cu": ("materialized.cuh",)}
+KERNEL_HEADERS = {"decode_grouped_sm103.cu": ("decode_grouped.cuh",), "materialized_sm103.cu": ("materialized.cuh",),
+                  "prefill_sm103.cu": ("mma_sync.cuh", "packed.cuh", "paged.cuh")}
 
 
 def kernel_hash(name: str) -> str:

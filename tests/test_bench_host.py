@@ -5,6 +5,7 @@ TFLOP/s, and the lookup of recorded DRAM traffic by kernel source hash."""
 import io
 import json
 import os
+import re
 import sys
 import types
 from contextlib import redirect_stdout
@@ -95,6 +96,21 @@ def test_recorded_traffic_follows_the_source_hash(tmp_path, monkeypatch):
     assert bench.recorded_traffic("decode_sm103.cu", "w_missing") is None
     # each kernel source has its own hash (a record of one kernel never matches another)
     assert bench.kernel_hash("decode_grouped_sm103.cu") != bench.kernel_hash("decode_sm103.cu")
+
+
+def test_kernel_hash_covers_the_included_headers():
+    """A kernel's recorded traffic goes stale when any header it includes changes (the checking build's aside)."""
+    csrc = os.path.join(bench.ROOT, "io_aware_exact_fa_gb300", "csrc")
+
+    def included(name):
+        out = set()
+        for h in re.findall(r'#include "(\w+\.cuh)"', open(os.path.join(csrc, name)).read()):
+            out |= {h} | included(h)
+        return out
+
+    for f in ("prefill_sm103.cu", "decode_sm103.cu", "backward_sm103.cu", "decode_grouped_sm103.cu",
+              "materialized_sm103.cu"):
+        assert included(f) - {"fa_ptx.cuh", "fa_common.cuh", "fa_debug.cuh"} == set(bench.KERNEL_HEADERS.get(f, ())), f
 
 
 def test_whole_job_rate_and_peaks():
