@@ -347,14 +347,12 @@ def _own_weigh(st):
 
 def _own_evict(st):
     from io_aware_exact_fa_gb300 import fa
-    if "new_weights" not in st:  # buffers of the cache that the rows move to
+    if "new_weights" not in st:  # a buffer of the cache that the rows move to
         st["new_weights"] = torch.empty(st["B"], st["Hkv"], st["width"], device="cuda")
-        st["ws"] = torch.empty(max(1, fa.evict_paged_workspace_size(st["B"], st["Hkv"], st["keep"], st["max_len"])),
-                               dtype=torch.uint8, device="cuda")
     kept, lens, weights, offsets = fa.evict_paged(
         st["weights"], st["k_pages"], st["v_pages"], st["table"], st["lens"], st["new_table"], st["keep"],
         first=st["first"], recent=st["recent"], k_scale=st["k_scale"], v_scale=st["v_scale"], offsets=st["offsets"],
-        new_weights=st["new_weights"], workspace=st["ws"])
+        new_weights=st["new_weights"])
     out = {"kept": kept, "lens": lens, "weights": weights, "offsets": offsets}
     if st["read"]:
         out["k"], out["v"] = fa.read_paged(st["k_pages"], st["v_pages"], st["new_table"], lens, st["read_cu"],
