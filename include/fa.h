@@ -416,6 +416,117 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
                           int Nq, int d, int num_pages, int page, int max_len, int e4m3, float scale, int num_splits,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* fa_append_paged on a cache that lost rows (fa_evict_paged).
+ *   offsets  int32 [B], position of row 0 of each sequence: token i of n_b is still
+ *            stored in row r = L_b - n_b + i, and turned for position
+ *            r + offsets[b], which lies in [0, 2^31). NULL: 0. */
+fa_status fa_append_paged_at(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
+                             void* v_pages, float* k_scale, float* v_scale, const int* block_table,
+                             int64_t table_stride, const int* seqlens_k, const int* cu_seqlens, const int* offsets,
+                             const int64_t* turns, const void* q_weight, const void* k_weight, const int64_t* strides,
+                             int B, int T, int H, int Hkv, int d, int num_pages, int page, int table_width, int e4m3,
+                             int rot, int interleaved, float rot_scale, float eps, int max_new, void* stream);
+
+/* ---- 4-bit pages -------------------------------------------------------------
+ * k_pages, v_pages  [num_pages, Hkv, page, d/2] bytes: e2m1 codes (values 0, 0.5, 1,
+ *     1.5, 2, 3, 4, 6, bit 3 the sign), element 2i in the lower half of byte i;
+ *     16-byte aligned.
+ * k_scale, v_scale  [num_pages, Hkv, page, d/16] bytes, 16-byte aligned: the scale of
+ *     each 16 neighbouring elements, unsigned with 5 exponent bits (bias 15) and 3
+ *     mantissa bits (an f16's upper byte without its sign). A value is code * scale,
+ *     exact in f16 and in bf16.
+ * A row takes 9/32 of its bf16 bytes. Append sets a group's scale to its largest
+ * magnitude / 6, rounded to nearest even, within [2^-17, 10240] (0 for a group of
+ * zeros; larger magnitudes saturate at 61440), and its codes to the nearest of
+ * x / scale (ties to the even code). An infinity or NaN makes its group of 16 NaN. */
+
+/* fa_append_paged_at into 4-bit pages. k is quantised as k_out holds it, in bf16;
+ * every row is on its own, so nothing written earlier changes. */
+fa_status fa_append_paged_fp4(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
+                              void* v_pages, uint8_t* k_scale, uint8_t* v_scale, const int* block_table,
+                              int64_t table_stride, const int* seqlens_k, const int* cu_seqlens, const int* offsets,
+                              const int64_t* turns, const void* q_weight, const void* k_weight, const int64_t* strides,
+                              int B, int T, int H, int Hkv, int d, int num_pages, int page, int table_width, int rot,
+                              int interleaved, float rot_scale, float eps, int max_new, void* stream);
+
+/* fa_decode_paged over 4-bit pages, and its workspace. Products run in f16 on
+ * code * scale, with the bounds that fa_decode_paged gives for q and the weights. */
+size_t fa_decode_paged_fp4_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int num_splits);
+fa_status fa_decode_paged_fp4(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
+                              const uint8_t* k_scale, const uint8_t* v_scale, const int* block_table,
+                              int64_t table_stride, const int* seqlens_k, void* o, const int64_t* o_strides, float* lse,
+                              int B, int H, int Hkv, int Nq, int d, int num_pages, int page, int max_len, float scale,
+                              int num_splits, void* workspace, size_t workspace_bytes, void* stream);
+
+/* What the pages of the calls below hold (`kind`), with their scales: none (NULL),
+ * fp32 [num_pages, Hkv], or the bytes of 4-bit pages. */
+#define FA_PAGES_BF16 0
+#define FA_PAGES_E4M3 1
+#define FA_PAGES_FP4 2
+
+/* Rows of a paged cache as packed bf16 k and v, as fa_fwd_packed takes them (the
+ * chunks of a prompt after its first attend to what the cache holds).
+ *   cu_seqlens  int32 [B+1] on the device: the last n_b = cu[b+1] - cu[b] rows of
+ *           sequence b go to rows cu[b] .. cu[b+1]-1 of k_out and v_out.
+ *   k_out, v_out  bf16 [total, Hkv, d]; strides  int64 [4], host memory: token and
+ *           head strides of k_out and v_out, as fa_append_paged's outputs have them.
+ * A sequence of length 0 is padding; output rows that no row of the cache belongs to
+ * are left as they were (rows asked for past a sequence's beginning, pages outside
+ * the pool, offsets that decrease or pass `total`: also reported). e4m3 values are
+ * rounded once to bf16. total = 0 is a no-op. One launch. Errors as for
+ * fa_append_paged, plus FA_ERR_INVALID_ARG for an unknown kind. */
+fa_status fa_read_paged(const void* k_pages, const void* v_pages, const void* k_scale, const void* v_scale, int kind,
+                        const int* block_table, int64_t table_stride, const int* seqlens_k, const int* cu_seqlens,
+                        void* k_out, void* v_out, const int64_t* strides, int B, int total, int Hkv, int d,
+                        int num_pages, int page, int table_width, void* stream);
+
+/* Adds the attention weights that the last Nq tokens of every sequence give its keys:
+ *   weights[b, hk, j] += sum over the group's heads h and tokens t that see key j of
+ *                        exp(scale <q, k_j> - lse[b, h, t])
+ *   q, q_strides, scale  as for fa_decode_paged; lse  fp32 [B, H, Nq], what
+ *           fa_decode_paged (or a prefill over the same keys) returned; rows with
+ *           lse = -inf add nothing.
+ *   weights fp32, the row of (b, hk) at (b * Hkv + hk) * weights_stride, at least
+ *           max_len long; only keys that a sequence holds are written.
+ *   max_len as for fa_decode_paged: longer sequences are clipped and reported.
+ * Sums run in fp32 in a fixed order. Keys of pages outside the pool get nothing, and
+ * the call is reported. One launch, no workspace. Errors as for fa_decode_paged,
+ * plus FA_ERR_INVALID_ARG for an unknown kind or a weights_stride below max_len. */
+fa_status fa_weigh_paged(const void* q, const int64_t* q_strides, const float* lse, const void* k_pages,
+                         const void* k_scale, int kind, const int* block_table, int64_t table_stride,
+                         const int* seqlens_k, float* weights, int64_t weights_stride, int B, int H, int Hkv, int Nq,
+                         int d, int num_pages, int page, int max_len, float scale, void* stream);
+
+/* Cuts sequences to `keep` rows. Of the L_b rows of a longer one every K/V head keeps
+ * its first `first` and last `recent`, and of the others the keep - first - recent
+ * with the largest weights (ties to the lowest index, NaN below all others); a
+ * sequence of at most `keep` rows keeps all. Row i of those that stay is copied to
+ * position i of the pages that new_table lists.
+ *   weights, weights_stride  as fa_weigh_paged leaves them.
+ *   block_table, new_table  int32 [B, ..] over the same pool. Pages of new_table are
+ *           listed once, and none of them is read by the call (block_table's pages may
+ *           be shared between sequences; the caller frees them afterwards).
+ *   kept         int32 [B, Hkv, keep]: old row of each new one, -1 past them.
+ *   new_seqlens  int32 [B]: min(L_b, keep).
+ *   new_offsets  int32 [B]: offsets[b] (NULL: 0) + L_b - new_seqlens[b], the position
+ *                of row 0 for the appends to come (the rows before the new ones keep
+ *                the rotation of their old positions). May be offsets.
+ *   new_weights  fp32 [B, Hkv, new_width] with rows new_weights_stride apart,
+ *                new_width >= keep: the kept rows' weights, then zeros.
+ * Rows of 4-bit and bf16 pages are copied as they are. The scale of a new e4m3 page is
+ * the largest of its rows' old ones (positive factors), and codes of smaller scales
+ * are rounded to it. Rows past the new length keep what the pages held. Pages outside
+ * the pool are skipped, lengths over max_len clipped, and reported. Two launches.
+ * Errors: FA_ERR_INVALID_ARG for NULL arrays, sizes, first + recent > keep, an unknown
+ * kind, strides that do not hold the rows, or new_weights, new_seqlens or new_table
+ * that are the arrays read; FA_ERR_UNSUPPORTED as for fa_append_paged. */
+fa_status fa_evict_paged(const float* weights, int64_t weights_stride, void* k_pages, void* v_pages, void* k_scale,
+                         void* v_scale, int kind, const int* block_table, int64_t table_stride, const int* seqlens_k,
+                         const int* offsets, const int* new_table, int64_t new_table_stride, int* kept,
+                         int* new_seqlens, int* new_offsets, float* new_weights, int64_t new_weights_stride,
+                         int new_width, int B, int Hkv, int d, int num_pages, int page, int max_len, int keep,
+                         int first, int recent, void* stream);
+
 /* Synchronises `stream`, then returns and clears the device status word of
  * the current device: FA_ERR_TIMEOUT if a bounded wait gave up since the
  * last call, FA_ERR_CUDA if the stream reported an error, FA_ERR_INVALID_ARG if

@@ -26,7 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa_gb300.so")
 LIB_DEBUG = os.path.join(PKG, "libfa_gb300_debug.so")
 SOURCES = ["fa_api.cu", "prefill_sm103.cu", "decode_sm103.cu", "backward_sm103.cu", "decode_grouped_sm103.cu",
-           "materialized_sm103.cu", "append_paged_sm103.cu", "decode_paged_sm103.cu"]
+           "materialized_sm103.cu", "append_paged_sm103.cu", "decode_paged_sm103.cu",
+           "read_paged_sm103.cu", "weigh_paged_sm103.cu", "evict_paged_sm103.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

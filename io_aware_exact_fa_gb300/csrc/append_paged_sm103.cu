@@ -41,6 +41,7 @@
 #include <cfloat>
 #include <climits>
 
+#include "fp4.cuh"
 #include "mma_sync.cuh"
 #include "paged.cuh"
 
@@ -52,7 +53,7 @@ constexpr int AP_THREADS = 256;        // of a block, at most
 constexpr int AP_STEP_THREADS = 64;    // and at least
 // Blocks of AP_THREADS that an SM should hold: four where 64 registers do without spilling (interleaved, bf16 cache:
 // 32 against 34 us for 9.1k tokens of 28 heads), else three (half layout: 111 against 121 us for 26.7k prompt tokens).
-constexpr int ap_ctas(bool f8, bool inter) { return !f8 && inter ? 4 : 3; }
+constexpr int ap_ctas(int kind, bool inter) { return kind == PAGES_BF16 && inter ? 4 : 3; }
 #ifndef AP_RING
 #define AP_RING 3       // heads of a row whose copies a query thread has in flight
 #endif
@@ -316,6 +317,11 @@ __device__ __forceinline__ bool tokens_of(const AppendPagedParams& p, int b, int
   return false;
 }
 
+// What is added to a row of sequence b to give the position that its rotation counts from.
+__device__ __forceinline__ unsigned offset_of(const AppendPagedParams& p, int b) {
+  return p.offsets == nullptr ? 0u : static_cast<unsigned>(__ldg(p.offsets + b));
+}
+
 // ---- query block: rows tok0 .. of the step, all heads
 template <int D, bool INTER>
 __device__ __forceinline__ void query_block(const AppendPagedParams& p, int block, int* s_pos, uint4* ring) {
@@ -331,7 +337,7 @@ __device__ __forceinline__ void query_block(const AppendPagedParams& p, int bloc
     for (int r = tid; r < rows; r += nt) {
       const int tok = tok0 + r, b = tok / n;
       const int L = tok < p.T ? __ldg(p.seqlens + b) : 0;
-      s_pos[r] = L != 0 ? static_cast<int>(static_cast<unsigned>(L) - n + (tok - b * n)) : NONE;
+      s_pos[r] = L != 0 ? static_cast<int>(static_cast<unsigned>(L) - n + (tok - b * n) + offset_of(p, b)) : NONE;
     }
   } else {
     for (int r = tid; r < rows; r += nt) s_pos[r] = NONE;
@@ -343,7 +349,8 @@ __device__ __forceinline__ void query_block(const AppendPagedParams& p, int bloc
       if (a < e) {
         const int L = __ldg(p.seqlens + b);
         if (L != 0)  // (a position that wraps lies outside the cache, which the K/V blocks report)
-          for (int t = a; t < e; ++t) s_pos[t - tok0] = static_cast<int>(static_cast<unsigned>(L) - all + (t - t0));
+          for (int t = a; t < e; ++t)
+            s_pos[t - tok0] = static_cast<int>(static_cast<unsigned>(L) - all + (t - t0) + offset_of(p, b));
       }
     }
   }
@@ -399,9 +406,10 @@ __device__ __forceinline__ void query_block(const AppendPagedParams& p, int bloc
 }
 
 // ---- K/V block: the new rows of one page, one K/V head
-template <int D, bool F8, bool INTER>
+template <int D, int KIND, bool INTER>
 __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, unsigned int* s_amax, uint4* stash) {
   constexpr int LPR = D / 16;
+  constexpr bool F8 = KIND == PAGES_E4M3, F4 = KIND == PAGES_FP4;
   const int tid = threadIdx.x, nt = blockDim.x;
   const int groups = nt / LPR;
   const int hk = block % p.Hkv, c = block / p.Hkv;
@@ -441,11 +449,15 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
   const int nrows = r1 - r0;
   const int tok0 = t0 + static_cast<int>(first + r0 - start);    // token of row r0
 
+  const uint32_t offset = offset_of(p, b);
+
   // the table entry and the first rows are asked for together
   const bool in_table = page0 >= 0 && page0 < p.width;
   const int id = in_table ? __ldg(p.table + b * p.table_stride + page0) : -1;
   const int grp = tid / LPR, u = tid % LPR;
   const UnitPlace<INTER> at(u, p.rot);
+  // (a 4-bit row's values are taken 16 neighbours at a time, the elements of one scale)
+  const int vc0 = F4 ? 16 * u : at.c0, vc1 = F4 ? 16 * u + 8 : at.c1;
   const uint16_t* kb = static_cast<const uint16_t*>(p.k) + tok0 * p.kst + hk * p.ksh;
   const uint16_t* vb = static_cast<const uint16_t*>(p.v) + tok0 * p.vst + hk * p.vsh;
   // every round's rows are copied to this thread's own pieces of shared memory: 0, 1 the key, 4, 5 the value
@@ -458,8 +470,8 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
     const uint16_t* vs = vb + (nb ? r * p.vst : 0);
     cp_async16_ca(mine, ks + at.c0, nb);
     cp_async16_ca(mine + nt * 16, ks + at.c1, nb);
-    cp_async16_ca(mine + VP * nt * 16, vs + at.c0, nb);
-    cp_async16_ca(mine + (VP + 1) * nt * 16, vs + at.c1, nb);
+    cp_async16_ca(mine + VP * nt * 16, vs + vc0, nb);
+    cp_async16_ca(mine + (VP + 1) * nt * 16, vs + vc1, nb);
   }
   cp_async_commit();
   const long long pbase = paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, 0, D);
@@ -491,21 +503,53 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
         x.b[j] = fmul2(x.b[j], w.b[j]);
       }
     }
-    if (!ok) continue;
+    if (!F4 && !ok) continue;  // (4-bit rows: whole warps shuffle below)
     if (at.turned) {
       Angles t;
-      angles_at(t, static_cast<uint32_t>(first) + r0 + r, p.turns + 8 * u, p.rot_scale);
+      angles_at(t, static_cast<uint32_t>(first) + r0 + r + offset, p.turns + 8 * u, p.rot_scale);
       turn(x, t);
     }
     float y[16];
     in_order<INTER>(x, y);
     const uint4 y0 = pack8(y), y1 = pack8(y + 8);
-    if (kob != nullptr) {
+    if (kob != nullptr && ok) {
       *reinterpret_cast<uint4*>(kob + r * p.kost + at.c0) = y0;
       *reinterpret_cast<uint4*>(kob + r * p.kost + at.c1) = y1;
     }
     if (!store) continue;
-    if constexpr (F8) {
+    if constexpr (F4) {
+      // The key as k_out gives it, in bf16. A scale's 16 neighbours are blocks 2i and 2i + 1 of eight elements; this thread
+      // has blocks c0 / 8 and c1 / 8, and the other one of each pair may be another thread's of the same row.
+      uint32_t m0 = bf16x8_amax_bits(y0), m1 = bf16x8_amax_bits(y1);
+      if (INTER || !at.turned) m0 = m1 = max(m0, m1);
+      if (!INTER) {
+        const int turned = p.rot / 16;  // units that are
+        auto other = [&](int block) {   // largest magnitude of block ^ 1
+          const int k = block ^ 1;
+          const int from = k < turned ? k : k < 2 * turned ? k - turned : turned + (k - 2 * turned) / 2;
+          const uint32_t a = __shfl_sync(0xffffffffu, m0, from, LPR), c = __shfl_sync(0xffffffffu, m1, from, LPR);
+          return k < turned ? a : c;
+        };
+        const uint32_t o0 = other(at.c0 / 8), o1 = other(at.c1 / 8);
+        m0 = max(m0, o0);
+        m1 = max(m1, o1);
+      }
+      if (!ok) continue;
+      const uint4 v0 = mine[VP * nt], v1 = mine[(VP + 1) * nt];
+      float i0, i1, iv;
+      const uint32_t s0 = fp4_scale_byte(m0, i0), s1 = fp4_scale_byte(m1, i1);
+      const uint32_t sv = fp4_scale_byte(max(bf16x8_amax_bits(v0), bf16x8_amax_bits(v1)), iv);
+      const long long row = pbase / D + r0 + r;
+      uint8_t* kd = static_cast<uint8_t*>(p.k_pages) + row * (D / 2);
+      uint8_t* vd = static_cast<uint8_t*>(p.v_pages) + row * (D / 2);
+      *reinterpret_cast<uint32_t*>(kd + at.c0 / 2) = fp4_codes8(y0, i0);
+      *reinterpret_cast<uint32_t*>(kd + at.c1 / 2) = fp4_codes8(y1, i1);
+      *reinterpret_cast<uint2*>(vd + 8 * u) = make_uint2(fp4_codes8(v0, iv), fp4_codes8(v1, iv));
+      // (both threads of a group have the same scale; the one with the even block writes it)
+      if ((at.c0 & 8) == 0) p.k_scale4[row * (D / 16) + at.c0 / 16] = static_cast<uint8_t>(s0);
+      if ((at.c1 & 8) == 0) p.k_scale4[row * (D / 16) + at.c1 / 16] = static_cast<uint8_t>(s1);
+      p.v_scale4[row * (D / 16) + u] = static_cast<uint8_t>(sv);
+    } else if constexpr (F8) {
       am_k = fmaxf(am_k, finite_amax(y));
       // the turned key, in fp32, over pieces 0 .. 3
 #pragma unroll
@@ -590,8 +634,8 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
 
 }  // namespace
 
-template <int D, bool F8, bool INTER>
-__global__ void __launch_bounds__(AP_THREADS, ap_ctas(F8, INTER)) fa_append_paged_kernel(const AppendPagedParams p) {
+template <int D, int KIND, bool INTER>
+__global__ void __launch_bounds__(AP_THREADS, ap_ctas(KIND, INTER)) fa_append_paged_kernel(const AppendPagedParams p) {
   extern __shared__ __align__(16) uint4 ap_stash[];  // 16-byte pieces, one of each thread next to one another
   __shared__ int s_pos[AP_THREADS / (D / 16)];
   __shared__ unsigned int s_amax[2];
@@ -600,7 +644,7 @@ __global__ void __launch_bounds__(AP_THREADS, ap_ctas(F8, INTER)) fa_append_page
   // rows, the page's largest value), which the query blocks beside it fill.
   const unsigned long long blocks = gridDim.x;
   const int before = static_cast<int>(static_cast<unsigned long long>(block) * p.kv_blocks / blocks);  // K/V blocks before this one
-  if (static_cast<int>((block + 1ull) * p.kv_blocks / blocks) > before) kv_block<D, F8, INTER>(p, before, s_amax, ap_stash);
+  if (static_cast<int>((block + 1ull) * p.kv_blocks / blocks) > before) kv_block<D, KIND, INTER>(p, before, s_amax, ap_stash);
   else query_block<D, INTER>(p, block - before, s_pos, ap_stash);
 }
 
@@ -609,21 +653,27 @@ static int ap_smem_bytes(int D, bool f8, int rows, int threads) {
   const int groups = threads / (D / 16);
   return std::max((rows + groups - 1) / groups * (f8 ? 6 : 4), 2 * AP_RING) * threads * 16;
 }
-template <int D, bool F8, bool INTER>
+template <int D, int KIND, bool INTER>
 static cudaError_t ap_attr() {
-  return cudaFuncSetAttribute(fa_append_paged_kernel<D, F8, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ap_smem_bytes(D, F8, 128, AP_THREADS));
+  return cudaFuncSetAttribute(fa_append_paged_kernel<D, KIND, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              ap_smem_bytes(D, KIND == PAGES_E4M3, 128, AP_THREADS));
+}
+template <int KIND>
+static cudaError_t ap_attrs() {
+  cudaError_t e = cudaSuccess;
+  for (cudaError_t x : {ap_attr<64, KIND, false>(), ap_attr<64, KIND, true>(), ap_attr<128, KIND, false>(),
+                        ap_attr<128, KIND, true>()})
+    if (x != cudaSuccess) e = x;
+  return e;
 }
 cudaError_t append_paged_set_attributes() {
   cudaError_t e = cudaSuccess;
-  for (cudaError_t x : {ap_attr<64, false, false>(), ap_attr<64, false, true>(), ap_attr<64, true, false>(),
-                        ap_attr<64, true, true>(), ap_attr<128, false, false>(), ap_attr<128, false, true>(),
-                        ap_attr<128, true, false>(), ap_attr<128, true, true>()})
+  for (cudaError_t x : {ap_attrs<PAGES_BF16>(), ap_attrs<PAGES_E4M3>(), ap_attrs<PAGES_FP4>()})
     if (x != cudaSuccess) e = x;
   return e;
 }
 
-template <int D, bool F8, bool INTER>
+template <int D, int KIND, bool INTER>
 static cudaError_t ap_launch(AppendPagedParams p, cudaStream_t stream) {
   // As many threads as a page's new rows occupy, so that an SM holds many blocks of small pages or short steps (256
   // sequences of one token, 8 K/V heads: 8 us, 21 with 256 threads; 26.7k prompt tokens into pages of 16: 125 us, 170).
@@ -639,17 +689,21 @@ static cudaError_t ap_launch(AppendPagedParams p, cudaStream_t stream) {
   p.q_slots = slots;
   const int rows = groups / slots;
   const long long q_blocks = (static_cast<long long>(p.T) + rows - 1) / rows;
-  const size_t smem = ap_smem_bytes(D, F8, p.max_rows, threads);
-  fa_append_paged_kernel<D, F8, INTER><<<static_cast<unsigned>(p.kv_blocks + q_blocks), threads, smem, stream>>>(p);
+  const size_t smem = ap_smem_bytes(D, KIND == PAGES_E4M3, p.max_rows, threads);
+  fa_append_paged_kernel<D, KIND, INTER><<<static_cast<unsigned>(p.kv_blocks + q_blocks), threads, smem, stream>>>(p);
   return cudaGetLastError();
 }
-template <int D>
-static cudaError_t ap_launch_d(bool f8, const AppendPagedParams& p, cudaStream_t stream) {
-  if (p.interleaved) return f8 ? ap_launch<D, true, true>(p, stream) : ap_launch<D, false, true>(p, stream);
-  return f8 ? ap_launch<D, true, false>(p, stream) : ap_launch<D, false, false>(p, stream);
+template <int D, int KIND>
+static cudaError_t ap_launch_kind(const AppendPagedParams& p, cudaStream_t stream) {
+  return p.interleaved ? ap_launch<D, KIND, true>(p, stream) : ap_launch<D, KIND, false>(p, stream);
 }
-cudaError_t launch_append_paged(bool f8, const AppendPagedParams& p, cudaStream_t stream) {
-  return p.d == 64 ? ap_launch_d<64>(f8, p, stream) : ap_launch_d<128>(f8, p, stream);
+template <int D>
+static cudaError_t ap_launch_d(int kind, const AppendPagedParams& p, cudaStream_t stream) {
+  if (kind == PAGES_FP4) return ap_launch_kind<D, PAGES_FP4>(p, stream);
+  return kind == PAGES_E4M3 ? ap_launch_kind<D, PAGES_E4M3>(p, stream) : ap_launch_kind<D, PAGES_BF16>(p, stream);
+}
+cudaError_t launch_append_paged(int kind, const AppendPagedParams& p, cudaStream_t stream) {
+  return p.d == 64 ? ap_launch_d<64>(kind, p, stream) : ap_launch_d<128>(kind, p, stream);
 }
 
 }  // namespace fa

@@ -49,6 +49,7 @@
 
 #include <type_traits>
 
+#include "fp4.cuh"
 #include "mma_sync.cuh"
 #include "paged.cuh"
 
@@ -62,26 +63,27 @@ constexpr int DP_THREADS = 32 * DP_WARPS;
 // Where the weights 2^(z - M) lie: the base M is set so that a row's largest z is TOP above it, and moves when one passes
 // it by more than LIMIT. bf16 weights have fp32's exponents; f16 ends at 2^16, and its weights lie as high as that allows,
 // to leave room below for pages whose scales are smaller, up to 2^-GAP times (see `far`).
-template <bool F8>
+template <bool F16>
 struct DpBase {
-  static constexpr float TOP = F8 ? 7.f : 0.f, LIMIT = F8 ? 15.f : 8.f, GAP = TOP;
+  static constexpr float TOP = F16 ? 7.f : 0.f, LIMIT = F16 ? 15.f : 8.f, GAP = TOP;
 };
 
-template <int D, bool F8, int NR>
+template <int D, int KIND, int NR>
 struct DpCfg {
+  static constexpr bool F8 = KIND == PAGES_E4M3, F4 = KIND == PAGES_FP4;
   static constexpr int ROWS = 8 * NR;            // query rows of a warp
-  static constexpr int ESZ = F8 ? 1 : 2;
-  static constexpr int RB = D * ESZ;             // bytes of a key's row: 64, 128 or 256
+  static constexpr int RB = paged_row_bytes(KIND, D);  // bytes of a key's row: 32, 64, 128 or 256
   static constexpr int CR = RB / 16;             // 16-byte pieces of a row
-  static constexpr int HALF = 4096;              // K (or V) bytes of a tile
-  static constexpr int KS = HALF / RB;           // its keys
+  static constexpr int KS = F4 ? 64 : 4096 / RB; // keys of a tile
+  static constexpr int HALF = KS * RB;           // its K (or V) bytes
   static constexpr int KG = KS / 16;             // its 16-key groups
-  static constexpr int EPC = 16 / ESZ;           // elements of a piece
+  static constexpr int EPC = D / CR;             // elements of a piece
   static constexpr int DL = D / 4;               // elements of a K row that one lane holds
-  static constexpr int NPK = DL / EPC;           // as pieces
+  static constexpr int NPK = DL / EPC;           // as pieces (of which a lane holds half one in 4-bit rows of d = 64)
   static constexpr int KST = D / 16;             // k-steps of S^T, and M tiles of O^T
+  static constexpr int SB = F4 ? D / 16 : 0;     // scale bytes of a 4-bit row
   static constexpr int META = KG * 2 * 4;        // e4m3 scales of a tile
-  static constexpr int STAGE = 2 * HALF;
+  static constexpr int STAGE = 2 * HALF + 2 * KS * SB;
   // Tiles in each warp's ring: what fits beside the warps an SM holds. (Three tiles for eight warps against two for
   // twelve: 136 against 130 us at 8 rows, e4m3, d = 128. Tiles of half the size, four to a ring: 134. Sixteen warps
   // of those: 133.)
@@ -94,22 +96,24 @@ struct DpCfg {
 // Byte offset of 16-byte piece c of row r in a tile of RB-byte rows.
 template <int RB>
 __device__ __forceinline__ uint32_t dp_swz(uint32_t r, uint32_t c) {
-  if constexpr (RB == 64)
+  if constexpr (RB == 32)
+    return (r >> 2) * 128u + (((((r & 3u) << 1) | c) ^ (((r >> 2) & 1u) << 1)) << 4);
+  else if constexpr (RB == 64)
     return (r >> 1) * 128u + (((((r & 1u) << 2) | c) ^ (((r >> 1) & 3u) << 1)) << 4);
   else
     return r * RB + (((c & ~7u) | ((c ^ r) & 7u)) << 4);
 }
 
 // The piece of a K row that lane tig holds i-th.
-template <int D, bool F8>
+template <int D, int KIND>
 __device__ __forceinline__ int dp_k_piece(int tig, int i) {
-  if constexpr (F8 && D == 64) return tig;
+  if constexpr (paged_row_bytes(KIND, D) == 64) return tig;
   else return 2 * tig + (i & 1) + 8 * (i >> 1);
 }
 // First of the four output elements 4 jj .. 4 jj + 3 (of its D / 8) that lane group gid holds: M tile j has 2j, 2j + 1.
-template <int D, bool F8>
+template <int D, int KIND>
 __device__ __forceinline__ int dp_o_elem(int gid, int jj) {
-  if constexpr (!F8 && D == 128) return (gid + 8 * (jj >> 1)) * 8 + (jj & 1) * 4;
+  if constexpr (KIND == PAGES_BF16 && D == 128) return (gid + 8 * (jj >> 1)) * 8 + (jj & 1) * 4;
   else return gid * (D / 8) + 4 * jj;
 }
 
@@ -131,9 +135,10 @@ __device__ __forceinline__ int dp_len(const DecodePagedParams& p, int b) {
 
 }  // namespace
 
-template <int D, bool F8, int NR>
+template <int D, int KIND, int NR>
 __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_decode_paged_kernel(const DecodePagedParams p) {
-  using C = DpCfg<D, F8, NR>;
+  using C = DpCfg<D, KIND, NR>;
+  constexpr bool F8 = C::F8, F4 = C::F4, F16 = F8 || F4;  // e4m3 codes, 4-bit rows; products in f16
   extern __shared__ __align__(128) uint8_t dp_smem[];
   const uint32_t sbase = smem_u32(dp_smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
   };
   int id = page_of();
   constexpr int RPI = 32 / C::CR;                                        // rows of one copy instruction of the warp
-  constexpr int PERIOD = C::RB == 64 ? 1 : (8 / RPI > 1 ? 8 / RPI : 1);  // after which the swizzle repeats
+  constexpr int PERIOD = C::RB <= 64 ? 1 : (8 / RPI > 1 ? 8 / RPI : 1);  // after which the swizzle repeats
   const int piece = lane % C::CR, rin = lane / C::CR;
   uint32_t dst[PERIOD];
 #pragma unroll
@@ -250,8 +255,8 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
       for (int g = 0; g < C::KG; ++g) {
         const long long goff = __shfl_sync(ALL, off, g);
         const int left = goff < 0 ? 0 : cL - (key0 + 16 * g);  // rows of the group to read
-        const uint8_t* kg = static_cast<const uint8_t*>(p.k) + (goff < 0 ? 0 : goff) * C::ESZ;
-        const uint8_t* vg = static_cast<const uint8_t*>(p.v) + (goff < 0 ? 0 : goff) * C::ESZ;
+        const uint8_t* kg = static_cast<const uint8_t*>(p.k) + (goff < 0 ? 0 : F4 ? goff >> 1 : goff * (C::RB / D));
+        const uint8_t* vg = static_cast<const uint8_t*>(p.v) + (goff < 0 ? 0 : F4 ? goff >> 1 : goff * (C::RB / D));
         if (left >= 16) {
           kg += src_lane;
           vg += src_lane;
@@ -270,6 +275,18 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
             cp_async16(to, kg + so, n);
             cp_async16(to + C::HALF, vg + so, n);
           }
+        }
+      }
+      if constexpr (F4) {  // a group's scales are SB 16-byte pieces; first those of K, then those of V
+        constexpr int PIECES = C::KG * C::SB;
+#pragma unroll
+        for (int x0 = 0; x0 < 2 * PIECES; x0 += 32) {
+          const int x = (x0 + lane) % PIECES, g = x / C::SB, pc = x % C::SB;
+          const bool is_v = x0 + lane >= PIECES;
+          const long long goff = __shfl_sync(ALL, off, g);
+          const int n = goff < 0 ? 0 : min(max((cL - (key0 + 16 * g)) * C::SB - 16 * pc, 0), 16);
+          const uint8_t* src = (is_v ? p.v_scale4 : p.k_scale4) + (n > 0 ? (goff >> 4) + 16 * pc : 0);
+          cp_async16(kdst + 2 * C::HALF + (x0 + lane) * 16, src, n);
         }
       }
       ++copied;
@@ -300,13 +317,13 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
       uint2 raw[C::KST];
 #pragma unroll
       for (int j = 0; j < C::KST; ++j) {  // elements 4j .. 4j + 3 of the lane's
-        const int d0 = dp_k_piece<D, F8>(tig, 4 * j / C::EPC) * C::EPC + (4 * j) % C::EPC;
+        const int d0 = F4 ? tig * C::DL + 4 * j : dp_k_piece<D, KIND>(tig, 4 * j / C::EPC) * C::EPC + (4 * j) % C::EPC;
         raw[j] = in ? __ldg(reinterpret_cast<const uint2*>(qr + d0)) : make_uint2(0u, 0u);
       }
       float row_factor = 1.f;
-      if constexpr (F8) {
-        // The products with the codes run in f16 (every e4m3 code is an f16
-        // value). The row's power of two 2^x brings its largest element to [1, 2):
+      if constexpr (F16) {
+        // The products with the codes run in f16 (every e4m3 code, and every e2m1
+        // code times its scale, is an f16 value). The row's power of two 2^x brings its largest element to [1, 2):
         // elements down to 2^-14 of it keep all their 8 bits, smaller ones are
         // off by at most 2^-25 of 2^x: a score by d 2^-25 max|q| max|k| at most.
         float amax = 0.f;
@@ -336,7 +353,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        c1[n][e] = p.scale_log2 * (F8 ? __shfl_sync(ALL, row_factor, (2 * tig + e) * 4) : 1.f);
+        c1[n][e] = p.scale_log2 * (F16 ? __shfl_sync(ALL, row_factor, (2 * tig + e) * 4) : 1.f);
         const int r2 = rt * C::ROWS + n * 8 + 2 * tig + e;
         lim[n][e] = min(L - 1, r2 < p.R ? L - p.Nq + r2 % p.Nq : L - 1);
       }
@@ -370,29 +387,65 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
         for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+        if constexpr (F4) {
+          constexpr int NW = D / 32;  // words of the lane's codes in a row: 4 or 2, two of them (d = 128) to a scale
+          uint32_t w[2][NW], f[2];
 #pragma unroll
-        for (int i2 = 0; i2 < C::NPK; ++i2) {
-          const int piece = dp_k_piece<D, F8>(tig, i2);
-          const uint4 ra = *reinterpret_cast<const uint4*>(kt + dp_swz<C::RB>(16 * g + gid, piece));
-          const uint4 rb = *reinterpret_cast<const uint4*>(kt + dp_swz<C::RB>(16 * g + gid + 8, piece));
-          const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-          if constexpr (F8) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16x2x2(wa[w], a0, a2);
-              e4m3x4_to_f16x2x2(wb[w], a1, a3);
-#pragma unroll
-              for (int n = 0; n < NR; ++n)
-                mma_16816<true>(s[n], a0, a1, a2, a3, qf[n][i2 * 4 + w][0], qf[n][i2 * 4 + w][1]);
+          for (int h = 0; h < 2; ++h) {
+            const int r = 16 * g + gid + 8 * h;
+            const uint8_t* sp = vt + C::HALF + r * C::SB;
+            if constexpr (D == 128) {
+              const uint4 y = *reinterpret_cast<const uint4*>(kt + dp_swz<C::RB>(r, tig));
+              w[h][0] = y.x, w[h][1] = y.y, w[h][2] = y.z, w[h][3] = y.w;
+              f[h] = *reinterpret_cast<const uint16_t*>(sp + 2 * tig);
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(kt + dp_swz<C::RB>(r, tig >> 1) + (tig & 1) * 8u);
+              w[h][0] = y.x, w[h][1] = y.y;
+              f[h] = sp[tig];
             }
-          } else {
+          }
+          const uint32_t fa[2] = {fp4_scale2<0>(f[0]), fp4_scale2<1>(f[0])}, fb[2] = {fp4_scale2<0>(f[1]), fp4_scale2<1>(f[1])};
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
+          for (int x = 0; x < NW; ++x) {
+            uint32_t a[4], b4[4];
+            e2m1x8_to_f16x2x4(w[0][x], a);
+            e2m1x8_to_f16x2x4(w[1][x], b4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[e] = hmul2_bits(a[e], fa[x >> 1]);
+              b4[e] = hmul2_bits(b4[e], fb[x >> 1]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int n = 0; n < NR; ++n)
-                mma_16816<false>(s[n], wa[2 * w], wb[2 * w], wa[2 * w + 1], wb[2 * w + 1], qf[n][i2 * 2 + w][0],
-                                 qf[n][i2 * 2 + w][1]);
+                mma_16816<true>(s[n], a[2 * h], b4[2 * h], a[2 * h + 1], b4[2 * h + 1], qf[n][2 * x + h][0], qf[n][2 * x + h][1]);
+          }
+        } else {
+#pragma unroll
+          for (int i2 = 0; i2 < C::NPK; ++i2) {
+            const int piece = dp_k_piece<D, KIND>(tig, i2);
+            const uint4 ra = *reinterpret_cast<const uint4*>(kt + dp_swz<C::RB>(16 * g + gid, piece));
+            const uint4 rb = *reinterpret_cast<const uint4*>(kt + dp_swz<C::RB>(16 * g + gid + 8, piece));
+            const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+            if constexpr (F8) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16x2x2(wa[w], a0, a2);
+                e4m3x4_to_f16x2x2(wb[w], a1, a3);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                  mma_16816<true>(s[n], a0, a1, a2, a3, qf[n][i2 * 4 + w][0], qf[n][i2 * 4 + w][1]);
+              }
+            } else {
+#pragma unroll
+              for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                  mma_16816<false>(s[n], wa[2 * w], wb[2 * w], wa[2 * w + 1], wb[2 * w + 1], qf[n][i2 * 2 + w][0],
+                                   qf[n][i2 * 2 + w][1]);
+            }
           }
         }
       };
@@ -454,7 +507,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          over = over || mx[n][e] > (M[n][e] == -INFINITY ? -INFINITY : DpBase<F8>::LIMIT);
+          over = over || mx[n][e] > (M[n][e] == -INFINITY ? -INFINITY : DpBase<F16>::LIMIT);
       if (__any_sync(ALL, over)) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -465,7 +518,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
             up = fmaxf(up, __shfl_xor_sync(ALL, up, 8));
             up = fmaxf(up, __shfl_xor_sync(ALL, up, 16));
             const bool none = M[n][e] == -INFINITY;
-            up -= DpBase<F8>::TOP;
+            up -= DpBase<F16>::TOP;
             if (none) M[n][e] = up;                 // (still -inf when this tile shows the row nothing)
             else M[n][e] += up = fmaxf(up, 0.f);    // the base only rises
             up = up == -INFINITY ? 0.f : up;
@@ -494,15 +547,53 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
           const uint64_t ws = fadd2(f2pack(w0, w1), f2pack(w2, w3));
           const uint64_t l2 = f2pack(l[n][0], l[n][1]);
           f2unpack(F8 ? ffma2(ws, f2pack(rv[g], rv[g]), l2) : fadd2(l2, ws), l[n][0], l[n][1]);
-          pf[g][n][0] = movmatrix_trans(F8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1));
-          pf[g][n][1] = movmatrix_trans(F8 ? pack_f16x2(w2, w3) : pack_bf16x2(w2, w3));
+          pf[g][n][0] = movmatrix_trans(F16 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1));
+          pf[g][n][1] = movmatrix_trans(F16 ? pack_f16x2(w2, w3) : pack_bf16x2(w2, w3));
         }
       // ---- O^T += V^T W^T
       // (FAR: times f for each row)
       auto product = [&](int g, const uint32_t (&w)[NR][2], auto far_group, const float (&f)[NR][2]) {
         constexpr bool FAR = decltype(far_group)::value;
         const uint32_t r0 = 16 * g + 2 * tig;
-        if constexpr (F8) {
+        if constexpr (F4) {
+          constexpr int NW = D / 64;  // 32-bit words of the lane's codes in a row: 2 or 1, all of one scale
+          uint32_t v[4][NW], f[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t row = r0 + (q & 1) + 8 * (q >> 1);
+            const uint8_t* sp = vt + C::HALF + (C::KS + row) * C::SB;
+            if constexpr (D == 128) {
+              const uint2 y = *reinterpret_cast<const uint2*>(vt + dp_swz<C::RB>(row, gid >> 1) + (gid & 1) * 8u);
+              v[q][0] = y.x, v[q][1] = y.y;
+              f[q] = sp[gid];
+            } else {
+              v[q][0] = *reinterpret_cast<const uint32_t*>(vt + dp_swz<C::RB>(row, gid >> 2) + (gid & 3) * 4u);
+              f[q] = sp[gid >> 1];
+            }
+          }
+          const uint32_t fx = fp4_scale_pair(f[0], f[1]), fy = fp4_scale_pair(f[2], f[3]);
+          // a byte of two neighbouring keys' codes of one element, the later key above: lower halves elements 0, 2, 4, 6
+          auto even = [](uint32_t a, uint32_t b2) { return (a & 0x0f0f0f0fu) | ((b2 << 4) & 0xf0f0f0f0u); };
+          auto odd = [](uint32_t a, uint32_t b2) { return ((a >> 4) & 0x0f0f0f0fu) | (b2 & 0xf0f0f0f0u); };
+#pragma unroll
+          for (int x = 0; x < NW; ++x) {
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            e2m1x8_to_f16x2x4(even(v[0][x], v[1][x]), a0);
+            e2m1x8_to_f16x2x4(odd(v[0][x], v[1][x]), a1);
+            e2m1x8_to_f16x2x4(even(v[2][x], v[3][x]), a2);
+            e2m1x8_to_f16x2x4(odd(v[2][x], v[3][x]), a3);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a0[e] = hmul2_bits(a0[e], fx);
+              a1[e] = hmul2_bits(a1[e], fx);
+              a2[e] = hmul2_bits(a2[e], fy);
+              a3[e] = hmul2_bits(a3[e], fy);
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                mma_16816<true>(oacc[n][4 * x + e], a0[e], a1[e], a2[e], a3[e], w[n][0], w[n][1]);
+            }
+          }
+        } else if constexpr (F8) {
           constexpr int NW32 = D / 32;  // 32-bit words of the lane's codes: 4 or 2
           uint32_t v[4][NW32];
 #pragma unroll
@@ -633,7 +724,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
           uint16_t* op = static_cast<uint16_t*>(p.o) + b * p.osb + h * p.osh + tok * p.ost;
 #pragma unroll
           for (int jj = 0; jj < C::KST / 2; ++jj)
-            *reinterpret_cast<uint2*>(op + dp_o_elem<D, F8>(gid, jj)) =
+            *reinterpret_cast<uint2*>(op + dp_o_elem<D, KIND>(gid, jj)) =
                 make_uint2(pack_bf16x2(out(oacc[n][2 * jj][e]), out(oacc[n][2 * jj][e + 2])),
                            pack_bf16x2(out(oacc[n][2 * jj + 1][e]), out(oacc[n][2 * jj + 1][e + 2])));
           if (p.lse != nullptr && gid == 0)
@@ -646,7 +737,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
           float* op = p.ws_o + part * D;
 #pragma unroll
           for (int jj = 0; jj < C::KST / 2; ++jj)
-            *reinterpret_cast<float4*>(op + dp_o_elem<D, F8>(gid, jj)) = make_float4(
+            *reinterpret_cast<float4*>(op + dp_o_elem<D, KIND>(gid, jj)) = make_float4(
                 oacc[n][2 * jj][e], oacc[n][2 * jj][e + 2], oacc[n][2 * jj + 1][e], oacc[n][2 * jj + 1][e + 2]);
           if (gid == 0) *reinterpret_cast<float2*>(p.ws_ml + part * 2) = make_float2(m, t);
         }
@@ -766,25 +857,30 @@ __global__ void __launch_bounds__(32 * DP_MERGE_WARPS) fa_decode_paged_merge_ker
     p.lse[row] = m == -INFINITY ? -INFINITY : (m + lg2_approx(lt)) * 0.69314718055994530942f;
 }
 
-template <int D, bool F8, int NR>
+template <int D, int KIND, int NR>
 static cudaError_t dp_attr() {
-  return cudaFuncSetAttribute(fa_decode_paged_kernel<D, F8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              DpCfg<D, F8, NR>::SMEM);
+  return cudaFuncSetAttribute(fa_decode_paged_kernel<D, KIND, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              DpCfg<D, KIND, NR>::SMEM);
+}
+template <int KIND>
+static cudaError_t dp_attrs() {
+  cudaError_t e = cudaSuccess;
+  for (cudaError_t x : {dp_attr<64, KIND, 1>(), dp_attr<64, KIND, 2>(), dp_attr<128, KIND, 1>(), dp_attr<128, KIND, 2>()})
+    if (x != cudaSuccess) e = x;
+  return e;
 }
 cudaError_t decode_paged_set_attributes() {
   cudaError_t e = cudaSuccess;
-  for (cudaError_t x : {dp_attr<64, false, 1>(), dp_attr<64, false, 2>(), dp_attr<64, true, 1>(), dp_attr<64, true, 2>(),
-                        dp_attr<128, false, 1>(), dp_attr<128, false, 2>(), dp_attr<128, true, 1>(),
-                        dp_attr<128, true, 2>()})
+  for (cudaError_t x : {dp_attrs<PAGES_BF16>(), dp_attrs<PAGES_E4M3>(), dp_attrs<PAGES_FP4>()})
     if (x != cudaSuccess) e = x;
   return e;
 }
 
-template <int D, bool F8, int NR>
+template <int D, int KIND, int NR>
 static cudaError_t dp_launch(const DecodePagedParams& p, cudaStream_t stream) {
-  using C = DpCfg<D, F8, NR>;
+  using C = DpCfg<D, KIND, NR>;
   const long long workers = static_cast<long long>(p.n_ranges) * p.row_tiles;
-  fa_decode_paged_kernel<D, F8, NR><<<static_cast<unsigned>((workers + DP_WARPS - 1) / DP_WARPS), DP_THREADS, C::SMEM, stream>>>(p);
+  fa_decode_paged_kernel<D, KIND, NR><<<static_cast<unsigned>((workers + DP_WARPS - 1) / DP_WARPS), DP_THREADS, C::SMEM, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the merge's CTAs may be set up while the last ranges run; those that read parts wait for them
@@ -805,13 +901,17 @@ static cudaError_t dp_launch(const DecodePagedParams& p, cudaStream_t stream) {
               : cudaLaunchKernelEx(&cfg, fa_decode_paged_merge_kernel<D, 1>, p, C::ROWS);
 }
 
-template <int D, bool F8>
+template <int D, int KIND>
 static cudaError_t dp_launch_rows(const DecodePagedParams& p, cudaStream_t stream) {
-  return decode_paged_rows(p.R) == 8 ? dp_launch<D, F8, 1>(p, stream) : dp_launch<D, F8, 2>(p, stream);
+  return decode_paged_rows(p.R) == 8 ? dp_launch<D, KIND, 1>(p, stream) : dp_launch<D, KIND, 2>(p, stream);
 }
-cudaError_t launch_decode_paged(int d, bool f8, const DecodePagedParams& p, cudaStream_t stream) {
-  if (d == 64) return f8 ? dp_launch_rows<64, true>(p, stream) : dp_launch_rows<64, false>(p, stream);
-  return f8 ? dp_launch_rows<128, true>(p, stream) : dp_launch_rows<128, false>(p, stream);
+template <int D>
+static cudaError_t dp_launch_kind(int kind, const DecodePagedParams& p, cudaStream_t stream) {
+  if (kind == PAGES_FP4) return dp_launch_rows<D, PAGES_FP4>(p, stream);
+  return kind == PAGES_E4M3 ? dp_launch_rows<D, PAGES_E4M3>(p, stream) : dp_launch_rows<D, PAGES_BF16>(p, stream);
+}
+cudaError_t launch_decode_paged(int d, int kind, const DecodePagedParams& p, cudaStream_t stream) {
+  return d == 64 ? dp_launch_kind<64>(kind, p, stream) : dp_launch_kind<128>(kind, p, stream);
 }
 
 }  // namespace fa

@@ -117,6 +117,8 @@ fa_status device_state(DeviceState** out) {
       return cuda_fail(e, "cudaFuncSetAttribute(paged append)");
     if ((e = fa::decode_paged_set_attributes()) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(paged decode)");
+    if ((e = fa::weigh_paged_set_attributes()) != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged weigh)");
+    if ((e = fa::evict_paged_set_attributes()) != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged evict)");
     if ((e = fa::decode_grouped_set_attributes(64)) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(grouped decode d=64)");
     if ((e = fa::decode_grouped_set_attributes(128)) != cudaSuccess)
@@ -833,17 +835,20 @@ bool paged_decode_sizes_ok(int B, int H, int Hkv, int Nq, int max_len, int num_s
          static_cast<long long>(B) * H * Nq <= INT_MAX;
 }
 
-// What the two paged entry points check of the pool alike.
-fa_status check_pool(const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
-                     const int* table, const int* seqlens, int num_pages, int page, int e4m3) {
+// What the paged entry points check of the pool alike. kind: a PageKind.
+fa_status check_pool(const void* k_pages, const void* v_pages, const void* k_scale, const void* v_scale,
+                     const int* table, const int* seqlens, int num_pages, int page, int kind) {
   if (!k_pages || !v_pages || !table || !seqlens)
     return fail(FA_ERR_INVALID_ARG, "k_pages, v_pages, block_table and seqlens_k must be non-NULL");
   if (num_pages < 1) return fail(FA_ERR_INVALID_ARG, "num_pages must be >= 1");
-  if (e4m3 && (!k_scale || !v_scale)) return fail(FA_ERR_INVALID_ARG, "e4m3 pages need k_scale and v_scale");
+  if (kind < fa::PAGES_BF16 || kind > fa::PAGES_FP4) return fail(FA_ERR_INVALID_ARG, "unknown kind of pages %d", kind);
+  if (kind != fa::PAGES_BF16 && (!k_scale || !v_scale))
+    return fail(FA_ERR_INVALID_ARG, "%s pages need k_scale and v_scale", kind == fa::PAGES_E4M3 ? "e4m3" : "4-bit");
+  if (kind == fa::PAGES_FP4 && (!aligned(k_scale, 16) || !aligned(v_scale, 16)))
+    return fail(FA_ERR_UNSUPPORTED, "scales of 4-bit pages must be 16-byte aligned");
   if (!fa::paged_page_ok(page)) return fail(FA_ERR_UNSUPPORTED, "page size %d unsupported (16, 32, 64 or 128)", page);
   if (!aligned(k_pages, 16) || !aligned(v_pages, 16)) return fail(FA_ERR_UNSUPPORTED, "k_pages and v_pages must be 16-byte aligned");
-  for (const void* x : {static_cast<const void*>(k_scale), static_cast<const void*>(v_scale),
-                        static_cast<const void*>(table), static_cast<const void*>(seqlens)})
+  for (const void* x : {k_scale, v_scale, static_cast<const void*>(table), static_cast<const void*>(seqlens)})
     if (!aligned(x, 4)) return fail(FA_ERR_UNSUPPORTED, "scales, block_table and seqlens_k must be 4-byte aligned");
   return FA_OK;
 }
@@ -870,14 +875,12 @@ bool rows_apart(const int64_t* strides, const int* extents, int dims, int d) {
   return true;
 }
 
-}  // namespace
-
-fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
-                          void* v_pages, float* k_scale, float* v_scale, const int* block_table, int64_t table_stride,
-                          const int* seqlens_k, const int* cu_seqlens, const int64_t* turns, const void* q_weight,
-                          const void* k_weight, const int64_t* strides, int B, int T, int H, int Hkv, int d,
-                          int num_pages, int page, int table_width, int e4m3, int rot, int interleaved,
-                          float rot_scale, float eps, int max_new, void* stream) {
+fa_status append_paged(int kind, const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
+                       void* v_pages, void* k_scale, void* v_scale, const int* block_table, int64_t table_stride,
+                       const int* seqlens_k, const int* cu_seqlens, const int* offsets, const int64_t* turns,
+                       const void* q_weight, const void* k_weight, const int64_t* strides, int B, int T, int H, int Hkv,
+                       int d, int num_pages, int page, int table_width, int rot, int interleaved, float rot_scale,
+                       float eps, int max_new, void* stream) {
   t_detail[0] = 0;
   if (B < 1 || T < 0 || H < 1 || Hkv < 1 || table_width < 1)
     return fail(FA_ERR_INVALID_ARG, "need B, H, Hkv, table_width >= 1 and T >= 0 (got %d %d %d %d %d)", B, H, Hkv,
@@ -894,13 +897,14 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
     return fail(FA_ERR_INVALID_ARG, "table_width * page is too large");
   if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
   if (rot % 16 != 0) return fail(FA_ERR_UNSUPPORTED, "rot (%d) must be a multiple of 16", rot);
-  if (fa_status s = check_pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, num_pages, page, e4m3)) return s;
+  if (fa_status s = check_pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, num_pages, page, kind)) return s;
   if (T == 0) return FA_OK;
   if (!q || !k || !v || !q_out || !strides) return fail(FA_ERR_INVALID_ARG, "q, k, v, q_out and strides must be non-NULL");
   if (rot > 0 && !turns) return fail(FA_ERR_INVALID_ARG, "a rotation needs turns");
   for (const void* x : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_out), q_weight, k_weight})
     if (!aligned(x, 16)) return fail(FA_ERR_UNSUPPORTED, "q, k, v, the outputs and the weights must be 16-byte aligned");
-  if (!aligned(turns, 16) || !aligned(cu_seqlens, 4)) return fail(FA_ERR_UNSUPPORTED, "turns must be 16-byte, cu_seqlens 4-byte aligned");
+  if (!aligned(turns, 16) || !aligned(cu_seqlens, 4) || !aligned(offsets, 4))
+    return fail(FA_ERR_UNSUPPORTED, "turns must be 16-byte, cu_seqlens and offsets 4-byte aligned");
   if (table_stride < table_width && B > 1) return fail(FA_ERR_INVALID_ARG, "table_stride is below table_width");
   for (int i = 0; i < 10; ++i) {  // token and head strides of q, k, v, q_out, k_out
     const int heads = (i == 1 || i == 7) ? H : Hkv;
@@ -920,8 +924,10 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
   if (fa_status s = device_state(&st)) return s;
   fa::AppendPagedParams p{};
   p.q = q, p.k = k, p.v = v, p.q_out = q_out, p.k_out = k_out;
-  p.k_pages = k_pages, p.v_pages = v_pages, p.k_scale = k_scale, p.v_scale = v_scale;
-  p.table = block_table, p.seqlens = seqlens_k, p.cu = cu_seqlens;
+  p.k_pages = k_pages, p.v_pages = v_pages;
+  if (kind == fa::PAGES_FP4) p.k_scale4 = static_cast<uint8_t*>(k_scale), p.v_scale4 = static_cast<uint8_t*>(v_scale);
+  else p.k_scale = static_cast<float*>(k_scale), p.v_scale = static_cast<float*>(v_scale);
+  p.table = block_table, p.seqlens = seqlens_k, p.cu = cu_seqlens, p.offsets = offsets;
   p.turns = reinterpret_cast<const long long*>(turns);
   p.q_weight = q_weight, p.k_weight = k_weight;
   p.qst = strides[0], p.qsh = strides[1], p.kst = strides[2], p.ksh = strides[3], p.vst = strides[4];
@@ -937,10 +943,45 @@ fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_o
   p.kv_blocks = static_cast<int>((use_rect ? rect * B : T / page + 2LL * B) * Hkv);
   p.max_rows = std::min(page, n_max);
   p.q_blocks_wanted = 6 * st->num_sms;
-  cudaError_t e = fa::launch_append_paged(e4m3 != 0, p, static_cast<cudaStream_t>(stream));
+  cudaError_t e = fa::launch_append_paged(kind, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
   t_launches += 1;
   return FA_OK;
+}
+
+}  // namespace
+
+fa_status fa_append_paged(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
+                          void* v_pages, float* k_scale, float* v_scale, const int* block_table, int64_t table_stride,
+                          const int* seqlens_k, const int* cu_seqlens, const int64_t* turns, const void* q_weight,
+                          const void* k_weight, const int64_t* strides, int B, int T, int H, int Hkv, int d,
+                          int num_pages, int page, int table_width, int e4m3, int rot, int interleaved,
+                          float rot_scale, float eps, int max_new, void* stream) {
+  return append_paged(e4m3 ? fa::PAGES_E4M3 : fa::PAGES_BF16, q, k, v, q_out, k_out, k_pages, v_pages, k_scale, v_scale,
+                      block_table, table_stride, seqlens_k, cu_seqlens, nullptr, turns, q_weight, k_weight, strides, B, T,
+                      H, Hkv, d, num_pages, page, table_width, rot, interleaved, rot_scale, eps, max_new, stream);
+}
+
+fa_status fa_append_paged_at(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
+                             void* v_pages, float* k_scale, float* v_scale, const int* block_table,
+                             int64_t table_stride, const int* seqlens_k, const int* cu_seqlens, const int* offsets,
+                             const int64_t* turns, const void* q_weight, const void* k_weight, const int64_t* strides,
+                             int B, int T, int H, int Hkv, int d, int num_pages, int page, int table_width, int e4m3,
+                             int rot, int interleaved, float rot_scale, float eps, int max_new, void* stream) {
+  return append_paged(e4m3 ? fa::PAGES_E4M3 : fa::PAGES_BF16, q, k, v, q_out, k_out, k_pages, v_pages, k_scale, v_scale,
+                      block_table, table_stride, seqlens_k, cu_seqlens, offsets, turns, q_weight, k_weight, strides, B, T,
+                      H, Hkv, d, num_pages, page, table_width, rot, interleaved, rot_scale, eps, max_new, stream);
+}
+
+fa_status fa_append_paged_fp4(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
+                              void* v_pages, uint8_t* k_scale, uint8_t* v_scale, const int* block_table,
+                              int64_t table_stride, const int* seqlens_k, const int* cu_seqlens, const int* offsets,
+                              const int64_t* turns, const void* q_weight, const void* k_weight, const int64_t* strides,
+                              int B, int T, int H, int Hkv, int d, int num_pages, int page, int table_width, int rot,
+                              int interleaved, float rot_scale, float eps, int max_new, void* stream) {
+  return append_paged(fa::PAGES_FP4, q, k, v, q_out, k_out, k_pages, v_pages, k_scale, v_scale, block_table,
+                      table_stride, seqlens_k, cu_seqlens, offsets, turns, q_weight, k_weight, strides, B, T, H, Hkv, d,
+                      num_pages, page, table_width, rot, interleaved, rot_scale, eps, max_new, stream);
 }
 
 size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int num_splits) {
@@ -948,11 +989,13 @@ size_t fa_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d, int 
   return paged_workspace(B, Hkv, H / Hkv * Nq, d, num_splits).bytes;
 }
 
-fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
-                          const float* k_scale, const float* v_scale, const int* block_table, int64_t table_stride,
-                          const int* seqlens_k, void* o, const int64_t* o_strides, float* lse, int B, int H, int Hkv,
-                          int Nq, int d, int num_pages, int page, int max_len, int e4m3, float scale, int num_splits,
-                          void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+
+fa_status decode_paged(int kind, const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
+                       const void* k_scale, const void* v_scale, const int* block_table, int64_t table_stride,
+                       const int* seqlens_k, void* o, const int64_t* o_strides, float* lse, int B, int H, int Hkv,
+                       int Nq, int d, int num_pages, int page, int max_len, float scale, int num_splits,
+                       void* workspace, size_t workspace_bytes, void* stream) {
   t_detail[0] = 0;
   if (!q || !o || !q_strides || !o_strides) return fail(FA_ERR_INVALID_ARG, "q, o and their strides must be non-NULL");
   if (B < 1 || H < 1 || Hkv < 1 || Nq < 1 || max_len < 0 || max_len > (1 << 30))
@@ -964,7 +1007,7 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
   const int R = H / Hkv > 128 ? 129 : H / Hkv * std::min(Nq, 129);
   if (R > 128) return fail(FA_ERR_UNSUPPORTED, "(H / Hkv) * Nq query rows per K/V head; at most 128");
-  if (fa_status s = check_pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, num_pages, page, e4m3)) return s;
+  if (fa_status s = check_pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, num_pages, page, kind)) return s;
   if (!aligned(q, 16) || !aligned(o, 16)) return fail(FA_ERR_UNSUPPORTED, "q and o must be 16-byte aligned");
   const int extent[3] = {B, H, Nq};
   for (int i = 0; i < 3; ++i)
@@ -986,7 +1029,9 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   if (static_cast<double>(B) * Hkv * max_len / 16 > 2e9 * ranges)  // (tiles of a range are counted in 32 bits)
     return fail(FA_ERR_INVALID_ARG, "B * Hkv * max_len is too large");
   fa::DecodePagedParams p{};
-  p.q = q, p.k = k_pages, p.v = v_pages, p.k_scale = k_scale, p.v_scale = v_scale;
+  p.q = q, p.k = k_pages, p.v = v_pages;
+  if (kind == fa::PAGES_FP4) p.k_scale4 = static_cast<const uint8_t*>(k_scale), p.v_scale4 = static_cast<const uint8_t*>(v_scale);
+  else p.k_scale = static_cast<const float*>(k_scale), p.v_scale = static_cast<const float*>(v_scale);
   p.table = block_table, p.table_stride = table_stride, p.seqlens = seqlens_k;
   p.o = o, p.lse = lse;
   p.qsb = q_strides[0], p.qsh = q_strides[1], p.qst = q_strides[2];
@@ -1001,8 +1046,172 @@ fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k
   p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.ml);
   p.ws_ends = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.ends);
   p.status = st->status;
-  cudaError_t e = fa::launch_decode_paged(d, e4m3 != 0, p, static_cast<cudaStream_t>(stream));
+  cudaError_t e = fa::launch_decode_paged(d, kind, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+  t_launches += 2;
+  return FA_OK;
+}
+
+}  // namespace
+
+fa_status fa_decode_paged(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
+                          const float* k_scale, const float* v_scale, const int* block_table, int64_t table_stride,
+                          const int* seqlens_k, void* o, const int64_t* o_strides, float* lse, int B, int H, int Hkv,
+                          int Nq, int d, int num_pages, int page, int max_len, int e4m3, float scale, int num_splits,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_paged(e4m3 ? fa::PAGES_E4M3 : fa::PAGES_BF16, q, q_strides, k_pages, v_pages, k_scale, v_scale, block_table,
+                      table_stride, seqlens_k, o, o_strides, lse, B, H, Hkv, Nq, d, num_pages, page, max_len, scale,
+                      num_splits, workspace, workspace_bytes, stream);
+}
+
+size_t fa_decode_paged_fp4_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int num_splits) {
+  return fa_decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits);
+}
+
+fa_status fa_decode_paged_fp4(const void* q, const int64_t* q_strides, const void* k_pages, const void* v_pages,
+                              const uint8_t* k_scale, const uint8_t* v_scale, const int* block_table,
+                              int64_t table_stride, const int* seqlens_k, void* o, const int64_t* o_strides, float* lse,
+                              int B, int H, int Hkv, int Nq, int d, int num_pages, int page, int max_len, float scale,
+                              int num_splits, void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_paged(fa::PAGES_FP4, q, q_strides, k_pages, v_pages, k_scale, v_scale, block_table, table_stride, seqlens_k,
+                      o, o_strides, lse, B, H, Hkv, Nq, d, num_pages, page, max_len, scale, num_splits, workspace,
+                      workspace_bytes, stream);
+}
+
+fa_status fa_read_paged(const void* k_pages, const void* v_pages, const void* k_scale, const void* v_scale, int kind,
+                        const int* block_table, int64_t table_stride, const int* seqlens_k, const int* cu_seqlens,
+                        void* k_out, void* v_out, const int64_t* strides, int B, int total, int Hkv, int d,
+                        int num_pages, int page, int table_width, void* stream) {
+  t_detail[0] = 0;
+  if (B < 1 || total < 0 || Hkv < 1 || table_width < 1)
+    return fail(FA_ERR_INVALID_ARG, "need B, Hkv, table_width >= 1 and total >= 0 (got %d %d %d %d)", B, Hkv, table_width, total);
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
+  if (fa_status s = check_pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, num_pages, page, kind)) return s;
+  if (total == 0) return FA_OK;
+  if (!cu_seqlens || !k_out || !v_out || !strides)
+    return fail(FA_ERR_INVALID_ARG, "cu_seqlens, k_out, v_out and strides must be non-NULL");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(cu_seqlens, 4))
+    return fail(FA_ERR_UNSUPPORTED, "the outputs must be 16-byte, cu_seqlens 4-byte aligned");
+  if (B > 1 && table_stride < table_width) return fail(FA_ERR_INVALID_ARG, "table_stride is below table_width");
+  const int extent[2] = {total, Hkv};
+  for (int i = 0; i < 4; ++i)
+    if (!stride_ok(strides[i], extent[i & 1])) return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements, >= 0");
+  if (!rows_apart(strides, extent, 2, d) || !rows_apart(strides + 2, extent, 2, d))
+    return fail(FA_ERR_UNSUPPORTED, "rows of k_out or v_out overlap");
+  if (static_cast<long long>(Hkv) * 32 * (d / 16) > INT_MAX / 2) return fail(FA_ERR_INVALID_ARG, "Hkv is too large");
+
+  DeviceState* st = nullptr;
+  if (fa_status s = device_state(&st)) return s;
+  fa::ReadPagedParams p{};
+  p.k = k_pages, p.v = v_pages, p.k_scale = k_scale, p.v_scale = v_scale;
+  p.table = block_table, p.seqlens = seqlens_k, p.cu = cu_seqlens, p.table_stride = table_stride;
+  p.k_out = k_out, p.v_out = v_out;
+  p.kst = strides[0], p.ksh = strides[1], p.vst = strides[2], p.vsh = strides[3];
+  p.B = B, p.total = total, p.Hkv = Hkv;
+  p.page = page, p.page_shift = log2_of(page), p.num_pages = num_pages, p.width = table_width;
+  p.status = st->status;
+  cudaError_t e = fa::launch_read_paged(d, kind, p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged read launch");
+  t_launches += 1;
+  return FA_OK;
+}
+
+fa_status fa_weigh_paged(const void* q, const int64_t* q_strides, const float* lse, const void* k_pages,
+                         const void* k_scale, int kind, const int* block_table, int64_t table_stride,
+                         const int* seqlens_k, float* weights, int64_t weights_stride, int B, int H, int Hkv, int Nq,
+                         int d, int num_pages, int page, int max_len, float scale, void* stream) {
+  t_detail[0] = 0;
+  if (!q || !q_strides || !lse || !weights) return fail(FA_ERR_INVALID_ARG, "q, its strides, lse and weights must be non-NULL");
+  if (B < 1 || H < 1 || Hkv < 1 || Nq < 1 || max_len < 0 || max_len > (1 << 30))
+    return fail(FA_ERR_INVALID_ARG, "need B, H, Hkv, Nq >= 1 and max_len in [0, 2^30] (got %d %d %d %d %d)", B, H, Hkv, Nq,
+                max_len);
+  if (H % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "H (%d) must be a multiple of Hkv (%d)", H, Hkv);
+  if (fa_status s = check_scale(scale)) return s;
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
+  const int R = H / Hkv > 128 ? 129 : H / Hkv * std::min(Nq, 129);
+  if (R > 128) return fail(FA_ERR_UNSUPPORTED, "(H / Hkv) * Nq query rows per K/V head; at most 128");
+  if (fa_status s = check_pool(k_pages, k_pages, k_scale, k_scale, block_table, seqlens_k, num_pages, page, kind)) return s;
+  if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(weights, 4))
+    return fail(FA_ERR_UNSUPPORTED, "q must be 16-byte, lse and weights 4-byte aligned");
+  const int extent[3] = {B, H, Nq};
+  for (int i = 0; i < 3; ++i)
+    if (!stride_ok(q_strides[i], extent[i])) return fail(FA_ERR_UNSUPPORTED, "strides must be multiples of 8 elements, >= 0");
+  const int64_t pages = (static_cast<int64_t>(max_len) + page - 1) / page;
+  if (B > 1 && table_stride < pages)
+    return fail(FA_ERR_INVALID_ARG, "max_len needs %lld pages a sequence, table_stride is %lld", static_cast<long long>(pages),
+                static_cast<long long>(table_stride));
+  if (static_cast<long long>(B) * H * Nq > INT_MAX - 16) return fail(FA_ERR_INVALID_ARG, "B * H * Nq is too large");
+  if (static_cast<long long>(B) * Hkv > 1 && weights_stride < max_len)
+    return fail(FA_ERR_INVALID_ARG, "weights_stride is below max_len");
+
+  DeviceState* st = nullptr;
+  if (fa_status s = device_state(&st)) return s;
+  fa::WeighPagedParams p{};
+  p.q = q, p.lse = lse, p.k = k_pages, p.k_scale = k_scale;
+  p.table = block_table, p.table_stride = table_stride, p.seqlens = seqlens_k;
+  p.weights = weights, p.wstride = weights_stride;
+  p.qsb = q_strides[0], p.qsh = q_strides[1], p.qst = q_strides[2];
+  p.B = B, p.H = H, p.Hkv = Hkv, p.G = H / Hkv, p.Nq = Nq, p.R = R, p.max_len = max_len;
+  p.page = page, p.page_shift = log2_of(page), p.num_pages = num_pages;
+  p.row_tiles = (R + 7) / 8;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.status = st->status;
+  cudaError_t e = fa::launch_weigh_paged(d, kind, p, st->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged weigh launch");
+  t_launches += 1;
+  return FA_OK;
+}
+
+fa_status fa_evict_paged(const float* weights, int64_t weights_stride, void* k_pages, void* v_pages, void* k_scale,
+                         void* v_scale, int kind, const int* block_table, int64_t table_stride, const int* seqlens_k,
+                         const int* offsets, const int* new_table, int64_t new_table_stride, int* kept,
+                         int* new_seqlens, int* new_offsets, float* new_weights, int64_t new_weights_stride,
+                         int new_width, int B, int Hkv, int d, int num_pages, int page, int max_len, int keep,
+                         int first, int recent, void* stream) {
+  t_detail[0] = 0;
+  if (!weights || !new_table || !kept || !new_seqlens || !new_offsets || !new_weights)
+    return fail(FA_ERR_INVALID_ARG, "weights, new_table and the outputs must be non-NULL");
+  if (B < 1 || Hkv < 1 || max_len < 0 || max_len > (1 << 30))
+    return fail(FA_ERR_INVALID_ARG, "need B, Hkv >= 1 and max_len in [0, 2^30] (got %d %d %d)", B, Hkv, max_len);
+  if (keep < 1 || keep > (1 << 30) || first < 0 || recent < 0 || first > keep || recent > keep - first)
+    return fail(FA_ERR_INVALID_ARG, "need keep in [1, 2^30], first, recent >= 0 and first + recent <= keep (got %d %d %d)",
+                keep, first, recent);
+  if (new_width < keep) return fail(FA_ERR_INVALID_ARG, "rows of new_weights (%d) are shorter than keep (%d)", new_width, keep);
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
+  if (fa_status s = check_pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, num_pages, page, kind)) return s;
+  for (const void* x : {static_cast<const void*>(weights), static_cast<const void*>(offsets),
+                        static_cast<const void*>(new_table), static_cast<const void*>(kept),
+                        static_cast<const void*>(new_seqlens), static_cast<const void*>(new_offsets),
+                        static_cast<const void*>(new_weights)})
+    if (!aligned(x, 4)) return fail(FA_ERR_UNSUPPORTED, "weights, offsets, new_table and the outputs must be 4-byte aligned");
+  if (static_cast<const void*>(new_weights) == weights || new_seqlens == seqlens_k || new_table == block_table)
+    return fail(FA_ERR_INVALID_ARG, "new_weights, new_seqlens and new_table must not be the arrays that the call reads");
+  const int64_t pages = (static_cast<int64_t>(max_len) + page - 1) / page;
+  const int64_t new_pages = (static_cast<int64_t>(std::min(keep, max_len)) + page - 1) / page;
+  if (B > 1 && (table_stride < pages || new_table_stride < new_pages))
+    return fail(FA_ERR_INVALID_ARG, "max_len needs %lld pages a sequence, the kept rows %lld: table strides are %lld and %lld",
+                static_cast<long long>(pages), static_cast<long long>(new_pages), static_cast<long long>(table_stride),
+                static_cast<long long>(new_table_stride));
+  const long long pairs = static_cast<long long>(B) * Hkv;
+  if (pairs > 1 && (weights_stride < max_len || new_weights_stride < new_width))
+    return fail(FA_ERR_INVALID_ARG, "weights_stride is below max_len or new_weights_stride below the new rows");
+  if (pairs * 8 > INT_MAX || pairs * ((static_cast<long long>(keep) + 127) / 128) > INT_MAX)
+    return fail(FA_ERR_INVALID_ARG, "B, Hkv and keep give too many blocks");
+
+  DeviceState* st = nullptr;
+  if (fa_status s = device_state(&st)) return s;
+  fa::EvictPagedParams p{};
+  p.weights = weights, p.wstride = weights_stride;
+  p.k = k_pages, p.v = v_pages, p.k_scale = k_scale, p.v_scale = v_scale;
+  p.table = block_table, p.table_stride = table_stride, p.seqlens = seqlens_k, p.offsets = offsets;
+  p.new_table = new_table, p.new_table_stride = new_table_stride;
+  p.kept = kept, p.new_seqlens = new_seqlens, p.new_offsets = new_offsets;
+  p.new_weights = new_weights, p.new_wstride = new_weights_stride, p.new_width = new_width;
+  p.B = B, p.Hkv = Hkv, p.max_len = max_len, p.keep = keep, p.first = first, p.recent = recent;
+  p.page = page, p.page_shift = log2_of(page), p.num_pages = num_pages;
+  p.status = st->status;
+  cudaError_t e = fa::launch_evict_paged(d, kind, p, st->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged evict launch");
   t_launches += 2;
   return FA_OK;
 }

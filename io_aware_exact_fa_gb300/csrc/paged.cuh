@@ -15,6 +15,13 @@ namespace fa {
 constexpr unsigned int FA_DEV_BAD_PAGE = 2u;  // status word: a block-table entry outside the pool was skipped
 constexpr unsigned int FA_DEV_BAD_LENS = 4u;  // status word: lengths or offsets outside their arrays were clipped
 
+// What a pool's pages hold: bf16 rows, e4m3 codes with a scale for each page and head, or 4-bit rows (fp4.cuh).
+enum PageKind : int { PAGES_BF16 = 0, PAGES_E4M3 = 1, PAGES_FP4 = 2 };
+// Bytes of a row (keys or values of one position and K/V head), without the scales of 4-bit rows (d / 16 more).
+__host__ __device__ constexpr int paged_row_bytes(int kind, int d) {
+  return kind == PAGES_BF16 ? 2 * d : kind == PAGES_E4M3 ? d : d / 2;
+}
+
 constexpr int PAGED_SCALE_EXP_MIN = -40;      // least exponent of an e4m3 page's scale
 
 inline bool paged_page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
@@ -39,6 +46,8 @@ struct DecodePagedParams {
   const void* v;             // pool of V pages
   const float* k_scale;      // e4m3: fp32 [num_pages, Hkv]
   const float* v_scale;
+  const uint8_t* k_scale4;   // 4-bit: bytes [num_pages, Hkv, page, d / 16]
+  const uint8_t* v_scale4;
   const int* table;          // int32 [B, >= max_len / page], row stride table_stride
   const int* seqlens;        // int32 [B]
   void* o;                   // bf16, element strides osb / osh / ost
@@ -88,8 +97,11 @@ struct AppendPagedParams {
   void* v_pages;
   float* k_scale;
   float* v_scale;
+  uint8_t* k_scale4;         // 4-bit rows' scales
+  uint8_t* v_scale4;
   const int* table;
   const int* seqlens;        // int32 [B]: lengths with the new tokens counted
+  const int* offsets;        // int32 [B]: position of row 0, which the rotation counts from; nullptr: 0
   const int* cu;             // int32 [B + 1]: first new token of each sequence, or nullptr (uniform)
   const long long* turns;    // int64 [rot / 2]: each pair's frequency in 2^-64 turns a position
   const void* q_weight;      // bf16 [d] or nullptr
@@ -109,9 +121,69 @@ struct AppendPagedParams {
 };
 
 cudaError_t append_paged_set_attributes();
-cudaError_t launch_append_paged(bool f8, const AppendPagedParams& p, cudaStream_t stream);
+cudaError_t launch_append_paged(int kind, const AppendPagedParams& p, cudaStream_t stream);
 
 cudaError_t decode_paged_set_attributes();
-cudaError_t launch_decode_paged(int d, bool f8, const DecodePagedParams& p, cudaStream_t stream);
+cudaError_t launch_decode_paged(int d, int kind, const DecodePagedParams& p, cudaStream_t stream);
+
+// Rows of a paged cache as packed bf16: row i of n_b goes to cu[b] + i, from row L_b - n_b + i of sequence b.
+struct ReadPagedParams {
+  const void* k;
+  const void* v;
+  const void* k_scale;
+  const void* v_scale;
+  const int* table;
+  const int* seqlens;
+  const int* cu;             // int32 [B + 1]
+  void* k_out;               // bf16, strides of token and head
+  void* v_out;
+  long long kst, ksh, vst, vsh, table_stride;
+  int B, total, Hkv, page, page_shift, num_pages, width;
+  unsigned int* status;
+};
+cudaError_t launch_read_paged(int d, int kind, const ReadPagedParams& p, cudaStream_t stream);
+
+// Adds each key's attention weights, summed over the query rows of its K/V head, to weights[b, hk, key].
+struct WeighPagedParams {
+  const void* q;             // bf16, element strides; d contiguous
+  const float* lse;          // fp32 [B, H, Nq], natural log
+  const void* k;
+  const void* k_scale;       // e4m3: fp32 [num_pages, Hkv]; 4-bit: bytes [num_pages, Hkv, page, d / 16]
+  const int* table;
+  const int* seqlens;
+  float* weights;            // fp32, rows of (b, hk) wstride apart
+  long long qsb, qsh, qst, table_stride, wstride;
+  int B, H, Hkv, G, Nq, R, max_len;
+  int page, page_shift, num_pages;
+  int chunk, chunks;         // keys of a block, and blocks of a sequence and K/V head (set by the launch)
+  int row_tiles;             // 8-row tiles of the R query rows
+  float scale_log2;
+  unsigned int* status;
+};
+cudaError_t weigh_paged_set_attributes();
+cudaError_t launch_weigh_paged(int d, int kind, WeighPagedParams p, int num_sms, cudaStream_t stream);
+
+// Chooses the rows that stay and moves them to the pages of new_table.
+struct EvictPagedParams {
+  const float* weights;      // fp32, rows of (b, hk) wstride apart
+  const void* k;             // the pool, read and written
+  const void* v;
+  const void* k_scale;
+  const void* v_scale;
+  const int* table;
+  const int* seqlens;
+  const int* offsets;        // int32 [B] or nullptr
+  const int* new_table;
+  int* kept;                 // int32 [B, Hkv, keep], -1 past the rows that stay
+  int* new_seqlens;          // int32 [B]
+  int* new_offsets;          // int32 [B]
+  float* new_weights;        // fp32, rows new_wstride apart; 0 past the rows that stay
+  long long wstride, table_stride, new_table_stride, new_wstride;
+  int B, Hkv, max_len, keep, first, recent, new_width;
+  int page, page_shift, num_pages;
+  unsigned int* status;
+};
+cudaError_t evict_paged_set_attributes();
+cudaError_t launch_evict_paged(int d, int kind, const EvictPagedParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace fa

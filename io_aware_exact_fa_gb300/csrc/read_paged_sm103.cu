@@ -1,0 +1,174 @@
+// Rows of a paged cache (bf16, e4m3 or 4-bit pages) as packed bf16 keys and values
+// for sm_103a: packed row cu[b] + i is row L_b - n_b + i of sequence b, where
+// n_b = cu[b + 1] - cu[b] rows are asked for, its last ones (all of them, or a
+// call's new tokens).
+//
+// An e4m3 value is code * scale, rounded once to bf16 (exact for a power of two); a
+// 4-bit value is exact in bf16. What bounds it: HBM, mostly the writes (d = 128,
+// 4-bit: 144 bytes read and 512 written for each row and K/V head). A block takes 32
+// packed rows of all heads: its first threads find their sequence (by bisection of
+// the offsets) and page, then every thread turns 16 elements of a key and of a value
+// into 32 bytes each. Neighbouring threads take a row's units, then the next row
+// of the same head, so reads run along the page.
+#include <cuda_fp16.h>
+
+#include "fp4.cuh"
+#include "mma_sync.cuh"
+#include "paged.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int RD_THREADS = 256;
+constexpr int RD_ROWS = 32;      // packed rows of a block
+constexpr int RD_FLIGHT = 2;     // units whose loads a thread has in flight
+
+// Sixteen elements as they lie in the page: 32, 16 or 8 bytes, and the scale (4-bit rows: its byte).
+template <int KIND>
+struct Unit {
+  uint4 a, b;
+  float scale;
+  uint32_t byte;
+};
+
+template <int D, int KIND>
+__device__ __forceinline__ void rd_load(Unit<KIND>& x, const void* pages, const void* scales, long long row, long long ph, int u) {
+  const uint8_t* at = static_cast<const uint8_t*>(pages) + row * paged_row_bytes(KIND, D) + u * (paged_row_bytes(KIND, D) / (D / 16));
+  if constexpr (KIND == PAGES_BF16) {
+    x.a = __ldg(reinterpret_cast<const uint4*>(at));
+    x.b = __ldg(reinterpret_cast<const uint4*>(at) + 1);
+  } else if constexpr (KIND == PAGES_E4M3) {
+    x.a = __ldg(reinterpret_cast<const uint4*>(at));
+    x.scale = __ldg(static_cast<const float*>(scales) + ph);
+  } else {
+    const uint2 c = __ldg(reinterpret_cast<const uint2*>(at));
+    x.a.x = c.x, x.a.y = c.y;
+    x.byte = __ldg(static_cast<const uint8_t*>(scales) + row * (D / 16) + u);
+  }
+}
+
+__device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t h, float f) {
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16x2(y.x * f, y.y * f);
+}
+
+template <int KIND>
+__device__ __forceinline__ void rd_store(const Unit<KIND>& x, uint16_t* dst) {
+  uint4 lo = x.a, hi = x.b;  // (bf16: as they are)
+  if constexpr (KIND != PAGES_BF16) {
+    uint32_t h[8];
+    float f = 1.f;
+    if constexpr (KIND == PAGES_E4M3) {
+      f = x.scale;
+      e4m3x4_to_f16x2x2(x.a.x, h[0], h[1]);
+      e4m3x4_to_f16x2x2(x.a.y, h[2], h[3]);
+      e4m3x4_to_f16x2x2(x.a.z, h[4], h[5]);
+      e4m3x4_to_f16x2x2(x.a.w, h[6], h[7]);
+    } else {
+      const uint32_t s2 = fp4_scale2<0>(x.byte);
+      uint32_t c0[4], c1[4];
+      e2m1x8_to_f16x2x4(x.a.x, c0);
+      e2m1x8_to_f16x2x4(x.a.y, c1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[i] = hmul2_bits(c0[i], s2);
+        h[4 + i] = hmul2_bits(c1[i], s2);
+      }
+    }
+    lo = make_uint4(half2_to_bf16x2(h[0], f), half2_to_bf16x2(h[1], f), half2_to_bf16x2(h[2], f), half2_to_bf16x2(h[3], f));
+    hi = make_uint4(half2_to_bf16x2(h[4], f), half2_to_bf16x2(h[5], f), half2_to_bf16x2(h[6], f), half2_to_bf16x2(h[7], f));
+  }
+  *reinterpret_cast<uint4*>(dst) = lo;
+  *reinterpret_cast<uint4*>(dst + 8) = hi;
+}
+
+}  // namespace
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(RD_THREADS) fa_read_paged_kernel(const ReadPagedParams p) {
+  constexpr int UNITS = D / 16;
+  __shared__ long long s_base[RD_ROWS];  // its row of K/V head 0 in the pool, or -1
+  const int tid = threadIdx.x;
+  const int t0 = static_cast<int>(blockIdx.x) * RD_ROWS;
+  if (blockIdx.x == 0) {  // offsets that decrease or pass the tensors are reported; rows outside are left alone below
+    bool bad = false;
+    for (int b = tid; b < p.B; b += RD_THREADS) {
+      const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1), L = __ldg(p.seqlens + b);
+      bad = bad || lo < 0 || hi < lo || hi > p.total || L < 0 || L > static_cast<long long>(p.width) * p.page ||
+            (L > 0 && hi - lo > L);
+    }
+    if (bad) atomicOr(p.status, FA_DEV_BAD_LENS);
+  }
+  if (tid < RD_ROWS) {
+    const int t = t0 + tid;
+    long long base = -1;
+    if (t < p.total) {
+      int lo = 0, n = p.B;  // the last sequence that starts at or before row t
+      while (n > 1) {
+        const int half = n / 2;
+        if (__ldg(p.cu + lo + half) <= t) {
+          lo += half;
+          n -= half;
+        } else {
+          n = half;
+        }
+      }
+      const int first = __ldg(p.cu + lo), end = __ldg(p.cu + lo + 1);
+      const int L = __ldg(p.seqlens + lo);
+      const long long row = static_cast<long long>(L) - (static_cast<long long>(end) - t);
+      if (t >= first && t < end && row >= 0 && row < static_cast<long long>(p.width) * p.page) {
+        const int id = __ldg(p.table + lo * p.table_stride + (row >> p.page_shift));
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages))
+          base = static_cast<long long>(id) * p.Hkv * p.page + (row & (p.page - 1));
+        else
+          atomicOr(p.status, FA_DEV_BAD_PAGE);
+      }
+    }
+    s_base[tid] = base;
+  }
+  __syncthreads();
+  const int rows = min(RD_ROWS, p.total - t0);
+  const int items = rows * p.Hkv * UNITS;
+  for (int x0 = tid; x0 < items; x0 += RD_FLIGHT * RD_THREADS) {
+    Unit<KIND> k[RD_FLIGHT], v[RD_FLIGHT];
+    bool ok[RD_FLIGHT];
+    int u[RD_FLIGHT], r[RD_FLIGHT], hk[RD_FLIGHT];
+#pragma unroll
+    for (int i = 0; i < RD_FLIGHT; ++i) {
+      const int x = x0 + i * RD_THREADS;
+      u[i] = x % UNITS;
+      hk[i] = (x / UNITS) / rows;
+      r[i] = (x / UNITS) % rows;
+      const long long base = x < items ? s_base[r[i]] : -1;
+      ok[i] = base >= 0;
+      if (ok[i]) {
+        const long long row = base + static_cast<long long>(hk[i]) * p.page;
+        const long long ph = row >> p.page_shift;  // page and head
+        rd_load<D, KIND>(k[i], p.k, p.k_scale, row, ph, u[i]);
+        rd_load<D, KIND>(v[i], p.v, p.v_scale, row, ph, u[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RD_FLIGHT; ++i) {
+      if (!ok[i]) continue;
+      const long long t = t0 + r[i];
+      rd_store<KIND>(k[i], static_cast<uint16_t*>(p.k_out) + t * p.kst + hk[i] * p.ksh + 16 * u[i]);
+      rd_store<KIND>(v[i], static_cast<uint16_t*>(p.v_out) + t * p.vst + hk[i] * p.vsh + 16 * u[i]);
+    }
+  }
+}
+
+template <int D>
+static cudaError_t rd_launch(int kind, const ReadPagedParams& p, cudaStream_t stream) {
+  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(p.total) + RD_ROWS - 1) / RD_ROWS);
+  if (kind == PAGES_FP4) fa_read_paged_kernel<D, PAGES_FP4><<<blocks, RD_THREADS, 0, stream>>>(p);
+  else if (kind == PAGES_E4M3) fa_read_paged_kernel<D, PAGES_E4M3><<<blocks, RD_THREADS, 0, stream>>>(p);
+  else fa_read_paged_kernel<D, PAGES_BF16><<<blocks, RD_THREADS, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+cudaError_t launch_read_paged(int d, int kind, const ReadPagedParams& p, cudaStream_t stream) {
+  return d == 64 ? rd_launch<64>(kind, p, stream) : rd_launch<128>(kind, p, stream);
+}
+
+}  // namespace fa

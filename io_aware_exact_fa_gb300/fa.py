@@ -50,6 +50,14 @@ EXPORTS = {
     "fa_append_paged": (_i, [_vp] * 9 + [_vp, _i64] + [_vp] * 6 + [_i] * 11 + [_f, _f, _i, _vp]),
     "fa_decode_paged_workspace_size": (_sz, [_i] * 7),
     "fa_decode_paged": (_i, [_vp] * 7 + [_i64, _vp, _vp, _vp, _vp] + [_i] * 9 + [_f, _i, _vp, _sz, _vp]),
+    "fa_append_paged_at": (_i, [_vp] * 9 + [_vp, _i64] + [_vp] * 7 + [_i] * 11 + [_f, _f, _i, _vp]),
+    "fa_append_paged_fp4": (_i, [_vp] * 9 + [_vp, _i64] + [_vp] * 7 + [_i] * 10 + [_f, _f, _i, _vp]),
+    "fa_decode_paged_fp4_workspace_size": (_sz, [_i] * 7),
+    "fa_decode_paged_fp4": (_i, [_vp] * 7 + [_i64, _vp, _vp, _vp, _vp] + [_i] * 8 + [_f, _i, _vp, _sz, _vp]),
+    "fa_read_paged": (_i, [_vp] * 4 + [_i, _vp, _i64] + [_vp] * 5 + [_i] * 7 + [_vp]),
+    "fa_weigh_paged": (_i, [_vp] * 5 + [_i, _vp, _i64, _vp, _vp, _i64] + [_i] * 8 + [_f, _vp]),
+    "fa_evict_paged": (_i, [_vp, _i64] + [_vp] * 4 + [_i, _vp, _i64, _vp, _vp, _vp, _i64] + [_vp] * 4 + [_i64] + [_i] * 10
+                       + [_vp]),
     "fa_materialized_workspace_size": (_sz, [_i, _i, _i, _i]),
     "fa_fwd_materialized": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
     "fa_bwd_workspace_size": (_sz, [_i, _i, _i, _i]),
@@ -467,35 +475,19 @@ def _call(dev: int, stream: Optional[torch.cuda.Stream], fn, args, where: str, m
 
 _I64x10 = ctypes.c_int64 * 10
 _I64x3 = ctypes.c_int64 * 3
+_I64x4 = ctypes.c_int64 * 4
 
 
-def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
-                 block_table: torch.Tensor, seqlens_k: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
-                 max_new: int = 0, turns: Optional[torch.Tensor] = None, interleaved: bool = False,
-                 rot_scale: float = 1.0, q_weight: Optional[torch.Tensor] = None,
-                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, k_scale: Optional[torch.Tensor] = None,
-                 v_scale: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
-                 k_out: Optional[torch.Tensor] = None, with_k: bool = True,
-                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
-    """Norms, rotates and appends a step's tokens to a paged cache (fa.h fa_append_paged).
-
-    q [T,H,d], k/v [T,Hkv,d] bf16 (parts of one projection are taken as they are); k_pages/v_pages
-    [num_pages,Hkv,page,d] bf16, or float8_e4m3fn / uint8 codes with fp32 scales [num_pages,Hkv]; block_table int32
-    [B,width]; seqlens_k int32 [B] with the new tokens counted; cu_seqlens int32 [B+1], or None for T / B tokens each.
-    ``turns`` (``rotary_turns``) sets the rotation, None for none; the weights bf16 [d] the norms, None for none.
-    Returns the turned q [T,H,d] and k [T,Hkv,d] (None without ``with_k``), contiguous unless given."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
-        raise ValueError("q must be a CUDA tensor [T, H, d]")
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be a CUDA tensor [T, Hkv, d]")
+def _append(q, k, v, pool, Hkv, n, page, B, width, fn, where, e4m3, cu_seqlens, max_new, turns, interleaved, rot_scale,
+            q_weight, k_weight, eps, offsets, q_out, k_out, with_k, stream):
+    """What the append calls do with everything but the cache, whose checks are made."""
     dev = q.get_device()
     T, H, d = q_shape = q.shape
-    kv_shape = (T, k.shape[1], d)
-    Hkv = kv_shape[1]
+    kv_shape = (T, Hkv, d)
     st = _heads(q, "q", dev, q_shape) + _heads(k, "k", dev, kv_shape) + _heads(v, "v", dev, kv_shape)
-    pool, n, page, e4m3, B, width = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, dev)
-    kp, vp, ks, vs, table, table_stride, lens = pool
     cu = None if cu_seqlens is None else _whole(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,))
+    at = () if offsets is None and fn is _lib.fa_append_paged else (
+        None if offsets is None else _whole(offsets, "offsets", _I32, dev, (B,)),)
     rot, tp = 0, None
     if turns is not None:
         tp = _whole(turns, "turns", torch.int64, dev)
@@ -514,36 +506,56 @@ def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: tor
         st += (Hkv * d, d)
     else:
         st += (0, 0)
-    _call(dev, stream, _lib.fa_append_paged,
-          (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), kp, vp,
-           ks, vs, table, table_stride, lens, cu, tp, qw, kw, _I64x10(*st), B, T, H, Hkv, d, n, page, width, e4m3, rot,
-           bool(interleaved), rot_scale, eps, max_new), "fa_append_paged", (q_out, k_out))
+    _call(dev, stream, fn,
+          (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), *pool, cu,
+           *at, tp, qw, kw, _I64x10(*st), B, T, H, Hkv, d, n, page, width, *e4m3, rot, bool(interleaved), rot_scale, eps,
+           max_new), where, (q_out, k_out))
     return q_out, k_out
+
+
+def _tokens(q, k) -> None:
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [T, H, d]")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [T, Hkv, d]")
+
+
+def append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 block_table: torch.Tensor, seqlens_k: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                 max_new: int = 0, turns: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 rot_scale: float = 1.0, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, with_k: bool = True, stream: Optional[torch.cuda.Stream] = None,
+                 offsets: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Norms, rotates and appends a step's tokens to a paged cache (fa.h fa_append_paged).
+
+    q [T,H,d], k/v [T,Hkv,d] bf16 (parts of one projection are taken as they are); k_pages/v_pages
+    [num_pages,Hkv,page,d] bf16, or float8_e4m3fn / uint8 codes with fp32 scales [num_pages,Hkv]; block_table int32
+    [B,width]; seqlens_k int32 [B] with the new tokens counted; cu_seqlens int32 [B+1], or None for T / B tokens each.
+    ``turns`` (``rotary_turns``) sets the rotation, None for none; the weights bf16 [d] the norms, None for none;
+    ``offsets`` int32 [B] the position of row 0 of a cache that lost rows (``evict_paged``).
+    Returns the turned q [T,H,d] and k [T,Hkv,d] (None without ``with_k``), contiguous unless given."""
+    _tokens(q, k)
+    Hkv = k.shape[1]
+    pool, n, page, e4m3, B, width = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, q.shape[2],
+                                          q.get_device())
+    at = offsets is not None
+    return _append(q, k, v, pool, Hkv, n, page, B, width, _lib.fa_append_paged_at if at else _lib.fa_append_paged,
+                   "fa_append_paged_at" if at else "fa_append_paged", (e4m3,), cu_seqlens, max_new, turns, interleaved,
+                   rot_scale, q_weight, k_weight, eps, offsets, q_out, k_out, with_k, stream)
 
 
 def decode_paged_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int, max_len: int, num_splits: int = 0) -> int:
     return int(_lib.fa_decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits))
 
 
-def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
-                 seqlens_k: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
-                 v_scale: Optional[torch.Tensor] = None, scale: Optional[float] = None,
-                 max_len: Optional[int] = None, num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
-                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, with_lse: bool = True,
-                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
-    """Grouped decode over a paged cache (fa.h fa_decode_paged): q [B,H,Nq,d] bf16, any strides with d contiguous
-    (``append_paged``'s q of B x Nq tokens is ``q.view(B, Nq, H, d).transpose(1, 2)``), the pool and table as for
-    ``append_paged`` -> (o [B,H,Nq,d] bf16, lse [B,H,Nq] fp32). ``max_len`` bounds the lengths (default: all that a
-    row of the table covers); ``num_splits`` 0 lets the library choose. Without ``out``, o is token-major where q is, else contiguous."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
-        raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
-        raise ValueError("k_pages must be a CUDA tensor [num_pages, Hkv, page, d]")
+def _decode(q, pool, Hkv, n, page, rows, width, fn, where, e4m3, scale, max_len, num_splits, workspace, out, lse, with_lse,
+            stream):
+    """What the decode calls do with everything but the cache, whose checks are made."""
     dev = q.get_device()
     B, H, Nq, d = q_shape = q.shape
     qs = _heads(q, "q", dev, q_shape)
-    Hkv = k_pages.shape[1]
-    pool, n, page, e4m3, rows, width = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, d, dev)
     if rows != B:
         raise ValueError("seqlens_k and block_table must have B rows")
     kp, vp, ks, vs, table, table_stride, lens = pool
@@ -569,11 +581,242 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
         workspace = q.new_empty(max(1, decode_paged_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits)),
                                 dtype=torch.uint8)
     wp = _whole(workspace, "workspace", workspace.dtype, dev)
-    _call(dev, stream, _lib.fa_decode_paged,
+    _call(dev, stream, fn,
           (q.data_ptr(), _I64x3(*qs), kp, vp, ks, vs, table, table_stride, lens, out.data_ptr(), _I64x3(*os_), lp, B, H,
-           Hkv, Nq, d, n, page, max_len, e4m3, scale, num_splits, wp, workspace.nbytes), "fa_decode_paged",
-          (out, lse, workspace))
+           Hkv, Nq, d, n, page, max_len, *e4m3, scale, num_splits, wp, workspace.nbytes), where, (out, lse, workspace))
     return out, lse
+
+
+def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                 seqlens_k: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                 max_len: Optional[int] = None, num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, with_lse: bool = True,
+                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Grouped decode over a paged cache (fa.h fa_decode_paged): q [B,H,Nq,d] bf16, any strides with d contiguous
+    (``append_paged``'s q of B x Nq tokens is ``q.view(B, Nq, H, d).transpose(1, 2)``), the pool and table as for
+    ``append_paged`` -> (o [B,H,Nq,d] bf16, lse [B,H,Nq] fp32). ``max_len`` bounds the lengths (default: all that a
+    row of the table covers); ``num_splits`` 0 lets the library choose. Without ``out``, o is token-major where q is, else contiguous."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a CUDA tensor [num_pages, Hkv, page, d]")
+    Hkv = k_pages.shape[1]
+    pool, n, page, e4m3, rows, width = _pool(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, q.shape[3],
+                                             q.get_device())
+    return _decode(q, pool, Hkv, n, page, rows, width, _lib.fa_decode_paged, "fa_decode_paged", (e4m3,), scale, max_len,
+                   num_splits, workspace, out, lse, with_lse, stream)
+
+
+# --------------------------------------------------------------------------- 4-bit pages, reading and eviction
+
+PAGES_BF16, PAGES_E4M3, PAGES_FP4 = range(3)
+_U8 = torch.uint8
+_FP4 = getattr(torch, "float4_e2m1fn_x2", torch.uint8)   # (two codes a byte)
+
+
+def _table(block_table, name: str, dev: int, B: int = -1) -> Tuple[int, int, int, int]:
+    """A block table: (its address, its row stride, B, width)."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not _I32 or block_table.get_device() != dev:
+        raise _refusal(block_table, name, _I32, dev, None, "")
+    tab, ts = block_table.shape, block_table.stride()
+    if len(tab) != 2 or (ts[1] != 1 and tab[1] > 1) or (B >= 0 and tab[0] != B):
+        raise ValueError(f"{name} must be [B, width] with contiguous rows")
+    return block_table.data_ptr(), ts[0], tab[0], tab[1]
+
+
+def _pages(pages, scale, name: str, dev: int, Hkv: int = -1, d: int = -1) -> Tuple[int, Optional[int], int, int, int, int, int]:
+    """One pool of pages: (its address, its scales' or None, kind, pages, Hkv, page, d). The scales' type tells the kind:
+    none, fp32 (e4m3) or uint8 (4-bit rows)."""
+    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or pages.dim() != 4:
+        raise ValueError(f"{name} must be a CUDA tensor [num_pages, Hkv, page, d] (4-bit rows: d / 2 bytes)")
+    n, heads, page, width = pages.shape
+    if (Hkv >= 0 and heads != Hkv) or (scale is not None and not isinstance(scale, torch.Tensor)):
+        raise ValueError(f"{name} must have {Hkv} K/V heads, and its scales be a tensor")
+    sname = name.split("_")[0] + "_scale"
+    if scale is None:
+        kind, got, want = PAGES_BF16, width, (_BF16,)
+        sp = None
+    elif scale.dtype is _U8:
+        kind, got, want = PAGES_FP4, 2 * width, (_U8, _FP4)
+        sp = _whole(scale, sname, _U8, dev, (n, heads, page, got // 16))
+    else:
+        kind, got, want = PAGES_E4M3, width, (_CODES, _U8)
+        sp = _whole(scale, sname, _F32, dev, (n, heads))
+    if d >= 0 and got != d:
+        raise ValueError(f"{name} holds rows of {got} elements, not {d}")
+    return _whole(pages, name, pages.dtype if pages.dtype in want else want[0], dev), sp, kind, n, heads, page, got
+
+
+def _both(k_pages, v_pages, k_scale, v_scale, dev: int):
+    """The pools of keys and values, which are alike."""
+    kp, ks, kind, n, Hkv, page, d = _pages(k_pages, k_scale, "k_pages", dev)
+    other = _pages(v_pages, v_scale, "v_pages", dev)
+    if other[2:] != (kind, n, Hkv, page, d):
+        raise ValueError("k_pages and v_pages must have the same shape and kind of rows")
+    return kp, other[0], ks, other[1], kind, n, Hkv, page, d
+
+
+def _pool4(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv: int, d: int, dev: int):
+    """_pool for 4-bit rows."""
+    kp, vp, ks, vs, kind, n, heads, page, got = _both(k_pages, v_pages, k_scale, v_scale, dev)
+    if kind != PAGES_FP4 or heads != Hkv or got != d:
+        raise ValueError(f"k_pages and v_pages must be [num_pages, {Hkv}, page, {d // 2}] bytes with uint8 scales "
+                         f"[num_pages, {Hkv}, page, {d // 16}]")
+    tp, ts, B, width = _table(block_table, "block_table", dev)
+    return (kp, vp, ks, vs, tp, ts, _whole(seqlens_k, "seqlens_k", _I32, dev, (B,))), n, page, B, width
+
+
+def append_paged_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                     k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor, seqlens_k: torch.Tensor,
+                     cu_seqlens: Optional[torch.Tensor] = None, max_new: int = 0, turns: Optional[torch.Tensor] = None,
+                     interleaved: bool = False, rot_scale: float = 1.0, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     offsets: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                     k_out: Optional[torch.Tensor] = None, with_k: bool = True,
+                     stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``append_paged`` into 4-bit pages (fa.h fa_append_paged_fp4): k_pages/v_pages [num_pages,Hkv,page,d/2] uint8 or
+    float4_e2m1fn_x2, k_scale/v_scale uint8 [num_pages,Hkv,page,d/16]; the rest as for ``append_paged``."""
+    _tokens(q, k)
+    Hkv = k.shape[1]
+    pool, n, page, B, width = _pool4(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, q.shape[2],
+                                     q.get_device())
+    return _append(q, k, v, pool, Hkv, n, page, B, width, _lib.fa_append_paged_fp4, "fa_append_paged_fp4", (), cu_seqlens,
+                   max_new, turns, interleaved, rot_scale, q_weight, k_weight, eps, offsets, q_out, k_out, with_k, stream)
+
+
+def decode_paged_fp4_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int, max_len: int, num_splits: int = 0) -> int:
+    return int(_lib.fa_decode_paged_fp4_workspace_size(B, H, Hkv, Nq, d, max_len, num_splits))
+
+
+def decode_paged_fp4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                     v_scale: torch.Tensor, block_table: torch.Tensor, seqlens_k: torch.Tensor,
+                     scale: Optional[float] = None, max_len: Optional[int] = None, num_splits: int = 0,
+                     workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, with_lse: bool = True,
+                     stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``decode_paged`` over 4-bit pages (fa.h fa_decode_paged_fp4), laid out as for ``append_paged_fp4``."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a CUDA tensor [num_pages, Hkv, page, d / 2]")
+    Hkv = k_pages.shape[1]
+    pool, n, page, rows, width = _pool4(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, q.shape[3],
+                                        q.get_device())
+    return _decode(q, pool, Hkv, n, page, rows, width, _lib.fa_decode_paged_fp4, "fa_decode_paged_fp4", (),
+                   scale, max_len, num_splits, workspace, out, lse, with_lse, stream)
+
+
+def read_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor, seqlens_k: torch.Tensor,
+               cu_seqlens: torch.Tensor, total: int, k_scale: Optional[torch.Tensor] = None,
+               v_scale: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+               v_out: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows of a paged cache as packed bf16 k, v [total,Hkv,d] (fa.h fa_read_paged), which ``fwd_packed`` takes: the last
+    cu_seqlens[b+1] - cu_seqlens[b] rows of sequence b go to rows cu_seqlens[b] .. of the outputs. Pages of any kind: bf16,
+    e4m3 with fp32 scales, or 4-bit rows with uint8 scales."""
+    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
+        raise ValueError("k_pages must be a CUDA tensor")
+    dev = k_pages.get_device()
+    kp, vp, ks, vs, kind, n, Hkv, page, d = _both(k_pages, v_pages, k_scale, v_scale, dev)
+    tp, ts, B, width = _table(block_table, "block_table", dev)
+    lens, cu = _whole(seqlens_k, "seqlens_k", _I32, dev, (B,)), _whole(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,))
+    if total < 0:
+        raise ValueError("total must be >= 0")
+    shape, st, outs = (total, Hkv, d), (), []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = _empty(shape, (Hkv * d, d, 1), _BF16, dev)
+            st += (Hkv * d, d)
+        else:
+            st += _heads(t, name, dev, shape)
+        outs.append(t)
+    _call(dev, stream, _lib.fa_read_paged, (kp, vp, ks, vs, kind, tp, ts, lens, cu, outs[0].data_ptr(), outs[1].data_ptr(),
+                                            _I64x4(*st), B, total, Hkv, d, n, page, width), "fa_read_paged", outs)
+    return outs[0], outs[1]
+
+
+def _weight_rows(t, name: str, dev: int, B: int, Hkv: int) -> Tuple[int, int, int]:
+    """fp32 [B, Hkv, width] whose rows are contiguous and evenly apart: (address, row stride, width)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.get_device() != dev:
+        raise _refusal(t, name, _F32, dev, None, "")
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[0] != B or sh[1] != Hkv or (st[2] != 1 and sh[2] > 1):
+        raise ValueError(f"{name} must be fp32 [{B}, {Hkv}, width] with contiguous rows")
+    step = st[1] if Hkv > 1 else st[0] if B > 1 else sh[2]
+    if (B > 1 and st[0] != Hkv * step) or (B * Hkv > 1 and step < sh[2]):
+        raise ValueError(f"the rows of {name} must be evenly apart and not overlap")
+    return t.data_ptr(), step, sh[2]
+
+
+def weigh_paged(q: torch.Tensor, lse: torch.Tensor, k_pages: torch.Tensor, block_table: torch.Tensor,
+                seqlens_k: torch.Tensor, weights: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                scale: Optional[float] = None, max_len: Optional[int] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Adds to ``weights`` [B,Hkv,width] fp32, in place, the attention weights that the last Nq tokens of every sequence
+    give its keys, summed over the heads of a K/V head's group (fa.h fa_weigh_paged). q [B,H,Nq,d] and lse [B,H,Nq] are those
+    of the ``decode_paged`` call; pages of any kind, as for ``read_paged``; ``max_len`` bounds the lengths (default: what
+    ``weights`` and a row of the table cover). Returns ``weights``."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
+    dev = q.get_device()
+    B, H, Nq, d = q_shape = q.shape
+    qs = _heads(q, "q", dev, q_shape)
+    kp, ks, kind, n, Hkv, page, _ = _pages(k_pages, k_scale, "k_pages", dev, d=d)
+    tp, ts, _, width = _table(block_table, "block_table", dev, B)
+    lens, lp = _whole(seqlens_k, "seqlens_k", _I32, dev, (B,)), _whole(lse, "lse", _F32, dev, (B, H, Nq))
+    wp, ws, most = _weight_rows(weights, "weights", dev, B, Hkv)
+    most = min(most, width * page)
+    if max_len is None:
+        max_len = most
+    elif not 0 <= max_len <= most:
+        raise ValueError(f"max_len must be in [0, {most}], what weights and a row of block_table cover")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    _call(dev, stream, _lib.fa_weigh_paged, (q.data_ptr(), _I64x3(*qs), lp, kp, ks, kind, tp, ts, lens, wp, ws, B, H, Hkv, Nq,
+                                             d, n, page, max_len, scale), "fa_weigh_paged")
+    return weights
+
+
+def evict_paged(weights: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                seqlens_k: torch.Tensor, new_table: torch.Tensor, keep: int, first: int = 0, recent: int = 0,
+                k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                offsets: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
+                new_weights: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Cuts sequences to ``keep`` rows (fa.h fa_evict_paged): every K/V head keeps its first ``first`` and last ``recent``
+    rows and, of the others, those with the largest ``weights`` [B,Hkv,width]; they are copied, in order, to the pages of
+    ``new_table`` (pages that nothing else uses). Returns the kept rows' old indices int32 [B,Hkv,keep] (-1 past them), the new
+    lengths, the new weights (``new_weights`` [B,Hkv,>= keep] where given; 0 past the kept ones) and the positions of
+    row 0 for ``append_paged``'s ``offsets``."""
+    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
+        raise ValueError("k_pages must be a CUDA tensor")
+    dev = k_pages.get_device()
+    kp, vp, ks, vs, kind, n, Hkv, page, d = _both(k_pages, v_pages, k_scale, v_scale, dev)
+    tp, ts, B, width = _table(block_table, "block_table", dev)
+    np_, ns, _, new_pages = _table(new_table, "new_table", dev, B)
+    lens = _whole(seqlens_k, "seqlens_k", _I32, dev, (B,))
+    op = None if offsets is None else _whole(offsets, "offsets", _I32, dev, (B,))
+    wp, ws, most = _weight_rows(weights, "weights", dev, B, Hkv)
+    most = min(most, width * page)
+    if max_len is None:
+        max_len = most
+    elif not 0 <= max_len <= most:
+        raise ValueError(f"max_len must be in [0, {most}], what weights and a row of block_table cover")
+    if not 1 <= keep <= 1 << 30:
+        raise ValueError("keep must be in [1, 2^30]")
+    if min(keep, max_len) > new_pages * page:
+        raise ValueError(f"a row of new_table covers {new_pages * page} rows, fewer than may be kept")
+    if new_weights is None:
+        new_weights = _empty((B, Hkv, keep), (Hkv * keep, keep, 1), _F32, dev)
+    nwp, nws, new_width = _weight_rows(new_weights, "new_weights", dev, B, Hkv)
+    kept = _empty((B, Hkv, keep), (Hkv * keep, keep, 1), _I32, dev)
+    new_lens, new_offsets = _empty((B,), (1,), _I32, dev), _empty((B,), (1,), _I32, dev)
+    _call(dev, stream, _lib.fa_evict_paged,
+          (wp, ws, kp, vp, ks, vs, kind, tp, ts, lens, op, np_, ns, kept.data_ptr(), new_lens.data_ptr(),
+           new_offsets.data_ptr(), nwp, nws, new_width, B, Hkv, d, n, page, max_len, keep, first, recent), "fa_evict_paged",
+          (kept, new_lens, new_offsets, new_weights))
+    return kept, new_lens, new_weights, new_offsets
 
 
 # --------------------------------------------------------------------------- packed prefill
