@@ -6,11 +6,13 @@
 // keeps all. The rows that stay are moved, in order, to the pages of a new table.
 //
 // Two launches. (1) Selection. A weight's bits, flipped so that they order as
-// unsigned integers, are compared through digits: the rows between are counted by
-// their top 11 bits, then those that share the border's digit by the next 11, then
-// by the last 10; after that the border value and how many of its ties stay are
-// known, exactly. A cluster of blocks shares one (sequence, K/V head): each holds a
-// contiguous part of its keys in shared memory (so the weights are read once), and
+// unsigned integers, are compared digit by digit: the rows between are counted by
+// their top 11 bits; those that share the border's digit, a few in a hundred, go on
+// a list, which the next 11 and the last 10 bits are counted on; after that the
+// border value and how many of its ties stay are known, exactly. (With four digits of
+// 8 bits counted over all rows the instructions for each weight were the bound: 42 us
+// in place of FIRST for 32 sequences of 8-16k and 8 K/V heads.) A cluster of blocks shares one (sequence, K/V head): each holds a
+// contiguous part of its weights in shared memory (so they are read once), and
 // the counts are summed over the cluster's shared memories. Then every warp counts
 // its contiguous run, and with the runs' sums before it writes indices and weights
 // in order. (2) The move: a block takes 128 new rows of one head and copies their
@@ -24,6 +26,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "mma_sync.cuh"
@@ -35,40 +38,65 @@ namespace fa {
 
 namespace {
 
-constexpr int EV_THREADS = 512;
-constexpr int EV_WARPS = EV_THREADS / 32;
-constexpr int EV_BINS = 2048;
+constexpr int EV_MAX_WARPS = 32;
+constexpr int EV_BINS = 2048;     // of a digit of eleven bits
+constexpr int EV_COPIES = 4;      // of the first digit's counters
+constexpr int EV_LIST = 4096;     // rows of the border's first digit that a block's warps list, at most
 constexpr int EV_MAX_CLUSTER = 8;
 constexpr int EV_HELD = 40960;    // keys that a block holds in shared memory, at most
+constexpr int EV_FLIGHT = 8;      // weights that a thread asks for at once
 constexpr int EV_ROWS = 128;      // new rows of a moving block
 constexpr int EV_MOVE_THREADS = 256;
+constexpr unsigned ALL = 0xffffffffu;
 
-// Order-preserving bits: larger weights have larger keys, -0 as 0, NaN as -inf.
+// Bits that order weights downwards: larger ones have smaller keys, -0 as 0, NaN as -inf.
 __device__ __forceinline__ uint32_t order_key(float w) {
-  if (w != w) w = -INFINITY;
-  const uint32_t u = __float_as_uint(w + 0.f);
-  return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+  const uint32_t u = __float_as_uint(fmaxf(w + 0.f, -INFINITY));
+  return u ^ (~static_cast<uint32_t>(static_cast<int>(u) >> 31) & 0x7fffffffu);
+}
+__device__ __forceinline__ float weight_of(uint32_t key) {
+  return __uint_as_float(key ^ (~static_cast<uint32_t>(static_cast<int>(key) >> 31) & 0x7fffffffu));
 }
 
-static_assert(EV_BINS == 4 * EV_THREADS, "a thread sums four bins");
-
-struct EvShared {
-  uint32_t hist[EV_BINS];   // this block's counts
-  uint32_t part[EV_WARPS];  // scans
-  uint32_t above[EV_WARPS], ties[EV_WARPS];
-  uint32_t digit, left;     // the border's digit and how many of its rows stay
-  uint32_t totals[2];       // kept and tied rows of this block
+struct alignas(16) EvShared {  // (the keys that a block holds lie behind it, and are read four at a time)
+  union {
+    uint32_t hist[EV_BINS][EV_COPIES];  // counts of the first digit
+    struct {
+      uint32_t digit2[EV_BINS], digit3[EV_BINS / 2];  // of the other two
+      uint32_t list[EV_LIST];                         // keys that share the border's first digit, of each warp's run
+    };
+  };
+  uint32_t digit1[EV_BINS];            // the first digit's counts, summed
+  uint32_t all[EV_BINS];               // a digit's counts of the whole cluster
+  uint32_t part[EV_MAX_WARPS];         // scans
+  uint32_t above[EV_MAX_WARPS], ties[EV_MAX_WARPS], listed[EV_MAX_WARPS];  // of each warp's run
+  uint32_t digit, left;                // the border's digit, and how many of its rows stay
+  uint2 totals;                        // kept and tied rows of this block
 };
+static_assert(sizeof(EvShared) % 16 == 0, "the keys behind it are 16-byte aligned");
+
+// Sum over the lanes before this one.
+__device__ __forceinline__ uint32_t before_in_warp(uint32_t x, int lane) {
+  uint32_t inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(ALL, inc, o);
+    if (lane >= o) inc += y;
+  }
+  return inc - x;
+}
 
 }  // namespace
 
-// HELD: a block's keys fit its shared memory; else they are read again for every pass.
-template <bool HELD>
-__global__ void __launch_bounds__(EV_THREADS) fa_evict_select_kernel(const EvictPagedParams p) {
+// HELD: the keys of a block's rows fit its shared memory; else they are read again for every pass.
+template <bool HELD, int EV_THREADS>
+__global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) fa_evict_select_kernel(const EvictPagedParams p) {
+  constexpr int EV_WARPS = EV_THREADS / 32, LIST = EV_LIST / EV_WARPS;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-  extern __shared__ uint32_t ev_keys[];
-  __shared__ EvShared sh;
+  extern __shared__ __align__(16) uint8_t ev_smem[];
+  EvShared& sh = *reinterpret_cast<EvShared*>(ev_smem);
+  uint32_t* held = reinterpret_cast<uint32_t*>(ev_smem + sizeof(EvShared));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int pair = static_cast<int>(blockIdx.x) / ranks;
   const int b = pair / p.Hkv, hk = pair % p.Hkv;
@@ -84,132 +112,239 @@ __global__ void __launch_bounds__(EV_THREADS) fa_evict_select_kernel(const Evict
   const float* w = p.weights + pair * p.wstride;
   int* kept = p.kept + static_cast<long long>(pair) * keep;
   float* nw = p.new_weights + pair * p.new_wstride;
-  // past the rows that stay
-  for (int i = n_new + rank * EV_THREADS + tid; i < p.new_width; i += ranks * EV_THREADS) {
-    if (i < keep) kept[i] = -1;
-    nw[i] = 0.f;
-  }
-  if (L <= keep) {  // (the same for the whole cluster)
-    for (int i = rank * EV_THREADS + tid; i < L; i += ranks * EV_THREADS) {
+  const int step = ranks * EV_THREADS, own = rank * EV_THREADS + tid;
+  // rows that are kept without a look: all, or the first and the most recent; and what lies past the rows that stay
+  const int lo = L <= keep ? L : p.first, hi = L - p.recent;
+  auto edges = [&]() {
+    for (int i = own; i < lo; i += step) {
       kept[i] = i;
-      nw[i] = w[i];
+      nw[i] = __ldg(w + i);
     }
+    if (L > keep)
+      for (int i = own; i < p.recent; i += step) {
+        kept[keep - p.recent + i] = hi + i;
+        nw[keep - p.recent + i] = __ldg(w + hi + i);
+      }
+    for (int i = n_new + own; i < p.new_width; i += step) {
+      if (i < keep) kept[i] = -1;
+      nw[i] = 0.f;
+    }
+  };
+  uint32_t want = static_cast<uint32_t>(keep - p.first - p.recent);  // of the rows between stay
+  if (L <= keep || want == 0u) {  // (the same for the whole cluster)
+    edges();
     return;
   }
-  // ---- this block's part of the rows, a multiple of 32 of them a warp
-  const int per_warp = ((L + ranks * EV_WARPS - 1) / (ranks * EV_WARPS) + 31) / 32 * 32;
-  const int part0 = min(static_cast<long long>(L), static_cast<long long>(rank) * per_warp * EV_WARPS);
-  const int part1 = min(static_cast<long long>(L), static_cast<long long>(rank + 1) * per_warp * EV_WARPS);
-  const int lo = p.first, hi = L - p.recent;            // rows between
-  uint32_t want = static_cast<uint32_t>(keep - p.first - p.recent);  // of them stay
-  uint32_t border = 0u, known = 0u;                     // the border's upper digits and their mask
-  bool exact = want == 0u;                              // border found: rows with key > border (and `want` ties) stay
-  if (want == 0u) border = 0xffffffffu;                 // (no weight has this key: it would be a NaN's)
-  auto key_at = [&](int j) { return HELD ? ev_keys[j - part0] : order_key(__ldg(w + j)); };
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int bins = pass == 2 ? 1024 : EV_BINS;
-    for (int i = tid; i < EV_BINS; i += EV_THREADS) sh.hist[i] = 0u;
-    __syncthreads();
-    if (pass == 0) {
-      for (int j = part0 + tid; j < part1; j += EV_THREADS) {
-        const uint32_t k = order_key(__ldg(w + j));
-        if (HELD) ev_keys[j - part0] = k;
-        if (!exact && j >= lo && j < hi) atomicAdd(&sh.hist[k >> 21], 1u);
+  // ---- this block's part of the rows between, in runs of a multiple of 32 for each warp, counted from row lo
+  const float* between = w + lo;
+  const int n = hi - lo;
+  const int per_warp = ((n + ranks * EV_WARPS - 1) / (ranks * EV_WARPS) + 31) / 32 * 32;
+  const int part0 = min(static_cast<long long>(n), static_cast<long long>(rank) * per_warp * EV_WARPS);
+  const int part1 = min(static_cast<long long>(n), static_cast<long long>(rank + 1) * per_warp * EV_WARPS);
+  uint32_t border = 0u;                                 // the key of the last row that stays, and how many of its ties do
+  auto key_at = [&](int j) { return HELD ? held[j - part0] : order_key(__ldg(between + j)); };
+  auto sync_all = [&]() {
+    if (ranks > 1) cluster.sync();
+    else __syncthreads();
+  };
+  // the digit of the border among counts that all blocks of the cluster made (in BINS bins; the counts stay as they are)
+  auto find = [&](const uint32_t* counts, auto bins) {
+    constexpr int BINS = decltype(bins)::value, PER = BINS / EV_THREADS;  // neighbouring bins of a thread: 4, 2 or 1
+    sync_all();
+    if (ranks > 1) {  // every block sums its share of the bins over the cluster, and gives all blocks the sums
+      const int share = BINS / ranks;
+      for (int i = rank * share + tid; i < (rank + 1) * share; i += EV_THREADS) {
+        uint32_t x[EV_MAX_CLUSTER], y = 0u;
+#pragma unroll
+        for (int r = 0; r < EV_MAX_CLUSTER; ++r) x[r] = cluster.map_shared_rank(counts, r & (ranks - 1))[i];
+#pragma unroll
+        for (int r = 0; r < EV_MAX_CLUSTER; ++r) y += r < ranks ? x[r] : 0u;
+#pragma unroll
+        for (int r = 0; r < EV_MAX_CLUSTER; ++r)
+          if (r < ranks) cluster.map_shared_rank(sh.all, r)[i] = y;
       }
-    } else if (!exact) {
-      for (int j = part0 + tid; j < part1; j += EV_THREADS) {
-        const uint32_t k = key_at(j);
-        if (j >= lo && j < hi && ((k ^ border) & known) == 0u) atomicAdd(&sh.hist[(k >> shift) & (bins - 1)], 1u);
-      }
+      cluster.sync();
+      counts = sh.all;
     }
-    cluster.sync();
-    if (!exact) {
-      // every block sums the cluster's counts for itself; a thread has four bins, the highest first
-      uint32_t c[4], sum = 0u;
+    uint32_t n[PER], sum = 0u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int bin = EV_BINS - 1 - (4 * tid + i);
-        c[i] = 0u;
-        for (int r = 0; r < ranks; ++r) c[i] += cluster.map_shared_rank(sh.hist, r)[bin];
-        sum += c[i];
-      }
-      uint32_t inc = sum;
+    for (int i = 0; i < PER; ++i) n[i] = counts[tid * PER + i];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) sh.part[warp] = inc;
-      __syncthreads();
-      uint32_t before = inc - sum;
-      for (int x = 0; x < warp; ++x) before += sh.part[x];
+    for (int i = 0; i < PER; ++i) sum += n[i];
+    const uint32_t mine = __reduce_add_sync(ALL, sum);
+    if (lane == 0) sh.part[warp] = mine;
+    __syncthreads();
+    uint32_t before = __reduce_add_sync(ALL, lane < warp ? sh.part[lane] : 0u);
+    if (before < want && want <= before + mine) {  // the border is one of this warp's bins
+      before += before_in_warp(sum, lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (before < want && want <= before + c[i]) {
-          sh.digit = EV_BINS - 1 - (4 * tid + i);
+      for (int i = 0; i < PER; ++i) {
+        if (before < want && want <= before + n[i]) {
+          sh.digit = PER * tid + i;
           sh.left = want - before;
         }
-        before += c[i];
+        before += n[i];
       }
-      __syncthreads();
-      border |= sh.digit << shift;
-      known |= static_cast<uint32_t>(bins - 1) << shift;
-      want = sh.left;
     }
-    cluster.sync();  // nobody reads the counts any more
-    if (exact) break;
+    __syncthreads();
+    want = sh.left;
+    return sh.digit;
+  };
+  // ---- the first digit; the weights are read
+  for (int i = tid; i < EV_BINS * EV_COPIES / 4; i += EV_THREADS)
+    reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  {
+    uint32_t* mine = &sh.hist[0][lane % EV_COPIES];
+    int j = part0 + tid;
+    for (; j + (EV_FLIGHT - 1) * EV_THREADS < part1; j += EV_FLIGHT * EV_THREADS) {
+      float x[EV_FLIGHT];
+#pragma unroll
+      for (int f = 0; f < EV_FLIGHT; ++f) x[f] = __ldg(between + j + f * EV_THREADS);
+#pragma unroll
+      for (int f = 0; f < EV_FLIGHT; ++f) {
+        const uint32_t k = order_key(x[f]);
+        if (HELD) held[j + f * EV_THREADS - part0] = k;
+        atomicAdd(mine + (k >> 21) * EV_COPIES, 1u);
+      }
+    }
+#pragma unroll 4
+    for (; j < part1; j += EV_THREADS) {
+      const uint32_t k = order_key(__ldg(between + j));
+      if (HELD) held[j - part0] = k;
+      atomicAdd(mine + (k >> 21) * EV_COPIES, 1u);
+    }
   }
-  // ---- each warp counts its run, then writes
+  __syncthreads();
   const int run0 = min(part1, part0 + warp * per_warp), run1 = min(part1, run0 + per_warp);
-  uint32_t above = 0u, ties = 0u;
-  for (int j0 = run0; j0 < run1; j0 += 32) {
-    const int j = j0 + lane;
-    const bool in = j < run1, sure = in && (j < lo || j >= hi);
-    const uint32_t k = in ? key_at(j) : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, sure || (in && k > border)));
-    ties += __popc(__ballot_sync(0xffffffffu, in && !sure && k == border));
+  // keys of rows j .. j + 3 of the warp's run (j - run0 a multiple of four); past its end the key of no weight
+  auto four = [&](int j, uint32_t (&k)[4]) {
+    if (HELD) {  // (the memory does not end inside a four)
+      const uint4 y = *reinterpret_cast<const uint4*>(held + (j - part0));
+      k[0] = y.x, k[1] = y.y, k[2] = y.z, k[3] = y.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e >= run1) k[e] = 0xffffffffu;
+      else if (!HELD) k[e] = order_key(__ldg(between + j + e));
+  };
+  if (lane == 0) sh.listed[warp] = 0u;
+  for (int i = tid; i < EV_BINS; i += EV_THREADS) {
+    const uint4 c = *reinterpret_cast<const uint4*>(sh.hist[i]);
+    sh.digit1[i] = c.x + c.y + c.z + c.w;
   }
+  __syncthreads();
+  for (int i = tid; i < EV_BINS; i += EV_THREADS) sh.digit2[i] = 0u;
+  for (int i = tid; i < EV_BINS / 2; i += EV_THREADS) sh.digit3[i] = 0u;
+  const uint32_t top = find(sh.digit1, std::integral_constant<int, EV_BINS>{});
+  border = top << 21;
+  // ---- the keys of that digit go on the warp's list; those above are counted
+  uint32_t above = 0u, ties = 0u;
+#pragma unroll 2
+  for (int j = run0 + 4 * lane; j < run1; j += 128) {
+    uint32_t k[4], here = 0u;
+    four(j, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      above += k[e] < border;
+      here += k[e] >> 21 == top;
+    }
+    if (here != 0u) {
+      uint32_t i = atomicAdd(&sh.listed[warp], here);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (k[e] >> 21 == top) {
+          if (i < LIST) sh.list[warp * LIST + i] = k[e];
+          ++i;
+        }
+    }
+  }
+  __syncwarp();
+  const uint32_t listed = sh.listed[warp];
+  // every key of that digit in the warp's run (too many for the list, most weights alike: looked for again)
+  auto each = [&](auto&& f) {
+    if (listed <= LIST) {
+      for (uint32_t i = lane; i < listed; i += 32) f(sh.list[warp * LIST + i]);
+    } else {
+      for (int j = run0 + lane; j < run1; j += 32) {
+        const uint32_t k = key_at(j);
+        if (k >> 21 == top) f(k);
+      }
+    }
+  };
+  each([&](uint32_t k) { atomicAdd(&sh.digit2[(k >> 10) & 2047u], 1u); });
+  border |= find(sh.digit2, std::integral_constant<int, EV_BINS>{}) << 10;
+  each([&](uint32_t k) {
+    if (k >> 10 == border >> 10) atomicAdd(&sh.digit3[k & 1023u], 1u);
+  });
+  border |= find(sh.digit3, std::integral_constant<int, EV_BINS / 2>{});
+  each([&](uint32_t k) {
+    above += k < border;
+    ties += k == border;
+  });
+  above = __reduce_add_sync(ALL, above);
+  ties = __reduce_add_sync(ALL, ties);
   if (lane == 0) sh.above[warp] = above, sh.ties[warp] = ties;
   __syncthreads();
-  if (tid == 0) {
-    uint32_t a = 0u, t = 0u;
-    for (int x = 0; x < EV_WARPS; ++x) {
-      const uint32_t a1 = sh.above[x], t1 = sh.ties[x];
-      sh.above[x] = a, sh.ties[x] = t;
-      a += a1, t += t1;
+  const uint32_t a_of = lane < EV_WARPS ? sh.above[lane] : 0u, t_of = lane < EV_WARPS ? sh.ties[lane] : 0u;
+  uint32_t at = lo + __reduce_add_sync(ALL, lane < warp ? a_of : 0u);
+  uint32_t tie = __reduce_add_sync(ALL, lane < warp ? t_of : 0u);
+  if (ranks > 1) {
+    if (warp == 0) {
+      const uint32_t all_above = __reduce_add_sync(ALL, a_of), all_ties = __reduce_add_sync(ALL, t_of);
+      if (lane == 0) sh.totals = make_uint2(all_above, all_ties);
     }
-    sh.totals[0] = a, sh.totals[1] = t;
+    cluster.sync();
+    const uint2 t = lane < rank ? *cluster.map_shared_rank(&sh.totals, lane) : make_uint2(0u, 0u);
+    at += __reduce_add_sync(ALL, t.x);
+    tie += __reduce_add_sync(ALL, t.y);
+    __syncthreads();
+    cluster.barrier_arrive();  // (waited for at the end: the totals are read before a block leaves)
   }
-  cluster.sync();
-  uint32_t at = sh.above[warp], tie = sh.ties[warp];
-  for (int r = 0; r < rank; ++r) {
-    const uint32_t* t = cluster.map_shared_rank(sh.totals, r);
-    at += t[0], tie += t[1];
-  }
-  for (int j0 = run0; j0 < run1; j0 += 32) {
-    const int j = j0 + lane;
-    const bool in = j < run1, sure = in && (j < lo || j >= hi);
-    const uint32_t k = in ? key_at(j) : 0u;
-    const unsigned a = __ballot_sync(0xffffffffu, sure || (in && k > border));
-    const unsigned t = __ballot_sync(0xffffffffu, in && !sure && k == border);
-    const unsigned below = (1u << lane) - 1u;
-    const uint32_t my_ties = tie + __popc(t & below);
-    const bool stays = ((a >> lane) & 1u) || (((t >> lane) & 1u) && my_ties < want);
-    if (stays) {
-      const uint32_t i = at + __popc(a & below) + min(my_ties, want);
-      kept[i] = j;
-      nw[i] = __ldg(w + j);
+  // ---- indices and weights of the warp's run, in order
+#pragma unroll 2
+  for (int j0 = run0; j0 < run1; j0 += 128) {
+    const int j = j0 + 4 * lane;
+    uint32_t k[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu}, over = 0u, tied = 0u;
+    if (j < run1) four(j, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      over += k[e] < border;
+      tied += k[e] == border;
     }
-    at += __popc(a);
-    tie += __popc(t);
+    // rows above and ties before this lane's (both below 129), summed as the halves of a word
+    uint32_t inc = over + (tied << 16);
+    const uint32_t mine = inc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(ALL, inc, o);
+      if (lane >= o) inc += y;
+    }
+    uint32_t my_at = at + ((inc - mine) & 0xffffu), my_tie = tie + ((inc - mine) >> 16);
+    const uint32_t all = __shfl_sync(ALL, inc, 31);
+    at += all & 0xffffu;
+    tie += all >> 16;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool t = k[e] == border;
+      if (k[e] < border || (t && my_tie < want)) {
+        const uint32_t i = my_at + min(my_tie, want);
+        kept[i] = lo + j + e;
+        nw[i] = weight_of(k[e]);
+        // (0 may have been -0, and -inf NaN: rare among the rows that stay)
+        if (k[e] == 0x7fffffffu || k[e] == 0xff800000u) nw[i] = __ldg(between + j + e);
+      }
+      my_at += k[e] < border;
+      my_tie += t;
+    }
   }
-  cluster.sync();  // the totals are read before a block leaves
+  edges();
+  if (ranks > 1) cluster.barrier_wait();
 }
 
 // ---- the move
 template <int D, int KIND>
-__global__ void __launch_bounds__(EV_MOVE_THREADS) fa_evict_move_kernel(const EvictPagedParams p) {
+__global__ void __launch_bounds__(EV_MOVE_THREADS, KIND == PAGES_E4M3 ? 5 : 6) fa_evict_move_kernel(const EvictPagedParams p) {
   constexpr int RB = paged_row_bytes(KIND, D), CR = RB / 16, SB = D / 16;
   __shared__ long long s_src[EV_ROWS], s_dst[EV_ROWS];  // rows in the pool, or -1
   __shared__ float s_scale[2][EV_ROWS];                  // e4m3: old scales of the rows
@@ -287,16 +422,17 @@ __global__ void __launch_bounds__(EV_MOVE_THREADS) fa_evict_move_kernel(const Ev
         const int r = (is_v ? x - items / 2 : x) / CR;
         const float old = s_scale[is_v][r];
         const float now = __uint_as_float(s_most[is_v][((row0 + r) >> p.page_shift) - (row0 >> p.page_shift)]);
-        if (old != now) {  // (a ratio of powers of two is exact; NaN codes stay NaN)
+        // In f16: for powers of two exact down to 2^-24, far below half the least code (2^-10), so the one rounding is that
+        // to e4m3; other ratios are off by 2^-11 of themselves. NaN codes stay NaN.
+        if (old != now) {
           const float f = old / now;
+          const uint32_t f2 = pack_f16x2(f, f);
           uint32_t* w[4] = {&y[i].x, &y[i].y, &y[i].z, &y[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t h0, h1;
             e4m3x4_to_f16x2x2(*w[e], h0, h1);
-            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-            const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-            *w[e] = pack_e4m3x4(a.x * f, a.y * f, c.x * f, c.y * f);
+            *w[e] = f16x2x2_to_e4m3x4(hmul2_bits(h0, f2), hmul2_bits(h1, f2));
           }
         }
       }
@@ -315,8 +451,36 @@ __global__ void __launch_bounds__(EV_MOVE_THREADS) fa_evict_move_kernel(const Ev
   }
 }
 
+template <int THREADS>
+static cudaError_t ev_attrs() {
+  const cudaError_t e = cudaFuncSetAttribute(fa_evict_select_kernel<true, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(sizeof(EvShared)) + EV_HELD * 4);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(fa_evict_select_kernel<false, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(sizeof(EvShared)));
+}
 cudaError_t evict_paged_set_attributes() {
-  return cudaFuncSetAttribute(fa_evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_HELD * 4);
+  const cudaError_t e = ev_attrs<512>();
+  return e != cudaSuccess ? e : ev_attrs<1024>();
+}
+
+template <int THREADS>
+static cudaError_t ev_select(const EvictPagedParams& p, int ranks, cudaStream_t stream) {
+  const int warps = ranks * (THREADS / 32);
+  const long long block = ((p.max_len + static_cast<long long>(warps) - 1) / warps + 31) / 32 * THREADS;  // keys of one, at most
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ranks, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.Hkv * ranks));
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = sizeof(EvShared);
+  if (block > EV_HELD) return cudaLaunchKernelEx(&cfg, fa_evict_select_kernel<false, THREADS>, p);
+  cfg.dynamicSmemBytes += block * 4;
+  return cudaLaunchKernelEx(&cfg, fa_evict_select_kernel<true, THREADS>, p);
 }
 
 template <int D>
@@ -328,23 +492,11 @@ static cudaError_t ev_move(int kind, const cudaLaunchConfig_t& cfg, const EvictP
 
 cudaError_t launch_evict_paged(int d, int kind, const EvictPagedParams& p, int num_sms, cudaStream_t stream) {
   const long long pairs = static_cast<long long>(p.B) * p.Hkv;
-  // Blocks of a cluster: more while a block would have over 4096 rows and the GPU has SMs left.
+  // Blocks of a cluster: more while a block would have over 4096 rows and the GPU an SM for each. Large blocks where each
+  // has an SM, but not in clusters: eight free SMs next to one another are not found for every one of them then.
   int ranks = 1;
-  while (ranks < EV_MAX_CLUSTER && p.max_len > 4096LL * ranks && pairs * ranks * 2 <= 2LL * num_sms) ranks *= 2;
-  const int per_warp = ((p.max_len + ranks * EV_WARPS - 1) / (ranks * EV_WARPS) + 31) / 32 * 32;
-  const bool held = per_warp * EV_WARPS <= EV_HELD;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = ranks, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs * ranks));
-  cfg.blockDim = dim3(EV_THREADS);
-  cfg.dynamicSmemBytes = held ? per_warp * EV_WARPS * 4 : 0;
-  cfg.stream = stream;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = held ? cudaLaunchKernelEx(&cfg, fa_evict_select_kernel<true>, p)
-                             : cudaLaunchKernelEx(&cfg, fa_evict_select_kernel<false>, p);
+  while (ranks < EV_MAX_CLUSTER && p.max_len > 4096LL * ranks && pairs * ranks * 2 <= num_sms) ranks *= 2;
+  const cudaError_t e = ranks == 1 && pairs <= num_sms ? ev_select<1024>(p, ranks, stream) : ev_select<512>(p, ranks, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t mv{};
   mv.gridDim = dim3(static_cast<unsigned>(pairs * ((p.keep + EV_ROWS - 1) / EV_ROWS)));
