@@ -51,7 +51,7 @@
 
 #include "fp4.cuh"
 #include "mma_sync.cuh"
-#include "paged.cuh"
+#include "paged_walk.cuh"
 
 namespace fa {
 
@@ -117,15 +117,6 @@ __device__ __forceinline__ int dp_o_elem(int gid, int jj) {
   else return gid * (D / 8) + 4 * jj;
 }
 
-// How the batch's tiles are shared out: tile t of the whole (sequence by
-// sequence, K/V head by K/V head) belongs to range t's; range r has tiles
-// begin(r) .. begin(r + 1) - 1, none of them empty.
-struct DpRanges {
-  long long tiles, n;  // all tiles; ranges
-  __device__ __forceinline__ DpRanges(long long tiles_, int most) : tiles(tiles_), n(most < tiles_ ? most : tiles_) {}
-  __device__ __forceinline__ long long begin(long long r) const { return r * tiles / n; }
-};
-
 // What a row's scores count from.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -150,66 +141,25 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
   const int worker = static_cast<int>(blockIdx.x) * DP_WARPS + warp;
   const int rt = worker % p.row_tiles;
   const int range = worker / p.row_tiles;
-  long long sum = 0;
   bool clipped = false;
-#pragma unroll 4
-  for (int b = lane; b < p.B; b += 32) {
-    const int raw = __ldg(p.seqlens + b), L = paged_clip_len(raw, p.max_len);
-    clipped = clipped || L != raw;
-    sum += (L + C::KS - 1) / C::KS;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(ALL, sum, o);
+  const long long sum = paged_count_tiles<C::KS>(p.seqlens, p.B, p.max_len, lane, clipped);
   if (worker == 0 && __any_sync(ALL, clipped) && lane == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
-  const DpRanges ranges(sum * p.Hkv, p.n_ranges);
+  const PagedRanges ranges(sum * p.Hkv, p.n_ranges);
   if (range >= ranges.n) return;
   const long long t0 = ranges.begin(range);
   int todo = static_cast<int>(ranges.begin(range + 1) - t0);  // tiles to compute (the host keeps a range below 2^31)
-  int b = 0, hk = 0, i = 0, L = 0, nt = 0;        // position: sequence, K/V head, tile; its length and tiles
-  {
-    long long base = 0;  // tiles of one K/V head of the sequences before
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int mine = b0 + lane < p.B ? dp_len(p, b0 + lane) : 0;
-      const int n = (mine + C::KS - 1) / C::KS;
-      int inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(ALL, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const unsigned past = __ballot_sync(ALL, (base + inc) * p.Hkv > t0);
-      if (past != 0u) {
-        const int at = __ffs(past) - 1;
-        b = b0 + at;
-        L = __shfl_sync(ALL, mine, at);
-        nt = __shfl_sync(ALL, n, at);
-        const long long rest = t0 - (base + __shfl_sync(ALL, inc, at) - nt) * p.Hkv;
-        hk = static_cast<int>(rest / nt);
-        i = static_cast<int>(rest % nt);
-        break;
-      }
-      base += __shfl_sync(ALL, inc, 31);
-    }
-  }
-  // the next tile after (b, hk, i)
-  auto advance = [&](int& b_, int& hk_, int& i_, int& L_, int& nt_) {
-    if (++i_ < nt_) return;
-    i_ = 0;
-    if (++hk_ < p.Hkv) return;
-    hk_ = 0;
-    do {
-      if (++b_ >= p.B) return;  // past the last tile
-      L_ = dp_len(p, b_);
-      nt_ = (L_ + C::KS - 1) / C::KS;
-    } while (nt_ == 0);
-  };
+  // position: sequence, K/V head, tile; its length and tiles
+  PagedTile at = paged_seek<C::KS>(p.seqlens, p.B, p.Hkv, p.max_len, t0, lane);
+  int &b = at.b, &hk = at.hk, &i = at.i, &L = at.L, &nt = at.nt;
+  auto advance = [&](PagedTile& t) { paged_next<C::KS>(t, p.seqlens, p.B, p.Hkv, p.max_len); };
 
   // ---- the copies, which run ahead of the computation: position of the next tile to copy, and its pages
   const uint32_t ring = sbase + warp * (C::DP_STAGES * C::STAGE);
   const uint32_t meta = sbase + C::META_OFF + warp * (C::DP_STAGES * C::META);
   const uint8_t* my_ring = dp_smem + warp * (C::DP_STAGES * C::STAGE);
   const uint8_t* my_meta = dp_smem + C::META_OFF + warp * (C::DP_STAGES * C::META);
-  int cb = b, chk = hk, ci = i, cL = L, cnt = nt;
+  PagedTile ahead = at;
+  int &cb = ahead.b, &chk = ahead.hk, &ci = ahead.i, &cL = ahead.L;
   int to_copy = todo;
   uint32_t copied = 0u;          // tiles copied so far
   uint32_t hidden = 0u;          // 4 bits for each of 8 tiles: groups whose page is not in the pool
@@ -291,7 +241,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
       }
       ++copied;
       --to_copy;
-      advance(cb, chk, ci, cL, cnt);
+      advance(ahead);
       id = page_of();
     }
     cp_async_commit();
@@ -751,7 +701,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
     todo -= i1 - i0;
     if (todo > 0) {
       i = nt - 1;  // the last tile of (b, hk) is done
-      advance(b, hk, i, L, nt);
+      advance(at);
     }
   }
   cp_async_wait<0>();

@@ -20,7 +20,7 @@
 
 #include "fp4.cuh"
 #include "mma_sync.cuh"
-#include "paged.cuh"
+#include "paged_walk.cuh"
 
 namespace fa {
 
@@ -28,6 +28,8 @@ namespace {
 
 constexpr int WG_WARPS = 4;
 constexpr int WG_THREADS = 32 * WG_WARPS;
+constexpr int WG_FEW_CTAS = 4;   // blocks of the kernel for few rows that an SM holds
+constexpr unsigned ALL = 0xffffffffu;
 
 template <int D, int KIND>
 struct WgCfg {
@@ -36,7 +38,7 @@ struct WgCfg {
   static constexpr int KST = D / 16;                 // k-steps
   static constexpr int LB = RB / 4;                  // bytes of a row that one lane holds: 8, 16, 32 or 64
   static constexpr int LW = LB / 4;                  // as words
-  static constexpr int KG = KIND == PAGES_FP4 ? 4 : 64 / LB;  // 16-key groups of a warp's tile
+  static constexpr int KG = KIND == PAGES_FP4 ? 4 : 64 / LB;  // 16-key groups of a warp's tile: 4, 2 or 1
   static constexpr int TILE = 16 * KG;
 };
 
@@ -47,7 +49,69 @@ struct WgRaw {
   uint32_t f[2];  // 4-bit rows: the lane's one or two scale bytes
 };
 
-// Lane tig and k-step j of the four elements 4 x .. 4 x + 3 of a row, in the order that the lanes hold keys: 16-byte
+// The lane's share of the rows gid, gid + 8 of a group whose first row is `row0` of the pool; rows from `rows` on (and all,
+// for row0 < 0) are zeros.
+template <int D, int KIND>
+__device__ __forceinline__ void wg_load(WgRaw<D, KIND>& x, const WeighPagedParams& p, long long row0, int rows, int gid, int tig) {
+  using C = WgCfg<D, KIND>;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = gid + 8 * h;
+    const bool in = row0 >= 0 && r < rows;
+    const uint8_t* src = static_cast<const uint8_t*>(p.k) + (in ? row0 + r : 0) * C::RB;
+    if constexpr (KIND == PAGES_FP4) {
+      const uint8_t* sp = static_cast<const uint8_t*>(p.k_scale) + (in ? row0 + r : 0) * (D / 16);
+      if constexpr (D == 128) {
+        const uint4 y = in ? __ldg(reinterpret_cast<const uint4*>(src) + tig) : make_uint4(0, 0, 0, 0);
+        x.w[h][0] = y.x, x.w[h][1] = y.y, x.w[h][2] = y.z, x.w[h][3] = y.w;
+        x.f[h] = in ? __ldg(reinterpret_cast<const uint16_t*>(sp) + tig) : 0u;
+      } else {
+        const uint2 y = in ? __ldg(reinterpret_cast<const uint2*>(src) + tig) : make_uint2(0, 0);
+        x.w[h][0] = y.x, x.w[h][1] = y.y;
+        x.f[h] = in ? __ldg(sp + tig) : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C::LW / 4; ++i) {
+        const uint4 y = in ? __ldg(reinterpret_cast<const uint4*>(src) + tig + 4 * i) : make_uint4(0, 0, 0, 0);
+        x.w[h][4 * i] = y.x, x.w[h][4 * i + 1] = y.y, x.w[h][4 * i + 2] = y.z, x.w[h][4 * i + 3] = y.w;
+      }
+    }
+  }
+}
+
+// The two rows' A fragments of every k-step, handed on as soon as they are made: f(k-step, a0, a1, a2, a3).
+template <int D, int KIND, class F>
+__device__ __forceinline__ void wg_fragments(const WgRaw<D, KIND>& x, F&& f) {
+  using C = WgCfg<D, KIND>;
+  if constexpr (KIND == PAGES_FP4) {
+    const uint32_t fa[2] = {fp4_scale2<0>(x.f[0]), fp4_scale2<1>(x.f[0])};
+    const uint32_t fb[2] = {fp4_scale2<0>(x.f[1]), fp4_scale2<1>(x.f[1])};
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t y[4], z[4];
+      e2m1x8_to_f16x2x4(x.w[0][i], y);
+      e2m1x8_to_f16x2x4(x.w[1][i], z);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        f(2 * i + e, hmul2_bits(y[2 * e], fa[i >> 1]), hmul2_bits(z[2 * e], fb[i >> 1]), hmul2_bits(y[2 * e + 1], fa[i >> 1]),
+          hmul2_bits(z[2 * e + 1], fb[i >> 1]));
+    }
+  } else if constexpr (KIND == PAGES_E4M3) {
+#pragma unroll
+    for (int i = 0; i < C::LW; ++i) {
+      uint32_t a0, a1, a2, a3;
+      e4m3x4_to_f16x2x2(x.w[0][i], a0, a2);
+      e4m3x4_to_f16x2x2(x.w[1][i], a1, a3);
+      f(i, a0, a1, a2, a3);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C::KST; ++i) f(i, x.w[0][2 * i], x.w[1][2 * i], x.w[0][2 * i + 1], x.w[1][2 * i + 1]);
+  }
+}
+
+// The four elements 4 x .. 4 x + 3 of a row belong to lane tig and k-step j, in the order that the lanes hold keys: 16-byte
 // pieces tig, tig + 4, ..., or a quarter of a 4-bit row.
 template <int D, int KIND>
 __device__ __forceinline__ void wg_place(int x, int& tig, int& j) {
@@ -60,13 +124,213 @@ __device__ __forceinline__ void wg_place(int x, int& tig, int& j) {
     j = x / Q / 4 * Q + x % Q;
   }
 }
+// And back: the first of those four elements.
+template <int D, int KIND>
+__device__ __forceinline__ int wg_elem(int tig, int j) {
+  if constexpr (KIND == PAGES_FP4) return 4 * (tig * (D / 16) + j);
+  constexpr int Q = KIND == PAGES_E4M3 ? 4 : 2;
+  return 4 * ((j / Q * 4 + tig) * Q + j % Q);
+}
+
+// Largest magnitude of four bf16 values.
+__device__ __forceinline__ float wg_amax(uint2 x) {
+  return fmaxf(fmaxf(fabsf(__uint_as_float(x.x << 16)), fabsf(__uint_as_float(x.x & 0xffff0000u))),
+               fmaxf(fabsf(__uint_as_float(x.y << 16)), fabsf(__uint_as_float(x.y & 0xffff0000u))));
+}
+// As in the paged decode, codes meet queries in f16: the row's power of two brings its largest element to [1, 2), so that all
+// but elements below 2^-14 of it are exact. `up` is the power.
+__device__ __forceinline__ float wg_powers(float amax, float& up) {
+  const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -120), 120);
+  up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+}
+__device__ __forceinline__ uint2 wg_to_f16(uint2 x, float down) {
+  return make_uint2(pack_f16x2(__uint_as_float(x.x << 16) * down, __uint_as_float(x.x & 0xffff0000u) * down),
+                    pack_f16x2(__uint_as_float(x.y << 16) * down, __uint_as_float(x.y & 0xffff0000u) * down));
+}
+
+// Sums v[g][h] (group g, key gid + 8 h) over the four lanes tig: afterwards v[x][0] of lane tig is that of group
+// g(x) = x + (tig / 2) KG / 2 and key gid + 8 (tig % 2); with one group lanes 2 and 3 hold what 0 and 1 do.
+template <int KG>
+__device__ __forceinline__ void wg_sum_lanes(float (&v)[KG][2], int tig) {
+#pragma unroll
+  for (int g = 0; g < KG; ++g) {
+    const float mine = (tig & 1) ? v[g][1] : v[g][0], other = (tig & 1) ? v[g][0] : v[g][1];
+    v[g][0] = mine + __shfl_xor_sync(ALL, other, 1);
+  }
+  if constexpr (KG == 1) {
+    v[0][0] += __shfl_xor_sync(ALL, v[0][0], 2);
+  } else {
+#pragma unroll
+    for (int x = 0; x < KG / 2; ++x) {
+      const float mine = (tig & 2) ? v[x + KG / 2][0] : v[x][0], other = (tig & 2) ? v[x][0] : v[x + KG / 2][0];
+      v[x][0] = mine + __shfl_xor_sync(ALL, other, 2);
+    }
+  }
+}
 
 }  // namespace
 
+// ---- up to 8 or 16 rows a K/V head: the queries' fragments stay in registers
+template <int D, int KIND, int NR>
+__global__ void __launch_bounds__(WG_THREADS, NR == 1 ? WG_FEW_CTAS : 3) fa_weigh_paged_few_kernel(const WeighPagedParams p) {
+  using C = WgCfg<D, KIND>;
+  constexpr int KG = C::KG;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int range = static_cast<int>(blockIdx.x) * WG_WARPS + warp;
+  bool clipped = false;
+  const long long sum = paged_count_tiles<C::TILE>(p.seqlens, p.B, p.max_len, lane, clipped);
+  if (range == 0 && __any_sync(ALL, clipped) && lane == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
+  const PagedRanges ranges(sum * p.Hkv, p.n_ranges);
+  if (range >= ranges.n) return;
+  const long long t0 = ranges.begin(range);
+  int todo = static_cast<int>(ranges.begin(range + 1) - t0);
+  PagedTile at = paged_seek<C::TILE>(p.seqlens, p.B, p.Hkv, p.max_len, t0, lane);
+
+  // ---- loads run a tile ahead (each group's as soon as the one before is used), page entries two
+  PagedTile ahead = at;
+  int to_load = todo;
+  auto page_of = [&]() -> int {
+    const int key = ahead.i * C::TILE + 16 * lane;
+    return (lane < KG && to_load > 0 && key < ahead.L) ? __ldg(p.table + ahead.b * p.table_stride + (key >> p.page_shift)) : -1;
+  };
+  int id = page_of();
+  WgRaw<D, KIND> raw[KG];
+  float ka[KG];
+  // of the tile that is loaded next: row of the lane's group, its rows, the groups to work on, e4m3 scale
+  long long off = -1;
+  int rows = 0;
+  unsigned next_live = 0u;
+  float scale = 1.f;
+  auto locate = [&]() {
+    const int key = ahead.i * C::TILE + 16 * lane;
+    const bool want = lane < KG && to_load > 0 && key < ahead.L;
+    off = want ? paged_row_offset(id, p.num_pages, p.Hkv, ahead.hk, p.page, key & (p.page - 1), 1) : -1;
+    if (__any_sync(ALL, want && off < 0) && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
+    rows = ahead.L - ahead.i * C::TILE;
+    next_live = __ballot_sync(ALL, off >= 0);
+    if constexpr (KIND == PAGES_E4M3)
+      scale = off >= 0 ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + ahead.hk) : 0.f;
+    if (to_load > 0) {
+      --to_load;
+      if (to_load > 0) paged_next<C::TILE>(ahead, p.seqlens, p.B, p.Hkv, p.max_len);
+      id = page_of();
+    }
+  };
+  locate();
+#pragma unroll
+  for (int g = 0; g < KG; ++g) {
+    wg_load<D, KIND>(raw[g], p, __shfl_sync(ALL, off, g), rows - 16 * g, gid, tig);
+    ka[g] = __shfl_sync(ALL, scale, g);
+  }
+  unsigned live = next_live;
+
+  while (todo > 0) {
+    // ================================================================ one segment: keys of (b, hk) from tile i on
+    const int b = at.b, hk = at.hk, L = at.L, i1 = todo < at.nt - at.i ? at.i + todo : at.nt;
+    uint2 qf[NR][C::KST];
+    float c1[NR][2], ls[NR][2];  // factors of the scores of rows 2 tig and 2 tig + 1, their log-sum-exp (log2 units)
+    int lim[NR][2];              // the last key they see; -1: the row adds nothing
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int r = n * 8 + gid;
+      const bool in = r < p.R;
+      const uint16_t* qr = static_cast<const uint16_t*>(p.q) + b * p.qsb + (hk * p.G + (in ? r / p.Nq : 0)) * p.qsh +
+                           (in ? r % p.Nq : 0) * p.qst;
+      float amax = 0.f, up = 1.f;
+#pragma unroll
+      for (int j = 0; j < C::KST; ++j) {
+        qf[n][j] = in ? __ldg(reinterpret_cast<const uint2*>(qr + wg_elem<D, KIND>(tig, j))) : make_uint2(0u, 0u);
+        if (C::F16) amax = fmaxf(amax, wg_amax(qf[n][j]));
+      }
+      if constexpr (C::F16) {
+        amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, 2));
+        const float down = wg_powers(amax, up);
+#pragma unroll
+        for (int j = 0; j < C::KST; ++j) qf[n][j] = wg_to_f16(qf[n][j], down);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        c1[n][e] = p.scale_log2 * (C::F16 ? __shfl_sync(ALL, up, (2 * tig + e) * 4) : 1.f);
+        const int r2 = n * 8 + 2 * tig + e;
+        const bool real = r2 < p.R;
+        const int h2 = hk * p.G + (real ? r2 / p.Nq : 0), tok = real ? r2 % p.Nq : 0;
+        const float lse = real ? __ldg(p.lse + (static_cast<long long>(b) * p.H + h2) * p.Nq + tok) : -INFINITY;
+        const bool none = lse == -INFINITY;
+        ls[n][e] = none ? 0.f : lse * 1.4426950408889634f;
+        lim[n][e] = none ? -1 : min(L - 1, L - p.Nq + tok);
+      }
+    }
+    const int full_lim = L - p.Nq;  // every row that adds anything sees the keys up to here
+    float* wrow = p.weights + (static_cast<long long>(b) * p.Hkv + hk) * p.wstride;
+
+    for (; at.i < i1; ++at.i) {
+      const int key0 = at.i * C::TILE;
+      // the weights of this lane's keys
+      constexpr int OWN = KG > 1 ? KG / 2 : 1;
+      float old[OWN];
+      int mine[OWN];
+      bool writes[OWN];
+#pragma unroll
+      for (int x = 0; x < OWN; ++x) {
+        const int g = x + (tig >> 1) * (KG / 2);
+        mine[x] = key0 + 16 * g + gid + 8 * (tig & 1);
+        writes[x] = ((live >> g) & 1u) && mine[x] < L && (KG > 1 || tig < 2);
+        old[x] = writes[x] ? wrow[mine[x]] : 0.f;
+      }
+      locate();
+      float v[KG][2];
+#pragma unroll
+      for (int g = 0; g < KG; ++g) {
+        float s[NR][4];
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+        wg_fragments<D, KIND>(raw[g], [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n) mma_16816<C::F16>(s[n], a0, a1, a2, a3, qf[n][j].x, qf[n][j].y);
+        });
+        const float kf = ka[g];
+        wg_load<D, KIND>(raw[g], p, __shfl_sync(ALL, off, g), rows - 16 * g, gid, tig);
+        ka[g] = __shfl_sync(ALL, scale, g);
+        v[g][0] = v[g][1] = 0.f;
+        const int key = key0 + 16 * g + gid;
+        const bool some = key0 + 16 * g + 15 > full_lim;  // keys that not every row sees
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          const float c0 = KIND == PAGES_E4M3 ? c1[n][0] * kf : c1[n][0], c2 = KIND == PAGES_E4M3 ? c1[n][1] * kf : c1[n][1];
+          float pr[4] = {ex2_approx(fmaf(s[n][0], c0, -ls[n][0])), ex2_approx(fmaf(s[n][1], c2, -ls[n][1])),
+                         ex2_approx(fmaf(s[n][2], c0, -ls[n][0])), ex2_approx(fmaf(s[n][3], c2, -ls[n][1]))};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (some ? key + 8 * (e >> 1) > lim[n][e & 1] : lim[n][e & 1] < 0) pr[e] = 0.f;
+          v[g][0] += pr[0] + pr[1];
+          v[g][1] += pr[2] + pr[3];
+        }
+      }
+      wg_sum_lanes<KG>(v, tig);
+#pragma unroll
+      for (int x = 0; x < OWN; ++x)
+        if (writes[x]) wrow[mine[x]] = old[x] + v[x][0];
+      live = next_live;
+      --todo;
+    }
+    if (todo > 0) {
+      --at.i;  // the last tile of (b, hk) is done
+      paged_next<C::TILE>(at, p.seqlens, p.B, p.Hkv, p.max_len);
+    }
+  }
+}
+
+// ---- more rows: fragments in shared memory, laid out once a block, pass by the keys' in registers
 template <int D, int KIND>
 __global__ void __launch_bounds__(WG_THREADS, 3) fa_weigh_paged_kernel(const WeighPagedParams p) {
   using C = WgCfg<D, KIND>;
-  constexpr unsigned ALL = 0xffffffffu;
+  constexpr int KG = C::KG;
+  constexpr int J = KG > 1 ? 2 : 1;  // groups that are worked on together: as many chains of products as that, and two row tiles
   extern __shared__ __align__(16) uint8_t wg_smem[];
   uint2* s_q = reinterpret_cast<uint2*>(wg_smem);                                   // [row tile][k-step][lane]
   float4* s_row = reinterpret_cast<float4*>(wg_smem + p.row_tiles * C::KST * 256);  // of rows 2i, 2i + 1: factors, lse
@@ -85,51 +349,29 @@ __global__ void __launch_bounds__(WG_THREADS, 3) fa_weigh_paged_kernel(const Wei
   int key0 = first + warp * C::TILE;
   auto page_of = [&](int k0) -> int {
     const int key = k0 + 16 * lane;
-    return (lane < C::KG && key < end) ? __ldg(p.table + b * p.table_stride + (key >> p.page_shift)) : -1;
+    return (lane < KG && key < end) ? __ldg(p.table + b * p.table_stride + (key >> p.page_shift)) : -1;
   };
-  WgRaw<D, KIND> raw[C::KG];
-  float ka[C::KG];
-  uint32_t live = 0u;  // groups that have keys, in a page of the pool
-  auto load = [&](int k0, int id) {
+  WgRaw<D, KIND> raw[KG];
+  float ka[KG];
+  long long off = -1;
+  unsigned next_live = 0u;
+  float scale = 1.f;
+  auto locate = [&](int k0, int id) {
     const int gkey = k0 + 16 * lane;
-    const bool want = lane < C::KG && gkey < end;
-    const long long off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, gkey & (p.page - 1), 1) : -1;
+    const bool want = lane < KG && gkey < end;
+    off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, gkey & (p.page - 1), 1) : -1;
     if (__any_sync(ALL, want && off < 0) && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
-    live = __ballot_sync(ALL, off >= 0);
-    float scale = 1.f;
+    next_live = __ballot_sync(ALL, off >= 0);
     if constexpr (KIND == PAGES_E4M3)
-      if (off >= 0) scale = __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk);
-#pragma unroll
-    for (int g = 0; g < C::KG; ++g) {
-      const long long row0 = __shfl_sync(ALL, off, g);
-      ka[g] = KIND == PAGES_E4M3 ? __shfl_sync(ALL, scale, g) : 1.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = gid + 8 * h;
-        const bool in = row0 >= 0 && k0 + 16 * g + r < end;
-        const uint8_t* src = static_cast<const uint8_t*>(p.k) + (in ? row0 + r : 0) * C::RB;
-        if constexpr (KIND == PAGES_FP4) {
-          const uint8_t* sp = static_cast<const uint8_t*>(p.k_scale) + (in ? row0 + r : 0) * (D / 16);
-          if constexpr (D == 128) {
-            const uint4 y = in ? __ldg(reinterpret_cast<const uint4*>(src) + tig) : make_uint4(0, 0, 0, 0);
-            raw[g].w[h][0] = y.x, raw[g].w[h][1] = y.y, raw[g].w[h][2] = y.z, raw[g].w[h][3] = y.w;
-            raw[g].f[h] = in ? __ldg(reinterpret_cast<const uint16_t*>(sp) + tig) : 0u;
-          } else {
-            const uint2 y = in ? __ldg(reinterpret_cast<const uint2*>(src) + tig) : make_uint2(0, 0);
-            raw[g].w[h][0] = y.x, raw[g].w[h][1] = y.y;
-            raw[g].f[h] = in ? __ldg(sp + tig) : 0u;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < C::LW / 4; ++i) {
-            const uint4 y = in ? __ldg(reinterpret_cast<const uint4*>(src) + tig + 4 * i) : make_uint4(0, 0, 0, 0);
-            raw[g].w[h][4 * i] = y.x, raw[g].w[h][4 * i + 1] = y.y, raw[g].w[h][4 * i + 2] = y.z, raw[g].w[h][4 * i + 3] = y.w;
-          }
-        }
-      }
-    }
+      scale = off >= 0 ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk) : 0.f;
   };
-  load(key0, page_of(key0));
+  locate(key0, page_of(key0));
+#pragma unroll
+  for (int g = 0; g < KG; ++g) {
+    wg_load<D, KIND>(raw[g], p, __shfl_sync(ALL, off, g), end - key0 - 16 * g, gid, tig);
+    ka[g] = __shfl_sync(ALL, scale, g);
+  }
+  unsigned live = next_live;
   constexpr int STEP = WG_WARPS * C::TILE;
   int id = page_of(key0 + STEP);
 
@@ -140,19 +382,12 @@ __global__ void __launch_bounds__(WG_THREADS, 3) fa_weigh_paged_kernel(const Wei
     uint2 x = make_uint2(0u, 0u);
     if (in && lane < D / 4)
       x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + b * p.qsb + h * p.qsh + tok * p.qst) + lane);
-    float factor = p.scale_log2;
+    float up = 1.f;
     if constexpr (C::F16) {
-      // as in the paged decode: the row's power of two brings its largest element to [1, 2), so that all but elements
-      // below 2^-14 of it are exact in f16
-      const float e[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-                          __uint_as_float(x.y & 0xffff0000u)};
-      float amax = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
+      float amax = wg_amax(x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, o));
-      const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -120), 120);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-      factor *= __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-      x = make_uint2(pack_f16x2(e[0] * down, e[1] * down), pack_f16x2(e[2] * down, e[3] * down));
+      x = wg_to_f16(x, wg_powers(amax, up));
     }
     if (lane < D / 4) {
       int qt, j;
@@ -163,7 +398,7 @@ __global__ void __launch_bounds__(WG_THREADS, 3) fa_weigh_paged_kernel(const Wei
       const float lse = in ? __ldg(p.lse + (static_cast<long long>(b) * p.H + h) * p.Nq + tok) : -INFINITY;
       const bool none = lse == -INFINITY;
       float* f = reinterpret_cast<float*>(s_row + r / 2) + (r & 1);
-      f[0] = factor;
+      f[0] = p.scale_log2 * up;
       f[2] = none ? 0.f : lse * 1.4426950408889634f;
       reinterpret_cast<int*>(s_lim + r / 2)[r & 1] = none ? -1 : min(L - 1, L - p.Nq + tok);
     }
@@ -172,72 +407,66 @@ __global__ void __launch_bounds__(WG_THREADS, 3) fa_weigh_paged_kernel(const Wei
 
   float* wrow = p.weights + (static_cast<long long>(b) * p.Hkv + hk) * p.wstride;
   for (; key0 < end; key0 += STEP) {
-    // this tile's rows become fragments group by group; the next tile's loads follow the last group
-    const uint32_t now = live;
+    locate(key0 + STEP, id);
+    id = page_of(key0 + 2 * STEP);
 #pragma unroll
-    for (int g = 0; g < C::KG; ++g) {
-      uint32_t a[C::KST][4];
-      const float kf = ka[g];
-      if constexpr (KIND == PAGES_FP4) {
-        const uint32_t fa[2] = {fp4_scale2<0>(raw[g].f[0]), fp4_scale2<1>(raw[g].f[0])};
-        const uint32_t fb[2] = {fp4_scale2<0>(raw[g].f[1]), fp4_scale2<1>(raw[g].f[1])};
+    for (int g0 = 0; g0 < KG; g0 += J) {
+      uint32_t a[J][C::KST][4];
+      float kf[J];
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          uint32_t y[4], z[4];
-          e2m1x8_to_f16x2x4(raw[g].w[0][x], y);
-          e2m1x8_to_f16x2x4(raw[g].w[1][x], z);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[2 * x + e / 2][2 * (e & 1)] = hmul2_bits(y[e], fa[x >> 1]);
-            a[2 * x + e / 2][2 * (e & 1) + 1] = hmul2_bits(z[e], fb[x >> 1]);
-          }
-        }
-      } else if constexpr (KIND == PAGES_E4M3) {
-#pragma unroll
-        for (int x = 0; x < C::LW; ++x) {
-          e4m3x4_to_f16x2x2(raw[g].w[0][x], a[x][0], a[x][2]);
-          e4m3x4_to_f16x2x2(raw[g].w[1][x], a[x][1], a[x][3]);
-        }
-      } else {
-#pragma unroll
-        for (int x = 0; x < C::KST; ++x) {
-          a[x][0] = raw[g].w[0][2 * x], a[x][2] = raw[g].w[0][2 * x + 1];
-          a[x][1] = raw[g].w[1][2 * x], a[x][3] = raw[g].w[1][2 * x + 1];
-        }
+      for (int g = 0; g < J; ++g) {
+        wg_fragments<D, KIND>(raw[g0 + g], [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          a[g][j][0] = a0, a[g][j][1] = a1, a[g][j][2] = a2, a[g][j][3] = a3;
+        });
+        kf[g] = ka[g0 + g];
+        wg_load<D, KIND>(raw[g0 + g], p, __shfl_sync(ALL, off, g0 + g), end - key0 - STEP - 16 * (g0 + g), gid, tig);
+        ka[g0 + g] = __shfl_sync(ALL, scale, g0 + g);
       }
-      if (g == C::KG - 1 && key0 + STEP < end) {
-        load(key0 + STEP, id);
-        id = page_of(key0 + 2 * STEP);
-      }
-      if (!((now >> g) & 1u)) continue;  // (the same in every lane)
-      const int key = key0 + 16 * g + gid;
-      const int mine = key + 8 * tig;    // the key whose weight this lane writes (tig 0 and 1)
-      const bool writes = tig < 2 && mine < end;
+      if (((live >> g0) & ((1u << J) - 1u)) == 0u) continue;  // (the same in every lane)
+      // the weight that this lane writes
+      const int grp = J == 2 ? tig >> 1 : 0, mine = key0 + 16 * (g0 + grp) + gid + 8 * (tig & 1);
+      const bool writes = ((live >> (g0 + grp)) & 1u) && mine < end && (J == 2 || tig < 2);
       const float old = writes ? wrow[mine] : 0.f;
-      float sum0 = 0.f, sum1 = 0.f;      // keys gid and gid + 8, rows 2 tig and 2 tig + 1 of each tile
-#pragma unroll 1
-      for (int n = 0; n < p.row_tiles; ++n) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+      float v[J][2];
+#pragma unroll
+      for (int g = 0; g < J; ++g) v[g][0] = v[g][1] = 0.f;
+      auto row_tile = [&](int n) {
+        float s[J][4];
+#pragma unroll
+        for (int g = 0; g < J; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[g][e] = 0.f;
         const uint2* qn = s_q + n * C::KST * 32 + lane;
 #pragma unroll
         for (int j = 0; j < C::KST; ++j) {
           const uint2 q = qn[j * 32];
-          mma_16816<C::F16>(s, a[j][0], a[j][1], a[j][2], a[j][3], q.x, q.y);
+#pragma unroll
+          for (int g = 0; g < J; ++g) mma_16816<C::F16>(s[g], a[g][j][0], a[g][j][1], a[g][j][2], a[g][j][3], q.x, q.y);
         }
         const float4 f = s_row[n * 4 + tig];
         const int2 lim = s_lim[n * 4 + tig];
-        const float c0 = KIND == PAGES_E4M3 ? f.x * kf : f.x, c1 = KIND == PAGES_E4M3 ? f.y * kf : f.y;
-        const float p0 = ex2_approx(fmaf(s[0], c0, -f.z)), p1 = ex2_approx(fmaf(s[1], c1, -f.w));
-        const float p2 = ex2_approx(fmaf(s[2], c0, -f.z)), p3 = ex2_approx(fmaf(s[3], c1, -f.w));
-        sum0 += (key <= lim.x ? p0 : 0.f) + (key <= lim.y ? p1 : 0.f);
-        sum1 += (key + 8 <= lim.x ? p2 : 0.f) + (key + 8 <= lim.y ? p3 : 0.f);
+#pragma unroll
+        for (int g = 0; g < J; ++g) {
+          const int key = key0 + 16 * (g0 + g) + gid;
+          const float c0 = KIND == PAGES_E4M3 ? f.x * kf[g] : f.x, c1 = KIND == PAGES_E4M3 ? f.y * kf[g] : f.y;
+          const float p0 = ex2_approx(fmaf(s[g][0], c0, -f.z)), p1 = ex2_approx(fmaf(s[g][1], c1, -f.w));
+          const float p2 = ex2_approx(fmaf(s[g][2], c0, -f.z)), p3 = ex2_approx(fmaf(s[g][3], c1, -f.w));
+          v[g][0] += (key <= lim.x ? p0 : 0.f) + (key <= lim.y ? p1 : 0.f);
+          v[g][1] += (key + 8 <= lim.x ? p2 : 0.f) + (key + 8 <= lim.y ? p3 : 0.f);
+        }
+      };
+      // (two at a time: their products do not wait for one another)
+      int n = 0;
+#pragma unroll 1
+      for (; n + 1 < p.row_tiles; n += 2) {
+        row_tile(n);
+        row_tile(n + 1);
       }
-      sum0 += __shfl_xor_sync(ALL, sum0, 1);
-      sum1 += __shfl_xor_sync(ALL, sum1, 1);
-      sum0 += __shfl_xor_sync(ALL, sum0, 2);
-      sum1 += __shfl_xor_sync(ALL, sum1, 2);
-      if (writes) wrow[mine] = old + (tig == 0 ? sum0 : sum1);
+      if (n < p.row_tiles) row_tile(n);
+      wg_sum_lanes<J>(v, tig);
+      if (writes) wrow[mine] = old + v[0][0];
     }
+    live = next_live;
   }
 }
 
@@ -260,8 +489,16 @@ cudaError_t weigh_paged_set_attributes() {
   return e;
 }
 
+template <int D, int KIND, int NR>
+static cudaError_t wg_launch_few(WeighPagedParams p, int num_sms, cudaStream_t stream) {
+  p.n_ranges = num_sms * (NR == 1 ? WG_FEW_CTAS : 3) * WG_WARPS;
+  fa_weigh_paged_few_kernel<D, KIND, NR><<<p.n_ranges / WG_WARPS, WG_THREADS, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 template <int D, int KIND>
 static cudaError_t wg_launch(WeighPagedParams p, int num_sms, cudaStream_t stream) {
+  if (p.R <= 8) return wg_launch_few<D, KIND, 1>(p, num_sms, stream);
+  if (p.R <= 16) return wg_launch_few<D, KIND, 2>(p, num_sms, stream);
   // Keys of a block: from two tiles a warp up to 64, as many as leave the GPU six blocks an SM.
   constexpr int STEP = WG_WARPS * WgCfg<D, KIND>::TILE;
   const long long pairs = static_cast<long long>(p.B) * p.Hkv;
