@@ -1146,6 +1146,8 @@ fa_status fa_weigh_paged(const void* q, const int64_t* q_strides, const float* l
 
   DeviceState* st = nullptr;
   if (fa_status s = device_state(&st)) return s;
+  if (static_cast<double>(B) * Hkv * max_len / 16 > 2e9 * st->num_sms)  // (tiles of a range are counted in 32 bits)
+    return fail(FA_ERR_INVALID_ARG, "B * Hkv * max_len is too large");
   fa::WeighPagedParams p{};
   p.q = q, p.lse = lse, p.k = k_pages, p.k_scale = k_scale;
   p.table = block_table, p.table_stride = table_stride, p.seqlens = seqlens_k;

@@ -155,9 +155,8 @@ struct WeighPagedParams {
   long long qsb, qsh, qst, table_stride, wstride;
   int B, H, Hkv, G, Nq, R, max_len;
   int page, page_shift, num_pages;
-  int chunk, chunks;         // keys of a block, and blocks of a sequence and K/V head (set by the launch)
   int row_tiles;             // 8-row tiles of the R query rows
-  int n_ranges;              // few rows: the batch's keys are shared out in at most so many ranges (set by the launch)
+  int n_ranges;              // the batch's keys are shared out in at most so many ranges (set by the launch)
   float scale_log2;
   unsigned int* status;
 };

@@ -13,11 +13,11 @@
 // memory, laid out once a block); a row's sum over the queries is then four lanes'
 // partial sums, so no atomics, and results do not depend on any order.
 //
-// A block takes `chunk` keys of one sequence and K/V head; its warps take tiles of
-// them in turn and load the next tile's rows, and the page entries of the one after,
-// before they work on the current one.
-#include <climits>
-
+// The batch's keys are shared out in equal contiguous ranges, as in the paged decode:
+// one for each warp that the GPU holds where a K/V head has up to 16 query rows
+// (whose fragments then stay in registers), one for each block above that. The
+// next tile's rows, and the page entries of the one after, are loaded before a
+// warp works on the current one.
 #include "fp4.cuh"
 #include "mma_sync.cuh"
 #include "paged_walk.cuh"
@@ -49,31 +49,31 @@ struct WgRaw {
   uint32_t f[2];  // 4-bit rows: the lane's one or two scale bytes
 };
 
-// The lane's share of the rows gid, gid + 8 of a group whose first row is `row0` of the pool; rows from `rows` on (and all,
-// for row0 < 0) are zeros.
+// The lane's share of the rows gid, gid + 8 of a group whose first row is `row0` of the pool. Past its `rows` rows the last
+// one is read again, and of a group that is not there (row0 < 0) the pool's first: every key's sum is its own, and those are
+// not written, so no load needs a branch.
 template <int D, int KIND>
 __device__ __forceinline__ void wg_load(WgRaw<D, KIND>& x, const WeighPagedParams& p, long long row0, int rows, int gid, int tig) {
   using C = WgCfg<D, KIND>;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int r = gid + 8 * h;
-    const bool in = row0 >= 0 && r < rows;
-    const uint8_t* src = static_cast<const uint8_t*>(p.k) + (in ? row0 + r : 0) * C::RB;
+    const long long row = row0 < 0 ? 0 : row0 + max(min(gid + 8 * h, rows - 1), 0);
+    const uint8_t* src = static_cast<const uint8_t*>(p.k) + row * C::RB;
     if constexpr (KIND == PAGES_FP4) {
-      const uint8_t* sp = static_cast<const uint8_t*>(p.k_scale) + (in ? row0 + r : 0) * (D / 16);
+      const uint8_t* sp = static_cast<const uint8_t*>(p.k_scale) + row * (D / 16);
       if constexpr (D == 128) {
-        const uint4 y = in ? __ldg(reinterpret_cast<const uint4*>(src) + tig) : make_uint4(0, 0, 0, 0);
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(src) + tig);
         x.w[h][0] = y.x, x.w[h][1] = y.y, x.w[h][2] = y.z, x.w[h][3] = y.w;
-        x.f[h] = in ? __ldg(reinterpret_cast<const uint16_t*>(sp) + tig) : 0u;
+        x.f[h] = __ldg(reinterpret_cast<const uint16_t*>(sp) + tig);
       } else {
-        const uint2 y = in ? __ldg(reinterpret_cast<const uint2*>(src) + tig) : make_uint2(0, 0);
+        const uint2 y = __ldg(reinterpret_cast<const uint2*>(src) + tig);
         x.w[h][0] = y.x, x.w[h][1] = y.y;
-        x.f[h] = in ? __ldg(sp + tig) : 0u;
+        x.f[h] = __ldg(sp + tig);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < C::LW / 4; ++i) {
-        const uint4 y = in ? __ldg(reinterpret_cast<const uint4*>(src) + tig + 4 * i) : make_uint4(0, 0, 0, 0);
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(src) + tig + 4 * i);
         x.w[h][4 * i] = y.x, x.w[h][4 * i + 1] = y.y, x.w[h][4 * i + 2] = y.z, x.w[h][4 * i + 3] = y.w;
       }
     }
@@ -263,7 +263,6 @@ __global__ void __launch_bounds__(WG_THREADS, NR == 1 ? WG_FEW_CTAS : 3) fa_weig
         lim[n][e] = none ? -1 : min(L - 1, L - p.Nq + tok);
       }
     }
-    const int full_lim = L - p.Nq;  // every row that adds anything sees the keys up to here
     float* wrow = p.weights + (static_cast<long long>(b) * p.Hkv + hk) * p.wstride;
 
     for (; at.i < i1; ++at.i) {
@@ -298,7 +297,6 @@ __global__ void __launch_bounds__(WG_THREADS, NR == 1 ? WG_FEW_CTAS : 3) fa_weig
         ka[g] = __shfl_sync(ALL, scale, g);
         v[g][0] = v[g][1] = 0.f;
         const int key = key0 + 16 * g + gid;
-        const bool some = key0 + 16 * g + 15 > full_lim;  // keys that not every row sees
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
           const float c0 = KIND == PAGES_E4M3 ? c1[n][0] * kf : c1[n][0], c2 = KIND == PAGES_E4M3 ? c1[n][1] * kf : c1[n][1];
@@ -306,7 +304,7 @@ __global__ void __launch_bounds__(WG_THREADS, NR == 1 ? WG_FEW_CTAS : 3) fa_weig
                          ex2_approx(fmaf(s[n][2], c0, -ls[n][0])), ex2_approx(fmaf(s[n][3], c2, -ls[n][1]))};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (some ? key + 8 * (e >> 1) > lim[n][e & 1] : lim[n][e & 1] < 0) pr[e] = 0.f;
+            pr[e] = key + 8 * (e >> 1) > lim[n][e & 1] ? 0.f : pr[e];
           v[g][0] += pr[0] + pr[1];
           v[g][1] += pr[2] + pr[3];
         }
@@ -325,148 +323,171 @@ __global__ void __launch_bounds__(WG_THREADS, NR == 1 ? WG_FEW_CTAS : 3) fa_weig
   }
 }
 
-// ---- more rows: fragments in shared memory, laid out once a block, pass by the keys' in registers
+// ---- more rows: fragments in shared memory, laid out once a segment, pass by the keys' in registers
 template <int D, int KIND>
 __global__ void __launch_bounds__(WG_THREADS, 3) fa_weigh_paged_kernel(const WeighPagedParams p) {
   using C = WgCfg<D, KIND>;
   constexpr int KG = C::KG;
-  constexpr int J = KG > 1 ? 2 : 1;  // groups that are worked on together: as many chains of products as that, and two row tiles
+  constexpr int J = KG > 1 ? 2 : 1;  // groups that are worked on together: as many chains of products, times two row tiles
   extern __shared__ __align__(16) uint8_t wg_smem[];
   uint2* s_q = reinterpret_cast<uint2*>(wg_smem);                                   // [row tile][k-step][lane]
   float4* s_row = reinterpret_cast<float4*>(wg_smem + p.row_tiles * C::KST * 256);  // of rows 2i, 2i + 1: factors, lse
   int2* s_lim = reinterpret_cast<int2*>(s_row + p.row_tiles * 4);                   // and the last key they see
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
-  const int part = static_cast<int>(blockIdx.x) % p.chunks, pair = static_cast<int>(blockIdx.x) / p.chunks;
-  const int b = pair / p.Hkv, hk = pair % p.Hkv;
-  const int raw_len = __ldg(p.seqlens + b), L = paged_clip_len(raw_len, p.max_len);
-  if (raw_len != L && part == 0 && hk == 0 && threadIdx.x == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
-  const int first = part * p.chunk;
-  if (first >= L) return;
-  const int end = min(L, first + p.chunk);
-
-  // ---- the warp's tiles: first + (warp + WG_WARPS i) TILE
-  int key0 = first + warp * C::TILE;
-  auto page_of = [&](int k0) -> int {
-    const int key = k0 + 16 * lane;
-    return (lane < KG && key < end) ? __ldg(p.table + b * p.table_stride + (key >> p.page_shift)) : -1;
-  };
-  WgRaw<D, KIND> raw[KG];
-  float ka[KG];
-  long long off = -1;
-  unsigned next_live = 0u;
-  float scale = 1.f;
-  auto locate = [&](int k0, int id) {
-    const int gkey = k0 + 16 * lane;
-    const bool want = lane < KG && gkey < end;
-    off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, gkey & (p.page - 1), 1) : -1;
-    if (__any_sync(ALL, want && off < 0) && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
-    next_live = __ballot_sync(ALL, off >= 0);
-    if constexpr (KIND == PAGES_E4M3)
-      scale = off >= 0 ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk) : 0.f;
-  };
-  locate(key0, page_of(key0));
+  const int range = static_cast<int>(blockIdx.x);
+  bool clipped = false;
+  const long long sum = paged_count_tiles<C::TILE>(p.seqlens, p.B, p.max_len, lane, clipped);
+  if (range == 0 && __any_sync(ALL, clipped) && threadIdx.x == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
+  const PagedRanges ranges(sum * p.Hkv, p.n_ranges);
+  if (range >= ranges.n) return;
+  const long long t0 = ranges.begin(range);
+  int todo = static_cast<int>(ranges.begin(range + 1) - t0);
+  PagedTile at = paged_seek<C::TILE>(p.seqlens, p.B, p.Hkv, p.max_len, t0, lane);
+  while (true) {
+    // ================================================================ one segment: tiles of (b, hk), the warps' in turn
+    const int b = at.b, hk = at.hk, L = at.L, i1 = todo < at.nt - at.i ? at.i + todo : at.nt;
+    const int end = min(L, i1 * C::TILE);
+    int key0 = (at.i + warp) * C::TILE;
+    auto page_of = [&](int k0) -> int {
+      const int key = k0 + 16 * lane;
+      return (lane < KG && key < end) ? __ldg(p.table + b * p.table_stride + (key >> p.page_shift)) : -1;
+    };
+    WgRaw<D, KIND> raw[KG];
+    float ka[KG];
+    long long off = -1;
+    unsigned next_live = 0u;
+    float scale = 1.f;
+    auto locate = [&](int k0, int id) {
+      const int gkey = k0 + 16 * lane;
+      const bool want = lane < KG && gkey < end;
+      off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, gkey & (p.page - 1), 1) : -1;
+      if (__any_sync(ALL, want && off < 0) && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
+      next_live = __ballot_sync(ALL, off >= 0);
+      if constexpr (KIND == PAGES_E4M3)
+        scale = off >= 0 ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk) : 0.f;
+    };
+    locate(key0, page_of(key0));
 #pragma unroll
-  for (int g = 0; g < KG; ++g) {
-    wg_load<D, KIND>(raw[g], p, __shfl_sync(ALL, off, g), end - key0 - 16 * g, gid, tig);
-    ka[g] = __shfl_sync(ALL, scale, g);
-  }
-  unsigned live = next_live;
-  constexpr int STEP = WG_WARPS * C::TILE;
-  int id = page_of(key0 + STEP);
-
-  // ---- the queries: a warp a row, a lane four of its elements
-  for (int r = warp; r < 8 * p.row_tiles; r += WG_WARPS) {
-    const bool in = r < p.R;
-    const int h = hk * p.G + (in ? r / p.Nq : 0), tok = in ? r % p.Nq : 0;
-    uint2 x = make_uint2(0u, 0u);
-    if (in && lane < D / 4)
-      x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + b * p.qsb + h * p.qsh + tok * p.qst) + lane);
-    float up = 1.f;
-    if constexpr (C::F16) {
-      float amax = wg_amax(x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, o));
-      x = wg_to_f16(x, wg_powers(amax, up));
+    for (int g = 0; g < KG; ++g) {
+      wg_load<D, KIND>(raw[g], p, __shfl_sync(ALL, off, g), end - key0 - 16 * g, gid, tig);
+      ka[g] = __shfl_sync(ALL, scale, g);
     }
-    if (lane < D / 4) {
-      int qt, j;
-      wg_place<D, KIND>(lane, qt, j);
-      s_q[((r / 8) * C::KST + j) * 32 + (r % 8) * 4 + qt] = x;
-    }
-    if (lane == 0) {
-      const float lse = in ? __ldg(p.lse + (static_cast<long long>(b) * p.H + h) * p.Nq + tok) : -INFINITY;
-      const bool none = lse == -INFINITY;
-      float* f = reinterpret_cast<float*>(s_row + r / 2) + (r & 1);
-      f[0] = p.scale_log2 * up;
-      f[2] = none ? 0.f : lse * 1.4426950408889634f;
-      reinterpret_cast<int*>(s_lim + r / 2)[r & 1] = none ? -1 : min(L - 1, L - p.Nq + tok);
-    }
-  }
-  __syncthreads();
+    unsigned live = next_live;
+    constexpr int STEP = WG_WARPS * C::TILE;
+    int id = page_of(key0 + STEP);
 
-  float* wrow = p.weights + (static_cast<long long>(b) * p.Hkv + hk) * p.wstride;
-  for (; key0 < end; key0 += STEP) {
-    locate(key0 + STEP, id);
-    id = page_of(key0 + 2 * STEP);
+    // ---- the queries: a warp a row, a lane four of its elements, four rows at a time
+    for (int r0 = warp; r0 < 8 * p.row_tiles; r0 += 4 * WG_WARPS) {
+      uint2 x[4];
+      float lse[4];
+      int tok[4];
 #pragma unroll
-    for (int g0 = 0; g0 < KG; g0 += J) {
-      uint32_t a[J][C::KST][4];
-      float kf[J];
-#pragma unroll
-      for (int g = 0; g < J; ++g) {
-        wg_fragments<D, KIND>(raw[g0 + g], [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-          a[g][j][0] = a0, a[g][j][1] = a1, a[g][j][2] = a2, a[g][j][3] = a3;
-        });
-        kf[g] = ka[g0 + g];
-        wg_load<D, KIND>(raw[g0 + g], p, __shfl_sync(ALL, off, g0 + g), end - key0 - STEP - 16 * (g0 + g), gid, tig);
-        ka[g0 + g] = __shfl_sync(ALL, scale, g0 + g);
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i * WG_WARPS;
+        const bool in = r < p.R;
+        const int h = hk * p.G + (in ? r / p.Nq : 0);
+        tok[i] = in ? r % p.Nq : 0;
+        x[i] = in && lane < D / 4
+                   ? __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + b * p.qsb + h * p.qsh + tok[i] * p.qst) + lane)
+                   : make_uint2(0u, 0u);
+        lse[i] = in ? __ldg(p.lse + (static_cast<long long>(b) * p.H + h) * p.Nq + tok[i]) : -INFINITY;
       }
-      if (((live >> g0) & ((1u << J) - 1u)) == 0u) continue;  // (the same in every lane)
-      // the weight that this lane writes
-      const int grp = J == 2 ? tig >> 1 : 0, mine = key0 + 16 * (g0 + grp) + gid + 8 * (tig & 1);
-      const bool writes = ((live >> (g0 + grp)) & 1u) && mine < end && (J == 2 || tig < 2);
-      const float old = writes ? wrow[mine] : 0.f;
-      float v[J][2];
 #pragma unroll
-      for (int g = 0; g < J; ++g) v[g][0] = v[g][1] = 0.f;
-      auto row_tile = [&](int n) {
-        float s[J][4];
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i * WG_WARPS;
+        if (r >= 8 * p.row_tiles) break;
+        float up = 1.f;
+        if constexpr (C::F16) {
+          float amax = wg_amax(x[i]);
 #pragma unroll
-        for (int g = 0; g < J; ++g)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[g][e] = 0.f;
-        const uint2* qn = s_q + n * C::KST * 32 + lane;
-#pragma unroll
-        for (int j = 0; j < C::KST; ++j) {
-          const uint2 q = qn[j * 32];
-#pragma unroll
-          for (int g = 0; g < J; ++g) mma_16816<C::F16>(s[g], a[g][j][0], a[g][j][1], a[g][j][2], a[g][j][3], q.x, q.y);
+          for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, o));
+          x[i] = wg_to_f16(x[i], wg_powers(amax, up));
         }
-        const float4 f = s_row[n * 4 + tig];
-        const int2 lim = s_lim[n * 4 + tig];
+        if (lane < D / 4) {
+          int qt, j;
+          wg_place<D, KIND>(lane, qt, j);
+          s_q[((r / 8) * C::KST + j) * 32 + (r % 8) * 4 + qt] = x[i];
+        }
+        if (lane == 0) {
+          const bool none = lse[i] == -INFINITY;
+          float* f = reinterpret_cast<float*>(s_row + r / 2) + (r & 1);
+          f[0] = p.scale_log2 * up;
+          f[2] = none ? 0.f : lse[i] * 1.4426950408889634f;
+          reinterpret_cast<int*>(s_lim + r / 2)[r & 1] = none ? -1 : min(L - 1, L - p.Nq + tok[i]);
+        }
+      }
+    }
+    __syncthreads();
+
+    float* wrow = p.weights + (static_cast<long long>(b) * p.Hkv + hk) * p.wstride;
+    for (; key0 < end; key0 += STEP) {
+      locate(key0 + STEP, id);
+      id = page_of(key0 + 2 * STEP);
+#pragma unroll
+      for (int g0 = 0; g0 < KG; g0 += J) {
+        uint32_t a[J][C::KST][4];
+        float kf[J];
 #pragma unroll
         for (int g = 0; g < J; ++g) {
-          const int key = key0 + 16 * (g0 + g) + gid;
-          const float c0 = KIND == PAGES_E4M3 ? f.x * kf[g] : f.x, c1 = KIND == PAGES_E4M3 ? f.y * kf[g] : f.y;
-          const float p0 = ex2_approx(fmaf(s[g][0], c0, -f.z)), p1 = ex2_approx(fmaf(s[g][1], c1, -f.w));
-          const float p2 = ex2_approx(fmaf(s[g][2], c0, -f.z)), p3 = ex2_approx(fmaf(s[g][3], c1, -f.w));
-          v[g][0] += (key <= lim.x ? p0 : 0.f) + (key <= lim.y ? p1 : 0.f);
-          v[g][1] += (key + 8 <= lim.x ? p2 : 0.f) + (key + 8 <= lim.y ? p3 : 0.f);
+          wg_fragments<D, KIND>(raw[g0 + g], [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            a[g][j][0] = a0, a[g][j][1] = a1, a[g][j][2] = a2, a[g][j][3] = a3;
+          });
+          kf[g] = ka[g0 + g];
+          wg_load<D, KIND>(raw[g0 + g], p, __shfl_sync(ALL, off, g0 + g), end - key0 - STEP - 16 * (g0 + g), gid, tig);
+          ka[g0 + g] = __shfl_sync(ALL, scale, g0 + g);
         }
-      };
-      // (two at a time: their products do not wait for one another)
-      int n = 0;
+        if (((live >> g0) & ((1u << J) - 1u)) == 0u) continue;  // (the same in every lane)
+        // the weight that this lane writes
+        const int grp = J == 2 ? tig >> 1 : 0, mine = key0 + 16 * (g0 + grp) + gid + 8 * (tig & 1);
+        const bool writes = ((live >> (g0 + grp)) & 1u) && mine < end && (J == 2 || tig < 2);
+        const float old = writes ? wrow[mine] : 0.f;
+        float v[J][2];
+#pragma unroll
+        for (int g = 0; g < J; ++g) v[g][0] = v[g][1] = 0.f;
+        auto row_tile = [&](int n) {
+          float s[J][4];
+#pragma unroll
+          for (int g = 0; g < J; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[g][e] = 0.f;
+          const uint2* qn = s_q + n * C::KST * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < C::KST; ++j) {
+            const uint2 q = qn[j * 32];
+#pragma unroll
+            for (int g = 0; g < J; ++g) mma_16816<C::F16>(s[g], a[g][j][0], a[g][j][1], a[g][j][2], a[g][j][3], q.x, q.y);
+          }
+          const float4 f = s_row[n * 4 + tig];
+          const int2 lim = s_lim[n * 4 + tig];
+#pragma unroll
+          for (int g = 0; g < J; ++g) {
+            const int key = key0 + 16 * (g0 + g) + gid;
+            const float c0 = KIND == PAGES_E4M3 ? f.x * kf[g] : f.x, c1 = KIND == PAGES_E4M3 ? f.y * kf[g] : f.y;
+            const float p0 = ex2_approx(fmaf(s[g][0], c0, -f.z)), p1 = ex2_approx(fmaf(s[g][1], c1, -f.w));
+            const float p2 = ex2_approx(fmaf(s[g][2], c0, -f.z)), p3 = ex2_approx(fmaf(s[g][3], c1, -f.w));
+            v[g][0] += (key <= lim.x ? p0 : 0.f) + (key <= lim.y ? p1 : 0.f);
+            v[g][1] += (key + 8 <= lim.x ? p2 : 0.f) + (key + 8 <= lim.y ? p3 : 0.f);
+          }
+        };
+        // (two at a time: their products do not wait for one another)
+        int n = 0;
 #pragma unroll 1
-      for (; n + 1 < p.row_tiles; n += 2) {
-        row_tile(n);
-        row_tile(n + 1);
+        for (; n + 1 < p.row_tiles; n += 2) {
+          row_tile(n);
+          row_tile(n + 1);
+        }
+        if (n < p.row_tiles) row_tile(n);
+        wg_sum_lanes<J>(v, tig);
+        if (writes) wrow[mine] = old + v[0][0];
       }
-      if (n < p.row_tiles) row_tile(n);
-      wg_sum_lanes<J>(v, tig);
-      if (writes) wrow[mine] = old + v[0][0];
+      live = next_live;
     }
-    live = next_live;
+    todo -= i1 - at.i;
+    if (todo == 0) return;
+    __syncthreads();  // the queries' memory is free again
+    at.i = at.nt - 1;
+    paged_next<C::TILE>(at, p.seqlens, p.B, p.Hkv, p.max_len);
   }
 }
 
@@ -499,16 +520,8 @@ template <int D, int KIND>
 static cudaError_t wg_launch(WeighPagedParams p, int num_sms, cudaStream_t stream) {
   if (p.R <= 8) return wg_launch_few<D, KIND, 1>(p, num_sms, stream);
   if (p.R <= 16) return wg_launch_few<D, KIND, 2>(p, num_sms, stream);
-  // Keys of a block: from two tiles a warp up to 64, as many as leave the GPU six blocks an SM.
-  constexpr int STEP = WG_WARPS * WgCfg<D, KIND>::TILE;
-  const long long pairs = static_cast<long long>(p.B) * p.Hkv;
-  long long chunk = 2LL * STEP;
-  auto blocks = [&](long long c) { return (p.max_len + c - 1) / c * pairs; };
-  while (chunk < p.max_len && ((chunk < 64LL * STEP && blocks(2 * chunk) >= 6LL * num_sms) || blocks(chunk) > INT_MAX)) chunk *= 2;
-  p.chunk = static_cast<int>(chunk);
-  p.chunks = static_cast<int>((p.max_len + chunk - 1) / chunk);
-  if (p.chunks == 0) return cudaSuccess;  // no keys
-  fa_weigh_paged_kernel<D, KIND><<<static_cast<unsigned>(blocks(chunk)), WG_THREADS, wg_smem<D, KIND>(p.row_tiles), stream>>>(p);
+  p.n_ranges = 3 * num_sms;
+  fa_weigh_paged_kernel<D, KIND><<<p.n_ranges, WG_THREADS, wg_smem<D, KIND>(p.row_tiles), stream>>>(p);
   return cudaGetLastError();
 }
 template <int D>
