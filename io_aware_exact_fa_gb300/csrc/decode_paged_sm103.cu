@@ -84,6 +84,7 @@ struct DpCfg {
   static constexpr int SB = F4 ? D / 16 : 0;     // scale bytes of a 4-bit row
   static constexpr int META = KG * 2 * 4;        // e4m3 scales of a tile
   static constexpr int STAGE = 2 * HALF + 2 * KS * SB;
+  // (4-bit rows: tiles of 32 keys took 101 us in place of 92 for 64 sequences of 4-8k, d = 128, three or four blocks an SM.)
   // Tiles in each warp's ring: what fits beside the warps an SM holds. (Three tiles for eight warps against two for
   // twelve: 136 against 130 us at 8 rows, e4m3, d = 128. Tiles of half the size, four to a ring: 134. Sixteen warps
   // of those: 133.)
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(DP_THREADS, decode_paged_ctas(D, 8 * NR)) fa_d
       }
       if constexpr (F4) {  // a group's scales are SB 16-byte pieces; first those of K, then those of V
         constexpr int PIECES = C::KG * C::SB;
+        static_assert(2 * PIECES % 32 == 0, "every lane copies a piece in every round");
 #pragma unroll
         for (int x0 = 0; x0 < 2 * PIECES; x0 += 32) {
           const int x = (x0 + lane) % PIECES, g = x / C::SB, pc = x % C::SB;
