@@ -1155,8 +1155,8 @@ fa_status fa_weigh_paged(const void* q, const int64_t* q_strides, const float* l
   p.qsb = q_strides[0], p.qsh = q_strides[1], p.qst = q_strides[2];
   p.B = B, p.H = H, p.Hkv = Hkv, p.G = H / Hkv, p.Nq = Nq, p.R = R, p.max_len = max_len;
   p.page = page, p.page_shift = log2_of(page), p.num_pages = num_pages;
-  p.row_tiles = (R + 7) / 8;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_limit_ns = g_wait_limit_ns.load();
   p.status = st->status;
   cudaError_t e = fa::launch_weigh_paged(d, kind, p, st->num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged weigh launch");

@@ -155,9 +155,9 @@ struct WeighPagedParams {
   long long qsb, qsh, qst, table_stride, wstride;
   int B, H, Hkv, G, Nq, R, max_len;
   int page, page_shift, num_pages;
-  int row_tiles;             // 8-row tiles of the R query rows
   int n_ranges;              // the batch's keys are shared out in at most so many ranges (set by the launch)
   float scale_log2;
+  uint64_t wait_limit_ns;
   unsigned int* status;
 };
 cudaError_t weigh_paged_set_attributes();

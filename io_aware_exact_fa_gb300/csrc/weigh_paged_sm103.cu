@@ -18,6 +18,8 @@
 // (whose fragments then stay in registers), one for each block above that. The
 // next tile's rows, and the page entries of the one after, are loaded before a
 // warp works on the current one.
+#include <type_traits>
+
 #include "fp4.cuh"
 #include "mma_sync.cuh"
 #include "paged_walk.cuh"
@@ -111,20 +113,8 @@ __device__ __forceinline__ void wg_fragments(const WgRaw<D, KIND>& x, F&& f) {
   }
 }
 
-// The four elements 4 x .. 4 x + 3 of a row belong to lane tig and k-step j, in the order that the lanes hold keys: 16-byte
-// pieces tig, tig + 4, ..., or a quarter of a 4-bit row.
-template <int D, int KIND>
-__device__ __forceinline__ void wg_place(int x, int& tig, int& j) {
-  if constexpr (KIND == PAGES_FP4) {
-    tig = x / (D / 16);
-    j = x % (D / 16);
-  } else {
-    constexpr int Q = KIND == PAGES_E4M3 ? 4 : 2;  // fours of elements in a piece
-    tig = (x / Q) % 4;
-    j = x / Q / 4 * Q + x % Q;
-  }
-}
-// And back: the first of those four elements.
+// First of the four elements that lane tig holds in k-step j: its keys are 16-byte pieces tig, tig + 4, ..., or a quarter of
+// a 4-bit row.
 template <int D, int KIND>
 __device__ __forceinline__ int wg_elem(int tig, int j) {
   if constexpr (KIND == PAGES_FP4) return 4 * (tig * (D / 16) + j);
@@ -323,68 +313,130 @@ __global__ void __launch_bounds__(WG_THREADS, NR == 1 ? WG_FEW_CTAS : 3) fa_weig
   }
 }
 
-// ---- more rows: fragments in shared memory, laid out once a segment, pass by the keys' in registers
+// ---- more rows: tensor-memory products, a tile of 128 keys on the lanes
+constexpr int WM_THREADS = 128;
+constexpr int WM_TILE = 128;
+
 template <int D, int KIND>
-__global__ void __launch_bounds__(WG_THREADS, 3) fa_weigh_paged_kernel(const WeighPagedParams p) {
-  using C = WgCfg<D, KIND>;
-  constexpr int KG = C::KG;
-  constexpr int J = KG > 1 ? 2 : 1;  // groups that are worked on together: as many chains of products, times two row tiles
-  extern __shared__ __align__(16) uint8_t wg_smem[];
-  uint2* s_q = reinterpret_cast<uint2*>(wg_smem);                                   // [row tile][k-step][lane]
-  float4* s_row = reinterpret_cast<float4*>(wg_smem + p.row_tiles * C::KST * 256);  // of rows 2i, 2i + 1: factors, lse
-  int2* s_lim = reinterpret_cast<int2*>(s_row + p.row_tiles * 4);                   // and the last key they see
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gid = lane >> 2, tig = lane & 3;
+struct WmCfg {
+  static constexpr int RB = paged_row_bytes(KIND, D);
+  static constexpr int PPR = RB / 16;               // 16-byte pieces of a row, and of the tile that one thread takes
+  static constexpr int LPR = PPR < 4 ? PPR : 4;     // lanes side by side on a row
+  static constexpr int RW = 32 / LPR;               // rows of one load of a warp: 8 or 16
+  static constexpr int SETS = WM_TILE / (4 * RW);   // of them, a warp's
+  static constexpr int BOX = WM_TILE * 128;         // 64 elements of every key, rows of 128 swizzled bytes
+  static constexpr int K_BYTES = BOX * (D / 64);
+  static constexpr int CTAS = KIND == PAGES_BF16 && D == 128 ? 3 : 4;  // by registers
+};
+__host__ __device__ constexpr int wm_cols(int rows) { return (rows + 31) / 32 * 32; }       // query rows, padded
+__host__ __device__ constexpr int wm_tmem(int cols) { return 2 * cols <= 64 ? 64 : 2 * cols <= 128 ? 128 : 256; }
+
+// Byte of element e of row r in an operand of `rows` rows.
+__device__ __forceinline__ uint32_t wm_at(int rows, int r, int e) {
+  return (e >> 6) * (rows * 128) + (r >> 3) * 1024 + (r & 7) * 128 + ((((e & 63) >> 3) ^ (r & 7)) << 4) + (e & 7) * 2;
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_paged_many_kernel(const WeighPagedParams p) {
+  using C = WmCfg<D, KIND>;
+  constexpr bool F16 = KIND != PAGES_BF16;
+  extern __shared__ uint8_t wm_raw[];
+  uint8_t* smem = wm_raw + ((1024u - (smem_u32(wm_raw) & 1023u)) & 1023u);
+  const int N = wm_cols(p.R);
+  uint8_t* s_k = smem;
+  uint8_t* s_q = smem + C::K_BYTES;
+  float4* s_row = reinterpret_cast<float4*>(s_q + N * D * 2);  // of rows 2i, 2i + 1: factors, and the log-sum-exp's negatives
+  int2* s_lim = reinterpret_cast<int2*>(s_row + N / 2);        // and the last key they see
+  uint64_t* done = reinterpret_cast<uint64_t*>(s_lim + N / 2); // a tile's products are in tensor memory
+  uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 1) + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int range = static_cast<int>(blockIdx.x);
   bool clipped = false;
-  const long long sum = paged_count_tiles<C::TILE>(p.seqlens, p.B, p.max_len, lane, clipped);
-  if (range == 0 && __any_sync(ALL, clipped) && threadIdx.x == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
+  const long long sum = paged_count_tiles<WM_TILE>(p.seqlens, p.B, p.max_len, lane, clipped);
+  if (range == 0 && __any_sync(ALL, clipped) && tid == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
   const PagedRanges ranges(sum * p.Hkv, p.n_ranges);
   if (range >= ranges.n) return;
   const long long t0 = ranges.begin(range);
   int todo = static_cast<int>(ranges.begin(range + 1) - t0);
-  PagedTile at = paged_seek<C::TILE>(p.seqlens, p.B, p.Hkv, p.max_len, t0, lane);
-  while (true) {
-    // ================================================================ one segment: tiles of (b, hk), the warps' in turn
-    const int b = at.b, hk = at.hk, L = at.L, i1 = todo < at.nt - at.i ? at.i + todo : at.nt;
-    const int end = min(L, i1 * C::TILE);
-    int key0 = (at.i + warp) * C::TILE;
-    auto page_of = [&](int k0) -> int {
-      const int key = k0 + 16 * lane;
-      return (lane < KG && key < end) ? __ldg(p.table + b * p.table_stride + (key >> p.page_shift)) : -1;
+  PagedTile at = paged_seek<WM_TILE>(p.seqlens, p.B, p.Hkv, p.max_len, t0, lane);
+
+  const uint32_t tmem_columns = wm_tmem(N);
+  if (tid == 0) {
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(slot, tmem_columns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const uint32_t my_lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  constexpr uint32_t DHI = sdesc_sw128_hi(1024);
+  const uint32_t k_lo = sdesc_sw128_lo(smem_u32(s_k), 16), q_lo = sdesc_sw128_lo(smem_u32(s_q), 16);
+  const uint32_t idesc = idesc_bf16_f32(WM_TILE, N, false) & (F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
+  // this thread's place in a load: row (of the warp's RW) and first piece
+  const int lr = (lane & 7) + 8 * ((lane >> 3) / C::LPR), lc = (lane >> 3) % C::LPR;
+  uint32_t issued = 0u;  // tiles whose products were started; the last of them is waited for before anything is reused
+  bool ok = true;
+
+  while (todo > 0 && ok) {
+    // ================================================================ one segment: tiles of (b, hk)
+    const int b = at.b, hk = at.hk, L = at.L, i0 = at.i, n = todo < at.nt - at.i ? todo : at.nt - at.i;
+    auto page_of = [&](int t) -> int {  // of 16-key group `lane` of the segment's tile t
+      const int key = (i0 + t) * WM_TILE + 16 * lane;
+      return (lane < 8 && t < n && key < L) ? __ldg(p.table + b * p.table_stride + (key >> p.page_shift)) : -1;
     };
-    WgRaw<D, KIND> raw[KG];
-    float ka[KG];
-    long long off = -1;
-    unsigned next_live = 0u;
-    float scale = 1.f;
-    auto locate = [&](int k0, int id) {
-      const int gkey = k0 + 16 * lane;
-      const bool want = lane < KG && gkey < end;
-      off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, gkey & (p.page - 1), 1) : -1;
+    uint4 raw[C::PPR];
+    uint32_t f[KIND == PAGES_FP4 ? C::PPR : 1];  // 4-bit rows: a piece's two scale bytes
+    // of the tile loaded last, the one before, and the one before that: groups in pages of the pool; e4m3: the scale of this
+    // thread's key
+    unsigned live = 0u, live1 = 0u, live2 = 0u;
+    float ka = 1.f, ka1 = 1.f, ka2 = 1.f;
+    auto load = [&](int t, int id) {
+      const int key = (i0 + t) * WM_TILE + 16 * lane;
+      const bool want = lane < 8 && t < n && key < L;
+      const long long off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, key & (p.page - 1), 1) : -1;
       if (__any_sync(ALL, want && off < 0) && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
-      next_live = __ballot_sync(ALL, off >= 0);
-      if constexpr (KIND == PAGES_E4M3)
-        scale = off >= 0 ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk) : 0.f;
-    };
-    locate(key0, page_of(key0));
+      live = __ballot_sync(ALL, off >= 0);
+      if constexpr (KIND == PAGES_E4M3) {
+        const float scale = off >= 0 ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk) : 0.f;
+        ka = __shfl_sync(ALL, scale, tid >> 4);
+      }
+      // (rows that are not there: the last one of the group, or the pool's first, whose sums are not written)
+      const int rows = L - (i0 + t) * WM_TILE;
 #pragma unroll
-    for (int g = 0; g < KG; ++g) {
-      wg_load<D, KIND>(raw[g], p, __shfl_sync(ALL, off, g), end - key0 - 16 * g, gid, tig);
-      ka[g] = __shfl_sync(ALL, scale, g);
-    }
-    unsigned live = next_live;
-    constexpr int STEP = WG_WARPS * C::TILE;
-    int id = page_of(key0 + STEP);
+      for (int s = 0; s < C::SETS; ++s) {
+        const int r0 = C::RW * (4 * s + warp), r = r0 + lr, g = r0 / 16;
+        const long long base = __shfl_sync(ALL, off, g);
+        const long long row = base < 0 ? 0 : base + max(min(r, rows - 1) - 16 * g, 0);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k) + row * C::RB);
+#pragma unroll
+        for (int y = 0; y < C::PPR / C::LPR; ++y) {
+          const int x = s * (C::PPR / C::LPR) + y;
+          raw[x] = __ldg(src + lc + C::LPR * y);
+          if constexpr (KIND == PAGES_FP4)
+            f[x] = __ldg(reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(p.k_scale) + row * (D / 16)) + lc + C::LPR * y);
+        }
+      }
+    };
+    load(0, page_of(0));
+    int id = page_of(1);
+    __syncthreads();  // the segment before is done with the queries' memory
 
     // ---- the queries: a warp a row, a lane four of its elements, four rows at a time
-    for (int r0 = warp; r0 < 8 * p.row_tiles; r0 += 4 * WG_WARPS) {
+    bool dead = false;  // a row adds nothing
+    for (int r0 = warp; r0 < N; r0 += 16) {
       uint2 x[4];
       float lse[4];
       int tok[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = r0 + i * WG_WARPS;
+        const int r = r0 + 4 * i;
         const bool in = r < p.R;
         const int h = hk * p.G + (in ? r / p.Nq : 0);
         tok[i] = in ? r % p.Nq : 0;
@@ -395,112 +447,163 @@ __global__ void __launch_bounds__(WG_THREADS, 3) fa_weigh_paged_kernel(const Wei
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = r0 + i * WG_WARPS;
-        if (r >= 8 * p.row_tiles) break;
+        const int r = r0 + 4 * i;  // (N is a multiple of 16)
         float up = 1.f;
-        if constexpr (C::F16) {
+        if constexpr (F16) {
           float amax = wg_amax(x[i]);
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, o));
           x[i] = wg_to_f16(x[i], wg_powers(amax, up));
         }
-        if (lane < D / 4) {
-          int qt, j;
-          wg_place<D, KIND>(lane, qt, j);
-          s_q[((r / 8) * C::KST + j) * 32 + (r % 8) * 4 + qt] = x[i];
-        }
+        if (lane < D / 4) *reinterpret_cast<uint2*>(s_q + wm_at(N, r, 4 * lane)) = x[i];
         if (lane == 0) {
           const bool none = lse[i] == -INFINITY;
-          float* f = reinterpret_cast<float*>(s_row + r / 2) + (r & 1);
-          f[0] = p.scale_log2 * up;
-          f[2] = none ? 0.f : lse[i] * 1.4426950408889634f;
-          reinterpret_cast<int*>(s_lim + r / 2)[r & 1] = none ? -1 : min(L - 1, L - p.Nq + tok[i]);
+          float* at2 = reinterpret_cast<float*>(s_row + r / 2) + (r & 1);
+          at2[0] = p.scale_log2 * up;
+          at2[2] = none ? 0.f : lse[i] * -1.4426950408889634f;
+          const int lim = none ? -1 : min(L - 1, L - p.Nq + tok[i]);
+          reinterpret_cast<int*>(s_lim + r / 2)[r & 1] = lim;
+          dead = dead || (lim < 0 && r < p.R);
         }
       }
     }
-    __syncthreads();
+
+    dead = __syncthreads_or(dead);
 
     float* wrow = p.weights + (static_cast<long long>(b) * p.Hkv + hk) * p.wstride;
-    for (; key0 < end; key0 += STEP) {
-      locate(key0 + STEP, id);
-      id = page_of(key0 + 2 * STEP);
+    for (int t = 0; t <= n; ++t) {
+      // tile t - 1: this thread's key and what its weight was
+      const int tile = (i0 + t - 1) * WM_TILE, key = tile + tid;
+      live2 = live1, live1 = live, ka2 = ka1, ka1 = ka;
+      const bool writes = t > 0 && key < L && ((live2 >> (tid >> 4)) & 1u);
+      const float old = writes ? wrow[key] : 0.f;
+      if (t > 0) {
+        ok = mbar_wait(done, (issued - 1u) & 1u, p.wait_limit_ns, p.status, abort_flag);
+        tc_fence_after();
+      }
+      if (t < n) {  // tile t becomes the products' operand (quarter warps write eight rows: every bank once)
 #pragma unroll
-      for (int g0 = 0; g0 < KG; g0 += J) {
-        uint32_t a[J][C::KST][4];
-        float kf[J];
+        for (int s = 0; s < C::SETS; ++s) {
+          const int r = C::RW * (4 * s + warp) + lr;
 #pragma unroll
-        for (int g = 0; g < J; ++g) {
-          wg_fragments<D, KIND>(raw[g0 + g], [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-            a[g][j][0] = a0, a[g][j][1] = a1, a[g][j][2] = a2, a[g][j][3] = a3;
-          });
-          kf[g] = ka[g0 + g];
-          wg_load<D, KIND>(raw[g0 + g], p, __shfl_sync(ALL, off, g0 + g), end - key0 - STEP - 16 * (g0 + g), gid, tig);
-          ka[g0 + g] = __shfl_sync(ALL, scale, g0 + g);
-        }
-        if (((live >> g0) & ((1u << J) - 1u)) == 0u) continue;  // (the same in every lane)
-        // the weight that this lane writes
-        const int grp = J == 2 ? tig >> 1 : 0, mine = key0 + 16 * (g0 + grp) + gid + 8 * (tig & 1);
-        const bool writes = ((live >> (g0 + grp)) & 1u) && mine < end && (J == 2 || tig < 2);
-        const float old = writes ? wrow[mine] : 0.f;
-        float v[J][2];
+          for (int y = 0; y < C::PPR / C::LPR; ++y) {
+            const int x = s * (C::PPR / C::LPR) + y, c = lc + C::LPR * y;
+            const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+            if constexpr (KIND == PAGES_FP4) {
+              const uint32_t f0 = fp4_scale2<0>(f[x]), f1 = fp4_scale2<1>(f[x]);
 #pragma unroll
-        for (int g = 0; g < J; ++g) v[g][0] = v[g][1] = 0.f;
-        auto row_tile = [&](int n) {
-          float s[J][4];
+              for (int e = 0; e < 4; ++e) {
+                uint32_t h[4];
+                e2m1x8_to_f16x2x4(w[e], h);
+                const uint32_t fe = e < 2 ? f0 : f1;
+                *reinterpret_cast<uint4*>(s_k + wm_at(WM_TILE, r, 32 * c + 8 * e)) =
+                    make_uint4(hmul2_bits(h[0], fe), hmul2_bits(h[1], fe), hmul2_bits(h[2], fe), hmul2_bits(h[3], fe));
+              }
+            } else if constexpr (KIND == PAGES_E4M3) {
 #pragma unroll
-          for (int g = 0; g < J; ++g)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[g][e] = 0.f;
-          const uint2* qn = s_q + n * C::KST * 32 + lane;
-#pragma unroll
-          for (int j = 0; j < C::KST; ++j) {
-            const uint2 q = qn[j * 32];
-#pragma unroll
-            for (int g = 0; g < J; ++g) mma_16816<C::F16>(s[g], a[g][j][0], a[g][j][1], a[g][j][2], a[g][j][3], q.x, q.y);
+              for (int e = 0; e < 2; ++e) {
+                uint4 h;
+                e4m3x4_to_f16x2x2(w[2 * e], h.x, h.y);
+                e4m3x4_to_f16x2x2(w[2 * e + 1], h.z, h.w);
+                *reinterpret_cast<uint4*>(s_k + wm_at(WM_TILE, r, 16 * c + 8 * e)) = h;
+              }
+            } else {
+              *reinterpret_cast<uint4*>(s_k + wm_at(WM_TILE, r, 8 * c)) = raw[x];
+            }
           }
-          const float4 f = s_row[n * 4 + tig];
-          const int2 lim = s_lim[n * 4 + tig];
+        }
+        fence_proxy_async_smem();  // the tensor core reads the operands through the async proxy
+      }
+      tc_fence_before();
+      ok = __syncthreads_and(ok);
+      if (!ok) break;
+      if (t < n) {
+        if (warp == 0) {
+          tc_fence_after();
 #pragma unroll
-          for (int g = 0; g < J; ++g) {
-            const int key = key0 + 16 * (g0 + g) + gid;
-            const float c0 = KIND == PAGES_E4M3 ? f.x * kf[g] : f.x, c1 = KIND == PAGES_E4M3 ? f.y * kf[g] : f.y;
-            const float p0 = ex2_approx(fmaf(s[g][0], c0, -f.z)), p1 = ex2_approx(fmaf(s[g][1], c1, -f.w));
-            const float p2 = ex2_approx(fmaf(s[g][2], c0, -f.z)), p3 = ex2_approx(fmaf(s[g][3], c1, -f.w));
-            v[g][0] += (key <= lim.x ? p0 : 0.f) + (key <= lim.y ? p1 : 0.f);
-            v[g][1] += (key + 8 <= lim.x ? p2 : 0.f) + (key + 8 <= lim.y ? p3 : 0.f);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t ko = static_cast<uint32_t>((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4;
+            const uint32_t qo = static_cast<uint32_t>((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4;
+            if (elect_one()) mma_ss_w(tmem + (t & 1) * N, k_lo + ko, DHI, q_lo + qo, DHI, idesc, kk > 0 ? 1u : 0u);
+          }
+          if (elect_one()) mma_commit(done);
+          __syncwarp();
+        }
+        ++issued;
+      }
+      if (t + 1 < n) {
+        load(t + 1, id);
+        id = page_of(t + 2);
+      }
+      if (t == 0) continue;
+      // ---- tile t - 1: this lane's key against every row, two at a time
+      const bool plain = tile + WM_TILE <= L - p.Nq && (p.R & 1) == 0 && !dead;  // every row sees every key
+      const uint64_t ka_2 = f2pack(ka2, ka2);
+      uint64_t acc = 0ull;
+      for (int c0 = 0; c0 < p.R; c0 += 32) {
+        uint32_t sv[32];
+        tmem_ld32(my_lanes + ((t - 1) & 1) * N + c0, sv);
+        tmem_ld_wait32(sv);
+        auto pairs = [&](auto masked) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = c0 + 2 * i;
+            if (c >= p.R) break;
+            const float4 cl = s_row[c / 2];
+            uint64_t y = f2pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+            if constexpr (KIND == PAGES_E4M3) y = fmul2(y, ka_2);
+            float y0, y1;
+            f2unpack(ffma2(y, f2pack(cl.x, cl.y), f2pack(cl.z, cl.w)), y0, y1);
+            y0 = ex2_approx(y0), y1 = ex2_approx(y1);
+            if constexpr (decltype(masked)::value) {
+              const int2 lim = s_lim[c / 2];
+              y0 = key <= lim.x ? y0 : 0.f;
+              y1 = key <= lim.y ? y1 : 0.f;
+            }
+            acc = fadd2(acc, f2pack(y0, y1));
           }
         };
-        // (two at a time: their products do not wait for one another)
-        int n = 0;
-#pragma unroll 1
-        for (; n + 1 < p.row_tiles; n += 2) {
-          row_tile(n);
-          row_tile(n + 1);
-        }
-        if (n < p.row_tiles) row_tile(n);
-        wg_sum_lanes<J>(v, tig);
-        if (writes) wrow[mine] = old + v[0][0];
+        if (plain) pairs(std::false_type{});
+        else pairs(std::true_type{});
       }
-      live = next_live;
+      float a0, a1;
+      f2unpack(acc, a0, a1);
+      if (writes) wrow[key] = old + (a0 + a1);
     }
-    todo -= i1 - at.i;
-    if (todo == 0) return;
-    __syncthreads();  // the queries' memory is free again
-    at.i = at.nt - 1;
-    paged_next<C::TILE>(at, p.seqlens, p.B, p.Hkv, p.max_len);
+    todo -= n;
+    if (todo > 0) {
+      at.i = at.nt - 1;
+      paged_next<WM_TILE>(at, p.seqlens, p.B, p.Hkv, p.max_len);
+    }
+  }
+  // (a wait that gave up: the products in flight end before their memory is given back)
+  if (!ok && issued > 0u) {
+    const uint64_t t1 = globaltimer_ns();
+    for (uint32_t i = 0; !mbar_try_wait(smem_u32(done), (issued - 1u) & 1u); ++i)
+      if ((i & 31u) == 31u && globaltimer_ns() - t1 > p.wait_limit_ns) break;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_columns);
   }
 }
 
 template <int D, int KIND>
-static int wg_smem(int row_tiles) {
-  return row_tiles * (WgCfg<D, KIND>::KST * 256 + 4 * 16 + 4 * 8);
+static int wm_smem(int cols) {
+  // operands, row arrays, barrier and flags, alignment; and no more blocks on an SM than its tensor memory holds
+  const int need = WmCfg<D, KIND>::K_BYTES + cols * D * 2 + cols * 12 + 32 + 1024;
+  const int ctas = 512 / wm_tmem(cols);
+  const int most = ctas >= WmCfg<D, KIND>::CTAS ? 0 : 228 * 1024 / (ctas + 1);
+  return need > most ? need : most;
 }
 template <int KIND>
 static cudaError_t wg_attrs() {
-  const cudaError_t a = cudaFuncSetAttribute(fa_weigh_paged_kernel<64, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             wg_smem<64, KIND>(16));
-  const cudaError_t b = cudaFuncSetAttribute(fa_weigh_paged_kernel<128, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             wg_smem<128, KIND>(16));
+  const cudaError_t a = cudaFuncSetAttribute(fa_weigh_paged_many_kernel<64, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             wm_smem<64, KIND>(128));
+  const cudaError_t b = cudaFuncSetAttribute(fa_weigh_paged_many_kernel<128, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             wm_smem<128, KIND>(128));
   return a != cudaSuccess ? a : b;
 }
 cudaError_t weigh_paged_set_attributes() {
@@ -520,8 +623,9 @@ template <int D, int KIND>
 static cudaError_t wg_launch(WeighPagedParams p, int num_sms, cudaStream_t stream) {
   if (p.R <= 8) return wg_launch_few<D, KIND, 1>(p, num_sms, stream);
   if (p.R <= 16) return wg_launch_few<D, KIND, 2>(p, num_sms, stream);
-  p.n_ranges = 3 * num_sms;
-  fa_weigh_paged_kernel<D, KIND><<<p.n_ranges, WG_THREADS, wg_smem<D, KIND>(p.row_tiles), stream>>>(p);
+  const int cols = wm_cols(p.R), ctas = 512 / wm_tmem(cols);
+  p.n_ranges = num_sms * (ctas < WmCfg<D, KIND>::CTAS ? ctas : WmCfg<D, KIND>::CTAS);
+  fa_weigh_paged_many_kernel<D, KIND><<<p.n_ranges, WM_THREADS, wm_smem<D, KIND>(cols), stream>>>(p);
   return cudaGetLastError();
 }
 template <int D>
