@@ -326,6 +326,7 @@ struct WmCfg {
   static constexpr int SETS = WM_TILE / (4 * RW);   // of them, a warp's
   static constexpr int BOX = WM_TILE * 128;         // 64 elements of every key, rows of 128 swizzled bytes
   static constexpr int K_BYTES = BOX * (D / 64);
+  static constexpr int CP = D / PPR / 8;            // 8-element chunks of a piece: 1, 2 or 4
   static constexpr int CTAS = KIND == PAGES_BF16 && D == 128 ? 3 : 4;  // by registers
 };
 __host__ __device__ constexpr int wm_cols(int rows) { return (rows + 31) / 32 * 32; }       // query rows, padded
@@ -381,6 +382,13 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
   const uint32_t idesc = idesc_bf16_f32(WM_TILE, N, false) & (F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
   // this thread's place in a load: row (of the warp's RW) and first piece
   const int lr = (lane & 7) + 8 * ((lane >> 3) / C::LPR), lc = (lane >> 3) % C::LPR;
+  // and where its chunks go: element wm_at(row, 8 (CP piece + e)), taken apart. A piece's chunks stay within a box, and so do
+  // the first LPR pieces (or, 4-bit rows of d = 128, pairs of them).
+  uint8_t* const to = s_k + (C::RW / 8 * warp + lr / 8) * 1024 + (lane & 7) * 128 + lc * C::CP / 8 * C::BOX;
+  auto chunk_at = [&](int s, int y, int e) {
+    return to + s * (C::RW / 2) * 1024 + C::LPR * C::CP * y / 8 * C::BOX +
+           (((lc * C::CP % 8 + C::LPR * C::CP * y % 8 + e) ^ (lane & 7)) << 4);
+  };
   uint32_t issued = 0u;  // tiles whose products were started; the last of them is waited for before anything is reused
   bool ok = true;
 
@@ -393,20 +401,18 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
     };
     uint4 raw[C::PPR];
     uint32_t f[KIND == PAGES_FP4 ? C::PPR : 1];  // 4-bit rows: a piece's two scale bytes
-    // of the tile loaded last, the one before, and the one before that: groups in pages of the pool; e4m3: the scale of this
-    // thread's key
+    // of the tile loaded last, the one before, and the one before that: groups in pages of the pool; e4m3: lane g holds the
+    // scale of group g (asked for with the rows, and handed out a tile later), then of this thread's key
     unsigned live = 0u, live1 = 0u, live2 = 0u;
-    float ka = 1.f, ka1 = 1.f, ka2 = 1.f;
+    float scale = 1.f, ka1 = 1.f, ka2 = 1.f;
     auto load = [&](int t, int id) {
       const int key = (i0 + t) * WM_TILE + 16 * lane;
       const bool want = lane < 8 && t < n && key < L;
       const long long off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, key & (p.page - 1), 1) : -1;
       if (__any_sync(ALL, want && off < 0) && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
       live = __ballot_sync(ALL, off >= 0);
-      if constexpr (KIND == PAGES_E4M3) {
-        const float scale = off >= 0 ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk) : 0.f;
-        ka = __shfl_sync(ALL, scale, tid >> 4);
-      }
+      if constexpr (KIND == PAGES_E4M3)
+        scale = off >= 0 ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk) : 0.f;
       // (rows that are not there: the last one of the group, or the pool's first, whose sums are not written)
       const int rows = L - (i0 + t) * WM_TILE;
 #pragma unroll
@@ -428,14 +434,15 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
     int id = page_of(1);
     __syncthreads();  // the segment before is done with the queries' memory
 
-    // ---- the queries: a warp a row, a lane four of its elements, four rows at a time
+    // ---- the queries: a warp a row, a lane four of its elements, eight rows at a time
+    constexpr int QB = 8;
     bool dead = false;  // a row adds nothing
-    for (int r0 = warp; r0 < N; r0 += 16) {
-      uint2 x[4];
-      float lse[4];
-      int tok[4];
+    for (int r0 = warp; r0 < N; r0 += 4 * QB) {  // (N is a multiple of 32)
+      uint2 x[QB];
+      float lse[QB];
+      int tok[QB];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < QB; ++i) {
         const int r = r0 + 4 * i;
         const bool in = r < p.R;
         const int h = hk * p.G + (in ? r / p.Nq : 0);
@@ -446,8 +453,8 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
         lse[i] = in ? __ldg(p.lse + (static_cast<long long>(b) * p.H + h) * p.Nq + tok[i]) : -INFINITY;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 4 * i;  // (N is a multiple of 16)
+      for (int i = 0; i < QB; ++i) {
+        const int r = r0 + 4 * i;
         float up = 1.f;
         if constexpr (F16) {
           float amax = wg_amax(x[i]);
@@ -474,7 +481,8 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
     for (int t = 0; t <= n; ++t) {
       // tile t - 1: this thread's key and what its weight was
       const int tile = (i0 + t - 1) * WM_TILE, key = tile + tid;
-      live2 = live1, live1 = live, ka2 = ka1, ka1 = ka;
+      live2 = live1, live1 = live, ka2 = ka1;
+      if constexpr (KIND == PAGES_E4M3) ka1 = __shfl_sync(ALL, scale, tid >> 4);
       const bool writes = t > 0 && key < L && ((live2 >> (tid >> 4)) & 1u);
       const float old = writes ? wrow[key] : 0.f;
       if (t > 0) {
@@ -484,10 +492,9 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
       if (t < n) {  // tile t becomes the products' operand (quarter warps write eight rows: every bank once)
 #pragma unroll
         for (int s = 0; s < C::SETS; ++s) {
-          const int r = C::RW * (4 * s + warp) + lr;
 #pragma unroll
           for (int y = 0; y < C::PPR / C::LPR; ++y) {
-            const int x = s * (C::PPR / C::LPR) + y, c = lc + C::LPR * y;
+            const int x = s * (C::PPR / C::LPR) + y;
             const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
             if constexpr (KIND == PAGES_FP4) {
               const uint32_t f0 = fp4_scale2<0>(f[x]), f1 = fp4_scale2<1>(f[x]);
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
                 uint32_t h[4];
                 e2m1x8_to_f16x2x4(w[e], h);
                 const uint32_t fe = e < 2 ? f0 : f1;
-                *reinterpret_cast<uint4*>(s_k + wm_at(WM_TILE, r, 32 * c + 8 * e)) =
+                *reinterpret_cast<uint4*>(chunk_at(s, y, e)) =
                     make_uint4(hmul2_bits(h[0], fe), hmul2_bits(h[1], fe), hmul2_bits(h[2], fe), hmul2_bits(h[3], fe));
               }
             } else if constexpr (KIND == PAGES_E4M3) {
@@ -505,10 +512,10 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
                 uint4 h;
                 e4m3x4_to_f16x2x2(w[2 * e], h.x, h.y);
                 e4m3x4_to_f16x2x2(w[2 * e + 1], h.z, h.w);
-                *reinterpret_cast<uint4*>(s_k + wm_at(WM_TILE, r, 16 * c + 8 * e)) = h;
+                *reinterpret_cast<uint4*>(chunk_at(s, y, e)) = h;
               }
             } else {
-              *reinterpret_cast<uint4*>(s_k + wm_at(WM_TILE, r, 8 * c)) = raw[x];
+              *reinterpret_cast<uint4*>(chunk_at(s, y, 0)) = raw[x];
             }
           }
         }
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
       }
       if (t == 0) continue;
       // ---- tile t - 1: this lane's key against every row, two at a time
-      const bool plain = tile + WM_TILE <= L - p.Nq && (p.R & 1) == 0 && !dead;  // every row sees every key
+      const bool plain = tile + WM_TILE <= L - p.Nq && !dead;  // every row sees every key
       const uint64_t ka_2 = f2pack(ka2, ka2);
       uint64_t acc = 0ull;
       for (int c0 = 0; c0 < p.R; c0 += 32) {
@@ -548,7 +555,6 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int c = c0 + 2 * i;
-            if (c >= p.R) break;
             const float4 cl = s_row[c / 2];
             uint64_t y = f2pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
             if constexpr (KIND == PAGES_E4M3) y = fmul2(y, ka_2);
@@ -563,8 +569,8 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
             acc = fadd2(acc, f2pack(y0, y1));
           }
         };
-        if (plain) pairs(std::false_type{});
-        else pairs(std::true_type{});
+        if (plain && c0 + 32 <= p.R) pairs(std::false_type{});
+        else pairs(std::true_type{});  // (padding rows see no key)
       }
       float a0, a1;
       f2unpack(acc, a0, a1);
