@@ -1,4 +1,4 @@
-"""Build libfa_gb300.so in-tree with nvcc for sm_103a (no cmake, no torch).
+"""Build libfa_gb300.so in-tree with nvcc for sm_103a, and the binding's C part _binding.so (no cmake, no torch).
 
     python -m io_aware_exact_fa_gb300.build [--verbose] [--ptxas-info] [--debug]
 
@@ -17,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +26,7 @@ BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa_gb300.so")
 LIB_DEBUG = os.path.join(PKG, "libfa_gb300_debug.so")
+BINDING = os.path.join(PKG, "_binding.so")   # argument checks of the paged calls, in C
 SOURCES = ["fa_api.cu", "prefill_sm103.cu", "decode_sm103.cu", "backward_sm103.cu", "decode_grouped_sm103.cu",
            "materialized_sm103.cu", "append_paged_sm103.cu", "decode_paged_sm103.cu",
            "read_paged_sm103.cu", "weigh_paged_sm103.cu", "evict_paged_sm103.cu"]
@@ -52,10 +54,25 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def _build_binding(force: bool) -> None:
+    if not force and up_to_date(BINDING):
+        return
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-std=c11", "-shared", "-fPIC", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.c"), "-o", tmp, "-lm"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        raise RuntimeError("the C compiler failed on binding.c")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False, debug: bool = False) -> str:
     """Compile and link the library (the checking build with debug=True); returns its path."""
     lib = LIB_DEBUG if debug else LIB
     bdir = BUILD + "_debug" if debug else BUILD
+    if not debug:
+        _build_binding(force)
     if not force and not ptxas_info and up_to_date(lib):
         return lib
     os.makedirs(bdir, exist_ok=True)

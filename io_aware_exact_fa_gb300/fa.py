@@ -22,6 +22,11 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(
         f"{LIB_PATH} is missing: build it with `python -m io_aware_exact_fa_gb300.build` "
         "(or __graft_entry__.build()); there is no non-CUDA fallback")
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError(f"{os.path.join(_HERE, '_binding.so')} is missing or of another Python: build it with "
+                      "`python -m io_aware_exact_fa_gb300.build`") from e
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -614,6 +619,19 @@ PAGES_BF16, PAGES_E4M3, PAGES_FP4 = range(3)
 _U8 = torch.uint8
 _FP4 = getattr(torch, "float4_e2m1fn_x2", torch.uint8)   # (two codes a byte)
 
+# The calls below go through _binding first, which makes the same checks in C and leaves to this module whatever does not
+# pass them (or comes on another stream): half the host's time of a small step.
+_binding.setup((torch.Tensor, _BF16, _F32, _I32, torch.int64, _U8, _CODES, _FP4), (_raw_stream, _current_device, _empty_here),
+               tuple(ctypes.cast(getattr(_lib, n), _vp).value for n in (
+                   "fa_append_paged_fp4", "fa_decode_paged_fp4", "fa_read_paged", "fa_weigh_paged", "fa_evict_paged")))
+
+
+def _done(r, where: str):
+    status, results = r
+    if status != FA_OK:
+        raise FAError(status, where)
+    return results
+
 
 def _table(block_table, name: str, dev: int, B: int = -1) -> Tuple[int, int, int, int]:
     """A block table: (its address, its row stride, B, width)."""
@@ -677,6 +695,10 @@ def append_paged_fp4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages:
                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """``append_paged`` into 4-bit pages (fa.h fa_append_paged_fp4): k_pages/v_pages [num_pages,Hkv,page,d/2] uint8 or
     float4_e2m1fn_x2, k_scale/v_scale uint8 [num_pages,Hkv,page,d/16]; the rest as for ``append_paged``."""
+    r = _binding.append_fp4(q, k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, cu_seqlens, max_new, turns,
+                            interleaved, rot_scale, q_weight, k_weight, eps, offsets, q_out, k_out, with_k, stream)
+    if r is not NotImplemented:
+        return _done(r, "fa_append_paged_fp4")
     _tokens(q, k)
     Hkv = k.shape[1]
     pool, n, page, B, width = _pool4(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, Hkv, q.shape[2],
@@ -696,6 +718,10 @@ def decode_paged_fp4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
                      lse: Optional[torch.Tensor] = None, with_lse: bool = True,
                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """``decode_paged`` over 4-bit pages (fa.h fa_decode_paged_fp4), laid out as for ``append_paged_fp4``."""
+    r = _binding.decode_fp4(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, scale, max_len, num_splits,
+                            workspace, out, lse, with_lse, stream)
+    if r is not NotImplemented:
+        return _done(r, "fa_decode_paged_fp4")
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
@@ -715,6 +741,9 @@ def read_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.
     """Rows of a paged cache as packed bf16 k, v [total,Hkv,d] (fa.h fa_read_paged), which ``fwd_packed`` takes: the last
     cu_seqlens[b+1] - cu_seqlens[b] rows of sequence b go to rows cu_seqlens[b] .. of the outputs. Pages of any kind: bf16,
     e4m3 with fp32 scales, or 4-bit rows with uint8 scales."""
+    r = _binding.read(k_pages, v_pages, block_table, seqlens_k, cu_seqlens, total, k_scale, v_scale, k_out, v_out, stream)
+    if r is not NotImplemented:
+        return _done(r, "fa_read_paged")
     if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
         raise ValueError("k_pages must be a CUDA tensor")
     dev = k_pages.get_device()
@@ -757,6 +786,9 @@ def weigh_paged(q: torch.Tensor, lse: torch.Tensor, k_pages: torch.Tensor, block
     give its keys, summed over the heads of a K/V head's group (fa.h fa_weigh_paged). q [B,H,Nq,d] and lse [B,H,Nq] are those
     of the ``decode_paged`` call; pages of any kind, as for ``read_paged``; ``max_len`` bounds the lengths (default: what
     ``weights`` and a row of the table cover). Returns ``weights``."""
+    r = _binding.weigh(q, lse, k_pages, block_table, seqlens_k, weights, k_scale, scale, max_len, stream)
+    if r is not NotImplemented:
+        return _done(r, "fa_weigh_paged")
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, H, Nq, d]")
     dev = q.get_device()
@@ -789,6 +821,10 @@ def evict_paged(weights: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
     ``new_table`` (pages that nothing else uses). Returns the kept rows' old indices int32 [B,Hkv,keep] (-1 past them), the new
     lengths, the new weights (``new_weights`` [B,Hkv,>= keep] where given; 0 past the kept ones) and the positions of
     row 0 for ``append_paged``'s ``offsets``."""
+    r = _binding.evict(weights, k_pages, v_pages, block_table, seqlens_k, new_table, keep, first, recent, k_scale, v_scale,
+                       offsets, max_len, new_weights, stream)
+    if r is not NotImplemented:
+        return _done(r, "fa_evict_paged")
     if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
         raise ValueError("k_pages must be a CUDA tensor")
     dev = k_pages.get_device()
