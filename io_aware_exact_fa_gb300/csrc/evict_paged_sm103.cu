@@ -15,10 +15,12 @@
 // contiguous part of its weights in shared memory (so they are read once), and
 // the counts are summed over the cluster's shared memories. Then every warp counts
 // its contiguous run, and with the runs' sums before it writes indices and weights
-// in order. (2) The move: a block takes 128 new rows of one head and copies their
-// keys and values, 16 bytes (4-bit rows: also the scale bytes) a thread. A new e4m3
-// page's scale is the largest of its rows' old ones, and codes whose scale grew are
-// rounded again.
+// in order. (2) The move: a warp takes 16 new rows of one
+// head, which lie in one page, and copies their keys and values, 16 bytes (4-bit
+// rows: also the scale bytes) a lane; no warp waits for another. A new e4m3 page's
+// scale is the largest of its rows' old ones, which each warp of the page finds for
+// itself, and codes whose scale grew are rounded again. (Blocks of 128 rows that met
+// at barriers: MOVE.)
 // What bounds it: HBM, the weights read and the kept rows read and written; for one
 // or two sequences the selection's chain of passes.
 #include <cooperative_groups.h>
@@ -45,8 +47,7 @@ constexpr int EV_LIST = 4096;     // rows of the border's first digit that a blo
 constexpr int EV_MAX_CLUSTER = 8;
 constexpr int EV_HELD = 40960;    // keys that a block holds in shared memory, at most
 constexpr int EV_FLIGHT = 8;      // weights that a thread asks for at once
-constexpr int EV_ROWS = 128;      // new rows of a moving block
-constexpr int EV_MOVE_THREADS = 256;
+constexpr int EV_MOVE_WARPS = 8;
 constexpr unsigned ALL = 0xffffffffu;
 
 // Bits that order weights downwards: larger ones have smaller keys, -0 as 0, NaN as -inf.
@@ -342,90 +343,88 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) fa_evict_select
   if (ranks > 1) cluster.barrier_wait();
 }
 
-// ---- the move
+// ---- the move: sixteen new rows of one K/V head a warp
 template <int D, int KIND>
-__global__ void __launch_bounds__(EV_MOVE_THREADS, KIND == PAGES_E4M3 ? 5 : 6) fa_evict_move_kernel(const EvictPagedParams p) {
+__global__ void __launch_bounds__(32 * EV_MOVE_WARPS) fa_evict_move_kernel(const EvictPagedParams p) {
   constexpr int RB = paged_row_bytes(KIND, D), CR = RB / 16, SB = D / 16;
-  __shared__ long long s_src[EV_ROWS], s_dst[EV_ROWS];  // rows in the pool, or -1
-  __shared__ float s_scale[2][EV_ROWS];                  // e4m3: old scales of the rows
-  __shared__ unsigned int s_most[2][EV_ROWS / 16];       // and the largest of each new page
-  const int tid = threadIdx.x;
-  const int parts = (p.keep + EV_ROWS - 1) / EV_ROWS;
-  const int part = static_cast<int>(blockIdx.x % parts), pair = static_cast<int>(blockIdx.x / parts);
-  const int b = pair / p.Hkv, hk = pair % p.Hkv;
-  const int row0 = part * EV_ROWS;
-  const int n_new = min(paged_clip_len(__ldg(p.seqlens + b), p.max_len), p.keep);
-  const int rows = min(EV_ROWS, n_new - row0);
-  if (KIND == PAGES_E4M3 && tid < 2 * (EV_ROWS / 16)) s_most[tid / (EV_ROWS / 16)][tid % (EV_ROWS / 16)] = 0u;
-  if (rows > 0 && tid < rows) {  // where the row goes does not depend on the selection
-    const int i = row0 + tid;
-    const int id = __ldg(p.new_table + b * p.new_table_stride + (i >> p.page_shift));
-    s_dst[tid] = paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, i & (p.page - 1), 1);
+  constexpr int RPL = 32 / CR;       // rows of one load of the warp
+  constexpr int N = 16 / RPL;        // loads of K, and of V
+  const int lane = threadIdx.x & 31;
+  const int groups = (p.keep + 15) / 16;
+  const long long unit = static_cast<long long>(blockIdx.x) * EV_MOVE_WARPS + (threadIdx.x >> 5);
+  const int pair = static_cast<int>(unit / groups), row0 = static_cast<int>(unit % groups) * 16;
+  const bool in = pair < p.B * p.Hkv;
+  const int b = in ? pair / p.Hkv : 0, hk = pair - b * p.Hkv;
+  const int n_new = in ? min(paged_clip_len(__ldg(p.seqlens + b), p.max_len), p.keep) : 0;
+  const int rows = min(16, n_new - row0);
+  // where the rows go does not depend on the selection: they lie in one page
+  long long dst = -1;
+  if (rows > 0) {
+    const int id = __ldg(p.new_table + b * p.new_table_stride + (row0 >> p.page_shift));
+    dst = paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, row0 & (p.page - 1), 1);
   }
-  __syncthreads();
   pdl_wait();
   if (rows <= 0) return;
-  bool bad = false;
-  if (tid < rows) {
-    const int j = __ldcg(p.kept + static_cast<long long>(pair) * p.keep + row0 + tid);
-    const int id = __ldg(p.table + b * p.table_stride + (j >> p.page_shift));
-    const long long src = paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, j & (p.page - 1), 1);
-    bad = src < 0 || s_dst[tid] < 0;
-    s_src[tid] = bad ? -1 : src;
-    if constexpr (KIND == PAGES_E4M3) {
-      if (!bad) {
-        const int at = ((row0 + tid) >> p.page_shift) - (row0 >> p.page_shift);
-        const long long ph = static_cast<long long>(id) * p.Hkv + hk;
-        const float ks = static_cast<const float*>(p.k_scale)[ph], vs = static_cast<const float*>(p.v_scale)[ph];
-        s_scale[0][tid] = ks, s_scale[1][tid] = vs;
-        // positive factors order as integers
-        if (ks > 0.f) atomicMax(&s_most[0][at], __float_as_uint(ks));
-        if (vs > 0.f) atomicMax(&s_most[1][at], __float_as_uint(vs));
-      }
-    }
-  }
-  if (bad) atomicOr(p.status, FA_DEV_BAD_PAGE);
-  __syncthreads();
+  // (page of the pool, and row there, of new row i: -1 where a table names none)
+  auto from = [&](int i, int& id) -> long long {
+    const int j = __ldcg(p.kept + static_cast<long long>(pair) * p.keep + i);
+    id = __ldg(p.table + b * p.table_stride + (j >> p.page_shift));
+    return paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, j & (p.page - 1), 1);
+  };
+  int my_id = 0;
+  long long src = lane < rows ? from(row0 + lane, my_id) : -1;
+  if (__any_sync(ALL, lane < rows && (src < 0 || dst < 0)) && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
+  if (dst < 0) return;  // (uniform)
   uint8_t* kp = static_cast<uint8_t*>(const_cast<void*>(p.k));
   uint8_t* vp = static_cast<uint8_t*>(const_cast<void*>(p.v));
+  // e4m3: the new page's scales are the largest over all of its rows, of which every warp of the page looks at all
+  float k_most = 0.f, v_most = 0.f, k_old = 0.f, v_old = 0.f;
   if constexpr (KIND == PAGES_E4M3) {
-    // (a page's first new row writes its scales; rows of a page are all in this block)
-    if (tid < rows && s_src[tid] >= 0) {
-      const int at = ((row0 + tid) >> p.page_shift) - (row0 >> p.page_shift);
-      const long long ph = s_dst[tid] >> p.page_shift;
-      static_cast<float*>(const_cast<void*>(p.k_scale))[ph] = __uint_as_float(s_most[0][at]);
-      static_cast<float*>(const_cast<void*>(p.v_scale))[ph] = __uint_as_float(s_most[1][at]);
+    float* ks = static_cast<float*>(const_cast<void*>(p.k_scale));
+    float* vs = static_cast<float*>(const_cast<void*>(p.v_scale));
+    if (src >= 0) {
+      k_old = ks[static_cast<long long>(my_id) * p.Hkv + hk];
+      v_old = vs[static_cast<long long>(my_id) * p.Hkv + hk];
     }
-  }
-  constexpr int FLIGHT = 4;
-  const int items = rows * CR * 2;  // pieces of K, then of V
-  for (int x0 = tid; x0 < items; x0 += FLIGHT * EV_MOVE_THREADS) {
-    uint4 y[FLIGHT];
-    long long to[FLIGHT];
-#pragma unroll
-    for (int i = 0; i < FLIGHT; ++i) {
-      const int x = x0 + i * EV_MOVE_THREADS;
-      const bool is_v = x >= items / 2;
-      const int r = (is_v ? x - items / 2 : x) / CR, c = x % CR;
-      to[i] = -1;
-      if (x < items && s_src[r] >= 0) {
-        y[i] = *reinterpret_cast<const uint4*>((is_v ? vp : kp) + s_src[r] * RB + c * 16);
-        to[i] = s_dst[r] * RB + c * 16;
+    const int first = row0 & ~(p.page - 1), end = min(n_new, first + p.page);
+    bool any = false;
+#pragma unroll 4
+    for (int i = first + lane; i < end; i += 32) {
+      int id;
+      if (from(i, id) >= 0) {
+        any = true;
+        k_most = fmaxf(k_most, ks[static_cast<long long>(id) * p.Hkv + hk]);
+        v_most = fmaxf(v_most, vs[static_cast<long long>(id) * p.Hkv + hk]);
       }
     }
+    // positive factors order as integers
+    k_most = __uint_as_float(__reduce_max_sync(ALL, __float_as_uint(k_most)));
+    v_most = __uint_as_float(__reduce_max_sync(ALL, __float_as_uint(v_most)));
+    any = __any_sync(ALL, any);
+    if (row0 == first && any && lane == 0) {
+      ks[dst >> p.page_shift] = k_most;
+      vs[dst >> p.page_shift] = v_most;
+    }
+  }
+  const int piece = lane % CR, lr = lane / CR;
+  auto load = [&](const uint8_t* pages, uint4 (&y)[N]) {
 #pragma unroll
-    for (int i = 0; i < FLIGHT; ++i) {
-      if (to[i] < 0) continue;
-      const int x = x0 + i * EV_MOVE_THREADS;
-      const bool is_v = x >= items / 2;
+    for (int i = 0; i < N; ++i) {
+      const long long at = __shfl_sync(ALL, src, i * RPL + lr);
+      if (at >= 0) y[i] = *reinterpret_cast<const uint4*>(pages + at * RB + piece * 16);
+    }
+  };
+  auto store = [&](uint8_t* pages, uint4 (&y)[N], [[maybe_unused]] float old, [[maybe_unused]] float most) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = i * RPL + lr;
+      const long long at = __shfl_sync(ALL, src, r);
       if constexpr (KIND == PAGES_E4M3) {
-        const int r = (is_v ? x - items / 2 : x) / CR;
-        const float old = s_scale[is_v][r];
-        const float now = __uint_as_float(s_most[is_v][((row0 + r) >> p.page_shift) - (row0 >> p.page_shift)]);
         // In f16: for powers of two exact down to 2^-24, far below half the least code (2^-10), so the one rounding is that
         // to e4m3; other ratios are off by 2^-11 of themselves. NaN codes stay NaN.
-        if (old != now) {
-          const float f = old / now;
+        const float was = __shfl_sync(ALL, old, r);
+        if (at >= 0 && was != most) {
+          const float f = was / most;
           const uint32_t f2 = pack_f16x2(f, f);
           uint32_t* w[4] = {&y[i].x, &y[i].y, &y[i].z, &y[i].w};
 #pragma unroll
@@ -436,19 +435,26 @@ __global__ void __launch_bounds__(EV_MOVE_THREADS, KIND == PAGES_E4M3 ? 5 : 6) f
           }
         }
       }
-      *reinterpret_cast<uint4*>((is_v ? vp : kp) + to[i]) = y[i];
+      if (at >= 0) *reinterpret_cast<uint4*>(pages + (dst + r) * RB + piece * 16) = y[i];
+    }
+  };
+  uint4 yk[N], yv[N];
+  load(kp, yk);
+  load(vp, yv);
+  if constexpr (KIND == PAGES_FP4) {  // the rows' scale bytes, a word a lane
+    const int r = lane / (SB / 4), c = lane % (SB / 4);
+    const long long at = __shfl_sync(ALL, src, r & 15);
+    uint8_t* ks = static_cast<uint8_t*>(const_cast<void*>(p.k_scale));
+    uint8_t* vs = static_cast<uint8_t*>(const_cast<void*>(p.v_scale));
+    if (r < 16 && at >= 0) {
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(ks + at * SB + 4 * c);
+      const uint32_t y = *reinterpret_cast<const uint32_t*>(vs + at * SB + 4 * c);
+      *reinterpret_cast<uint32_t*>(ks + (dst + r) * SB + 4 * c) = x;
+      *reinterpret_cast<uint32_t*>(vs + (dst + r) * SB + 4 * c) = y;
     }
   }
-  if constexpr (KIND == PAGES_FP4) {  // the rows' scale bytes: 8 or 4, a word at a time
-    const int words = SB / 4;
-    for (int x = tid; x < rows * words * 2; x += EV_MOVE_THREADS) {
-      const bool is_v = x >= rows * words;
-      const int y = is_v ? x - rows * words : x, r = y / words, c = y % words;
-      if (s_src[r] < 0) continue;
-      uint8_t* s = static_cast<uint8_t*>(const_cast<void*>(is_v ? p.v_scale : p.k_scale));
-      *reinterpret_cast<uint32_t*>(s + s_dst[r] * SB + 4 * c) = *reinterpret_cast<const uint32_t*>(s + s_src[r] * SB + 4 * c);
-    }
-  }
+  store(kp, yk, k_old, k_most);
+  store(vp, yv, v_old, v_most);
 }
 
 template <int THREADS>
@@ -499,8 +505,9 @@ cudaError_t launch_evict_paged(int d, int kind, const EvictPagedParams& p, int n
   const cudaError_t e = ranks == 1 && pairs <= num_sms ? ev_select<1024>(p, ranks, stream) : ev_select<512>(p, ranks, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t mv{};
-  mv.gridDim = dim3(static_cast<unsigned>(pairs * ((p.keep + EV_ROWS - 1) / EV_ROWS)));
-  mv.blockDim = dim3(EV_MOVE_THREADS);
+  const long long units = pairs * ((p.keep + 15) / 16);
+  mv.gridDim = dim3(static_cast<unsigned>((units + EV_MOVE_WARPS - 1) / EV_MOVE_WARPS));
+  mv.blockDim = dim3(32 * EV_MOVE_WARPS);
   mv.stream = stream;
   cudaLaunchAttribute pd{};
   pd.id = cudaLaunchAttributeProgrammaticStreamSerialization;

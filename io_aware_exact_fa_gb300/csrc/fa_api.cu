@@ -1197,7 +1197,7 @@ fa_status fa_evict_paged(const float* weights, int64_t weights_stride, void* k_p
   const long long pairs = static_cast<long long>(B) * Hkv;
   if (pairs > 1 && (weights_stride < max_len || new_weights_stride < new_width))
     return fail(FA_ERR_INVALID_ARG, "weights_stride is below max_len or new_weights_stride below the new rows");
-  if (pairs * 8 > INT_MAX || pairs * ((static_cast<long long>(keep) + 127) / 128) > INT_MAX)
+  if (pairs * 8 > INT_MAX || pairs * ((static_cast<long long>(keep) + 15) / 16) > INT_MAX)
     return fail(FA_ERR_INVALID_ARG, "B, Hkv and keep give too many blocks");
 
   DeviceState* st = nullptr;
