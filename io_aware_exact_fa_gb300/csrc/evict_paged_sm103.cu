@@ -405,26 +405,30 @@ __global__ void __launch_bounds__(32 * EV_MOVE_WARPS) fa_evict_move_kernel(const
       ks[dst >> p.page_shift] = k_most;
       vs[dst >> p.page_shift] = v_most;
     }
+    // from here on: what the row's codes are multiplied with
+    k_old /= k_most;
+    v_old /= v_most;
   }
+  const unsigned live = __ballot_sync(ALL, src >= 0);
   const int piece = lane % CR, lr = lane / CR;
   auto load = [&](const uint8_t* pages, uint4 (&y)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const long long at = __shfl_sync(ALL, src, i * RPL + lr);
-      if (at >= 0) y[i] = *reinterpret_cast<const uint4*>(pages + at * RB + piece * 16);
+      // (a row that is not there: the pool's first, which is not stored)
+      const long long at = max(__shfl_sync(ALL, src, i * RPL + lr), 0ll);
+      y[i] = *reinterpret_cast<const uint4*>(pages + at * RB + piece * 16);
     }
   };
-  auto store = [&](uint8_t* pages, uint4 (&y)[N], [[maybe_unused]] float old, [[maybe_unused]] float most) {
+  auto store = [&](uint8_t* pages, uint4 (&y)[N], [[maybe_unused]] float factor) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int r = i * RPL + lr;
-      const long long at = __shfl_sync(ALL, src, r);
+      const bool there = (live >> r) & 1u;
       if constexpr (KIND == PAGES_E4M3) {
         // In f16: for powers of two exact down to 2^-24, far below half the least code (2^-10), so the one rounding is that
         // to e4m3; other ratios are off by 2^-11 of themselves. NaN codes stay NaN.
-        const float was = __shfl_sync(ALL, old, r);
-        if (at >= 0 && was != most) {
-          const float f = was / most;
+        const float f = __shfl_sync(ALL, factor, r);
+        if (there && f != 1.f) {
           const uint32_t f2 = pack_f16x2(f, f);
           uint32_t* w[4] = {&y[i].x, &y[i].y, &y[i].z, &y[i].w};
 #pragma unroll
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(32 * EV_MOVE_WARPS) fa_evict_move_kernel(const
           }
         }
       }
-      if (at >= 0) *reinterpret_cast<uint4*>(pages + (dst + r) * RB + piece * 16) = y[i];
+      if (there) *reinterpret_cast<uint4*>(pages + (dst + r) * RB + piece * 16) = y[i];
     }
   };
   uint4 yk[N], yv[N];
@@ -453,8 +457,8 @@ __global__ void __launch_bounds__(32 * EV_MOVE_WARPS) fa_evict_move_kernel(const
       *reinterpret_cast<uint32_t*>(vs + (dst + r) * SB + 4 * c) = y;
     }
   }
-  store(kp, yk, k_old, k_most);
-  store(vp, yv, v_old, v_most);
+  store(kp, yk, k_old);
+  store(vp, yv, v_old);
 }
 
 template <int THREADS>
