@@ -321,12 +321,12 @@ template <int D, int KIND>
 struct WmCfg {
   static constexpr int RB = paged_row_bytes(KIND, D);
   static constexpr int PPR = RB / 16;               // 16-byte pieces of a row, and of the tile that one thread takes
-  static constexpr int LPR = PPR < 4 ? PPR : 4;     // lanes side by side on a row
-  static constexpr int RW = 32 / LPR;               // rows of one load of a warp: 8 or 16
-  static constexpr int SETS = WM_TILE / (4 * RW);   // of them, a warp's
+  static constexpr int CP = D / PPR / 8;            // 8-element chunks of a piece: 1, 2 or 4
   static constexpr int BOX = WM_TILE * 128;         // 64 elements of every key, rows of 128 swizzled bytes
   static constexpr int K_BYTES = BOX * (D / 64);
-  static constexpr int CP = D / PPR / 8;            // 8-element chunks of a piece: 1, 2 or 4
+  static constexpr int LPR = 8 / CP;                // lanes side by side on a row: a box's pieces
+  static constexpr int RW = 32 / LPR;               // rows of one load of a warp: 4, 8 or 16
+  static constexpr int SETS = WM_TILE / (4 * RW);   // of them, a warp's
   static constexpr int CTAS = KIND == PAGES_BF16 && D == 128 ? 3 : 4;  // by registers
 };
 __host__ __device__ constexpr int wm_cols(int rows) { return (rows + 31) / 32 * 32; }       // query rows, padded
@@ -380,14 +380,11 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
   constexpr uint32_t DHI = sdesc_sw128_hi(1024);
   const uint32_t k_lo = sdesc_sw128_lo(smem_u32(s_k), 16), q_lo = sdesc_sw128_lo(smem_u32(s_q), 16);
   const uint32_t idesc = idesc_bf16_f32(WM_TILE, N, false) & (F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
-  // this thread's place in a load: row (of the warp's RW) and first piece
-  const int lr = (lane & 7) + 8 * ((lane >> 3) / C::LPR), lc = (lane >> 3) % C::LPR;
-  // and where its chunks go: element wm_at(row, 8 (CP piece + e)), taken apart. A piece's chunks stay within a box, and so do
-  // the first LPR pieces (or, 4-bit rows of d = 128, pairs of them).
-  uint8_t* const to = s_k + (C::RW / 8 * warp + lr / 8) * 1024 + (lane & 7) * 128 + lc * C::CP / 8 * C::BOX;
-  auto chunk_at = [&](int s, int y, int e) {
-    return to + s * (C::RW / 2) * 1024 + C::LPR * C::CP * y / 8 * C::BOX +
-           (((lc * C::CP % 8 + C::LPR * C::CP * y % 8 + e) ^ (lane & 7)) << 4);
+  // This thread's place in a load: row (of the warp's RW) and piece of a box. Eight lanes read 128 bytes of one to four
+  // neighbouring rows, and their chunks of one e lie in different banks: the rows' chunk numbers differ by the swizzle.
+  const int lr = lane / C::LPR, lc = lane % C::LPR, to = C::RW * warp + lr;
+  auto chunk_at = [&](int s, int y, int e) {  // element wm_at(row, 64 y + 8 (CP lc + e)), taken apart
+    return s_k + s * (C::RW * 4 * 128) + y * C::BOX + (to * 128 + (((lc * C::CP + e) ^ (to & 7)) << 4));
   };
   uint32_t issued = 0u;  // tiles whose products were started; the last of them is waited for before anything is reused
   bool ok = true;
