@@ -343,6 +343,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       FA_I8(r, 0), FA_I8(r, 8)
       : "memory");
 }
+// Warp-collective: 16 lanes of tensor memory (the address's and the next 15), 8 N columns. A thread's registers 4 i .. 4 i + 3 are
+// columns 8 i + 2 (lane % 4) and the next one of lane lane / 4, then the same of lane lane / 4 + 8.
+template <int N>
+__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t* r) {
+  static_assert(N == 4 || N == 8, "");
+  if constexpr (N == 4)
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        FA_I8(r, 0), FA_I8(r, 8)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        FA_I8(r, 0), FA_I8(r, 8), FA_I8(r, 16), FA_I8(r, 24)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "

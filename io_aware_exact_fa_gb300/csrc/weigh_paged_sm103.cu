@@ -314,27 +314,70 @@ __global__ void __launch_bounds__(WG_THREADS, NR == 1 ? WG_FEW_CTAS : 3) fa_weig
 }
 
 // ---- more rows: tensor-memory products, a tile of 128 keys on the lanes
-constexpr int WM_THREADS = 128;
+//   warps 0-3  put a tile into tensor memory as the products' operand (f16 where it is codes) and turn the scores of the one
+//              before into weights: a lane has one key and sums over the rows
+//   warp 4     copies the tiles' rows to shared memory and issues the products
+constexpr int WM_ROLE = 128;  // threads of the first four warps
+constexpr int WM_THREADS = WM_ROLE + 32;
 constexpr int WM_TILE = 128;
 
 template <int D, int KIND>
 struct WmCfg {
   static constexpr int RB = paged_row_bytes(KIND, D);
-  static constexpr int PPR = RB / 16;               // 16-byte pieces of a row, and of the tile that one thread takes
-  static constexpr int CP = D / PPR / 8;            // 8-element chunks of a piece: 1, 2 or 4
-  static constexpr int BOX = WM_TILE * 128;         // 64 elements of every key, rows of 128 swizzled bytes
-  static constexpr int K_BYTES = BOX * (D / 64);
-  static constexpr int LPR = 8 / CP;                // lanes side by side on a row: a box's pieces
-  static constexpr int RW = 32 / LPR;               // rows of one load of a warp: 4, 8 or 16
-  static constexpr int SETS = WM_TILE / (4 * RW);   // of them, a warp's
-  static constexpr int CTAS = KIND == PAGES_BF16 && D == 128 ? 3 : 4;  // by registers
+  static constexpr int ROWS = WM_TILE * RB;         // bytes of a tile's rows
+  static constexpr int SCALES = KIND == PAGES_FP4 ? WM_TILE * (D / 16) : 0;
+  static constexpr int STAGES = ROWS > 16384 ? 1 : 2;  // tiles in shared memory
+  static constexpr int CTAS = 4;                    // by registers, shared and tensor memory
 };
 __host__ __device__ constexpr int wm_cols(int rows) { return (rows + 31) / 32 * 32; }       // query rows, padded
-__host__ __device__ constexpr int wm_tmem(int cols) { return 2 * cols <= 64 ? 64 : 2 * cols <= 128 ? 128 : 256; }
+__host__ __device__ constexpr int wm_tmem(int d, int cols) {                                 // scores and operand
+  return d / 2 + cols <= 64 ? 64 : d / 2 + cols <= 128 ? 128 : 256;
+}
 
 // Byte of element e of row r in an operand of `rows` rows.
 __device__ __forceinline__ uint32_t wm_at(int rows, int r, int e) {
   return (e >> 6) * (rows * 128) + (r >> 3) * 1024 + (r & 7) * 128 + ((((e & 63) >> 3) ^ (r & 7)) << 4) + (e & 7) * 2;
+}
+// Where elements 4 u .. 4 u + 3 of a row stand in the products: wg_elem's inverse, 16 j + 4 tig.
+template <int D, int KIND>
+__device__ __forceinline__ int wm_place(int u) {
+  if constexpr (KIND == PAGES_FP4) return 16 * (u % (D / 16)) + 4 * (u / (D / 16));
+  constexpr int Q = KIND == PAGES_E4M3 ? 4 : 2;
+  return 16 * (u / (4 * Q) * Q + u % Q) + 4 * (u / Q % 4);
+}
+// Rows gid and gid + 8 of a 16-key group in shared memory: the lane's share of each. (Of rows of 128 bytes and more the odd ones
+// are read in another order, so that the eight lanes of two neighbours meet every bank once.)
+template <int D, int KIND>
+__device__ __forceinline__ void wm_read(WgRaw<D, KIND>& x, const uint8_t* rows, const uint8_t* scales, int gid, int tig) {
+  using C = WgCfg<D, KIND>;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint8_t* src = rows + (gid + 8 * h) * C::RB;
+    if constexpr (KIND == PAGES_FP4) {
+      const uint8_t* sp = scales + (gid + 8 * h) * (D / 16);
+      if constexpr (D == 128) {
+        const uint4 y = reinterpret_cast<const uint4*>(src)[tig];
+        x.w[h][0] = y.x, x.w[h][1] = y.y, x.w[h][2] = y.z, x.w[h][3] = y.w;
+        x.f[h] = reinterpret_cast<const uint16_t*>(sp)[tig];
+      } else {
+        const uint2 y = reinterpret_cast<const uint2*>(src)[tig];
+        x.w[h][0] = y.x, x.w[h][1] = y.y;
+        x.f[h] = sp[tig];
+      }
+    } else if constexpr (C::RB < 128) {
+      const uint4 y = reinterpret_cast<const uint4*>(src)[tig];
+      x.w[h][0] = y.x, x.w[h][1] = y.y, x.w[h][2] = y.z, x.w[h][3] = y.w;
+    } else {
+      const int flip = gid & 1;
+#pragma unroll
+      for (int i = 0; i < C::LW / 4; i += 2) {
+        const uint4 y = reinterpret_cast<const uint4*>(src)[tig + 4 * (i + flip)], z = reinterpret_cast<const uint4*>(src)[tig + 4 * (i + 1 - flip)];
+        const uint4 a = flip ? z : y, b = flip ? y : z;
+        x.w[h][4 * i] = a.x, x.w[h][4 * i + 1] = a.y, x.w[h][4 * i + 2] = a.z, x.w[h][4 * i + 3] = a.w;
+        x.w[h][4 * i + 4] = b.x, x.w[h][4 * i + 5] = b.y, x.w[h][4 * i + 6] = b.z, x.w[h][4 * i + 7] = b.w;
+      }
+    }
+  }
 }
 
 template <int D, int KIND>
@@ -344,13 +387,19 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
   extern __shared__ uint8_t wm_raw[];
   uint8_t* smem = wm_raw + ((1024u - (smem_u32(wm_raw) & 1023u)) & 1023u);
   const int N = wm_cols(p.R);
-  uint8_t* s_k = smem;
-  uint8_t* s_q = smem + C::K_BYTES;
-  float4* s_row = reinterpret_cast<float4*>(s_q + N * D * 2);  // of rows 2i, 2i + 1: factors, and the log-sum-exp's negatives
+  uint8_t* s_q = smem;
+  uint8_t* s_rows = s_q + N * D * 2;                           // [stage] a tile's rows as they are in the pool
+  uint8_t* s_scale = s_rows + C::STAGES * C::ROWS;             // [stage] 4-bit rows: their scales
+  float4* s_row = reinterpret_cast<float4*>(s_scale + C::STAGES * C::SCALES);  // of rows 2i, 2i + 1: factors, and the log-sum-exp's negatives
   int2* s_lim = reinterpret_cast<int2*>(s_row + N / 2);        // and the last key they see
-  uint64_t* done = reinterpret_cast<uint64_t*>(s_lim + N / 2); // a tile's products are in tensor memory
+  float* s_ka = reinterpret_cast<float*>(s_lim + N / 2);       // [4][8]: e4m3 scales of a tile's 16-key groups
+  unsigned* s_live = reinterpret_cast<unsigned*>(s_ka + 32);   // [4]: which of them are in pages of the pool
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_live + 4);    // [stage] a tile's rows are there
+  uint64_t* empty = full + C::STAGES;                          // [stage] and taken
+  uint64_t* ready = empty + C::STAGES;                         // its operand is written, and the scores before it read
+  uint64_t* done = ready + 1;                                  // its products are in tensor memory
   uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 1) + 1;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int range = static_cast<int>(blockIdx.x);
   bool clipped = false;
@@ -362,232 +411,245 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
   int todo = static_cast<int>(ranges.begin(range + 1) - t0);
   PagedTile at = paged_seek<WM_TILE>(p.seqlens, p.B, p.Hkv, p.max_len, t0, lane);
 
-  const uint32_t tmem_columns = wm_tmem(N);
+  const uint32_t tmem_columns = wm_tmem(D, N);
   if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, WM_ROLE);
+    }
+    mbar_init(ready, WM_ROLE);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0) {
+  if (warp == 4) {
     tmem_alloc(slot, tmem_columns);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *slot;
-  const uint32_t my_lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-  constexpr uint32_t DHI = sdesc_sw128_hi(1024);
-  const uint32_t k_lo = sdesc_sw128_lo(smem_u32(s_k), 16), q_lo = sdesc_sw128_lo(smem_u32(s_q), 16);
-  const uint32_t idesc = idesc_bf16_f32(WM_TILE, N, false) & (F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
-  // This thread's place in a load: row (of the warp's RW) and piece of a box. Eight lanes read 128 bytes of one to four
-  // neighbouring rows, and their chunks of one e lie in different banks: the rows' chunk numbers differ by the swizzle.
-  const int lr = lane / C::LPR, lc = lane % C::LPR, to = C::RW * warp + lr;
-  auto chunk_at = [&](int s, int y, int e) {  // element wm_at(row, 64 y + 8 (CP lc + e)), taken apart
-    return s_k + s * (C::RW * 4 * 128) + y * C::BOX + (to * 128 + (((lc * C::CP + e) ^ (to & 7)) << 4));
-  };
-  uint32_t issued = 0u;  // tiles whose products were started; the last of them is waited for before anything is reused
+  const uint32_t tmem = *slot, operand = tmem + N;
+  uint32_t c0 = 0u;                    // tiles before the segment: the barriers' phases run on
+  uint32_t copied = 0u, issued = 0u;   // (warp 4) tiles whose copies, and whose products, were started
   bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t turn) {  // one answer for the warp
+    ok = ok && __all_sync(ALL, mbar_wait(bar, turn & 1u, p.wait_limit_ns, p.status, abort_flag));
+    return ok;
+  };
 
-  while (todo > 0 && ok) {
+  while (todo > 0) {
     // ================================================================ one segment: tiles of (b, hk)
     const int b = at.b, hk = at.hk, L = at.L, i0 = at.i, n = todo < at.nt - at.i ? todo : at.nt - at.i;
-    auto page_of = [&](int t) -> int {  // of 16-key group `lane` of the segment's tile t
-      const int key = (i0 + t) * WM_TILE + 16 * lane;
-      return (lane < 8 && t < n && key < L) ? __ldg(p.table + b * p.table_stride + (key >> p.page_shift)) : -1;
-    };
-    uint4 raw[C::PPR];
-    uint32_t f[KIND == PAGES_FP4 ? C::PPR : 1];  // 4-bit rows: a piece's two scale bytes
-    // of the tile loaded last, the one before, and the one before that: groups in pages of the pool; e4m3: lane g holds the
-    // scale of group g (asked for with the rows, and handed out a tile later), then of this thread's key
-    unsigned live = 0u, live1 = 0u, live2 = 0u;
-    float scale = 1.f, ka1 = 1.f, ka2 = 1.f;
-    auto load = [&](int t, int id) {
-      const int key = (i0 + t) * WM_TILE + 16 * lane;
-      const bool want = lane < 8 && t < n && key < L;
-      const long long off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, key & (p.page - 1), 1) : -1;
-      if (__any_sync(ALL, want && off < 0) && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
-      live = __ballot_sync(ALL, off >= 0);
-      if constexpr (KIND == PAGES_E4M3)
-        scale = off >= 0 ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk) : 0.f;
-      // (rows that are not there: the last one of the group, or the pool's first, whose sums are not written)
-      const int rows = L - (i0 + t) * WM_TILE;
-#pragma unroll
-      for (int s = 0; s < C::SETS; ++s) {
-        const int r0 = C::RW * (4 * s + warp), r = r0 + lr, g = r0 / 16;
-        const long long base = __shfl_sync(ALL, off, g);
-        const long long row = base < 0 ? 0 : base + max(min(r, rows - 1) - 16 * g, 0);
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k) + row * C::RB);
-#pragma unroll
-        for (int y = 0; y < C::PPR / C::LPR; ++y) {
-          const int x = s * (C::PPR / C::LPR) + y;
-          raw[x] = __ldg(src + lc + C::LPR * y);
-          if constexpr (KIND == PAGES_FP4)
-            f[x] = __ldg(reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(p.k_scale) + row * (D / 16)) + lc + C::LPR * y);
-        }
-      }
-    };
-    load(0, page_of(0));
-    int id = page_of(1);
-    __syncthreads();  // the segment before is done with the queries' memory
-
-    // ---- the queries: a warp a row, a lane four of its elements, eight rows at a time
-    constexpr int QB = 8;
-    bool dead = false;  // a row adds nothing
-    for (int r0 = warp; r0 < N; r0 += 4 * QB) {  // (N is a multiple of 32)
-      uint2 x[QB];
-      float lse[QB];
-      int tok[QB];
-#pragma unroll
-      for (int i = 0; i < QB; ++i) {
-        const int r = r0 + 4 * i;
-        const bool in = r < p.R;
-        const int h = hk * p.G + (in ? r / p.Nq : 0);
-        tok[i] = in ? r % p.Nq : 0;
-        x[i] = in && lane < D / 4
-                   ? __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + b * p.qsb + h * p.qsh + tok[i] * p.qst) + lane)
-                   : make_uint2(0u, 0u);
-        lse[i] = in ? __ldg(p.lse + (static_cast<long long>(b) * p.H + h) * p.Nq + tok[i]) : -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < QB; ++i) {
-        const int r = r0 + 4 * i;
-        float up = 1.f;
-        if constexpr (F16) {
-          float amax = wg_amax(x[i]);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, o));
-          x[i] = wg_to_f16(x[i], wg_powers(amax, up));
-        }
-        if (lane < D / 4) *reinterpret_cast<uint2*>(s_q + wm_at(N, r, 4 * lane)) = x[i];
+    if (warp == 4) {
+      // ------------------------------------------------------------ copies and products: lane g has 16-key group g of a tile
+      auto page_of = [&](int t) -> int {
+        const int key = (i0 + t) * WM_TILE + 16 * lane;
+        return (lane < 8 && t < n && key < L) ? __ldg(p.table + b * p.table_stride + (key >> p.page_shift)) : -1;
+      };
+      auto scale_of = [&](int id) {
+        return KIND == PAGES_E4M3 && static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages)
+                   ? __ldg(static_cast<const float*>(p.k_scale) + static_cast<long long>(id) * p.Hkv + hk)
+                   : 0.f;
+      };
+      int id = page_of(0), id1 = page_of(1);
+      float scale = scale_of(id);
+      auto copy = [&](int t) {
+        const uint32_t c = c0 + t;
+        const uint32_t stage = c % C::STAGES;
+        if (c >= C::STAGES && !wait(empty + stage, c / C::STAGES - 1u)) return;
+        const int key = (i0 + t) * WM_TILE + 16 * lane;
+        const bool want = lane < 8 && key < L;
+        const long long off = want ? paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, key & (p.page - 1), 1) : -1;
+        const unsigned live = __ballot_sync(ALL, off >= 0);
+        if (__any_sync(ALL, want && off < 0) && lane == 0) atomicOr(p.status, FA_DEV_BAD_PAGE);
+        if (KIND == PAGES_E4M3 && lane < 8) s_ka[(c & 3u) * 8 + lane] = scale;
+        __syncwarp();
         if (lane == 0) {
-          const bool none = lse[i] == -INFINITY;
-          float* at2 = reinterpret_cast<float*>(s_row + r / 2) + (r & 1);
-          at2[0] = p.scale_log2 * up;
-          at2[2] = none ? 0.f : lse[i] * -1.4426950408889634f;
-          const int lim = none ? -1 : min(L - 1, L - p.Nq + tok[i]);
-          reinterpret_cast<int*>(s_lim + r / 2)[r & 1] = lim;
-          dead = dead || (lim < 0 && r < p.R);
+          s_live[c & 3u] = live;
+          mbar_arrive_expect_tx(full + stage, __popc(live) * (16 * C::RB + C::SCALES / 8));
         }
-      }
-    }
-
-    dead = __syncthreads_or(dead);
-
-    float* wrow = p.weights + (static_cast<long long>(b) * p.Hkv + hk) * p.wstride;
-    for (int t = 0; t <= n; ++t) {
-      // tile t - 1: this thread's key and what its weight was
-      const int tile = (i0 + t - 1) * WM_TILE, key = tile + tid;
-      live2 = live1, live1 = live, ka2 = ka1;
-      if constexpr (KIND == PAGES_E4M3) ka1 = __shfl_sync(ALL, scale, tid >> 4);
-      const bool writes = t > 0 && key < L && ((live2 >> (tid >> 4)) & 1u);
-      const float old = writes ? wrow[key] : 0.f;
-      if (t > 0) {
-        ok = mbar_wait(done, (issued - 1u) & 1u, p.wait_limit_ns, p.status, abort_flag);
+        __syncwarp();
+        // A page's groups side by side are one copy, by the lane of its first. (Whole groups: rows past the sequence's last are
+        // the page's own, and their sums are not written.)
+        const int first = key & (p.page - 1);
+        if (off >= 0 && first == 0) {
+          const int rows = 16 * __popc(live & ((p.page >= WM_TILE ? 0xffu : (1u << (p.page / 16)) - 1u) << lane));
+          bulk_load_1d(s_rows + stage * C::ROWS + lane * 16 * C::RB, static_cast<const uint8_t*>(p.k) + off * C::RB, rows * C::RB, full + stage);
+          if constexpr (KIND == PAGES_FP4)
+            bulk_load_1d(s_scale + stage * C::SCALES + lane * D, static_cast<const uint8_t*>(p.k_scale) + off * (D / 16), rows * (D / 16), full + stage);
+        }
+        copied = c + 1u;
+        id = id1;
+        scale = scale_of(id);
+        id1 = page_of(t + 2);
+      };
+      copy(0);
+      __syncthreads_or(0);  // the queries are there
+      if (C::STAGES > 1 && n > 1) copy(1);
+      constexpr uint32_t DHI = sdesc_sw128_hi(1024);
+      const uint32_t q_lo = sdesc_sw128_lo(smem_u32(s_q), 16);
+      const uint32_t idesc = idesc_bf16_f32(WM_TILE, N, false) & (F16 ? ~((1u << 7) | (1u << 10)) : ~0u);
+      for (int t = 0; t < n && ok; ++t) {
+        if (!wait(ready, c0 + t)) break;
         tc_fence_after();
-      }
-      if (t < n) {  // tile t becomes the products' operand (quarter warps write eight rows: every bank once)
-#pragma unroll
-        for (int s = 0; s < C::SETS; ++s) {
-#pragma unroll
-          for (int y = 0; y < C::PPR / C::LPR; ++y) {
-            const int x = s * (C::PPR / C::LPR) + y;
-            const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-            if constexpr (KIND == PAGES_FP4) {
-              const uint32_t f0 = fp4_scale2<0>(f[x]), f1 = fp4_scale2<1>(f[x]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t h[4];
-                e2m1x8_to_f16x2x4(w[e], h);
-                const uint32_t fe = e < 2 ? f0 : f1;
-                *reinterpret_cast<uint4*>(chunk_at(s, y, e)) =
-                    make_uint4(hmul2_bits(h[0], fe), hmul2_bits(h[1], fe), hmul2_bits(h[2], fe), hmul2_bits(h[3], fe));
-              }
-            } else if constexpr (KIND == PAGES_E4M3) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint4 h;
-                e4m3x4_to_f16x2x2(w[2 * e], h.x, h.y);
-                e4m3x4_to_f16x2x2(w[2 * e + 1], h.z, h.w);
-                *reinterpret_cast<uint4*>(chunk_at(s, y, e)) = h;
-              }
-            } else {
-              *reinterpret_cast<uint4*>(chunk_at(s, y, 0)) = raw[x];
-            }
-          }
-        }
-        fence_proxy_async_smem();  // the tensor core reads the operands through the async proxy
-      }
-      tc_fence_before();
-      ok = __syncthreads_and(ok);
-      if (!ok) break;
-      if (t < n) {
-        if (warp == 0) {
-          tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t ko = static_cast<uint32_t>((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4;
             const uint32_t qo = static_cast<uint32_t>((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4;
-            if (elect_one()) mma_ss_w(tmem + (t & 1) * N, k_lo + ko, DHI, q_lo + qo, DHI, idesc, kk > 0 ? 1u : 0u);
+            mma_ts_w(tmem, operand + 8 * kk, q_lo + qo, DHI, idesc, kk > 0 ? 1u : 0u);
           }
-          if (elect_one()) mma_commit(done);
-          __syncwarp();
+          mma_commit(done);
         }
-        ++issued;
+        __syncwarp();
+        issued = c0 + t + 1u;
+        if (t + C::STAGES < n) copy(t + C::STAGES);
       }
-      if (t + 1 < n) {
-        load(t + 1, id);
-        id = page_of(t + 2);
-      }
-      if (t == 0) continue;
-      // ---- tile t - 1: this lane's key against every row, two at a time
-      const bool plain = tile + WM_TILE <= L - p.Nq && !dead;  // every row sees every key
-      const uint64_t ka_2 = f2pack(ka2, ka2);
-      uint64_t acc = 0ull;
-      for (int c0 = 0; c0 < p.R; c0 += 32) {
-        uint32_t sv[32];
-        tmem_ld32(my_lanes + ((t - 1) & 1) * N + c0, sv);
-        tmem_ld_wait32(sv);
-        auto pairs = [&](auto masked) {
+    } else {
+      // ------------------------------------------------------------ the queries: a lane eight elements of a row
+      constexpr int QL = D / 8, QR = 32 / QL, QB = 4;  // lanes of a row, rows of a warp's load, loads at a time
+      for (int r0 = warp * QR; r0 < N; r0 += 4 * QR * QB) {
+        uint4 x[QB];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = c0 + 2 * i;
-            const float4 cl = s_row[c / 2];
-            uint64_t y = f2pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
-            if constexpr (KIND == PAGES_E4M3) y = fmul2(y, ka_2);
-            float y0, y1;
-            f2unpack(ffma2(y, f2pack(cl.x, cl.y), f2pack(cl.z, cl.w)), y0, y1);
-            y0 = ex2_approx(y0), y1 = ex2_approx(y1);
-            if constexpr (decltype(masked)::value) {
-              const int2 lim = s_lim[c / 2];
-              y0 = key <= lim.x ? y0 : 0.f;
-              y1 = key <= lim.y ? y1 : 0.f;
-            }
-            acc = fadd2(acc, f2pack(y0, y1));
+        for (int i = 0; i < QB; ++i) {
+          const int r = r0 + 4 * QR * i + lane / QL;
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < p.R)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + b * p.qsb + (hk * p.G + r / p.Nq) * p.qsh +
+                                                        r % p.Nq * p.qst) + lane % QL);
+        }
+#pragma unroll
+        for (int i = 0; i < QB; ++i) {
+          const int r = r0 + 4 * QR * i + lane / QL;
+          float up = 1.f;
+          if constexpr (F16) {
+            uint2 lo = make_uint2(x[i].x, x[i].y), hi = make_uint2(x[i].z, x[i].w);
+            float amax = fmaxf(wg_amax(lo), wg_amax(hi));
+#pragma unroll
+            for (int o = QL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(ALL, amax, o));
+            const float down = wg_powers(amax, up);
+            lo = wg_to_f16(lo, down), hi = wg_to_f16(hi, down);
+            x[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
           }
-        };
-        if (plain && c0 + 32 <= p.R) pairs(std::false_type{});
-        else pairs(std::true_type{});  // (padding rows see no key)
+          if (r < N) {
+            *reinterpret_cast<uint2*>(s_q + wm_at(N, r, wm_place<D, KIND>(2 * (lane % QL)))) = make_uint2(x[i].x, x[i].y);
+            *reinterpret_cast<uint2*>(s_q + wm_at(N, r, wm_place<D, KIND>(2 * (lane % QL) + 1))) = make_uint2(x[i].z, x[i].w);
+            if (lane % QL == 0) reinterpret_cast<float*>(s_row + r / 2)[r & 1] = p.scale_log2 * up;
+          }
+        }
       }
-      float a0, a1;
-      f2unpack(acc, a0, a1);
-      if (writes) wrow[key] = old + (a0 + a1);
+      bool dead = false;  // a row adds nothing
+      if (tid < N) {
+        const bool in = tid < p.R;
+        const int h = hk * p.G + (in ? tid / p.Nq : 0), tok = in ? tid % p.Nq : 0;
+        const float lse = in ? __ldg(p.lse + (static_cast<long long>(b) * p.H + h) * p.Nq + tok) : -INFINITY;
+        const bool none = lse == -INFINITY;
+        const int lim = none ? -1 : min(L - 1, L - p.Nq + tok);
+        reinterpret_cast<float*>(s_row + tid / 2)[2 + (tid & 1)] = none ? 0.f : lse * -1.4426950408889634f;
+        reinterpret_cast<int*>(s_lim + tid / 2)[tid & 1] = lim;
+        dead = lim < 0 && in;
+      }
+      fence_proxy_async_smem();  // the tensor core reads the queries through the async proxy
+      dead = __syncthreads_or(dead);
+
+      // ------------------------------------------------------------ tiles
+      const uint32_t my_lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+      float* wrow = p.weights + (static_cast<long long>(b) * p.Hkv + hk) * p.wstride;
+      bool writes_next = false;
+      float old_next = 0.f, ka_next = 1.f;
+      for (int t = 0; t <= n; ++t) {
+        if (t > 0) {
+          if (!wait(done, c0 + t - 1u)) break;
+          tc_fence_after();
+        }
+        const bool writes = writes_next;
+        const float old = old_next, ka = ka_next;
+        if (t < n) {  // tile t becomes the products' operand
+          const uint32_t c = c0 + t, stage = c % C::STAGES;
+          if (!wait(full + stage, c / C::STAGES)) break;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            WgRaw<D, KIND> x;
+            wm_read<D, KIND>(x, s_rows + stage * C::ROWS + (2 * warp + g) * 16 * C::RB, s_scale + stage * C::SCALES + (2 * warp + g) * D,
+                             lane >> 2, lane & 3);
+            uint32_t a[D / 4];
+            wg_fragments<D, KIND>(x, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+              a[4 * j] = a0, a[4 * j + 1] = a2, a[4 * j + 2] = a1, a[4 * j + 3] = a3;
+            });
+            tmem_st_rows<D / 16>(operand + (static_cast<uint32_t>(32 * warp + 16 * g) << 16), a);
+          }
+          mbar_arrive(empty + stage);
+          tmem_st_wait();
+          // this thread's key, for the next turn: whether it is there, what its weight was, its scale
+          const uint32_t at4 = c & 3u;
+          const int next = (i0 + t) * WM_TILE + tid;
+          writes_next = next < L && ((s_live[at4] >> (tid >> 4)) & 1u);
+          old_next = writes_next ? wrow[next] : 0.f;
+          if constexpr (KIND == PAGES_E4M3) ka_next = s_ka[at4 * 8 + (tid >> 4)];
+          if (t == 0) {
+            tc_fence_before();
+            mbar_arrive(ready);
+            continue;
+          }
+        }
+        const int tile = (i0 + t - 1) * WM_TILE, key = tile + tid;
+        // ---- tile t - 1: this lane's key against every row, two at a time
+        const bool plain = tile + WM_TILE <= L - p.Nq && !dead;  // every row sees every key
+        const uint64_t ka_2 = f2pack(ka, ka);
+        uint64_t acc = 0ull;
+        for (int col = 0; col < p.R; col += 32) {
+          uint32_t sv[32];
+          tmem_ld32(my_lanes + col, sv);
+          tmem_ld_wait32(sv);
+          if (t < n && col + 32 >= p.R) {  // the last of them: the next products may begin
+            tc_fence_before();
+            mbar_arrive(ready);
+          }
+          auto pairs = [&](auto masked) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float4 cl = s_row[col / 2 + i];
+              uint64_t y = f2pack(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+              if constexpr (KIND == PAGES_E4M3) y = fmul2(y, ka_2);
+              float y0, y1;
+              f2unpack(ffma2(y, f2pack(cl.x, cl.y), f2pack(cl.z, cl.w)), y0, y1);
+              y0 = ex2_approx(y0), y1 = ex2_approx(y1);
+              if constexpr (decltype(masked)::value) {
+                const int2 lim = s_lim[col / 2 + i];
+                y0 = key <= lim.x ? y0 : 0.f;
+                y1 = key <= lim.y ? y1 : 0.f;
+              }
+              acc = fadd2(acc, f2pack(y0, y1));
+            }
+          };
+          if (plain && col + 32 <= p.R) pairs(std::false_type{});
+          else pairs(std::true_type{});  // (padding rows see no key)
+        }
+        float a0, a1;
+        f2unpack(acc, a0, a1);
+        if (writes) wrow[key] = old + (a0 + a1);
+      }
+      tc_fence_before();
     }
+    c0 += n;
     todo -= n;
+    ok = __syncthreads_and(ok);  // the segment is done with the queries' memory
+    if (!ok) break;
     if (todo > 0) {
       at.i = at.nt - 1;
       paged_next<WM_TILE>(at, p.seqlens, p.B, p.Hkv, p.max_len);
     }
   }
-  // (a wait that gave up: the products in flight end before their memory is given back)
-  if (!ok && issued > 0u) {
-    const uint64_t t1 = globaltimer_ns();
-    for (uint32_t i = 0; !mbar_try_wait(smem_u32(done), (issued - 1u) & 1u); ++i)
-      if ((i & 31u) == 31u && globaltimer_ns() - t1 > p.wait_limit_ns) break;
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0) {
+  if (warp == 4) {
+    // (a wait that gave up: copies and products in flight get the limit's time once more before their memory is given back)
+    if (!ok) {
+      const uint64_t t1 = globaltimer_ns();
+      auto ended = [&](uint64_t* bar, uint32_t turns) { return turns == 0u || mbar_try_wait(smem_u32(bar), (turns - 1u) & 1u); };
+      for (uint32_t i = 0; !(ended(full, (copied + C::STAGES - 1) / C::STAGES) && ended(full + C::STAGES - 1, copied / C::STAGES) &&
+                             ended(done, issued)); ++i)
+        if ((i & 31u) == 31u && globaltimer_ns() - t1 > p.wait_limit_ns) break;
+    }
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, tmem_columns);
   }
@@ -595,10 +657,11 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
 
 template <int D, int KIND>
 static int wm_smem(int cols) {
-  // operands, row arrays, barrier and flags, alignment; and no more blocks on an SM than its tensor memory holds
-  const int need = WmCfg<D, KIND>::K_BYTES + cols * D * 2 + cols * 12 + 32 + 1024;
-  const int ctas = 512 / wm_tmem(cols);
-  const int most = ctas >= WmCfg<D, KIND>::CTAS ? 0 : 228 * 1024 / (ctas + 1);
+  // queries, rows and scales, row arrays, barriers and flags, alignment; and no more blocks on an SM than its tensor memory holds
+  using C = WmCfg<D, KIND>;
+  const int need = cols * D * 2 + C::STAGES * (C::ROWS + C::SCALES) + cols * 12 + 128 + 16 + (2 * C::STAGES + 2) * 8 + 16 + 1024;
+  const int ctas = 512 / wm_tmem(D, cols);
+  const int most = ctas >= C::CTAS ? 0 : 228 * 1024 / (ctas + 1);
   return need > most ? need : most;
 }
 template <int KIND>
@@ -626,7 +689,7 @@ template <int D, int KIND>
 static cudaError_t wg_launch(WeighPagedParams p, int num_sms, cudaStream_t stream) {
   if (p.R <= 8) return wg_launch_few<D, KIND, 1>(p, num_sms, stream);
   if (p.R <= 16) return wg_launch_few<D, KIND, 2>(p, num_sms, stream);
-  const int cols = wm_cols(p.R), ctas = 512 / wm_tmem(cols);
+  const int cols = wm_cols(p.R), ctas = 512 / wm_tmem(D, cols);
   p.n_ranges = num_sms * (ctas < WmCfg<D, KIND>::CTAS ? ctas : WmCfg<D, KIND>::CTAS);
   fa_weigh_paged_many_kernel<D, KIND><<<p.n_ranges, WM_THREADS, wm_smem<D, KIND>(cols), stream>>>(p);
   return cudaGetLastError();
