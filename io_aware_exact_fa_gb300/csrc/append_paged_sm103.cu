@@ -6,7 +6,7 @@
 //     (a, b) -> (a cos - b sin, b cos + a sin),  angle 2 pi frac(p t_j / 2^64)
 // on the pairs j of its first `rot` elements: (j, j + rot / 2), or (2j, 2j + 1)
 // interleaved. q' and k' are written out in bf16; k' and v go to the row of
-// position p in the cache, in bf16 or as e4m3 codes.
+// position p in the cache, in bf16, as e4m3 or as 4-bit codes.
 //
 // The frequency t_j is a fraction of a turn in 64-bit fixed point, so p t_j mod
 // 2^64 is the exact angle, in turns, for any position: one integer product in
@@ -19,6 +19,11 @@
 // scale grow, dividing the codes already held by a power of two rounds again
 // only where they fall below the smallest normal code. The values are rounded
 // once, from the fp32 result, not through bf16.
+//
+// 4-bit pages hold e2m1 codes and, for every 16 neighbours of a row, one byte of scale:
+// amax / 6, rounded to three mantissa bits. Rows do not depend on one another there; the
+// keys are rounded from the bf16 value that k_out gets, so the cache and a prompt's own
+// attention see the same keys.
 //
 // Two kinds of blocks in one launch. A K/V block takes the new rows of one page of
 // one sequence and one K/V head: those rows are all that the page's scales depend
@@ -33,7 +38,7 @@
 // arithmetic; with one kind of block for both 147 us in place of 132), launch and
 // load latency for a step of single tokens. Measured, 32 query and 8 K/V heads,
 // d = 128, e4m3: 26.7k prompt tokens with norms 115 us (5.7 TB/s, 0.85 of the copy
-// rate); 256 sequences of one token 8.1 us.
+// rate); 256 sequences of one token 8.1 us; 4-bit: 26k prompt tokens 114 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
