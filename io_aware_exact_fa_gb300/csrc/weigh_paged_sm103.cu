@@ -651,13 +651,13 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
     }
   }
   if (warp == 4) {
-    // (a wait that gave up: copies and products in flight get the limit's time once more before their memory is given back)
+    // (a wait that gave up: copies and products in flight get the limit's time, or a second, before their memory is given back)
     if (!ok) {
       const uint64_t t1 = globaltimer_ns();
       auto ended = [&](uint64_t* bar, uint32_t turns) { return turns == 0u || mbar_try_wait(smem_u32(bar), (turns - 1u) & 1u); };
       for (uint32_t i = 0; !(ended(full, (copied + C::STAGES - 1) / C::STAGES) && ended(full + C::STAGES - 1, copied / C::STAGES) &&
                              ended(done, issued)); ++i)
-        if ((i & 31u) == 31u && globaltimer_ns() - t1 > p.wait_limit_ns) break;
+        if ((i & 31u) == 31u && globaltimer_ns() - t1 > (p.wait_limit_ns > 1000000000ull ? p.wait_limit_ns : 1000000000ull)) break;
     }
     __syncwarp();
     tc_fence_after();

@@ -1,0 +1,250 @@
+"""The paged operators over batches that give every block or warp several tiles and sequences, against fp64 on the GPU, and
+the ways to call them: with and without the compiled argument checks, on two streams at once, from two graphs.
+
+The tolerance of a weight is that of test_evict_gpu: what it derives holds for any length.
+"""
+
+import math
+
+import pytest
+import torch
+
+from test_paged_gpu import cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from io_aware_exact_fa_gb300 import build
+    build.build()
+    from io_aware_exact_fa_gb300 import fa as lib
+    return lib
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def random_pool(kind, n, Hkv, page, d, g):
+    """Pages and scales of k and v (None for bf16), drawn on the GPU; no codes of NaN, scales powers of two for e4m3."""
+    out = []
+    for _ in range(2):
+        if kind == "bf16":
+            out += [torch.randn(n, Hkv, page, d, device="cuda", generator=g).to(torch.bfloat16), None]
+        elif kind == "e4m3":
+            codes = torch.randn(n, Hkv, page, d, device="cuda", generator=g).mul(60).to(torch.float8_e4m3fn)
+            out += [codes, 2.0 ** torch.randint(-7, -4, (n, Hkv), device="cuda", generator=g).float()]
+        else:
+            # scales of 2^-3 to 2^1: bytes of f16's upper half
+            out += [torch.randint(0, 256, (n, Hkv, page, d // 2), device="cuda", generator=g, dtype=torch.uint8),
+                    torch.randint(48, 64, (n, Hkv, page, d // 16), device="cuda", generator=g, dtype=torch.uint8)]
+    return out
+
+
+def batch(lens, page, g, spare=1):
+    """A table over shuffled pages, and how many pages the pool needs."""
+    count = [(L + page - 1) // page for L in lens]
+    n = sum(count) + spare
+    order = torch.randperm(n, device="cuda", generator=g).int()
+    table = torch.full((len(lens), max(count) + 1), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, c in enumerate(count):
+        table[b, :c] = order[at:at + c]
+        at += c
+    return table, n
+
+
+def packed_keys(fa, kp, vp, ks, vs, table, lens):
+    """Every sequence's keys in fp64 [L, Hkv, d]: reading back is exact here (bf16 holds every value)."""
+    cu = torch.tensor([0] + lens).cumsum(0).int().cuda()
+    k, _ = fa.read_paged(kp, vp, table, cuda(lens, torch.int32), cu, sum(lens), k_scale=ks, v_scale=vs)
+    return [x.double() for x in k.split(lens)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp4"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,Nq,page,many", [(4, 1, 16, False), (5, 3, 64, True), (3, 7, 128, False), (7, 5, 32, True), (4, 16, 64, False),
+                                           (9, 11, 16, True), (8, 16, 64, False)])
+def test_weigh_over_long_ranges(fa, G, Nq, page, many, d, kind):
+    """Ranges of several tiles, and of several short sequences, at 4 to 128 rows a K/V head; rows with lse = -inf among them,
+    one page that is not there."""
+    g = gen(G * Nq + d)
+    r = torch.Generator().manual_seed(G + Nq)
+    lens = ([int(x) for x in torch.randint(0, 400, (700,), generator=r)] if many
+            else [int(x) for x in torch.randint(3000, 30001, (12,), generator=r)] + [0, 1, 127, 129])
+    Hkv, H, B, scale = 2, 2 * G, len(lens), 1 / math.sqrt(d)
+    table, n = batch(lens, page, g)
+    kp, ks, vp, vs = random_pool(kind, n, Hkv, page, d, g)
+    rows = packed_keys(fa, kp, vp, ks, vs, table, lens)
+    q = torch.randn(B, Nq, H, d, device="cuda", generator=g).to(torch.bfloat16).transpose(1, 2)
+    # (any lse will do: weights are what the formula gives)
+    lse = 6 + torch.rand(B, H, Nq, device="cuda", generator=g)
+    lse[torch.rand(B, H, Nq, device="cuda", generator=g) < 0.05] = -math.inf
+    gone = (B // 2, 1)  # a sequence and page that the table does not name
+    if lens[gone[0]] > page:
+        table[gone] = n + 3
+    W = max(lens) + 3
+    base = torch.rand(B, Hkv, W, device="cuda", generator=g)
+    w = base.clone()
+    assert fa.weigh_paged(q, lse, kp, table, cuda(lens, torch.int32), w, k_scale=ks) is w
+    assert fa.device_status() == (fa.FA_ERR_INVALID_ARG if lens[gone[0]] > page else fa.FA_OK)
+    for b, L in enumerate(lens):
+        assert torch.equal(w[b, :, L:], base[b, :, L:])
+        if L == 0:
+            continue
+        x = q[b].double().reshape(Hkv, G * Nq, d)
+        k = rows[b].transpose(0, 1)                                  # [Hkv, L, d]
+        l = lse[b].double().reshape(Hkv, G * Nq, 1)
+        dead = l == -math.inf
+        j, t = torch.arange(L, device="cuda"), torch.arange(Nq, device="cuda").repeat(G)
+        sees = (j <= (L - Nq + t)[:, None]) & ~dead
+        l = l.masked_fill(dead, 0.0)
+        size = scale * x.abs() @ k.abs().transpose(1, 2)
+        off = size * (d / 16 + 4) * 2.0 ** -22 + scale * x.abs().amax(-1, keepdim=True) * k.abs().sum(-1)[:, None] * 2.0 ** -25
+        rel = (off + 3 * 2.0 ** -24 * (size + l.abs())).masked_fill(~sees, 0).amax(1)
+        add = torch.exp(scale * x @ k.transpose(1, 2) - l).masked_fill(~sees, 0).sum(1)
+        if b == gone[0]:
+            add[:, page:2 * page] = 0
+        want = base[b, :, :L].double() + add
+        bound = add * (torch.expm1(rel) + 2.0 ** -22 + 128 * 2.0 ** -24) + want.abs() * 2.0 ** -24 + 1e-37
+        assert ((w[b, :, :L] - want).abs() <= bound).all(), b
+
+
+def state(fa, kind, seed):
+    """One set of arguments for every operator."""
+    g = gen(seed)
+    lens, Hkv, H, d, page, Nq = [90, 300, 41], 2, 8, 128, 16, 2
+    table, n = batch(lens, page, g, spare=20)
+    kp, ks, vp, vs = random_pool(kind, n, Hkv, page, d, g)
+    free = sorted(set(range(n)) - set(table.flatten().tolist()))
+    new = torch.tensor(free[:12], dtype=torch.int32, device="cuda").view(3, 4)
+    q = torch.randn(3, H, Nq, d, device="cuda", generator=g).to(torch.bfloat16)
+    k, v = (torch.randn(3 * Nq, Hkv, d, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    big = torch.rand(3, Hkv, 330, device="cuda", generator=g)
+    return dict(kp=kp, vp=vp, ks=ks, vs=vs, table=table, lens=cuda(lens, torch.int32), new=new, q=q, k=k, v=v, w=big[:, :, 7:320],
+                cu=cuda([0, 90, 390, 431], torch.int32), turns=fa.rotary_turns(d, 10000.0), lse=5 + torch.rand(3, H, Nq, device="cuda", generator=g),
+                ws=torch.empty(fa.decode_paged_fp4_workspace_size(3, H, Hkv, Nq, d, int(table.shape[1]) * page), dtype=torch.uint8, device="cuda"),
+                qt=torch.randn(3 * Nq, H, d, device="cuda", generator=g).to(torch.bfloat16), norm=torch.rand(d, device="cuda", generator=g).to(torch.bfloat16))
+
+
+def every_call(fa, s, kind):
+    """All the operators that take pages of this kind, one after another; their results and what they wrote."""
+    out = []
+    if kind == "fp4":
+        off = cuda([3, 0, 1000], torch.int32)
+        out += fa.append_paged_fp4(s["qt"], s["k"], s["v"], s["kp"], s["vp"], s["ks"], s["vs"], s["table"], s["lens"], turns=s["turns"],
+                                   q_weight=s["norm"], k_weight=s["norm"], offsets=off)
+        out += [x for x in fa.append_paged_fp4(s["qt"], s["k"], s["v"], s["kp"], s["vp"], s["ks"], s["vs"], s["table"], s["lens"],
+                                               with_k=False) if x is not None]
+        out += fa.decode_paged_fp4(s["q"], s["kp"], s["vp"], s["ks"], s["vs"], s["table"], s["lens"], workspace=s["ws"])
+        o = torch.zeros_like(s["q"].transpose(1, 2).contiguous()).transpose(1, 2)
+        out += [x for x in fa.decode_paged_fp4(s["q"], s["kp"], s["vp"], s["ks"], s["vs"], s["table"], s["lens"], scale=1, max_len=250,
+                                               out=o, with_lse=False) if x is not None]
+        assert fa.device_status() == fa.FA_ERR_INVALID_ARG  # (a length was clipped)
+    out += fa.read_paged(s["kp"], s["vp"], s["table"], s["lens"], s["cu"], 431, k_scale=s["ks"], v_scale=s["vs"])
+    out.append(fa.weigh_paged(s["q"], s["lse"], s["kp"], s["table"], s["lens"], s["w"], k_scale=s["ks"]))
+    out.append(fa.weigh_paged(s["q"], s["lse"], s["kp"], s["table"], s["lens"], s["w"], k_scale=s["ks"], scale=-1, max_len=313))
+    out += fa.evict_paged(s["w"], s["kp"], s["vp"], s["table"], s["lens"], s["new"], 64, first=3, recent=20, k_scale=s["ks"], v_scale=s["vs"])
+    out += [s[x] for x in ("kp", "vp", "ks", "vs") if s[x] is not None]
+    return [x.clone() for x in out]
+
+
+def same(a, b):
+    assert len(a) == len(b)
+    for x, y in zip(a, b):
+        assert x.dtype == y.dtype and x.shape == y.shape and torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp4"])
+def test_both_ways_of_checking_arguments(fa, kind, monkeypatch):
+    """The compiled checks and the Python ones make the same call."""
+    fast = every_call(fa, state(fa, kind, 1), kind)
+
+    class Off:
+        def __getattr__(self, name):
+            return lambda *a: NotImplemented
+
+    monkeypatch.setattr(fa, "_binding", Off())
+    slow = every_call(fa, state(fa, kind, 1), kind)
+    same(fast, slow)
+    assert fa.device_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp4"])
+def test_two_streams_at_once(fa, kind):
+    """Two programs on two streams, each with its own cache, interleaved: as each alone; also with the stream as an argument."""
+    want = [every_call(fa, state(fa, kind, seed), kind) for seed in (2, 3)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        states = [state(fa, kind, seed) for seed in (2, 3)]
+        torch.cuda.synchronize()
+        got = []
+        for st, s in zip(streams, states):
+            with torch.cuda.stream(st):
+                got.append(every_call(fa, s, kind) if kind != "fp4" else None)
+        if kind == "fp4":  # (one after another on the host: the status is read between the calls)
+            for i, st in enumerate(streams):
+                with torch.cuda.stream(st):
+                    got[i] = every_call(fa, states[i], kind)
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            same(a, b)
+    s = state(fa, kind, 2)
+    torch.cuda.synchronize()
+    a = s["w"].clone()
+    b = s["w"].clone()
+    torch.cuda.synchronize()
+    fa.weigh_paged(s["q"], s["lse"], s["kp"], s["table"], s["lens"], a, k_scale=s["ks"], stream=streams[0])
+    fa.weigh_paged(s["q"], s["lse"], s["kp"], s["table"], s["lens"], b, k_scale=s["ks"])
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
+def test_two_graphs_with_workspaces_of_their_own(fa):
+    """Decodes and weights captured twice and replayed in turn on two streams, with lengths changed between replays."""
+    states = [state(fa, "fp4", seed) for seed in (4, 5)]
+    graphs, outs = [], []
+    for s in states:
+        s["w"].zero_()
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            o, lse = fa.decode_paged_fp4(s["q"], s["kp"], s["vp"], s["ks"], s["vs"], s["table"], s["lens"], workspace=s["ws"])
+            fa.weigh_paged(s["q"], lse, s["kp"], s["table"], s["lens"], s["w"], k_scale=s["ks"])
+        graphs.append(g)
+        outs.append((o, lse))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for lens in ([90, 300, 41], [2, 17, 0], [90, 1, 33]):
+        for s in states:
+            s["lens"].copy_(cuda(lens, torch.int32))
+            s["w"].zero_()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for s, (o, lse) in zip(states, outs):
+            want, wl = fa.decode_paged_fp4(s["q"], s["kp"], s["vp"], s["ks"], s["vs"], s["table"], s["lens"])
+            w = torch.zeros_like(s["w"])
+            for _ in range(4):
+                fa.weigh_paged(s["q"], wl, s["kp"], s["table"], s["lens"], w, k_scale=s["ks"])
+            assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(s["w"], w)
+    assert fa.device_status() == fa.FA_OK
+
+
+def test_keep_past_every_length(fa):
+    """A budget that no sequence reaches: all rows move, the rest of kept is -1 and of the new weights 0."""
+    s = state(fa, "bf16", 6)
+    s["lens"].copy_(cuda([5, 64, 0], torch.int32))
+    kept, nl, nw, no = fa.evict_paged(s["w"], s["kp"], s["vp"], s["table"], s["lens"], s["new"], 5000, first=70, recent=900, max_len=64)
+    assert fa.device_status() == fa.FA_OK and nl.tolist() == [5, 64, 0] and no.tolist() == [0, 0, 0]
+    for b, L in enumerate([5, 64, 0]):
+        assert (kept[b, :, :L] == torch.arange(L, device="cuda")).all() and (kept[b, :, L:] == -1).all()
+        assert torch.equal(nw[b, :, :L], s["w"][b, :, :L]) and (nw[b, :, L:] == 0).all()
+        for i in range(0, L, 16):
+            m = min(16, L - i)
+            assert torch.equal(s["kp"][s["new"][b, i // 16], :, :m], s["kp"][s["table"][b, i // 16], :, :m])
