@@ -1,4 +1,5 @@
-"""Build libfa_gb300.so in-tree with nvcc for sm_103a, and the binding's C part _binding.so (no cmake, no torch).
+"""Build libfa_gb300.so in-tree with nvcc for sm_103a (no cmake, no torch), and the binding's compiled part _binding.so with
+g++ against the installed torch's headers.
 
     python -m io_aware_exact_fa_gb300.build [--verbose] [--ptxas-info] [--debug]
 
@@ -13,6 +14,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -26,7 +28,8 @@ BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa_gb300.so")
 LIB_DEBUG = os.path.join(PKG, "libfa_gb300_debug.so")
-BINDING = os.path.join(PKG, "_binding.so")   # argument checks of the paged calls, in C
+BINDING = os.path.join(PKG, "_binding.so")   # argument checks of the paged calls
+BINDING_STAMP = os.path.join(BUILD, "binding.torch")   # the torch that it was built against
 SOURCES = ["fa_api.cu", "prefill_sm103.cu", "decode_sm103.cu", "backward_sm103.cu", "decode_grouped_sm103.cu",
            "materialized_sm103.cu", "append_paged_sm103.cu", "decode_paged_sm103.cu",
            "read_paged_sm103.cu", "weigh_paged_sm103.cu", "evict_paged_sm103.cu"]
@@ -55,25 +58,34 @@ def up_to_date(lib: str = LIB) -> bool:
 
 
 def _build_binding(force: bool) -> None:
-    if not force and up_to_date(BINDING):
-        return
+    torch = os.path.realpath(list(importlib.util.find_spec("torch").submodule_search_locations)[0])
+    with open(os.path.join(torch, "version.py")) as f:
+        built_with = torch + "\n" + sys.version + "\n" + f.read()
+    if not force and up_to_date(BINDING) and os.path.exists(BINDING_STAMP):
+        with open(BINDING_STAMP) as f:
+            if f.read() == built_with:
+                return
+    os.makedirs(BUILD, exist_ok=True)
     tmp = BINDING + ".tmp"
-    cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-std=c11", "-shared", "-fPIC", "-I", INCLUDE, "-I",
-           sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.c"), "-o", tmp, "-lm"]
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE, "-I",
+           os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-        raise RuntimeError("the C compiler failed on binding.c")
+        raise RuntimeError("the C++ compiler failed on binding.cpp")
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(built_with)
 
 
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False, debug: bool = False) -> str:
     """Compile and link the library (the checking build with debug=True); returns its path."""
     lib = LIB_DEBUG if debug else LIB
     bdir = BUILD + "_debug" if debug else BUILD
-    if not debug:
-        _build_binding(force)
+    binding = lambda: None if debug else _build_binding(force)   # noqa: E731
     if not force and not ptxas_info and up_to_date(lib):
+        binding()
         return lib
     os.makedirs(bdir, exist_ok=True)
     cc = nvcc()
@@ -89,13 +101,15 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False, 
         return src, obj, cmd, r
 
     objs = []
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bound = ex.submit(binding)
         for src, obj, cmd, r in ex.map(compile_one, SOURCES):
             if verbose or ptxas_info or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
                 raise RuntimeError(f"nvcc failed on {src}")
             objs.append(obj)
+        bound.result()
     tmp = lib + ".tmp"
     # cuBLAS (the materialising baseline's GEMMs) is opened at run time with dlopen, not linked
     cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static", "-ldl"]

@@ -25,7 +25,7 @@ if not os.path.exists(LIB_PATH):
 try:
     from . import _binding
 except ImportError as e:
-    raise ImportError(f"{os.path.join(_HERE, '_binding.so')} is missing or of another Python: build it with "
+    raise ImportError(f"{os.path.join(_HERE, '_binding.so')} is missing or of another Python or torch: build it with "
                       "`python -m io_aware_exact_fa_gb300.build`") from e
 
 _lib = ctypes.CDLL(LIB_PATH)
@@ -619,9 +619,9 @@ PAGES_BF16, PAGES_E4M3, PAGES_FP4 = range(3)
 _U8 = torch.uint8
 _FP4 = getattr(torch, "float4_e2m1fn_x2", torch.uint8)   # (two codes a byte)
 
-# The calls below go through _binding first, which makes the same checks in C and leaves to this module whatever does not
+# The calls below go through _binding first, which makes the same checks in C++ and leaves to this module whatever does not
 # pass them (or comes on another stream): half the host's time of a small step.
-_binding.setup((torch.Tensor, _BF16, _F32, _I32, torch.int64, _U8, _CODES, _FP4), (_raw_stream, _current_device, _empty_here),
+_binding.setup((_raw_stream, _current_device),
                tuple(ctypes.cast(getattr(_lib, n), _vp).value for n in (
                    "fa_append_paged_fp4", "fa_decode_paged_fp4", "fa_read_paged", "fa_weigh_paged", "fa_evict_paged")))
 
