@@ -20,7 +20,7 @@
 // rows: also the scale bytes) a lane; no warp waits for another. A new e4m3 page's
 // scale is the largest of its rows' old ones, which each warp of the page finds for
 // itself, and codes whose scale grew are rounded again. (For those 32 sequences, 4001 rows
-// kept, e4m3, and for 2 of 90-131k, 32768 kept, 4-bit, both launches take 130 and 123 us;
+// kept, e4m3, and for 2 of 90-131k, 32768 kept, 4-bit (then read back), a call takes 130-135 and 123 us;
 // with 32 rows a warp, 106 registers, 162 and 126; with blocks of 128 rows that meet at
 // barriers 130 and 127.)
 // What bounds it: HBM, the weights read and the kept rows read and written; for one
@@ -304,42 +304,28 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) fa_evict_select
     __syncthreads();
     cluster.barrier_arrive();  // (waited for at the end: the totals are read before a block leaves)
   }
-  // ---- indices and weights of the warp's run, in order
-#pragma unroll 2
-  for (int j0 = run0; j0 < run1; j0 += 128) {
-    const int j = j0 + 4 * lane;
-    uint32_t k[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu}, over = 0u, tied = 0u;
-    if (j < run1) four(j, k);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      over += k[e] < border;
-      tied += k[e] == border;
+  // ---- indices and weights of the warp's run, in order: 32 rows at a time, those before a lane's own counted by ballots
+  const unsigned before_me = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int j0 = run0; j0 < run1; j0 += 32) {
+    const int j = j0 + lane;
+    const uint32_t k = j < run1 ? key_at(j) : 0xffffffffu;  // (the key of no weight)
+    const unsigned over = __ballot_sync(ALL, k < border), tied = __ballot_sync(ALL, k == border);
+    uint32_t i = at + __popc(over & before_me) + min(tie, want);
+    bool stays = k < border;
+    if (tied != 0u) {  // (uniform)
+      const uint32_t my_tie = tie + __popc(tied & before_me);
+      stays = stays || (k == border && my_tie < want);
+      i += min(my_tie, want) - min(tie, want);
+      tie += __popc(tied);
     }
-    // rows above and ties before this lane's (both below 129), summed as the halves of a word
-    uint32_t inc = over + (tied << 16);
-    const uint32_t mine = inc;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(ALL, inc, o);
-      if (lane >= o) inc += y;
+    if (stays) {
+      kept[i] = lo + j;
+      nw[i] = weight_of(k);
+      // (0 may have been -0, and -inf NaN: rare among the rows that stay)
+      if (k == 0x7fffffffu || k == 0xff800000u) nw[i] = __ldg(between + j);
     }
-    uint32_t my_at = at + ((inc - mine) & 0xffffu), my_tie = tie + ((inc - mine) >> 16);
-    const uint32_t all = __shfl_sync(ALL, inc, 31);
-    at += all & 0xffffu;
-    tie += all >> 16;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool t = k[e] == border;
-      if (k[e] < border || (t && my_tie < want)) {
-        const uint32_t i = my_at + min(my_tie, want);
-        kept[i] = lo + j + e;
-        nw[i] = weight_of(k[e]);
-        // (0 may have been -0, and -inf NaN: rare among the rows that stay)
-        if (k[e] == 0x7fffffffu || k[e] == 0xff800000u) nw[i] = __ldg(between + j + e);
-      }
-      my_at += k[e] < border;
-      my_tie += t;
-    }
+    at += __popc(over);
   }
   edges();
   if (ranks > 1) cluster.barrier_wait();
