@@ -19,10 +19,10 @@
 // head, which lie in one page, and copies their keys and values, 16 bytes (4-bit
 // rows: also the scale bytes) a lane; no warp waits for another. A new e4m3 page's
 // scale is the largest of its rows' old ones, which each warp of the page finds for
-// itself, and codes whose scale grew are rounded again. (For those 32 sequences, 4001 rows
-// kept, e4m3, and for 2 of 90-131k, 32768 kept, 4-bit (then read back), a call takes 130-135 and 123 us;
-// with 32 rows a warp, 106 registers, 162 and 126; with blocks of 128 rows that meet at
-// barriers 130 and 127.)
+// itself, and codes whose scale grew are rounded again. (Those 32 sequences, 4001 rows
+// kept, e4m3, take 130-135 us in all; 2 of 90-131k, 32768 rows kept and read back, 4-bit,
+// 123; with 32 rows a warp, 106 registers, 162 and 126; with blocks of 128 rows that meet
+// at barriers 130 and 127.)
 // What bounds it: HBM, the weights read and the kept rows read and written; for one
 // or two sequences the selection's chain of passes.
 #include <cooperative_groups.h>
