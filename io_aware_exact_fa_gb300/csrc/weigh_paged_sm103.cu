@@ -20,10 +20,11 @@
 // (2 d operations and one exponential for each row and key) bound it. A block has a range:
 // one warp copies rows to shared memory in bulk and issues tcgen05 products, four warps
 // turn codes into f16 operands and scores into weights. The keys' operand stands in tensor
-// memory: 16 tokens of 32/8 heads over 16 sequences of 1-16k keys, e4m3, take 43 us (0.48
-// of the bytes' time). The operand in shared memory, at once the products' and the
-// conversions' traffic, 59 us with bulk copies and 67 with each warp's own loads; products
-// at warp level 80; loads that touched 32 rows at once 81.
+// memory: 16 tokens of 32/8 heads over 16 sequences of 1-16k keys, e4m3, take 41 us (0.50
+// of the bytes' time; a new (sequence, head)'s queries 6,500 cycles, then 3,100 a tile).
+// The operand in shared memory, at once the products' and the conversions' traffic, 59 us
+// with bulk copies and 67 with each warp's own loads; products at warp level 80; loads
+// that touched 32 rows at once 81.
 //
 // The rule's 16 rows: over 16 sequences of 1-16k keys, 8 heads, 4-bit / e4m3 / bf16, d = 128,
 // 16 rows a head take 25 / 38 / 74 us from registers and 29 / 40 / 71 in tensor memory;
@@ -516,21 +517,26 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
         if (t + C::STAGES < n) copy(t + C::STAGES);
       }
     } else {
-      // ------------------------------------------------------------ the queries: a lane eight elements of a row
-      constexpr int QL = D / 8, QR = 32 / QL, QB = 4;  // lanes of a row, rows of a warp's load, loads at a time
-      for (int r0 = warp * QR; r0 < N; r0 += 4 * QR * QB) {
+      // ------------------------------------------------------------ the queries: a warp N / 4 rows, a lane eight elements of one
+      constexpr int QL = D / 8, QR = 32 / QL, QB = 8;  // lanes of a row, rows of a warp's load, loads at a time
+      const int rows = N / 4, r_of = warp * rows + lane;  // lane m finds row m's place
+      const bool in = lane < rows && r_of < p.R;
+      const int h = hk * p.G + (in ? r_of / p.Nq : 0), tok = in ? r_of % p.Nq : 0;
+      const long long off = b * p.qsb + h * p.qsh + tok * p.qst;
+      const float lse = in ? __ldg(p.lse + (static_cast<long long>(b) * p.H + h) * p.Nq + tok) : -INFINITY;
+      const unsigned real = __ballot_sync(ALL, in);
+      for (int m0 = 0; m0 < rows; m0 += QR * QB) {
         uint4 x[QB];
 #pragma unroll
         for (int i = 0; i < QB; ++i) {
-          const int r = r0 + 4 * QR * i + lane / QL;
+          const int m = (m0 + QR * i + lane / QL) & 31;
+          const long long at_row = __shfl_sync(ALL, off, m);
           x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < p.R)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + b * p.qsb + (hk * p.G + r / p.Nq) * p.qsh +
-                                                        r % p.Nq * p.qst) + lane % QL);
+          if ((real >> m) & 1u) x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at_row) + lane % QL);
         }
 #pragma unroll
         for (int i = 0; i < QB; ++i) {
-          const int r = r0 + 4 * QR * i + lane / QL;
+          const int m = m0 + QR * i + lane / QL, r = warp * rows + m;
           float up = 1.f;
           if constexpr (F16) {
             uint2 lo = make_uint2(x[i].x, x[i].y), hi = make_uint2(x[i].z, x[i].w);
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
             lo = wg_to_f16(lo, down), hi = wg_to_f16(hi, down);
             x[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
           }
-          if (r < N) {
+          if (m < rows) {
             *reinterpret_cast<uint2*>(s_q + wm_at(N, r, wm_place<D, KIND>(2 * (lane % QL)))) = make_uint2(x[i].x, x[i].y);
             *reinterpret_cast<uint2*>(s_q + wm_at(N, r, wm_place<D, KIND>(2 * (lane % QL) + 1))) = make_uint2(x[i].z, x[i].w);
             if (lane % QL == 0) reinterpret_cast<float*>(s_row + r / 2)[r & 1] = p.scale_log2 * up;
@@ -549,14 +555,11 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
         }
       }
       bool dead = false;  // a row adds nothing
-      if (tid < N) {
-        const bool in = tid < p.R;
-        const int h = hk * p.G + (in ? tid / p.Nq : 0), tok = in ? tid % p.Nq : 0;
-        const float lse = in ? __ldg(p.lse + (static_cast<long long>(b) * p.H + h) * p.Nq + tok) : -INFINITY;
+      if (lane < rows) {
         const bool none = lse == -INFINITY;
         const int lim = none ? -1 : min(L - 1, L - p.Nq + tok);
-        reinterpret_cast<float*>(s_row + tid / 2)[2 + (tid & 1)] = none ? 0.f : lse * -1.4426950408889634f;
-        reinterpret_cast<int*>(s_lim + tid / 2)[tid & 1] = lim;
+        reinterpret_cast<float*>(s_row + r_of / 2)[2 + (r_of & 1)] = none ? 0.f : lse * -1.4426950408889634f;
+        reinterpret_cast<int*>(s_lim + r_of / 2)[r_of & 1] = lim;
         dead = lim < 0 && in;
       }
       fence_proxy_async_smem();  // the tensor core reads the queries through the async proxy
