@@ -70,6 +70,8 @@ def _build_binding(force: bool) -> None:
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE, "-I",
            os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", tmp,
            "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if os.path.exists(os.path.join(torch, "lib", "libtorch_cuda.so")):   # (else nothing is ever allocated on a GPU)
+        cmd += ["-DFA_TORCH_CUDA", "-Wl,--no-as-needed", "-ltorch_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
