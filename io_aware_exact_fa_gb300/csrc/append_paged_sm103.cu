@@ -21,7 +21,8 @@
 // once, from the fp32 result, not through bf16.
 //
 // 4-bit pages hold e2m1 codes and, for every 16 neighbours of a row, one byte of scale:
-// amax / 6, rounded to three mantissa bits. Rows do not depend on one another there; the
+// amax / 6, rounded to three mantissa bits. Rows do not depend on one another there, so a
+// K/V block takes several heads of a page and works a row's angles out once for them; the
 // keys are rounded from the bf16 value that k_out gets, so the cache and a prompt's own
 // attention see the same keys.
 //
@@ -38,7 +39,8 @@
 // arithmetic; with one kind of block for both 147 us in place of 132), launch and
 // load latency for a step of single tokens. Measured, 32 query and 8 K/V heads,
 // d = 128, e4m3: 26.7k prompt tokens with norms 115 us (5.7 TB/s, 0.85 of the copy
-// rate); 256 sequences of one token 8.1 us; 4-bit: 26k prompt tokens 114 us.
+// rate); 256 sequences of one token 8.1 us; 4-bit: 26k prompt tokens 106 us (114 with a K/V
+// block for each head, like e4m3).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -61,6 +63,12 @@ constexpr int AP_STEP_THREADS = 64;    // and at least
 constexpr int ap_ctas(int kind, bool inter) { return kind == PAGES_BF16 && inter ? 4 : 3; }
 #ifndef AP_RING
 #define AP_RING 3       // heads of a row whose copies a query thread has in flight
+#endif
+#ifndef AP_KV_RING
+#define AP_KV_RING 2    // the same of a K/V block of 4-bit rows
+#endif
+#ifndef AP_KV_HEADS
+#define AP_KV_HEADS 4   // K/V heads of such a block, at most
 #endif
 
 // A unit's 16 elements as four fp32 pairs a (first of each rotation pair) and four
@@ -410,49 +418,169 @@ __device__ __forceinline__ void query_block(const AppendPagedParams& p, int bloc
   cp_async_wait<0>();
 }
 
-// ---- K/V block: the new rows of one page, one K/V head
-template <int D, int KIND, bool INTER>
-__device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, unsigned int* s_amax, uint4* stash) {
-  constexpr int LPR = D / 16;
-  constexpr bool F8 = KIND == PAGES_E4M3, F4 = KIND == PAGES_FP4;
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int groups = nt / LPR;
-  const int hk = block % p.Hkv, c = block / p.Hkv;
-  int b, i;
-  if constexpr (F8) {
-    if (tid < 2) s_amax[tid] = 0u;
-    __syncthreads();
-  }
+// The new rows of one page that K/V block c takes: those of sequence b, from row r0 of page `page0` of the sequence on, whose
+// first position is `first`; token tok0 is the first of them. Uniform over the block; `nrows` 0: nothing to do.
+struct PageRows {
+  int b, page0, r0, nrows, tok0;
+  long long first;
+};
+__device__ __forceinline__ PageRows rows_of(const AppendPagedParams& p, int c) {
+  PageRows w{};
+  int i;
   if (p.per_seq > 0) {
-    b = c / p.per_seq;
-    i = c - b * p.per_seq;
+    w.b = c / p.per_seq;
+    i = c - w.b * p.per_seq;
   } else {
     // Sequence b owns the blocks from cu[b] / page + 2 b on: at least as many as its tokens can touch pages. Every warp
     // finds the last b that starts at or before block c for itself, 32 candidates at a time.
     auto base = [&](int x) { return (max(__ldg(p.cu + x), 0) >> p.page_shift) + 2 * x; };
     int lo = 0, n = p.B;
     while (n > 1) {
-      const int step = (n + 31) / 32, x = lo + (tid & 31) * step;
+      const int step = (n + 31) / 32, x = lo + static_cast<int>(threadIdx.x & 31) * step;
       const unsigned at_or_before = __ballot_sync(0xffffffffu, x < lo + n && base(x) <= c);
       const int skip = max(__popc(at_or_before) - 1, 0) * step;
       lo += skip;
       n = min(step, n - skip);
     }
-    b = lo;
-    i = c - base(b);
+    w.b = lo;
+    i = c - base(lo);
   }
   int t0, n, all;
-  (void)tokens_of(p, b, t0, n, all);
-  const int L = __ldg(p.seqlens + b);
-  const long long start = static_cast<long long>(L) - all, end = start + n;     // positions
-  const int page0 = static_cast<int>(start >> p.page_shift) + i; // this block's page of the sequence
-  const long long first = static_cast<long long>(page0) << p.page_shift;
-  // (uniform over the block; blocks below the first sequence's, where tokens come before it, have i < 0)
-  if (n == 0 || L == 0 || i < 0 || first >= end) return;
-  const int r0 = start > first ? static_cast<int>(start - first) : 0;           // its new rows r0 .. r1 - 1
-  const int r1 = static_cast<int>(end - first < p.page ? end - first : p.page);
-  const int nrows = r1 - r0;
-  const int tok0 = t0 + static_cast<int>(first + r0 - start);    // token of row r0
+  (void)tokens_of(p, w.b, t0, n, all);
+  const int L = __ldg(p.seqlens + w.b);
+  const long long start = static_cast<long long>(L) - all, end = start + n;       // positions
+  w.page0 = static_cast<int>(start >> p.page_shift) + i;                          // this block's page of the sequence
+  w.first = static_cast<long long>(w.page0) << p.page_shift;
+  // (blocks below the first sequence's, where tokens come before it, have i < 0)
+  if (n == 0 || L == 0 || i < 0 || w.first >= end) return w;
+  w.r0 = start > w.first ? static_cast<int>(start - w.first) : 0;                 // its new rows r0 .. r0 + nrows - 1
+  w.nrows = static_cast<int>(end - w.first < p.page ? end - w.first : p.page) - w.r0;
+  w.tok0 = t0 + static_cast<int>(w.first + w.r0 - start);                         // token of row r0
+  return w;
+}
+
+// ---- K/V block of 4-bit rows: the new rows of one page, p.kv_heads K/V heads
+// Rows do not depend on one another, so a block streams them, head after head, through a ring of copies, each thread's own,
+// and the angles of a row are worked out once for its heads.
+template <int D, bool INTER>
+__device__ __forceinline__ void kv_block4(const AppendPagedParams& p, int block, uint4* ring) {
+  constexpr int LPR = D / 16;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int groups = nt / LPR;
+  const int parts = (p.Hkv + p.kv_heads - 1) / p.kv_heads;
+  const int hk0 = block % parts * p.kv_heads, heads = min(p.kv_heads, p.Hkv - hk0);
+  const PageRows w = rows_of(p, block / parts);
+  if (w.nrows == 0) return;
+  const bool in_table = w.page0 >= 0 && w.page0 < p.width;
+  const int id = in_table ? __ldg(p.table + w.b * p.table_stride + w.page0) : -1;
+  const int grp = tid / LPR, u = tid % LPR;
+  const UnitPlace<INTER> at(u, p.rot);
+  const int rounds = (w.nrows + groups - 1) / groups;             // (the same in every thread)
+  const uint16_t* kb = static_cast<const uint16_t*>(p.k) + w.tok0 * p.kst + hk0 * p.ksh;
+  const uint16_t* vb = static_cast<const uint16_t*>(p.v) + w.tok0 * p.vst + hk0 * p.vsh;
+  // copies: the key's blocks of eight elements that this thread turns, the value's 16 neighbours of one scale
+  int fr = 0, fh = 0;                                             // round and head of the next
+  auto fetch = [&](int slot) {
+    const int r = fr * groups + grp;
+    const uint32_t nb = r < w.nrows ? 16u : 0u, mine = smem_u32(ring + slot * 4 * nt + tid);  // (past the last round: none)
+    const uint16_t* ks = kb + (nb ? r * p.kst + fh * p.ksh : 0);
+    const uint16_t* vs = vb + (nb ? r * p.vst + fh * p.vsh : 0);
+    cp_async16_ca(mine, ks + at.c0, nb);
+    cp_async16_ca(mine + nt * 16, ks + at.c1, nb);
+    cp_async16_ca(mine + 2 * nt * 16, vs + 16 * u, nb);
+    cp_async16_ca(mine + 3 * nt * 16, vs + 16 * u + 8, nb);
+    cp_async_commit();
+    if (++fh == heads) fh = 0, ++fr;
+  };
+#pragma unroll
+  for (int i = 0; i < AP_KV_RING; ++i) fetch(i);
+  const long long pbase = paged_row_offset(id, p.num_pages, p.Hkv, hk0, p.page, 0, 1);
+  const bool store = pbase >= 0;
+  if (!store && tid == 0 && hk0 == 0) atomicOr(p.status, in_table ? FA_DEV_BAD_PAGE : FA_DEV_BAD_LENS);
+  const uint32_t pos0 = static_cast<uint32_t>(w.first) + w.r0 + offset_of(p, w.b);
+  // A scale's 16 neighbours are blocks 2i and 2i + 1 of eight elements. This thread has blocks c0 / 8 and c1 / 8, and the
+  // other one of each pair may be another thread's of the same row: lane `from` has it, as its first or its second.
+  const int turned = p.rot / 16;                                  // units that are
+  auto holder = [&](int k) { return k < turned ? k : k < 2 * turned ? k - turned : turned + (k - 2 * turned) / 2; };
+  const int k0 = (at.c0 / 8) ^ 1, k1 = (at.c1 / 8) ^ 1, from0 = holder(k0), from1 = holder(k1);
+  int slot = 0;
+  for (int it = 0; it < rounds; ++it) {
+    const int r = it * groups + grp;
+    const bool ok = r < w.nrows;
+    Angles t;
+    if (at.turned) angles_at(t, pos0 + r, p.turns + 8 * u, p.rot_scale);
+    const long long row = pbase + w.r0 + r;
+    for (int h = 0; h < heads; ++h) {
+      cp_async_wait<AP_KV_RING - 1>();
+      const uint4* mine = ring + slot * 4 * nt + tid;
+      Unit16 x = unpack16<INTER>(mine[0], mine[nt]);
+      if (p.k_weight != nullptr) {
+        normalise<D>(x, p.eps);
+        const uint16_t* wt = static_cast<const uint16_t*>(p.k_weight);
+        const Unit16 f = unpack16<INTER>(__ldg(reinterpret_cast<const uint4*>(wt + at.c0)), __ldg(reinterpret_cast<const uint4*>(wt + at.c1)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x.a[j] = fmul2(x.a[j], f.a[j]);
+          x.b[j] = fmul2(x.b[j], f.b[j]);
+        }
+      }
+      if (at.turned) turn(x, t);
+      float y[16];
+      in_order<INTER>(x, y);
+      const uint4 y0 = pack8(y), y1 = pack8(y + 8);
+      // the key as k_out gives it, in bf16 (whole warps shuffle)
+      uint32_t m0 = bf16x8_amax_bits(y0), m1 = bf16x8_amax_bits(y1);
+      if (INTER || !at.turned) m0 = m1 = max(m0, m1);
+      if (!INTER) {
+        const uint32_t a0 = __shfl_sync(0xffffffffu, m0, from0, LPR), b0 = __shfl_sync(0xffffffffu, m1, from0, LPR);
+        const uint32_t a1 = __shfl_sync(0xffffffffu, m0, from1, LPR), b1 = __shfl_sync(0xffffffffu, m1, from1, LPR);
+        m0 = max(m0, k0 < turned ? a0 : b0);
+        m1 = max(m1, k1 < turned ? a1 : b1);
+      }
+      const uint4 v0 = mine[2 * nt], v1 = mine[3 * nt];
+      fetch(slot);  // (the slot has been read)
+      slot = slot + 1 == AP_KV_RING ? 0 : slot + 1;
+      if (!ok) continue;
+      if (p.k_out != nullptr) {
+        uint16_t* ko = static_cast<uint16_t*>(p.k_out) + (w.tok0 + static_cast<long long>(r)) * p.kost + (hk0 + h) * p.kosh;
+        *reinterpret_cast<uint4*>(ko + at.c0) = y0;
+        *reinterpret_cast<uint4*>(ko + at.c1) = y1;
+      }
+      if (!store) continue;
+      float i0, i1, iv;
+      const uint32_t s0 = fp4_scale_byte(m0, i0), s1 = fp4_scale_byte(m1, i1);
+      const uint32_t sv = fp4_scale_byte(max(bf16x8_amax_bits(v0), bf16x8_amax_bits(v1)), iv);
+      const long long at_row = row + static_cast<long long>(h) * p.page;
+      uint8_t* kd = static_cast<uint8_t*>(p.k_pages) + at_row * (D / 2);
+      uint8_t* vd = static_cast<uint8_t*>(p.v_pages) + at_row * (D / 2);
+      *reinterpret_cast<uint32_t*>(kd + at.c0 / 2) = fp4_codes8(y0, i0);
+      *reinterpret_cast<uint32_t*>(kd + at.c1 / 2) = fp4_codes8(y1, i1);
+      *reinterpret_cast<uint2*>(vd + 8 * u) = make_uint2(fp4_codes8(v0, iv), fp4_codes8(v1, iv));
+      // (both threads of a group have the same scale; the one with the even block writes it)
+      if ((at.c0 & 8) == 0) p.k_scale4[at_row * (D / 16) + at.c0 / 16] = static_cast<uint8_t>(s0);
+      if ((at.c1 & 8) == 0) p.k_scale4[at_row * (D / 16) + at.c1 / 16] = static_cast<uint8_t>(s1);
+      p.v_scale4[at_row * (D / 16) + u] = static_cast<uint8_t>(sv);
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// ---- K/V block of bf16 or e4m3 rows: the new rows of one page, one K/V head
+template <int D, int KIND, bool INTER>
+__device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, unsigned int* s_amax, uint4* stash) {
+  constexpr int LPR = D / 16;
+  constexpr bool F8 = KIND == PAGES_E4M3;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int groups = nt / LPR;
+  const int hk = block % p.Hkv;
+  if constexpr (F8) {
+    if (tid < 2) s_amax[tid] = 0u;
+    __syncthreads();
+  }
+  const PageRows w = rows_of(p, block / p.Hkv);
+  const int b = w.b, page0 = w.page0, r0 = w.r0, nrows = w.nrows, tok0 = w.tok0;
+  const long long first = w.first;
+  if (nrows == 0) return;  // (uniform over the block)
 
   const uint32_t offset = offset_of(p, b);
 
@@ -461,8 +589,6 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
   const int id = in_table ? __ldg(p.table + b * p.table_stride + page0) : -1;
   const int grp = tid / LPR, u = tid % LPR;
   const UnitPlace<INTER> at(u, p.rot);
-  // (a 4-bit row's values are taken 16 neighbours at a time, the elements of one scale)
-  const int vc0 = F4 ? 16 * u : at.c0, vc1 = F4 ? 16 * u + 8 : at.c1;
   const uint16_t* kb = static_cast<const uint16_t*>(p.k) + tok0 * p.kst + hk * p.ksh;
   const uint16_t* vb = static_cast<const uint16_t*>(p.v) + tok0 * p.vst + hk * p.vsh;
   // every round's rows are copied to this thread's own pieces of shared memory: 0, 1 the key, 4, 5 the value
@@ -475,8 +601,8 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
     const uint16_t* vs = vb + (nb ? r * p.vst : 0);
     cp_async16_ca(mine, ks + at.c0, nb);
     cp_async16_ca(mine + nt * 16, ks + at.c1, nb);
-    cp_async16_ca(mine + VP * nt * 16, vs + vc0, nb);
-    cp_async16_ca(mine + (VP + 1) * nt * 16, vs + vc1, nb);
+    cp_async16_ca(mine + VP * nt * 16, vs + at.c0, nb);
+    cp_async16_ca(mine + (VP + 1) * nt * 16, vs + at.c1, nb);
   }
   cp_async_commit();
   const long long pbase = paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, 0, D);
@@ -508,7 +634,7 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
         x.b[j] = fmul2(x.b[j], w.b[j]);
       }
     }
-    if (!F4 && !ok) continue;  // (4-bit rows: whole warps shuffle below)
+    if (!ok) continue;
     if (at.turned) {
       Angles t;
       angles_at(t, static_cast<uint32_t>(first) + r0 + r + offset, p.turns + 8 * u, p.rot_scale);
@@ -517,44 +643,12 @@ __device__ __forceinline__ void kv_block(const AppendPagedParams& p, int block, 
     float y[16];
     in_order<INTER>(x, y);
     const uint4 y0 = pack8(y), y1 = pack8(y + 8);
-    if (kob != nullptr && ok) {
+    if (kob != nullptr) {
       *reinterpret_cast<uint4*>(kob + r * p.kost + at.c0) = y0;
       *reinterpret_cast<uint4*>(kob + r * p.kost + at.c1) = y1;
     }
     if (!store) continue;
-    if constexpr (F4) {
-      // The key as k_out gives it, in bf16. A scale's 16 neighbours are blocks 2i and 2i + 1 of eight elements; this thread
-      // has blocks c0 / 8 and c1 / 8, and the other one of each pair may be another thread's of the same row.
-      uint32_t m0 = bf16x8_amax_bits(y0), m1 = bf16x8_amax_bits(y1);
-      if (INTER || !at.turned) m0 = m1 = max(m0, m1);
-      if (!INTER) {
-        const int turned = p.rot / 16;  // units that are
-        auto other = [&](int block) {   // largest magnitude of block ^ 1
-          const int k = block ^ 1;
-          const int from = k < turned ? k : k < 2 * turned ? k - turned : turned + (k - 2 * turned) / 2;
-          const uint32_t a = __shfl_sync(0xffffffffu, m0, from, LPR), c = __shfl_sync(0xffffffffu, m1, from, LPR);
-          return k < turned ? a : c;
-        };
-        const uint32_t o0 = other(at.c0 / 8), o1 = other(at.c1 / 8);
-        m0 = max(m0, o0);
-        m1 = max(m1, o1);
-      }
-      if (!ok) continue;
-      const uint4 v0 = mine[VP * nt], v1 = mine[(VP + 1) * nt];
-      float i0, i1, iv;
-      const uint32_t s0 = fp4_scale_byte(m0, i0), s1 = fp4_scale_byte(m1, i1);
-      const uint32_t sv = fp4_scale_byte(max(bf16x8_amax_bits(v0), bf16x8_amax_bits(v1)), iv);
-      const long long row = pbase / D + r0 + r;
-      uint8_t* kd = static_cast<uint8_t*>(p.k_pages) + row * (D / 2);
-      uint8_t* vd = static_cast<uint8_t*>(p.v_pages) + row * (D / 2);
-      *reinterpret_cast<uint32_t*>(kd + at.c0 / 2) = fp4_codes8(y0, i0);
-      *reinterpret_cast<uint32_t*>(kd + at.c1 / 2) = fp4_codes8(y1, i1);
-      *reinterpret_cast<uint2*>(vd + 8 * u) = make_uint2(fp4_codes8(v0, iv), fp4_codes8(v1, iv));
-      // (both threads of a group have the same scale; the one with the even block writes it)
-      if ((at.c0 & 8) == 0) p.k_scale4[row * (D / 16) + at.c0 / 16] = static_cast<uint8_t>(s0);
-      if ((at.c1 & 8) == 0) p.k_scale4[row * (D / 16) + at.c1 / 16] = static_cast<uint8_t>(s1);
-      p.v_scale4[row * (D / 16) + u] = static_cast<uint8_t>(sv);
-    } else if constexpr (F8) {
+    if constexpr (F8) {
       am_k = fmaxf(am_k, finite_amax(y));
       // the turned key, in fp32, over pieces 0 .. 3
 #pragma unroll
@@ -649,19 +743,24 @@ __global__ void __launch_bounds__(AP_THREADS, ap_ctas(KIND, INTER)) fa_append_pa
   // rows, the page's largest value), which the query blocks beside it fill.
   const unsigned long long blocks = gridDim.x;
   const int before = static_cast<int>(static_cast<unsigned long long>(block) * p.kv_blocks / blocks);  // K/V blocks before this one
-  if (static_cast<int>((block + 1ull) * p.kv_blocks / blocks) > before) kv_block<D, KIND, INTER>(p, before, s_amax, ap_stash);
-  else query_block<D, INTER>(p, block - before, s_pos, ap_stash);
+  const bool kv = static_cast<int>((block + 1ull) * p.kv_blocks / blocks) > before;
+  if constexpr (KIND == PAGES_FP4) {
+    if (kv) kv_block4<D, INTER>(p, before, ap_stash);
+  } else {
+    if (kv) kv_block<D, KIND, INTER>(p, before, s_amax, ap_stash);
+  }
+  if (!kv) query_block<D, INTER>(p, block - before, s_pos, ap_stash);
 }
 
-// Bytes of a block's pieces: a page's rounds of keys and values, or a query block's ring.
-static int ap_smem_bytes(int D, bool f8, int rows, int threads) {
-  const int groups = threads / (D / 16);
-  return std::max((rows + groups - 1) / groups * (f8 ? 6 : 4), 2 * AP_RING) * threads * 16;
+// Bytes of a block's pieces: a page's rounds of keys and values (4-bit rows: their ring), or a query block's ring.
+static int ap_smem_bytes(int D, int kind, int rows, int threads) {
+  const int groups = threads / (D / 16), rounds = (rows + groups - 1) / groups;
+  return std::max(kind == PAGES_FP4 ? 4 * AP_KV_RING : rounds * (kind == PAGES_E4M3 ? 6 : 4), 2 * AP_RING) * threads * 16;
 }
 template <int D, int KIND, bool INTER>
 static cudaError_t ap_attr() {
   return cudaFuncSetAttribute(fa_append_paged_kernel<D, KIND, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ap_smem_bytes(D, KIND == PAGES_E4M3, 128, AP_THREADS));
+                              ap_smem_bytes(D, KIND, 128, AP_THREADS));
 }
 template <int KIND>
 static cudaError_t ap_attrs() {
@@ -692,9 +791,21 @@ static cudaError_t ap_launch(AppendPagedParams p, cudaStream_t stream) {
   while (slots < groups && slots < p.H && static_cast<long long>(p.T) * slots < static_cast<long long>(groups) * p.q_blocks_wanted)
     slots *= 2;
   p.q_slots = slots;
+  if constexpr (KIND == PAGES_FP4) {
+    // K/V heads of a block, which share a row's angles: as long as a page's rows fill the block, two blocks an SM (a third of
+    // the query blocks wanted) are left, and a block has no more than eight turns. 26k prompt tokens, 32/8 heads: pages of 64
+    // with 1, 2, 4, 8 heads 114, 107, 106, 119 us; 10k in pages of 16 and 128 (read back too) 78, 68, 62, 64 and 79, 75, 78, 92.
+    const long long pages = p.kv_blocks / p.Hkv;
+    const int rounds = (p.max_rows + groups - 1) / groups;
+    p.kv_heads = 1;
+    while (p.kv_heads < AP_KV_HEADS && p.kv_heads < p.Hkv && p.max_rows >= groups && 2 * p.kv_heads * rounds <= 8 &&
+           pages * p.Hkv >= 2LL * p.kv_heads * (p.q_blocks_wanted / 3))
+      p.kv_heads *= 2;
+    p.kv_blocks = static_cast<int>(pages * ((p.Hkv + p.kv_heads - 1) / p.kv_heads));
+  }
   const int rows = groups / slots;
   const long long q_blocks = (static_cast<long long>(p.T) + rows - 1) / rows;
-  const size_t smem = ap_smem_bytes(D, KIND == PAGES_E4M3, p.max_rows, threads);
+  const size_t smem = ap_smem_bytes(D, KIND, p.max_rows, threads);
   fa_append_paged_kernel<D, KIND, INTER><<<static_cast<unsigned>(p.kv_blocks + q_blocks), threads, smem, stream>>>(p);
   return cudaGetLastError();
 }

@@ -116,6 +116,7 @@ struct AppendPagedParams {
   int max_rows;              // most new rows of one page
   int q_blocks_wanted;       // query blocks that fill the GPU a few times over
   int q_slots;               // heads of a row that a query block takes side by side
+  int kv_heads;              // 4-bit rows: K/V heads of a K/V block
   float rot_scale, eps;
   unsigned int* status;
 };

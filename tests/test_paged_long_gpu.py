@@ -112,6 +112,42 @@ def test_weigh_over_long_ranges(fa, G, Nq, page, many, d, kind):
         assert ((w[b, :, :L] - want).abs() <= bound).all(), b
 
 
+@pytest.mark.parametrize("inter,norm", [(False, True), (True, False)], ids=["half-norm", "interleaved"])
+@pytest.mark.parametrize("page,Hkv,d,rot,T", [(16, 3, 128, 128, 6000), (64, 8, 64, 48, 12000), (128, 5, 128, 64, 20000), (32, 2, 64, 64, 14000)])
+def test_a_large_append_is_its_sequences_appends(fa, page, Hkv, d, rot, T, inter, norm):
+    """Many prompts at once (whose blocks take several K/V heads) leave what one call for each sequence leaves."""
+    g = gen(page)
+    r = torch.Generator().manual_seed(page)
+    B, H = 24, Hkv * 2
+    new = torch.randint(1, 2 * T // B, (B,), generator=r).tolist()
+    past = torch.randint(0, 300, (B,), generator=r).tolist()
+    lens = [a + b for a, b in zip(new, past)]
+    table, n = batch(lens, page, g)
+    q, k, v = (torch.randn(sum(new), h, d, device="cuda", generator=g).to(torch.bfloat16) for h in (H, Hkv, Hkv))
+    k[::7] *= 100.0
+    v[3::5] *= 1e-3
+    w = torch.rand(d, device="cuda", generator=g).to(torch.bfloat16) if norm else None
+    kw = dict(turns=fa.rotary_turns(rot), interleaved=inter, q_weight=w, k_weight=w)
+    cu = [0]
+    for x in new:
+        cu.append(cu[-1] + x)
+
+    def pool():
+        return ([torch.full((n, Hkv, page, d // 2), 7, dtype=torch.uint8, device="cuda") for _ in range(2)]
+                + [torch.full((n, Hkv, page, d // 16), 9, dtype=torch.uint8, device="cuda") for _ in range(2)])
+
+    one, many = pool(), pool()
+    qo, ko = fa.append_paged_fp4(q, k, v, *one, table, cuda(lens, torch.int32), cu_seqlens=cuda(cu, torch.int32), **kw)
+    for b in range(B):
+        part = slice(cu[b], cu[b + 1])
+        qb, kb = fa.append_paged_fp4(q[part], k[part], v[part], *many, table[b:b + 1], cuda(lens[b:b + 1], torch.int32),
+                                     cu_seqlens=cuda([0, new[b]], torch.int32), **kw)
+        assert torch.equal(qo[part], qb) and torch.equal(ko[part], kb), b
+    assert fa.device_status() == fa.FA_OK
+    for x, y in zip(one, many):
+        assert torch.equal(x, y)
+
+
 def state(fa, kind, seed):
     """One set of arguments for every operator."""
     g = gen(seed)
