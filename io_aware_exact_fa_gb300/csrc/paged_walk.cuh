@@ -19,15 +19,22 @@ struct PagedTile {
   int b, hk, i, L, nt;
 };
 
+// A sequence's tiles for one K/V head. EXTRA: what starting on them costs, in tiles, counted before the first one, so that
+// ranges with many short sequences take no longer than others.
+template <int KS, int EXTRA = 0>
+__device__ __forceinline__ int paged_tiles_of(int L) {
+  return L > 0 ? (L + KS - 1) / KS + EXTRA : 0;
+}
+
 // Tiles of one K/V head of all sequences; `clipped`: a length outside [0, most] was met.
-template <int KS>
+template <int KS, int EXTRA = 0>
 __device__ __forceinline__ long long paged_count_tiles(const int* seqlens, int B, int most, int lane, bool& clipped) {
   long long sum = 0;
 #pragma unroll 4
   for (int b = lane; b < B; b += 32) {
     const int raw = __ldg(seqlens + b), L = paged_clip_len(raw, most);
     clipped = clipped || L != raw;
-    sum += (L + KS - 1) / KS;
+    sum += paged_tiles_of<KS, EXTRA>(L);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -35,14 +42,14 @@ __device__ __forceinline__ long long paged_count_tiles(const int* seqlens, int B
 }
 
 // Tile t0 of all.
-template <int KS>
+template <int KS, int EXTRA = 0>
 __device__ __forceinline__ PagedTile paged_seek(const int* seqlens, int B, int Hkv, int most, long long t0, int lane) {
   constexpr unsigned ALL = 0xffffffffu;
   PagedTile t{};
   long long base = 0;  // tiles of one K/V head of the sequences before
   for (int b0 = 0; b0 < B; b0 += 32) {
     const int mine = b0 + lane < B ? paged_clip_len(__ldg(seqlens + b0 + lane), most) : 0;
-    const int n = (mine + KS - 1) / KS;
+    const int n = paged_tiles_of<KS, EXTRA>(mine);
     int inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -66,7 +73,7 @@ __device__ __forceinline__ PagedTile paged_seek(const int* seqlens, int B, int H
 }
 
 // The next tile; past the last one b is B.
-template <int KS>
+template <int KS, int EXTRA = 0>
 __device__ __forceinline__ void paged_next(PagedTile& t, const int* seqlens, int B, int Hkv, int most) {
   if (++t.i < t.nt) return;
   t.i = 0;
@@ -75,7 +82,7 @@ __device__ __forceinline__ void paged_next(PagedTile& t, const int* seqlens, int
   do {
     if (++t.b >= B) return;
     t.L = paged_clip_len(__ldg(seqlens + t.b), most);
-    t.nt = (t.L + KS - 1) / KS;
+    t.nt = paged_tiles_of<KS, EXTRA>(t.L);
   } while (t.nt == 0);
 }
 

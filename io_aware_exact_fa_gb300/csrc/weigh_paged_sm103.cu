@@ -20,11 +20,11 @@
 // (2 d operations and one exponential for each row and key) bound it. A block has a range:
 // one warp copies rows to shared memory in bulk and issues tcgen05 products, four warps
 // turn codes into f16 operands and scores into weights. The keys' operand stands in tensor
-// memory: 16 tokens of 32/8 heads over 16 sequences of 1-16k keys, e4m3, take 41 us (0.50
+// memory: 16 tokens of 32/8 heads over 16 sequences of 1-16k keys, e4m3, take 39 us (0.53
 // of the bytes' time; a new (sequence, head)'s queries 6,500 cycles, then 3,100 a tile).
 // The operand in shared memory, at once the products' and the conversions' traffic, 59 us
 // with bulk copies and 67 with each warp's own loads; products at warp level 80; loads
-// that touched 32 rows at once 81.
+// that touched 32 rows at once 81. The ranges count a head's start as tiles: 41 without.
 //
 // The rule's 16 rows: over 16 sequences of 1-16k keys, 8 heads, 4-bit / e4m3 / bf16, d = 128,
 // 16 rows a head take 25 / 38 / 74 us from registers and 29 / 40 / 71 in tensor memory;
@@ -339,6 +339,10 @@ struct WmCfg {
   static constexpr int SCALES = KIND == PAGES_FP4 ? WM_TILE * (D / 16) : 0;
   static constexpr int STAGES = ROWS > 16384 ? 1 : 2;  // tiles in shared memory
   static constexpr int CTAS = 4;                    // by registers, shared and tensor memory
+  // Tiles' time that a new (sequence, head)'s queries take, by which its range is shorter. 16 sequences of 1-16k, e4m3, 64 / 128
+  // rows: d = 128 with 2 45 / 63 us, with 0 50 / 73; d = 64 (half the queries) with 2 35 / 55, with 1 37 / 55, with 0 35 / 57, but
+  // bf16 38 / 66, 38 / 66 and 36 / 62.
+  static constexpr int START = D == 128 ? 2 : 0;
 };
 __host__ __device__ constexpr int wm_cols(int rows) { return (rows + 31) / 32 * 32; }       // query rows, padded
 __host__ __device__ constexpr int wm_tmem(int d, int cols) {                                 // scores and operand
@@ -414,13 +418,13 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int range = static_cast<int>(blockIdx.x);
   bool clipped = false;
-  const long long sum = paged_count_tiles<WM_TILE>(p.seqlens, p.B, p.max_len, lane, clipped);
+  const long long sum = paged_count_tiles<WM_TILE, C::START>(p.seqlens, p.B, p.max_len, lane, clipped);
   if (range == 0 && __any_sync(ALL, clipped) && tid == 0) atomicOr(p.status, FA_DEV_BAD_LENS);
   const PagedRanges ranges(sum * p.Hkv, p.n_ranges);
   if (range >= ranges.n) return;
   const long long t0 = ranges.begin(range);
   int todo = static_cast<int>(ranges.begin(range + 1) - t0);
-  PagedTile at = paged_seek<WM_TILE>(p.seqlens, p.B, p.Hkv, p.max_len, t0, lane);
+  PagedTile at = paged_seek<WM_TILE, C::START>(p.seqlens, p.B, p.Hkv, p.max_len, t0, lane);
 
   const uint32_t tmem_columns = wm_tmem(D, N);
   if (tid == 0) {
@@ -451,8 +455,11 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
 
   while (todo > 0) {
     // ================================================================ one segment: tiles of (b, hk)
-    const int b = at.b, hk = at.hk, L = at.L, i0 = at.i, n = todo < at.nt - at.i ? todo : at.nt - at.i;
-    if (warp == 4) {
+    const int counted = todo < at.nt - at.i ? todo : at.nt - at.i;  // (the first C::START of a head's are none)
+    const int b = at.b, hk = at.hk, L = at.L, i0 = max(at.i - C::START, 0), n = at.i + counted - C::START - i0;
+    if (n <= 0) {
+      // (the range ends, or the head's tiles begin in the next one)
+    } else if (warp == 4) {
       // ------------------------------------------------------------ copies and products: lane g has 16-key group g of a tile
       auto page_of = [&](int t) -> int {
         const int key = (i0 + t) * WM_TILE + 16 * lane;
@@ -644,13 +651,13 @@ __global__ void __launch_bounds__(WM_THREADS, WmCfg<D, KIND>::CTAS) fa_weigh_pag
       }
       tc_fence_before();
     }
-    c0 += n;
-    todo -= n;
+    c0 += max(n, 0);
+    todo -= counted;
     ok = __syncthreads_and(ok);  // the segment is done with the queries' memory
     if (!ok) break;
     if (todo > 0) {
       at.i = at.nt - 1;
-      paged_next<WM_TILE>(at, p.seqlens, p.B, p.Hkv, p.max_len);
+      paged_next<WM_TILE, C::START>(at, p.seqlens, p.B, p.Hkv, p.max_len);
     }
   }
   if (warp == 4) {
