@@ -739,6 +739,7 @@ __global__ void __launch_bounds__(AP_THREADS, ap_ctas(KIND, INTER)) fa_append_pa
   __shared__ int s_pos[AP_THREADS / (D / 16)];
   __shared__ unsigned int s_amax[2];
   const int block = static_cast<int>(blockIdx.x);
+  pdl_launch_dependents();  // (a read of the rows may be launched beside the last blocks; it waits for all of them)
   // The two kinds are spread evenly over the launch: a K/V block is mostly a chain of waits (which sequence, its page, its
   // rows, the page's largest value), which the query blocks beside it fill.
   const unsigned long long blocks = gridDim.x;

@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(32 * EV_MOVE_WARPS) fa_evict_move_kernel(const
     dst = paged_row_offset(id, p.num_pages, p.Hkv, hk, p.page, row0 & (p.page - 1), 1);
   }
   pdl_wait();
+  pdl_launch_dependents();  // (as in the append)
   if (rows <= 0) return;
   // (page of the pool, and row there, of new row i: -1 where a table names none)
   auto from = [&](int i, int& id) -> long long {
