@@ -20,9 +20,9 @@
 // rows: also the scale bytes) a lane; no warp waits for another. A new e4m3 page's
 // scale is the largest of its rows' old ones, which each warp of the page finds for
 // itself, and codes whose scale grew are rounded again. (Those 32 sequences, 4001 rows
-// kept, e4m3, take 130-135 us in all; 2 of 90-131k, 32768 rows kept and read back, 4-bit,
-// 123; with 32 rows a warp, 106 registers, 162 and 126; with blocks of 128 rows that meet
-// at barriers 130 and 127.)
+// kept, e4m3, take 112 us in all; 2 of 90-131k, 32768 rows kept and read back, 4-bit, 121.
+// While launched beside the selection's tail 135 and 123; then, with 32 rows a warp, 106
+// registers, 162 and 126; with blocks of 128 rows that meet at barriers 130 and 127.)
 // What bounds it: HBM, the weights read and the kept rows read and written; for one
 // or two sequences the selection's chain of passes.
 #include <cooperative_groups.h>
@@ -50,6 +50,7 @@ constexpr int EV_MAX_CLUSTER = 8;
 constexpr int EV_HELD = 40960;    // keys that a block holds in shared memory, at most
 constexpr int EV_FLIGHT = 8;      // weights that a thread asks for at once
 constexpr int EV_MOVE_WARPS = 8;
+constexpr size_t EV_BESIDE = 96 * 1024;  // shared memory of the selection on an SM up to which the move is set up beside it
 constexpr unsigned ALL = 0xffffffffu;
 
 // Bits that order weights downwards: larger ones have smaller keys, -0 as 0, NaN as -inf.
@@ -463,8 +464,9 @@ cudaError_t evict_paged_set_attributes() {
   return e != cudaSuccess ? e : ev_attrs<1024>();
 }
 
+// `smem`: what a block takes of shared memory.
 template <int THREADS>
-static cudaError_t ev_select(const EvictPagedParams& p, int ranks, cudaStream_t stream) {
+static cudaError_t ev_select(const EvictPagedParams& p, int ranks, size_t& smem, cudaStream_t stream) {
   const int warps = ranks * (THREADS / 32);
   const long long block = ((p.max_len + static_cast<long long>(warps) - 1) / warps + 31) / 32 * THREADS;  // keys of one, at most
   cudaLaunchAttribute at{};
@@ -476,9 +478,9 @@ static cudaError_t ev_select(const EvictPagedParams& p, int ranks, cudaStream_t 
   cfg.stream = stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  cfg.dynamicSmemBytes = sizeof(EvShared);
+  cfg.dynamicSmemBytes = smem = sizeof(EvShared);
   if (block > EV_HELD) return cudaLaunchKernelEx(&cfg, fa_evict_select_kernel<false, THREADS>, p);
-  cfg.dynamicSmemBytes += block * 4;
+  cfg.dynamicSmemBytes = smem += block * 4;
   return cudaLaunchKernelEx(&cfg, fa_evict_select_kernel<true, THREADS>, p);
 }
 
@@ -495,7 +497,8 @@ cudaError_t launch_evict_paged(int d, int kind, const EvictPagedParams& p, int n
   // has an SM, but not in clusters: eight free SMs next to one another are not found for every one of them then.
   int ranks = 1;
   while (ranks < EV_MAX_CLUSTER && p.max_len > 4096LL * ranks && pairs * ranks * 2 <= num_sms) ranks *= 2;
-  const cudaError_t e = ranks == 1 && pairs <= num_sms ? ev_select<1024>(p, ranks, stream) : ev_select<512>(p, ranks, stream);
+  size_t smem = 0;
+  const cudaError_t e = ranks == 1 && pairs <= num_sms ? ev_select<1024>(p, ranks, smem, stream) : ev_select<512>(p, ranks, smem, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t mv{};
   const long long units = pairs * ((p.keep + 15) / 16);
@@ -506,7 +509,12 @@ cudaError_t launch_evict_paged(int d, int kind, const EvictPagedParams& p, int n
   pd.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pd.val.programmaticStreamSerializationAllowed = 1;
   mv.attrs = &pd;
-  mv.numAttrs = 1;
+  // Set up beside the selection's tail the move starts 1 to 4 us earlier, but keeps the split of the SM's memory that the
+  // selection took, for all of its time, and its loads in flight live in what that left to L1. 32 sequences of 8-16k, two
+  // blocks of 106 KB an SM: 135 us, on its own 112; 2 of 90-131k, one of 98 KB, 123 and 121; one of 100k, 91 KB, 38 and 39; 16
+  // of 4k, 57 KB, 26 and 28; 4 of 1.4k 12 and 14.
+  const long long on_an_sm = std::min<long long>((pairs * ranks + num_sms - 1) / num_sms, 2);
+  mv.numAttrs = on_an_sm * smem < EV_BESIDE ? 1 : 0;
   return d == 64 ? ev_move<64>(kind, mv, p) : ev_move<128>(kind, mv, p);
 }
 
