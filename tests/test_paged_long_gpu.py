@@ -284,3 +284,57 @@ def test_keep_past_every_length(fa):
         for i in range(0, L, 16):
             m = min(16, L - i)
             assert torch.equal(s["kp"][s["new"][b, i // 16], :, :m], s["kp"][s["table"][b, i // 16], :, :m])
+
+
+def test_a_captured_prompt_and_its_read(fa):
+    """Prompts appended, read back and cut in one graph, large enough that launches overlap: each replay reads what it wrote."""
+    page, Hkv, H, d, lens, keep = 64, 2, 4, 128, [9000, 11000, 400], 2000
+    g = gen(9)
+    table, n = batch(lens, page, g, spare=120)
+    free = sorted(set(range(n)) - set(table.flatten().tolist()))
+    new = torch.tensor(free[:96], dtype=torch.int32, device="cuda").view(3, 32)
+    pool = [torch.zeros(n, Hkv, page, d // 2, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pool += [torch.zeros(n, Hkv, page, d // 16, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    T = sum(lens)
+    q, k, v = (torch.zeros(T, h, d, dtype=torch.bfloat16, device="cuda") for h in (H, Hkv, Hkv))
+    w = torch.rand(3, Hkv, max(lens), device="cuda", generator=g)
+    cu, ln = torch.tensor([0] + lens).cumsum(0).int().cuda(), cuda(lens, torch.int32)
+    kept_lens = cuda([0, keep, 2 * keep, 2 * keep + 400], torch.int32)
+    turns = fa.rotary_turns(d)
+
+    def step():
+        _, ko = fa.append_paged_fp4(q, k, v, *pool, table, ln, cu_seqlens=cu, turns=turns)
+        whole = fa.read_paged(*pool[:2], table, ln, cu, T, k_scale=pool[2], v_scale=pool[3])
+        kept, nl, _, _ = fa.evict_paged(w, *pool[:2], table, ln, new, keep, recent=50, k_scale=pool[2], v_scale=pool[3])
+        part = fa.read_paged(*pool[:2], new, nl, kept_lens, 2 * keep + 400, k_scale=pool[2], v_scale=pool[3])
+        return ko, *whole, kept, *part
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (1, 2, 3):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, device="cuda", generator=gen(seed)))
+        w.copy_(torch.rand(w.shape, device="cuda", generator=gen(10 + seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in out]
+        for x in pool:
+            x.zero_()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            torch.cuda.synchronize()
+            assert torch.equal(a, b)
+        ko, rk, _, kept, pk, _ = got
+        # (a held value is off by half the widest step, a scale, and by the scale's own sixteenth: 1/6 (1 + 1/16) of its group's largest)
+        near = (rk.float() - ko.float()).abs() <= ko.float().abs().unflatten(-1, (-1, 16)).amax(-1, keepdim=True).expand(-1, -1, -1, 16).flatten(-2) / 5
+        assert near.all()
+        at = 0
+        for b, L in enumerate(lens):
+            m = min(L, keep)
+            for h in range(Hkv):
+                assert torch.equal(pk[at:at + m, h], rk[cu[b] + kept[b, h, :m].long(), h])
+            at += m
+    assert fa.device_status() == fa.FA_OK
