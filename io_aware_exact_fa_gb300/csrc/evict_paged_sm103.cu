@@ -20,7 +20,7 @@
 // rows: also the scale bytes) a lane; no warp waits for another. A new e4m3 page's
 // scale is the largest of its rows' old ones, which each warp of the page finds for
 // itself, and codes whose scale grew are rounded again. (Those 32 sequences, 4001 rows
-// kept, e4m3, take 112 us in all; 2 of 90-131k, 32768 rows kept and read back, 4-bit, 121.
+// kept, e4m3, take 110 us in all; 2 of 90-131k, 32768 rows kept and read back, 4-bit, 119.
 // While launched beside the selection's tail 135 and 123; then, with 32 rows a warp, 106
 // registers, 162 and 126; with blocks of 128 rows that meet at barriers 130 and 127.)
 // What bounds it: HBM, the weights read and the kept rows read and written; for one
@@ -305,28 +305,44 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) fa_evict_select
     __syncthreads();
     cluster.barrier_arrive();  // (waited for at the end: the totals are read before a block leaves)
   }
-  // ---- indices and weights of the warp's run, in order: 32 rows at a time, those before a lane's own counted by ballots
+  // ---- indices and weights of the warp's run, in order: 32 rows side by side, those before a lane's own counted by ballots
   const unsigned before_me = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int j0 = run0; j0 < run1; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t k = j < run1 ? key_at(j) : 0xffffffffu;  // (the key of no weight)
-    const unsigned over = __ballot_sync(ALL, k < border), tied = __ballot_sync(ALL, k == border);
-    uint32_t i = at + __popc(over & before_me) + min(tie, want);
-    bool stays = k < border;
-    if (tied != 0u) {  // (uniform)
+  auto write = [&](uint32_t i, int j, uint32_t k) {
+    kept[i] = lo + j;
+    nw[i] = weight_of(k);
+    // (0 may have been -0, and -inf NaN: rare among the rows that stay)
+    if (k == 0x7fffffffu || k == 0xff800000u) nw[i] = __ldg(between + j);
+  };
+  if (ties == 0u) {  // no row of the run has the border's key (as in most runs; 7,000 cycles of a block in place of 9,500 for 14k rows)
+    constexpr int AT_ONCE = 4;
+    at += min(tie, want);
+    for (int j0 = run0; j0 < run1; j0 += 32 * AT_ONCE) {
+      uint32_t k[AT_ONCE], i[AT_ONCE];
+#pragma unroll
+      for (int e = 0; e < AT_ONCE; ++e) {
+        const int j = j0 + 32 * e + lane;
+        k[e] = j < run1 ? key_at(j) : 0xffffffffu;  // (the key of no weight)
+      }
+#pragma unroll
+      for (int e = 0; e < AT_ONCE; ++e) {
+        const unsigned over = __ballot_sync(ALL, k[e] < border);
+        i[e] = at + __popc(over & before_me);
+        at += __popc(over);
+      }
+#pragma unroll
+      for (int e = 0; e < AT_ONCE; ++e)
+        if (k[e] < border) write(i[e], j0 + 32 * e + lane, k[e]);
+    }
+  } else {
+    for (int j0 = run0; j0 < run1; j0 += 32) {
+      const int j = j0 + lane;
+      const uint32_t k = j < run1 ? key_at(j) : 0xffffffffu;
+      const unsigned over = __ballot_sync(ALL, k < border), tied = __ballot_sync(ALL, k == border);
       const uint32_t my_tie = tie + __popc(tied & before_me);
-      stays = stays || (k == border && my_tie < want);
-      i += min(my_tie, want) - min(tie, want);
+      if (k < border || (k == border && my_tie < want)) write(at + __popc(over & before_me) + min(my_tie, want), j, k);
+      at += __popc(over);
       tie += __popc(tied);
     }
-    if (stays) {
-      kept[i] = lo + j;
-      nw[i] = weight_of(k);
-      // (0 may have been -0, and -inf NaN: rare among the rows that stay)
-      if (k == 0x7fffffffu || k == 0xff800000u) nw[i] = __ldg(between + j);
-    }
-    at += __popc(over);
   }
   edges();
   if (ranks > 1) cluster.barrier_wait();
@@ -511,7 +527,7 @@ cudaError_t launch_evict_paged(int d, int kind, const EvictPagedParams& p, int n
   mv.attrs = &pd;
   // Set up beside the selection's tail the move starts 1 to 4 us earlier, but keeps the split of the SM's memory that the
   // selection took, for all of its time, and its loads in flight live in what that left to L1. 32 sequences of 8-16k, two
-  // blocks of 106 KB an SM: 135 us, on its own 112; 2 of 90-131k, one of 98 KB, 123 and 121; one of 100k, 91 KB, 38 and 39; 16
+  // blocks of 106 KB an SM: 135 us, on its own 112; 2 of 90-131k, one of 98 KB, 123 and 121 (with the read); one of 100k, 91 KB, 38 and 39; 16
   // of 4k, 57 KB, 26 and 28; 4 of 1.4k 12 and 14.
   const long long on_an_sm = std::min<long long>((pairs * ranks + num_sms - 1) / num_sms, 2);
   mv.numAttrs = on_an_sm * smem < EV_BESIDE ? 1 : 0;
