@@ -438,7 +438,13 @@ fa_status fa_append_paged_at(const void* q, const void* k, const void* v, void* 
  * A row takes 9/32 of its bf16 bytes. Append sets a group's scale to its largest
  * magnitude / 6, rounded to nearest even, within [2^-17, 10240] (0 for a group of
  * zeros; larger magnitudes saturate at 61440), and its codes to the nearest of
- * x / scale (ties to the even code). An infinity or NaN makes its group of 16 NaN. */
+ * x / scale (ties to the even code). An infinity or NaN makes its group of 16 NaN.
+ *
+ * Codes are steps of the key, so the way to the bf16 key is fixed in every operation, each
+ * rounded to nearest in fp32: x * rsqrt(mean + eps) * weight from the left, where the mean's
+ * sum takes squares 32 elements apart in order, then neighbouring sums in pairs; the two
+ * products of a rotation, then their sum; cosines and sines within 2^-30 of the exact ones
+ * before their rounding. q is computed as for the other kinds. */
 
 /* fa_append_paged_at into 4-bit pages. k is quantised as k_out holds it, in bf16;
  * every row is on its own, so nothing written earlier changes. */

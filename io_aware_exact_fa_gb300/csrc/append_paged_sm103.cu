@@ -24,7 +24,11 @@
 // amax / 6, rounded to three mantissa bits. Rows do not depend on one another there, so a
 // K/V block takes several heads of a page and works a row's angles out once for them; the
 // keys are rounded from the bf16 value that k_out gets, so the cache and a prompt's own
-// attention see the same keys.
+// attention see the same keys. A code is a step function of the key: two computations that
+// round apart in the last bit of fp32 hold, now and then, values half a scale apart. So the
+// way from the input to the bf16 key is fixed, operation by operation, each rounded to
+// nearest in fp32 (the order of a norm's sum, no fused products, cosines and sines to
+// within 2^-30 of the rounded value), and whoever computes the same steps gets the same codes.
 //
 // Two kinds of blocks in one launch. A K/V block takes the new rows of one page of
 // one sequence and one K/V head: those rows are all that the page's scales depend
@@ -119,6 +123,12 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 // fraction's bits past the 32nd moves the angle by less than 2e-9 as well; fp32
 // rounds by 6e-8.
 __device__ __forceinline__ uint64_t dup2(float x) { return f2pack(x, x); }
+// Sine and cosine q quarter turns on.
+__device__ __forceinline__ void place_quarter(int q, float sn, float cn, float& so, float& co) {
+  const float a = (q & 1) ? cn : sn, b = (q & 1) ? sn : cn;
+  so = __uint_as_float(__float_as_uint(a) ^ ((static_cast<uint32_t>(q) & 2u) << 30));
+  co = __uint_as_float(__float_as_uint(b) ^ ((static_cast<uint32_t>(q + 1) & 2u) << 30));
+}
 __device__ __forceinline__ void sincos_turns2(int t0, int t1, float scale, uint64_t& s2, uint64_t& c2) {
   const int q0 = static_cast<int>(static_cast<uint32_t>(t0) + 0x20000000u) >> 30;
   const int q1 = static_cast<int>(static_cast<uint32_t>(t1) + 0x20000000u) >> 30;
@@ -138,14 +148,9 @@ __device__ __forceinline__ void sincos_turns2(int t0, int t1, float scale, uint6
   float s0, s1, c0, c1;
   f2unpack(fmul2(sx, sc), s0, s1);
   f2unpack(fmul2(ffma2(z, pc, dup2(1.f)), sc), c0, c1);
-  auto place = [](int q, float sn, float cn, float& so, float& co) {
-    const float a = (q & 1) ? cn : sn, b = (q & 1) ? sn : cn;
-    so = __uint_as_float(__float_as_uint(a) ^ ((static_cast<uint32_t>(q) & 2u) << 30));
-    co = __uint_as_float(__float_as_uint(b) ^ ((static_cast<uint32_t>(q + 1) & 2u) << 30));
-  };
   float so0, so1, co0, co1;
-  place(q0, s0, c0, so0, co0);
-  place(q1, s1, c1, so1, co1);
+  place_quarter(q0, s0, c0, so0, co0);
+  place_quarter(q1, s1, c1, so1, co1);
   s2 = f2pack(so0, so1);
   c2 = f2pack(co0, co1);
 }
@@ -235,6 +240,64 @@ __device__ __forceinline__ void angles_at(Angles& f, uint32_t pos, const long lo
 }
 constexpr uint64_t NEG2 = 0x8000000080000000ull;  // flips both signs of a pair
 
+// Cosine and sine of 2 pi f for two fractions of a turn f = t / 2^64, rounded to fp32 (off from the exact values by less than
+// 2^-30 of them before that rounding). With x = xh + xl the angle that is left of the nearest quarter turn, in two parts:
+//     sin x = xh - xh^3 / 6 + (xl + x^5 / 120 - ..),   cos x = 1 - xh^2 / 2 + (- xh xl + x^4 / 24 - ..)
+// where the first two terms and their errors are kept apart and the rest, below 2^-5 of the result, is in fp32.
+__device__ __forceinline__ void sincos_turns2_rounded(uint64_t t0, uint64_t t1, float scale, uint64_t& s2, uint64_t& c2) {
+  auto angle = [](uint64_t t, int& q, float& a, float& b) {  // t = q 2^62 + (a + b) 2^32
+    q = static_cast<int>((t + 0x2000000000000000ull) >> 62);
+    const int64_t r = static_cast<int64_t>(t - (static_cast<uint64_t>(q) << 62));
+    const int h = static_cast<int>(r >> 32);
+    a = static_cast<float>(h);
+    b = fmaf(static_cast<float>(static_cast<uint32_t>(r)), 2.3283064365386963e-10f, static_cast<float>(h - static_cast<int>(a)));
+  };
+  int q0, q1;
+  float a0, a1, b0, b1;
+  angle(t0, q0, a0, b0);
+  angle(t1, q1, a1, b1);
+  constexpr double UNIT = 6.283185307179586476925 / 4294967296.0;  // 2 pi / 2^32
+  constexpr float UH = static_cast<float>(UNIT), UL = static_cast<float>(UNIT - static_cast<double>(UH));
+  constexpr float SIXTH = 1.f / 6.f, SIXTH_L = static_cast<float>(1.0 / 6.0 - static_cast<double>(SIXTH));
+  const uint64_t a = f2pack(a0, a1), b = f2pack(b0, b1);
+  const uint64_t xh = fmul2(a, dup2(UH));
+  const uint64_t xl = ffma2(b, dup2(UH), ffma2(a, dup2(UL), ffma2(a, dup2(UH), xh ^ NEG2)));
+  const uint64_t zh = fmul2(xh, xh), zl = ffma2(xh, xh, zh ^ NEG2);           // xh^2
+  const uint64_t wh = fmul2(xh, zh), wl = ffma2(xh, zl, ffma2(xh, zh, wh ^ NEG2));  // xh^3
+  const uint64_t th = fmul2(wh, dup2(-SIXTH));
+  const uint64_t tl = ffma2(wl, dup2(-SIXTH), ffma2(wh, dup2(-SIXTH_L), ffma2(wh, dup2(-SIXTH), th ^ NEG2)));
+  uint64_t ps = ffma2(zh, dup2(-2.5052108e-8f), dup2(2.7557319e-6f));         // 1/11!, 1/9!
+  ps = ffma2(zh, ps, dup2(-1.9841270e-4f));
+  ps = ffma2(zh, ps, dup2(8.3333333e-3f));
+  const uint64_t half_z = fmul2(zh, dup2(0.5f));
+  const uint64_t turn_xl = ffma2(xl, half_z ^ NEG2, xl);                      // xl cos x
+  const uint64_t rs = fadd2(tl, ffma2(fmul2(wh, zh), ps, turn_xl));
+  const uint64_t s1 = fadd2(xh, th), es = fadd2(th, fadd2(s1, xh ^ NEG2) ^ NEG2);
+  const uint64_t sn = fadd2(s1, fadd2(es, rs));
+  uint64_t pc = ffma2(zh, dup2(-2.7557319e-7f), dup2(2.4801587e-5f));         // 1/10!, 1/8!
+  pc = ffma2(zh, pc, dup2(-1.3888889e-3f));
+  pc = ffma2(zh, pc, dup2(4.1666667e-2f));
+  const uint64_t one = dup2(1.f);
+  const uint64_t c1 = fadd2(one, half_z ^ NEG2), ec = fadd2(fadd2(one, c1 ^ NEG2), half_z ^ NEG2);
+  const uint64_t rc = ffma2(fmul2(zh, zh), pc, ffma2(zl, dup2(-0.5f), fmul2(xh, xl) ^ NEG2));
+  const uint64_t cn = fadd2(c1, fadd2(ec, rc));
+  const uint64_t sc = dup2(scale);
+  float sa, sb, ca, cb, so0, so1, co0, co1;
+  f2unpack(fmul2(sn, sc), sa, sb);
+  f2unpack(fmul2(cn, sc), ca, cb);
+  place_quarter(q0, sa, ca, so0, co0);
+  place_quarter(q1, sb, cb, so1, co1);
+  s2 = f2pack(so0, so1);
+  c2 = f2pack(co0, co1);
+}
+__device__ __forceinline__ void angles_rounded_at(Angles& f, uint32_t pos, const long long* turns8, float rot_scale) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const ulonglong2 t2 = __ldg(reinterpret_cast<const ulonglong2*>(turns8) + j);
+    sincos_turns2_rounded(pos * t2.x, pos * t2.y, rot_scale, f.s[j], f.c[j]);
+  }
+}
+
 // The same with a norm's weights multiplied in, for rows with many heads:
 // a' = a e0 + b e1, b' = b e2 + a e3 (e1, e3 only where the unit is turned).
 struct Factors {
@@ -311,6 +374,23 @@ __device__ __forceinline__ void turn(Unit16& x, const Angles& t) {
     const uint64_t a = x.a[i];
     x.a[i] = ffma2(x.b[i], t.s[i] ^ NEG2, fmul2(a, t.c[i]));
     x.b[i] = ffma2(a, t.s[i], fmul2(x.b[i], t.c[i]));
+  }
+}
+
+// The same with every product rounded before the sum (sums of single values, which the compiler never fuses with a product,
+// as it does packed ones).
+__device__ __forceinline__ uint64_t add_apart(uint64_t x, uint64_t y) {
+  float x0, x1, y0, y1;
+  f2unpack(x, x0, x1);
+  f2unpack(y, y0, y1);
+  return f2pack(__fadd_rn(x0, y0), __fadd_rn(x1, y1));
+}
+__device__ __forceinline__ void turn_rounded(Unit16& x, const Angles& t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t a = x.a[i];
+    x.a[i] = add_apart(fmul2(a, t.c[i]), fmul2(x.b[i], t.s[i] ^ NEG2));
+    x.b[i] = add_apart(fmul2(x.b[i], t.c[i]), fmul2(a, t.s[i]));
   }
 }
 
@@ -501,30 +581,72 @@ __device__ __forceinline__ void kv_block4(const AppendPagedParams& p, int block,
   // A scale's 16 neighbours are blocks 2i and 2i + 1 of eight elements. This thread has blocks c0 / 8 and c1 / 8, and the
   // other one of each pair may be another thread's of the same row: lane `from` has it, as its first or its second.
   const int turned = p.rot / 16;                                  // units that are
-  auto holder = [&](int k) { return k < turned ? k : k < 2 * turned ? k - turned : turned + (k - 2 * turned) / 2; };
+  auto holder = [&](int k) { return INTER ? k / 2 : k < turned ? k : k < 2 * turned ? k - turned : turned + (k - 2 * turned) / 2; };
+  auto piece_of = [&](int k) { return INTER ? k & 1 : k < turned ? 0 : k < 2 * turned ? 1 : k & 1; };  // first or second there
   const int k0 = (at.c0 / 8) ^ 1, k1 = (at.c1 / 8) ^ 1, from0 = holder(k0), from1 = holder(k1);
+  // A norm's sum of squares: elements 32 apart in order, then neighbours in pairs, whatever the rotation's layout. This thread
+  // adds up elements SPAN u .. SPAN u + SPAN - 1 and those 32, 64, .. on, which lie in pieces of the row's other threads.
+  constexpr int SPAN = 32 / LPR, CHAIN = D / 32;
+  int sq_at[CHAIN];
+#pragma unroll
+  for (int j = 0; j < CHAIN; ++j) {
+    const int k = 4 * j + SPAN * u / 8;
+    sq_at[j] = 16 * (piece_of(k) * nt + tid - u + holder(k)) + 2 * (SPAN * u % 8);  // (bytes)
+  }
   int slot = 0;
   for (int it = 0; it < rounds; ++it) {
     const int r = it * groups + grp;
     const bool ok = r < w.nrows;
     Angles t;
-    if (at.turned) angles_at(t, pos0 + r, p.turns + 8 * u, p.rot_scale);
+    if (at.turned) angles_rounded_at(t, pos0 + r, p.turns + 8 * u, p.rot_scale);
     const long long row = pbase + w.r0 + r;
     for (int h = 0; h < heads; ++h) {
       cp_async_wait<AP_KV_RING - 1>();
       const uint4* mine = ring + slot * 4 * nt + tid;
       Unit16 x = unpack16<INTER>(mine[0], mine[nt]);
       if (p.k_weight != nullptr) {
-        normalise<D>(x, p.eps);
+        __syncwarp();  // the row's other threads' copies have landed
+        uint64_t sq[SPAN / 2];
+#pragma unroll
+        for (int j = 0; j < CHAIN; ++j) {
+          const uint8_t* from = reinterpret_cast<const uint8_t*>(ring + slot * 4 * nt) + sq_at[j];
+          uint32_t y[SPAN / 2];
+          if constexpr (SPAN == 8) {
+            const uint4 z = *reinterpret_cast<const uint4*>(from);
+            y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
+          } else {
+            const uint2 z = *reinterpret_cast<const uint2*>(from);
+            y[0] = z.x, y[1] = z.y;
+          }
+#pragma unroll
+          for (int i = 0; i < SPAN / 2; ++i) {  // (squares of bf16 values are exact: one rounding, that of the sum)
+            const uint64_t e = f2pack(__uint_as_float(y[i] << 16), __uint_as_float(y[i] & 0xffff0000u));
+            sq[i] = j == 0 ? fmul2(e, e) : ffma2(e, e, sq[i]);
+          }
+        }
+        __syncwarp();  // (fetch may write the slot)
+        float part[SPAN / 2];
+#pragma unroll
+        for (int i = 0; i < SPAN / 2; ++i) {
+          float e0, e1;
+          f2unpack(sq[i], e0, e1);
+          part[i] = __fadd_rn(e0, e1);
+        }
+        float ss = __fadd_rn(part[0], part[1]);
+        if constexpr (SPAN == 8) ss = __fadd_rn(ss, __fadd_rn(part[2], part[3]));
+#pragma unroll
+        for (int o = 1; o < LPR; o *= 2) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+        const float rs = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+        const uint64_t rs2 = f2pack(rs, rs);
         const uint16_t* wt = static_cast<const uint16_t*>(p.k_weight);
         const Unit16 f = unpack16<INTER>(__ldg(reinterpret_cast<const uint4*>(wt + at.c0)), __ldg(reinterpret_cast<const uint4*>(wt + at.c1)));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x.a[j] = fmul2(x.a[j], f.a[j]);
-          x.b[j] = fmul2(x.b[j], f.b[j]);
+          x.a[j] = fmul2(fmul2(x.a[j], rs2), f.a[j]);
+          x.b[j] = fmul2(fmul2(x.b[j], rs2), f.b[j]);
         }
       }
-      if (at.turned) turn(x, t);
+      if (at.turned) turn_rounded(x, t);
       float y[16];
       in_order<INTER>(x, y);
       const uint4 y0 = pack8(y), y1 = pack8(y + 8);
