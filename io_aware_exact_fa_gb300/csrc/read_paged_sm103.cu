@@ -22,6 +22,9 @@ namespace fa {
 
 namespace {
 
+// All loads are __ldcg, past L1 and never through the read-only path: a large launch begins while the launch that writes these
+// rows, scales and lengths still runs, so the memory is not constant for its duration, and an SM's L1 may hold what that one
+// read there before (the scales of eight pages and heads share a sector).
 constexpr int RD_THREADS = 256;
 constexpr int RD_ROWS = 32;      // packed rows of a block
 constexpr int RD_FLIGHT = 4;     // units of K and V whose loads a thread has in flight
@@ -41,14 +44,14 @@ __device__ __forceinline__ void rd_load(Unit& x, const void* pages, const void* 
   constexpr int RB = paged_row_bytes(KIND, D);
   const uint8_t* at = static_cast<const uint8_t*>(pages) + row * RB + u * (RB / (D / 8));
   if constexpr (KIND == PAGES_BF16) {
-    x.a = __ldg(reinterpret_cast<const uint4*>(at));
+    x.a = __ldcg(reinterpret_cast<const uint4*>(at));
   } else if constexpr (KIND == PAGES_E4M3) {
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(at));
+    const uint2 c = __ldcg(reinterpret_cast<const uint2*>(at));
     x.a.x = c.x, x.a.y = c.y;
-    x.scale = __ldg(static_cast<const float*>(scales) + ph);
+    x.scale = __ldcg(static_cast<const float*>(scales) + ph);
   } else {
-    x.a.x = __ldg(reinterpret_cast<const uint32_t*>(at));
-    x.byte = __ldg(static_cast<const uint8_t*>(scales) + row * (D / 16) + u / 2);
+    x.a.x = __ldcg(reinterpret_cast<const uint32_t*>(at));
+    x.byte = __ldcg(static_cast<const uint8_t*>(scales) + row * (D / 16) + u / 2);
   }
 }
 
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(RD_THREADS) fa_read_paged_kernel(const ReadPag
   if (blockIdx.x == 0) {  // offsets that decrease or pass the tensors are reported; rows outside are left alone below
     bool bad = false;
     for (int b = tid; b < p.B; b += RD_THREADS) {
-      const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1), L = __ldg(p.seqlens + b);
+      const int lo = __ldcg(p.cu + b), hi = __ldcg(p.cu + b + 1), L = __ldcg(p.seqlens + b);
       bad = bad || lo < 0 || hi < lo || hi > p.total || L < 0 || L > static_cast<long long>(p.width) * p.page ||
             (L > 0 && hi - lo > L);
     }
@@ -103,18 +106,18 @@ __global__ void __launch_bounds__(RD_THREADS) fa_read_paged_kernel(const ReadPag
       int lo = 0, n = p.B;  // the last sequence that starts at or before row t
       while (n > 1) {
         const int half = n / 2;
-        if (__ldg(p.cu + lo + half) <= t) {
+        if (__ldcg(p.cu + lo + half) <= t) {
           lo += half;
           n -= half;
         } else {
           n = half;
         }
       }
-      const int first = __ldg(p.cu + lo), end = __ldg(p.cu + lo + 1);
-      const int L = __ldg(p.seqlens + lo);
+      const int first = __ldcg(p.cu + lo), end = __ldcg(p.cu + lo + 1);
+      const int L = __ldcg(p.seqlens + lo);
       const long long row = static_cast<long long>(L) - (static_cast<long long>(end) - t);
       if (t >= first && t < end && row >= 0 && row < static_cast<long long>(p.width) * p.page) {
-        const int id = __ldg(p.table + lo * p.table_stride + (row >> p.page_shift));
+        const int id = __ldcg(p.table + lo * p.table_stride + (row >> p.page_shift));
         if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages))
           base = static_cast<long long>(id) * p.Hkv * p.page + (row & (p.page - 1));
         else
