@@ -1,5 +1,6 @@
-"""Build libfa_gb300.so in-tree with nvcc for sm_103a (no cmake, no torch), and the binding's compiled part _binding.so with
-g++ against the installed torch's headers.
+"""Build libfa_gb300.so in-tree with nvcc for sm_103a (no cmake, no torch), and, where torch, its headers, Python's and a C++
+compiler are there, the binding's compiled part _binding.so. Without that part the binding makes the same calls in Python, with
+about twice the time on the host.
 
     python -m io_aware_exact_fa_gb300.build [--verbose] [--ptxas-info] [--debug]
 
@@ -57,8 +58,24 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
-def _build_binding(force: bool) -> None:
-    torch = os.path.realpath(list(importlib.util.find_spec("torch").submodule_search_locations)[0])
+def _build_binding(force: bool) -> bool:
+    """Builds _binding.so; False, with a line on stderr and no old one left, where that is not possible."""
+    try:
+        _compile_binding(force)
+        return True
+    except Exception as e:   # (the library does not need it)
+        sys.stderr.write(f"_binding.so was not built ({e}): the paged calls check their arguments in Python\n")
+        for old in (BINDING, BINDING_STAMP):
+            if os.path.exists(old):
+                os.remove(old)
+        return False
+
+
+def _compile_binding(force: bool) -> None:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("no torch")
+    torch = os.path.realpath(list(spec.submodule_search_locations)[0])
     with open(os.path.join(torch, "version.py")) as f:
         built_with = torch + "\n" + sys.version + "\n" + f.read()
     if not force and up_to_date(BINDING) and os.path.exists(BINDING_STAMP):

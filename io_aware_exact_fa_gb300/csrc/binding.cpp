@@ -8,7 +8,8 @@
  * twelve, and a new one 0.9 us: a decode step 8 us in place of 12, append and read
  * back 12.6 in place of 20.)
  *
- * A function that made its call returns (status, results). No exception leaves them. */
+ * A function that made its call returns (status, results). No C++ exception leaves them; where a result could not be
+ * allocated they return NULL with Python's exception set. */
 #define PY_SSIZE_T_CLEAN
 #ifdef FA_TORCH_CUDA
 #include <ATen/cuda/EmptyTensor.h>
@@ -21,6 +22,7 @@
 #include <math.h>
 #include <stddef.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "fa.h"
 
@@ -103,6 +105,9 @@ static int heads(PyObject* o, Tensor* t, int dims) {
   return tensor_of(o, t) && t->dtype == at::kBFloat16 && t->dims == dims && t->stride[dims - 1] == 1;
 }
 
+/* Bytes, or pairs of 4-bit values (by name: older torch has no such type). */
+static int fp4_bytes(at::ScalarType t) { return t == at::kByte || strcmp(c10::toString(t), "Float4_e2m1fn_x2") == 0; }
+
 typedef struct {
   Address p, s;
   int kind, pages, Hkv, page, d;
@@ -122,7 +127,7 @@ static int pool_of(PyObject* pages, PyObject* scale, int dev, Pool* x) {
   if (s.dtype == at::kByte) {
     if (p.shape[3] > 1024) return 0;
     x->kind = FA_PAGES_FP4, x->d *= 2;
-    return (p.dtype == at::kByte || p.dtype == at::kFloat4_e2m1fn_x2) && s.dims == 4 && s.shape[2] == p.shape[2] && s.shape[3] == x->d / 16;
+    return fp4_bytes(p.dtype) && s.dims == 4 && s.shape[2] == p.shape[2] && s.shape[3] == x->d / 16;
   }
   x->kind = FA_PAGES_E4M3;
   return s.dtype == at::kFloat && s.dims == 2 && (p.dtype == at::kFloat8_e4m3fn || p.dtype == at::kByte);
