@@ -520,8 +520,8 @@ fa_status fa_weigh_paged(const void* q, const int64_t* q_strides, const float* l
  *   new_weights  fp32 [B, Hkv, new_width] with rows new_weights_stride apart,
  *                new_width >= keep: the kept rows' weights, then zeros.
  * Rows of 4-bit and bf16 pages are copied as they are. The scale of a new e4m3 page is
- * the largest of its rows' old ones (positive factors), and codes of smaller scales
- * are rounded to it. Rows past the new length keep what the pages held. Pages outside
+ * the largest of its rows' old ones (factors >= 0, none NaN), and codes of smaller scales
+ * are rounded to it: code * (old / new), ratio and product in fp32, to the nearest code. Rows past the new length keep what the pages held. Pages outside
  * the pool are skipped, lengths over max_len clipped, and reported. Two launches.
  * Errors: FA_ERR_INVALID_ARG for NULL arrays, sizes, first + recent > keep, an unknown
  * kind, strides that do not hold the rows, or new_weights, new_seqlens or new_table

@@ -411,9 +411,9 @@ __global__ void __launch_bounds__(32 * EV_MOVE_WARPS) fa_evict_move_kernel(const
       ks[dst >> p.page_shift] = k_most;
       vs[dst >> p.page_shift] = v_most;
     }
-    // from here on: what the row's codes are multiplied with
-    k_old /= k_most;
-    v_old /= v_most;
+    // from here on: what the row's codes are multiplied with (where all scales are 0 all values are, and codes stay)
+    k_old = k_most > 0.f ? k_old / k_most : 1.f;
+    v_old = v_most > 0.f ? v_old / v_most : 1.f;
   }
   const unsigned live = __ballot_sync(ALL, src >= 0);
   const int piece = lane % CR, lr = lane / CR;
@@ -431,17 +431,23 @@ __global__ void __launch_bounds__(32 * EV_MOVE_WARPS) fa_evict_move_kernel(const
       const int r = i * RPL + lr;
       const bool there = (live >> r) & 1u;
       if constexpr (KIND == PAGES_E4M3) {
-        // In f16: for powers of two exact down to 2^-24, far below half the least code (2^-10), so the one rounding is that
-        // to e4m3; other ratios are off by 2^-11 of themselves. NaN codes stay NaN.
+        // In fp32: exact for powers of two, so the one rounding is that to e4m3; other ratios and products are off by 2^-24 of
+        // themselves before it (in f16, by 2^-11 each, 0.4 % of the codes came out as their neighbours). NaN codes stay NaN.
         const float f = __shfl_sync(ALL, factor, r);
         if (there && f != 1.f) {
-          const uint32_t f2 = pack_f16x2(f, f);
+          const uint64_t f2 = f2pack(f, f);
           uint32_t* w[4] = {&y[i].x, &y[i].y, &y[i].z, &y[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            uint32_t h0, h1;
-            e4m3x4_to_f16x2x2(*w[e], h0, h1);
-            *w[e] = f16x2x2_to_e4m3x4(hmul2_bits(h0, f2), hmul2_bits(h1, f2));
+            uint32_t h[2];
+            e4m3x4_to_f16x2x2(*w[e], h[0], h[1]);
+            float z[4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[x]));
+              f2unpack(fmul2(f2pack(a.x, a.y), f2), z[2 * x], z[2 * x + 1]);
+            }
+            *w[e] = pack_e4m3x4(z[0], z[1], z[2], z[3]);
           }
         }
       }
