@@ -524,8 +524,8 @@ fa_status fa_weigh_paged(const void* q, const int64_t* q_strides, const float* l
  * are rounded to it: code * (old / new), ratio and product in fp32, to the nearest code. Rows past the new length keep what the pages held. Pages outside
  * the pool are skipped, lengths over max_len clipped, and reported. Two launches.
  * Errors: FA_ERR_INVALID_ARG for NULL arrays, sizes, first + recent > keep, an unknown
- * kind, strides that do not hold the rows, or new_weights, new_seqlens or new_table
- * that are the arrays read; FA_ERR_UNSUPPORTED as for fa_append_paged. */
+ * kind, strides that do not hold the rows, new_weights that share an element with the
+ * weights read, or new_seqlens or new_table that are the arrays read; FA_ERR_UNSUPPORTED as for fa_append_paged. */
 fa_status fa_evict_paged(const float* weights, int64_t weights_stride, void* k_pages, void* v_pages, void* k_scale,
                          void* v_scale, int kind, const int* block_table, int64_t table_stride, const int* seqlens_k,
                          const int* offsets, const int* new_table, int64_t new_table_stride, int* kept,

@@ -875,6 +875,17 @@ bool rows_apart(const int64_t* strides, const int* extents, int dims, int d) {
   return true;
 }
 
+// Whether two arrays of `rows` fp32 rows share an element: rows of a_len, `a_step` apart from `a` on, and those of b. (Columns of
+// one wider array, with equal steps, do not.)
+bool rows_meet(const float* a, int64_t a_step, int64_t a_len, const float* b, int64_t b_step, int64_t b_len, int64_t rows) {
+  if (a_len == 0 || b_len == 0) return false;
+  const int64_t ahead = (reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / 4;  // of b's first element
+  if (ahead >= (rows - 1) * a_step + a_len || -ahead >= (rows - 1) * b_step + b_len) return false;
+  if (rows == 1 || a_step != b_step) return true;
+  const int64_t column = (ahead % a_step + a_step) % a_step;
+  return column < a_len || column + b_len > a_step;
+}
+
 fa_status append_paged(int kind, const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pages,
                        void* v_pages, void* k_scale, void* v_scale, const int* block_table, int64_t table_stride,
                        const int* seqlens_k, const int* cu_seqlens, const int* offsets, const int64_t* turns,
@@ -1197,6 +1208,8 @@ fa_status fa_evict_paged(const float* weights, int64_t weights_stride, void* k_p
   const long long pairs = static_cast<long long>(B) * Hkv;
   if (pairs > 1 && (weights_stride < max_len || new_weights_stride < new_width))
     return fail(FA_ERR_INVALID_ARG, "weights_stride is below max_len or new_weights_stride below the new rows");
+  if (rows_meet(weights, weights_stride, max_len, new_weights, new_weights_stride, new_width, pairs))
+    return fail(FA_ERR_INVALID_ARG, "new_weights overlaps the weights that the call reads");
   if (pairs * 8 > INT_MAX || pairs * ((static_cast<long long>(keep) + 15) / 16) > INT_MAX)
     return fail(FA_ERR_INVALID_ARG, "B, Hkv and keep give too many blocks");
 
