@@ -265,7 +265,9 @@ __global__ void __launch_bounds__(EV_THREADS, 1024 / EV_THREADS) fa_evict_select
   }
   __syncwarp();
   const uint32_t listed = sh.listed[warp];
-  // every key of that digit in the warp's run (too many for the list, most weights alike: looked for again)
+  // Every key of that digit in the warp's run. The digit has four bins an octave and a list 128 or 256 keys, so weights within
+  // an octave or so overflow it, and the run is looked through again in each of the three steps left: 7 us more (2
+  // sequences of 110k, 32768 kept, all weights in one bin: 66 in place of 59 us; 32 of 12k 86 in place of 81).
   auto each = [&](auto&& f) {
     if (listed <= LIST) {
       for (uint32_t i = lane; i < listed; i += 32) f(sh.list[warp * LIST + i]);

@@ -63,8 +63,9 @@ __device__ __forceinline__ uint32_t fp4_scale_byte(uint32_t amax, float& inv) {
 }
 
 // Eight bf16 values (pairs in order) to eight codes. x * inv is off from x / s by less than 2^-23 of it, and x / s (eight
-// significant bits over four) is a border between two codes or at least 2^-8 of one away from it: rounding to a multiple
-// of 2^-11 first (the spacing of fp32 at 6144) puts it back on the border, where the tie goes to the even code.
+// significant bits over four) is a border between two codes or at least 2^-10 away from it (255 2^-7 over 8
+// from 1/4; every pair was looked at): rounding to a multiple of 2^-11 first (the spacing of fp32 at 6144) puts it back on
+// the border, where the tie goes to the even code, and leaves the others on their side.
 __device__ __forceinline__ uint32_t fp4_codes8(uint4 x, float inv) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   const uint64_t i2 = f2pack(inv, inv), up = f2pack(6144.f, 6144.f), down = f2pack(-6144.f, -6144.f);

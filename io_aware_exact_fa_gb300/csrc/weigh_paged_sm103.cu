@@ -28,7 +28,11 @@
 //
 // The rule's 16 rows: over 16 sequences of 1-16k keys, 8 heads, 4-bit / e4m3 / bf16, d = 128,
 // 16 rows a head take 25 / 38 / 74 us from registers and 29 / 40 / 71 in tensor memory;
-// 8 rows 25 / 31 / 50 against 35 / 37 / 53. (From registers more rows do not fit.)
+// 8 rows 25 / 31 / 50 against 35 / 37 / 53. (From registers more rows do not fit.) bf16 of d = 128 with 9 to 16 rows
+// is 2 to 5 % faster in tensor memory where keys are many (143 against 138 us for 64 sequences of 4-8k), but a third slower
+// where they are few (6.4 against 8.4 us for one of 700 keys, 22.6 against 28.9 for 200 of up to 300), and the host does not
+// see the lengths: it stays with the registers. bf16 of d = 128 in tensor memory, 64 rows 57 us, 128 rows 86: a row's 256 bytes
+// leave one stage at four blocks an SM, and 64 bytes of registers are spilled.
 #include <type_traits>
 
 #include "fp4.cuh"
