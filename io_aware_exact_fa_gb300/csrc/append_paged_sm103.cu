@@ -43,8 +43,8 @@
 // arithmetic; with one kind of block for both 147 us in place of 132), launch and
 // load latency for a step of single tokens. Measured, 32 query and 8 K/V heads,
 // d = 128, e4m3: 26.7k prompt tokens with norms 115 us (5.7 TB/s, 0.85 of the copy
-// rate); 256 sequences of one token 8.1 us; 4-bit: 26k prompt tokens 106 us (114 with a K/V
-// block for each head, like e4m3).
+// rate); 256 sequences of one token 8.1 us; 4-bit: 26k prompt tokens 112 us (132 with a K/V
+// block for each head, like e4m3; 106 with fused products and less exact angles).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -916,8 +916,8 @@ static cudaError_t ap_launch(AppendPagedParams p, cudaStream_t stream) {
   p.q_slots = slots;
   if constexpr (KIND == PAGES_FP4) {
     // K/V heads of a block, which share a row's angles: as long as a page's rows fill the block, two blocks an SM (a third of
-    // the query blocks wanted) are left, and a block has no more than eight turns. 26k prompt tokens, 32/8 heads: pages of 64
-    // with 1, 2, 4, 8 heads 114, 107, 106, 119 us; 10k in pages of 16 and 128 (read back too) 78, 68, 62, 64 and 79, 75, 78, 92.
+    // the query blocks wanted) are left, and a block has no more than eight turns. 26k prompt tokens, 32/8 heads, 1, 2, 4, 8
+    // heads: pages of 64 132, 114, 112, 122 us; pages of 16 149, 124, 109, 104; pages of 128 127, 121, 127, 126.
     const long long pages = p.kv_blocks / p.Hkv;
     const int rounds = (p.max_rows + groups - 1) / groups;
     p.kv_heads = 1;

@@ -42,10 +42,14 @@
 // kernel joins the parts. About 8 us of a call are fixed: launches, the chain
 // lengths -> page -> first tile, the merge.
 //
-// 4-bit pages are bound by instructions: 11 of a warp's 19.6 for a key (d = 128) turn codes
-// into f16 (a word of 8 codes: 4 conversions, 3 moves, 4 multiplications). 64 sequences of
-// 4-8k take 92 us, 0.72 of the bytes' time. Measured and not kept: tiles of 32 keys 101 us,
-// two chains of products 93, the softmax in halves of a tile 93, bulk copies 97.
+// 4-bit pages are bound by latency: no unit is full (64 sequences of 4-8k, d = 128: issue
+// slots 60 %, ALU 50, DRAM 65; 4 tokens over long ones, d = 64: 58, 45, 37). A warp's tile is
+// one chain of conversions, products, maxima, exponentials, transposes and products, and
+// three warps a scheduler cover each other's waits only in part; conversions (4 a word of 8
+// codes, with 3 moves and 4 multiplications) are 11 of its 19.6 instructions a key and so most
+// of the chain. 64 sequences take 92 us, 0.72 of the bytes' time. Measured and not kept: tiles
+// of 32 keys 101 us, two chains of products 93, the softmax in halves of a tile 93, bulk
+// copies 97. (Two tiles in one warp at once were not tried.)
 //
 // A tile's 16-key groups may lie in different pages; one lane per group looks the
 // page up, a tile ahead. The fragments are read straight from the copied rows: the

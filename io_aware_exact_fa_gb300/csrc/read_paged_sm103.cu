@@ -28,8 +28,8 @@ namespace {
 constexpr int RD_THREADS = 256;
 constexpr int RD_ROWS = 32;      // packed rows of a block
 constexpr int RD_FLIGHT = 4;     // units of K and V whose loads a thread has in flight
-// Blocks from which on the launch is a dependent one, beside the tail of what comes before: it saves the GPU 1 to 2 us (137 ->
-// 135 us for 26k rows appended and read back, 62 -> 60 for 9 chunks) and costs the host 3 to 5 (12 -> 16 us for 8 rows).
+// Blocks from which on the launch is a dependent one, beside the tail of what comes before: it saves the GPU 1 to 3 us (143.5 ->
+// 142 us for 26k rows appended and read back, 64 -> 62 for 9 chunks, 122 -> 120 behind an eviction) and costs the host 3 to 5 (12 -> 16 us for 8 rows).
 constexpr unsigned RD_BESIDE = 512;
 
 // Eight elements as they lie in the page: 16, 8 or 4 bytes, and their scale (4-bit rows: its byte).
