@@ -178,3 +178,17 @@ def test_selection_of_weights_that_are_nearly_alike(fa, B, Hkv, L, keep, spread)
     assert fa.device_status() == fa.FA_OK
     top = w.sort(dim=-1, descending=True, stable=True).indices[..., :keep].sort(dim=-1).values
     assert torch.equal(kept, top.int()) and torch.equal(nw, w.gather(2, top))
+
+
+@pytest.mark.skipif(not hasattr(torch, "float4_e2m1fn_x2"), reason="a torch without the type")
+def test_pairs_of_4bit_values_as_their_own_type(fa):
+    """Pages of float4_e2m1fn_x2 are taken by the compiled checks too, and read as the same bytes."""
+    s = state(fa, "fp4", 3)
+    pages = [x.view(torch.float4_e2m1fn_x2) for x in (s["kp"], s["vp"])]
+    want = fa.read_paged(s["kp"], s["vp"], s["table"], s["lens"], s["cu"], 431, k_scale=s["ks"], v_scale=s["vs"])
+    r = fa._binding.read(*pages, s["table"], s["lens"], s["cu"], 431, s["ks"], s["vs"], None, None, None)
+    if hasattr(fa._binding, "__file__"):
+        assert r is not NotImplemented and r[0] == fa.FA_OK
+        assert all(torch.equal(a, b) for a, b in zip(want, r[1]))
+    got = fa.read_paged(*pages, s["table"], s["lens"], s["cu"], 431, k_scale=s["ks"], v_scale=s["vs"])
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and fa.device_status() == fa.FA_OK
